@@ -7,7 +7,8 @@ There is no CPU fallback: importing fails loudly when the library is missing.
 
 The names mirror the C ABI in ``include/pop_ffn.h`` (``pop_ffn_create``,
 ``pop_prefill_partition``, ``pop_decode_step``, ``pop_ffn_dense_ref``, ...);
-``PopFFN`` wraps a handle for convenience.
+``PopFFN`` wraps a handle for convenience. Routing (``PopRouter``, ``include/pop_route.h``) and the
+8-bit operators (``quantize_rows``, ``PopQLinear``, ``PopQMoE``, ``include/pop_quant.h``) follow below.
 """
 from __future__ import annotations
 
@@ -20,6 +21,9 @@ LIB_PATH = os.path.join(_PKG, "libpopffn.so")
 POP_OK, POP_ERR_INVALID_ARG, POP_ERR_STATE, POP_ERR_CUDA, POP_ERR_OOM, POP_ERR_TIMEOUT, POP_ERR_UNSUPPORTED, \
     POP_ERR_DEVICE = range(8)
 POP_MAX_D, POP_MAX_D_FF, POP_MAX_BATCH, POP_STATIC_MAX_D_FF = 16384, 49152, 64, 49152
+POP_ROUTE_SOFTMAX, POP_ROUTE_SIGMOID = 0, 1
+POP_ROUTE_MAX_EXPERTS, POP_ROUTE_MAX_TOP_K = 256, 16
+POP_QUANT_BLOCK, POP_QUANT_MAX_DIM, POP_QMOE_MAX_EXPERTS, POP_QMOE_MAX_TOP_K = 128, 65536, 256, 16
 
 
 class pop_config(ctypes.Structure):
@@ -36,6 +40,21 @@ class pop_counts(ctypes.Structure):
         return {f: getattr(self, f) for f, _ in self._fields_}
 
 
+class pop_route_config(ctypes.Structure):
+    _fields_ = [("n_experts", ctypes.c_int), ("top_k", ctypes.c_int), ("score", ctypes.c_int),
+                ("n_groups", ctypes.c_int), ("top_groups", ctypes.c_int), ("group_sum", ctypes.c_int),
+                ("renorm", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class pop_qlinear_config(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int), ("K", ctypes.c_int), ("max_tokens", ctypes.c_int), ("out_f32", ctypes.c_int)]
+
+
+class pop_qmoe_config(ctypes.Structure):
+    _fields_ = [("n_experts", ctypes.c_int), ("top_k", ctypes.c_int), ("D", ctypes.c_int), ("D_FF", ctypes.c_int),
+                ("max_tokens", ctypes.c_int), ("out_f32", ctypes.c_int)]
+
+
 class PopError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"{status_name(status)}: {message}")
@@ -43,6 +62,7 @@ class PopError(RuntimeError):
 
 
 _vp, _i32, _f64, _u64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_double, ctypes.c_uint64
+_i64 = ctypes.c_longlong
 _ip, _fp = ctypes.POINTER(ctypes.c_int), ctypes.POINTER(ctypes.c_float)
 SIGNATURES = {
     "pop_region_counts": (_i32, [_i32, _f64, _f64, ctypes.POINTER(pop_counts)]),
@@ -79,6 +99,21 @@ SIGNATURES = {
     "pop_moe_check": (_i32, [_vp]),
     "pop_moe_set_concurrent": (_i32, [_vp, _i32]),
     "pop_moe_last_error": (ctypes.c_char_p, [_vp]),
+    # routing (include/pop_route.h)
+    "pop_route": (_i32, [ctypes.POINTER(pop_route_config), _vp, _i32, _i64, _vp, _i32, _vp, _vp, _vp, _vp]),
+    "pop_route_last_error": (ctypes.c_char_p, []),
+    # 8-bit operators (include/pop_quant.h)
+    "pop_quantize_rows": (_i32, [_vp, _i32, _i64, _i32, _i32, _vp, _i64, _vp, _vp]),
+    "pop_qlinear_create": (_i32, [ctypes.POINTER(pop_qlinear_config), _vp, _vp, _vp, ctypes.POINTER(_vp)]),
+    "pop_qlinear_destroy": (None, [_vp]),
+    "pop_qlinear_forward": (_i32, [_vp, _vp, _i64, _i32, _vp, _i64, _vp]),
+    "pop_qlinear_forward_quantized": (_i32, [_vp, _vp, _i64, _vp, _i64, _i32, _vp, _i64, _vp]),
+    "pop_qlinear_check": (_i32, [_vp]),
+    "pop_qmoe_create": (_i32, [ctypes.POINTER(pop_qmoe_config)] + [ctypes.POINTER(_vp)] * 6 + [_vp, ctypes.POINTER(_vp)]),
+    "pop_qmoe_destroy": (None, [_vp]),
+    "pop_qmoe_forward": (_i32, [_vp, _vp, _i64, _vp, _vp, _i32, _vp, _i64, _vp]),
+    "pop_qmoe_check": (_i32, [_vp]),
+    "pop_quant_last_error": (ctypes.c_char_p, []),
 }
 
 _lib = None
@@ -457,6 +492,252 @@ class PopMoE:
         """Experts' decode kernels on streams of their own (True, the default) or one after another
         on the caller's stream (False: for per-kernel timing)."""
         _check_moe(load_library().pop_moe_set_concurrent(self.handle, 1 if on else 0), self.handle)
+
+
+# ------------------------------------------------------------------ routing
+
+def _check_with(last_error: str, status: int):
+    if status != POP_OK:
+        msg = getattr(load_library(), last_error)()
+        raise PopError(status, msg.decode() if msg else "")
+
+
+def _bad(what: str):
+    raise PopError(POP_ERR_INVALID_ARG, what)
+
+
+def _rows_arg(t, name, dtypes, cols, align):
+    """Checks a [rows, cols] CUDA tensor whose elements of a row are contiguous (the rows may lie
+    farther apart). Returns its row stride in elements."""
+    if t.dtype not in dtypes or t.dim() != 2 or t.shape[1] != cols or not t.is_cuda:
+        _bad(f"{name}: expected a CUDA tensor of shape (*, {cols}) and type {' or '.join(map(str, dtypes))}, got "
+             f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    if (cols > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < cols):
+        _bad(f"{name}: the elements of a row must be contiguous, its rows apart; strides are {tuple(t.stride())}")
+    ld = t.stride(0) if t.shape[0] > 1 else -(-cols // 8) * 8
+    if align > 1 and t.shape[0] > 0 and (t.data_ptr() % align or (ld * t.element_size()) % align):
+        _bad(f"{name}: rows must start on {align}-byte boundaries")
+    return ld
+
+
+def _whole_arg(t, name, dtype, shape):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or not t.is_cuda:
+        _bad(f"{name}: expected a contiguous CUDA {dtype} tensor of shape {tuple(shape)}, got {t.dtype} "
+             f"{tuple(t.shape)} on {t.device}")
+
+
+class _On:
+    """The stream of a call. New outputs belong to it, and inputs that another stream allocated are not
+    given to others before it is done with them."""
+
+    def __init__(self, stream, *inputs):
+        import torch
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+        self.stream, here = stream, torch.cuda.current_stream()
+        self.other = stream is not None and stream.cuda_stream != here.cuda_stream
+        self.raw = here.cuda_stream if stream is None else stream.cuda_stream
+        if self.other:
+            for t in inputs:
+                if t is not None:
+                    t.record_stream(stream)
+
+    def empty(self, shape, dtype, device):
+        import torch
+        if not self.other:
+            return torch.empty(shape, dtype=dtype, device=device)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=device)
+
+
+class PopRouter:
+    """Routes tokens to experts (``pop_route``): softmax or sigmoid scores, an optional bias for
+    balance, groups of experts, the ``top_k`` best, their weights. ``include/pop_route.h`` has the
+    formulas and what masked experts, ties and rows without an expert give."""
+
+    def __init__(self, n_experts: int, top_k: int, score: str = "softmax", n_groups: int = 1, top_groups: int = 1,
+                 group_sum: int = 1, renorm: bool = True, scale: float = 1.0):
+        kinds = {"softmax": POP_ROUTE_SOFTMAX, "sigmoid": POP_ROUTE_SIGMOID}
+        if score not in kinds:
+            _bad(f"score must be 'softmax' or 'sigmoid', got {score!r}")
+        self.cfg = pop_route_config(n_experts=n_experts, top_k=top_k, score=kinds[score], n_groups=n_groups,
+                                    top_groups=top_groups, group_sum=group_sum, renorm=1 if renorm else 0, scale=scale)
+
+    def route(self, logits, bias=None, counts=None, stream=None):
+        """logits: [T, n_experts] float32 or bf16 (rows may be strided); bias: float32 [n_experts];
+        counts: int32 [n_experts] that receives the slots given to each expert.
+        Returns (experts int32 [T, top_k], weights float32 [T, top_k])."""
+        import torch
+        E, k = self.cfg.n_experts, self.cfg.top_k
+        ld = _rows_arg(logits, "logits", (torch.float32, torch.bfloat16), E, 1)
+        if bias is not None:
+            _whole_arg(bias, "bias", torch.float32, (E,))
+        if counts is not None:
+            _whole_arg(counts, "counts", torch.int32, (E,))
+        T = logits.shape[0]
+        on = _On(stream, logits, bias, counts)
+        experts = on.empty((T, k), torch.int32, logits.device)
+        weights = on.empty((T, k), torch.float32, logits.device)
+        _check_with("pop_route_last_error", load_library().pop_route(
+            ctypes.byref(self.cfg), _ptr(logits), 1 if logits.dtype == torch.bfloat16 else 0, ld, _ptr(bias), T,
+            _ptr(experts), _ptr(weights), _ptr(counts), on.raw))
+        return experts, weights
+
+
+# ------------------------------------------------------------------ 8-bit operators
+
+def _check_quant(status: int):
+    _check_with("pop_quant_last_error", status)
+
+
+def _blocks(n: int) -> int:
+    return -(-n // POP_QUANT_BLOCK)
+
+
+def quantize_rows(x, stream=None):
+    """x: [M, K] bf16 or float32, K a multiple of 8 (rows may be strided). Returns (q float8_e4m3fn
+    [M, K], scales float32 [M, ceil(K/128)]): element (m, k) stands for scales[m, k // 128] * q[m, k]."""
+    import torch
+    if x.dim() != 2:
+        _bad(f"x: expected two dimensions, got {tuple(x.shape)}")
+    M, K = x.shape
+    ld = _rows_arg(x, "x", (torch.bfloat16, torch.float32), K, 16)
+    on = _On(stream, x)
+    q = on.empty((M, K), torch.float8_e4m3fn, x.device)
+    s = on.empty((M, _blocks(K)), torch.float32, x.device)
+    _check_quant(load_library().pop_quantize_rows(_ptr(x), 1 if x.dtype == torch.float32 else 0, ld, M, K, _ptr(q), K,
+                                                  _ptr(s), on.raw))
+    return q, s
+
+
+class _QHandle:
+    """Owns a handle of include/pop_quant.h."""
+    _destroy = _checker = ""
+    handle = None
+
+    def close(self):
+        if self.handle:
+            getattr(load_library(), self._destroy)(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def out_dtype(self):
+        import torch
+        return torch.float32 if self.cfg.out_f32 else torch.bfloat16
+
+    def check(self):
+        """Syncs and raises the first device-side failure since the last check."""
+        _check_quant(getattr(load_library(), self._checker)(self.handle))
+
+    def _output(self, y, rows, cols, device, on, align):
+        """(y, its row stride): a new [rows, cols] tensor, or the caller's, checked."""
+        if y is None:
+            y = on.empty((rows, cols), self.out_dtype(), device)
+        if y.dim() != 2 or y.shape[0] != rows:
+            _bad(f"y: expected {rows} rows, got {tuple(y.shape)}")
+        return y, _rows_arg(y, "y", (self.out_dtype(),), cols, align)
+
+
+def _matrix_arg(W, S, name):
+    """Checks one matrix: bf16 [N, K] (S None), or e4m3 [N, K] with float32 scales S."""
+    import torch
+    if W.dim() != 2:
+        _bad(f"{name}: expected a matrix, got {tuple(W.shape)}")
+    _whole_arg(W, name, torch.bfloat16 if S is None else torch.float8_e4m3fn, W.shape)
+    if S is not None:
+        _whole_arg(S, name + " scales", torch.float32, (_blocks(W.shape[0]), _blocks(W.shape[1])))
+
+
+class PopQLinear(_QHandle):
+    """y = x W^T with W kept in e4m3 and a scale per 128 x 128 block (``pop_qlinear``).
+
+    W: torch bf16 [N, K], quantised here, or float8_e4m3fn [N, K] with float32 scales S
+    [ceil(N/128), ceil(K/128)]. The handle keeps its own copy. max_tokens: rows that the workspace is
+    made for; longer calls run in chunks."""
+    _destroy, _checker = "pop_qlinear_destroy", "pop_qlinear_check"
+
+    def __init__(self, W, S=None, max_tokens: int = 2048, out_f32: bool = False, stream=None):
+        _matrix_arg(W, S, "W")
+        self.N, self.K = W.shape
+        self.cfg = pop_qlinear_config(N=self.N, K=self.K, max_tokens=max_tokens, out_f32=1 if out_f32 else 0)
+        h = _vp()
+        _check_quant(load_library().pop_qlinear_create(ctypes.byref(self.cfg), _ptr(W), _ptr(S), _stream(stream),
+                                                       ctypes.byref(h)))
+        self.handle = h.value
+
+    def forward(self, x, y=None, stream=None):
+        """x: bf16 [M, K], quantised on the way. Returns y [M, N] of out_dtype()."""
+        import torch
+        ld = _rows_arg(x, "x", (torch.bfloat16,), self.K, 16)
+        on = _On(stream, x, y)
+        y, ldy = self._output(y, x.shape[0], self.N, x.device, on, 1)
+        _check_quant(load_library().pop_qlinear_forward(self.handle, _ptr(x), ld, x.shape[0], _ptr(y), ldy, on.raw))
+        return y
+
+    def forward_q(self, xq, xs, y=None, stream=None):
+        """The same for rows that quantize_rows gave: xq float8_e4m3fn [M, K], xs float32."""
+        import torch
+        ldq = _rows_arg(xq, "xq", (torch.float8_e4m3fn,), self.K, 8)
+        lds = _rows_arg(xs, "xs", (torch.float32,), _blocks(self.K), 1)
+        if xs.shape[0] != xq.shape[0]:
+            _bad(f"xs: expected {xq.shape[0]} rows, got {xs.shape[0]}")
+        on = _On(stream, xq, xs, y)
+        y, ldy = self._output(y, xq.shape[0], self.N, xq.device, on, 1)
+        _check_quant(load_library().pop_qlinear_forward_quantized(self.handle, _ptr(xq), ldq, _ptr(xs), lds,
+                                                                  xq.shape[0], _ptr(y), ldy, on.raw))
+        return y
+
+
+class PopQMoE(_QHandle):
+    """Gated-MLP experts in e4m3 with a scale per block (``pop_qmoe``), for tokens that a router has
+    given experts and weights.
+
+    Wg, W1: [D_FF, D] per expert, W2: [D, D_FF] per expert. Each is a sequence (or a stacked tensor) of
+    bf16 matrices, quantised here, or a pair of such sequences: float8_e4m3fn matrices and their scales."""
+    _destroy, _checker = "pop_qmoe_destroy", "pop_qmoe_check"
+
+    def __init__(self, Wg, W1, W2, top_k: int, max_tokens: int = 2048, out_f32: bool = False, stream=None):
+        scaled = [isinstance(w, tuple) and len(w) == 2 and w[0][0].dim() == 2 for w in (Wg, W1, W2)]
+        if any(scaled) and not all(scaled):
+            _bad("Wg, W1 and W2 must all be bf16 or all be (e4m3, scales) pairs")
+        mats = [list(w[0]) if all(scaled) else list(w) for w in (Wg, W1, W2)]
+        scales = [list(w[1]) for w in (Wg, W1, W2)] if all(scaled) else [[None] * len(m) for m in mats]
+        self.E = len(mats[0])
+        if self.E < 1 or any(len(m) != self.E for m in mats + scales):
+            _bad("Wg, W1, W2 and their scales must have one entry per expert")
+        self.N, self.D = mats[0][0].shape
+        for name, ms, ss, shape in zip(("Wg", "W1", "W2"), mats, scales,
+                                       ((self.N, self.D), (self.N, self.D), (self.D, self.N))):
+            for m, s in zip(ms, ss):
+                _matrix_arg(m, s, name)
+                if tuple(m.shape) != shape:
+                    _bad(f"{name}: expected matrices of shape {shape}, got {tuple(m.shape)}")
+        self.cfg = pop_qmoe_config(n_experts=self.E, top_k=top_k, D=self.D, D_FF=self.N, max_tokens=max_tokens,
+                                   out_f32=1 if out_f32 else 0)
+        arrays = [(_vp * self.E)(*[_ptr(m) for m in ms]) for ms in mats]
+        arrays += [(_vp * self.E)(*[_ptr(s) for s in ss]) if all(scaled) else None for ss in scales]
+        h = _vp()
+        _check_quant(load_library().pop_qmoe_create(ctypes.byref(self.cfg), *arrays, _stream(stream), ctypes.byref(h)))
+        self.handle = h.value
+
+    def forward(self, x, experts, weights, y=None, stream=None):
+        """x: bf16 [T, D]; experts int32 and weights float32 [T, top_k], as PopRouter.route gives them.
+        Returns y [T, D] of out_dtype()."""
+        import torch
+        ld = _rows_arg(x, "x", (torch.bfloat16,), self.D, 16)
+        T = x.shape[0]
+        _whole_arg(experts, "experts", torch.int32, (T, self.cfg.top_k))
+        _whole_arg(weights, "weights", torch.float32, (T, self.cfg.top_k))
+        on = _On(stream, x, experts, weights, y)
+        y, ldy = self._output(y, T, self.D, x.device, on, 16)
+        _check_quant(load_library().pop_qmoe_forward(self.handle, _ptr(x), ld, _ptr(experts), _ptr(weights), T, _ptr(y),
+                                                     ldy, on.raw))
+        return y
 
 
 load_library()

@@ -1,0 +1,94 @@
+// Internal interface of the routing and 8-bit operators (pop_route.h, pop_quant.h).
+//
+// Operand images. The 8-bit products take both operands as shared-memory images: a k-block (128 values
+// of k) of a run of rows is `rows` x 128 bytes in the 128-byte swizzle (row r's 16-byte chunk c lies at
+// chunk c ^ (r % 8)), one contiguous piece of memory that a bulk copy brings into place as it is.
+//   - a matrix [N, K]: tiles of 128 rows, [ceil(N/128)][ceil(K/128)][16 KB]; rows past N and bytes past K
+//     are zero. Its scales are [ceil(N/128)][ceil(K/128)] float32. The gate and up matrices of a gated MLP
+//     share one image, [tile][k-block][gate 16 KB | up 16 KB], and their scales [tile][k-block][2].
+//   - rows (tokens): runs of G rows (G = 16 or 128), [run][k-block][G x 128 bytes]; scales
+//     [k-block][row]. Bytes past K are zero; what rows without a token hold is not used.
+// Tokens of an expert stand together: expert e's rows are the runs [run0[e], run0[e + 1]).
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "pop_quant.h"
+
+namespace pop {
+
+// POP_OK if the current device is a GB300 (sm_103). Looked up once per device.
+pop_status device_supported();
+
+constexpr int QB = 128;              // block of a scale, and of an operand image in k
+constexpr int QTILE = QB * QB;       // bytes of a 128 x 128 image
+__host__ __device__ constexpr int qceil(int a, int b) { return (a + b - 1) / b; }
+
+// Byte of (row, k) within an image of 128-byte rows.
+__host__ __device__ constexpr uint32_t image_at(uint32_t row, uint32_t k) {
+  return row * 128u + ((((k >> 4) ^ row) & 7u) << 4) + (k & 15u);
+}
+
+struct QRowsArgs {       // rows to quantise, or in e4m3 already
+  const void* x;
+  long long ldx;         // elements between rows
+  int kind;              // 0 bf16, 1 float32, 2 e4m3 with scales xs
+  const float* xs;
+  long long lds;
+  int M, K;
+};
+struct QRowsOut {
+  uint8_t* q;            // plain: [M][ldq]; image: runs of G rows
+  float* s;              // plain: [M][KB]; image: [KB][rows]
+  long long ldq;
+  int G, rows;           // G = 0: plain
+  // image: rows of token t (NULL: row t itself): row_of[t * k + j] for j < k, < 0 for none
+  const int* row_of;
+  int k;
+};
+cudaError_t launch_quantize_rows(const QRowsArgs& in, const QRowsOut& out, cudaStream_t st);
+
+// One matrix [N, K] (e4m3 with scales Ws, or bf16 with Ws NULL) into its place in an image: tile t,
+// k-block b goes to img + ((t * KB + b) * step + part) * QTILE, its scale to s[(t * KB + b) * step + part].
+cudaError_t launch_pack_matrix(const void* W, const float* Ws, int N, int K, uint8_t* img, float* s, int step,
+                               int part, cudaStream_t st);
+
+// Groups the pairs (token, slot) by expert: counts[e], run0[e] (of runs of G rows) and every pair's row,
+// in ascending pair order within an expert; -1 for a pair without an expert.
+cudaError_t launch_plan(const int* experts, int pairs, int E, int G, int* counts, int* run0, int* row_of,
+                        unsigned* err, cudaStream_t st);
+
+// y[t] = sum over j of weights[t, j] * o[row_of[t, j]]
+cudaError_t launch_combine(const float* o, const int* row_of, const float* weights, int T, int k, int D, void* y,
+                           long long ldy, int out_f32, cudaStream_t st);
+
+struct QGemmArgs {
+  const uint8_t* act;    // rows
+  const float* act_s;
+  int G, rows;           // rows: capacity (stride of act_s)
+  const uint8_t* w;      // E matrices (gated: E gate/up images), w_stride bytes apart
+  const float* ws;       // ws_stride floats apart
+  size_t w_stride, ws_stride;
+  int N, K;
+  int E;                 // groups: experts, or 1
+  const int* counts;     // device [E] rows of each group, or NULL: one group of M rows
+  const int* run0;       // device [E + 1] first run of each group (NULL: 0)
+  int M;                 // rows in all, as far as the host knows: the exact number without counts, else
+                         // the number of pairs
+  // outputs. gated: rows in e4m3 for the next product (same G and rows); else y
+  uint8_t* h;
+  float* h_s;
+  void* y;
+  long long ldy;
+  int out_f32;
+  unsigned* err;
+  int num_sms;
+};
+cudaError_t launch_qgemm(const QGemmArgs& a, bool gated, cudaStream_t st);
+
+enum : unsigned {
+  QERR_EXPERT = 1u << 0,   // an expert index outside [-1, n_experts)
+  QERR_TIMEOUT = 1u << 1,  // a wait of a product ran out
+};
+
+}  // namespace pop
