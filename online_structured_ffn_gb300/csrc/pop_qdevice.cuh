@@ -1,0 +1,194 @@
+// Device helpers of the 8-bit operators: e4m3 rounding, bulk copies, the e4m3 tensor-core product.
+#pragma once
+#include <cuda_fp8.h>
+
+#include "pop_device.cuh"
+#include "pop_qinternal.h"
+
+namespace pop {
+
+// ------------------------------------------------------------------ e4m3
+// 512 * ((0.875 * x) / a), which e4m3x2 rounds. y = 1 / a, correctly rounded. The quotient is q0 = t y
+// corrected once by its exact remainder (Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990): a quotient that is an fp32 number, as every tie between two e4m3
+// values is, comes out exactly. 1 / a must be a normal number: larger a take the division itself.
+__device__ __forceinline__ float q_ratio(float x, float a, float y, bool huge) {
+  const float t = 0.875f * x;
+  if (huge) return 512.f * __fdiv_rn(t, a);
+  const float q0 = t * y;
+  return 512.f * fmaf(fmaf(-q0, a, t), y, q0);
+}
+__device__ __forceinline__ bool q_huge(float a) { return a > 0x1p120f; }
+__device__ __forceinline__ float q_recip(float a, bool huge) { return huge ? 0.f : __frcp_rn(a); }
+
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+
+__device__ __forceinline__ uint4 e4m3x16(const float* v, float a) {
+  const bool huge = q_huge(a);
+  const float y = q_recip(a, huge);
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = e4m3x2(q_ratio(v[4 * i], a, y, huge), q_ratio(v[4 * i + 1], a, y, huge)) |
+           (e4m3x2(q_ratio(v[4 * i + 2], a, y, huge), q_ratio(v[4 * i + 3], a, y, huge)) << 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The bits of |x| are ordered as the numbers are, with NaN above infinity: a block with a NaN gets a
+// NaN for its largest value.
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+constexpr uint32_t AMAX_MIN_BITS = 0x1f800000u;  // 2^-64
+
+// SiLU(g) u. __expf and __fdividef are off by a few units of 2^-23, far less than the e4m3 rounding of
+// the result; the full-precision forms take about three times the instructions.
+__device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
+
+// ------------------------------------------------------------------ launches
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <class K, class... Args>
+cudaError_t launch_q(K kernel, dim3 grid, int block, size_t smem, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// ------------------------------------------------------------------ copies and products
+__device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(smem_dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+// D[tmem] (+)= A[smem desc] * B[smem desc], kind::f8f6f4 (e4m3 inputs, fp32 accumulate), one CTA.
+__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor, kind::f8f6f4 with e4m3 A and B (format 0), both K-major, and fp32 D.
+__host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// One k-block (128 bytes of k: four products of 32) of A's and B's images.
+__device__ __forceinline__ void umma_block(uint32_t d_tmem, uint32_t a_smem, uint32_t b_smem, uint32_t idesc) {
+  const uint64_t ad = smem_desc_sw128(a_smem, 16u, 1024u), bd = smem_desc_sw128(b_smem, 16u, 1024u);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) umma_e4m3(d_tmem, ad + 2 * k, bd + 2 * k, idesc, k > 0 ? 1u : 0u);
+}
+
+// Waits for this thread's tensor-memory loads; r names what they fill, so that nothing reads it before.
+__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+__device__ __forceinline__ void tmem_wait16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15])
+               :
+               : "memory");
+}
+
+// Barrier 1 of the block's N epilogue threads: whether `bad` holds in any of them, the same for all.
+template <int N>
+__device__ __forceinline__ bool epi_any(bool bad) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, r;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred r, 1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, r;\n\t}"
+      : "=r"(any)
+      : "r"(bad ? 1u : 0u), "n"(N)
+      : "memory");
+  return any != 0;
+}
+
+// Two fp32 fused multiply-adds: a += d * f.
+__device__ __forceinline__ void fma2(float2& a, float dx, float dy, float f) {
+  uint64_t v, w, s;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(dx), "f"(dy));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(w) : "f"(f));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(s) : "f"(a.x), "f"(a.y));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(s) : "l"(v), "l"(w));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(s));
+}
+
+// ------------------------------------------------------------------ groups
+// The tiles of every group, in order: group e has ceil(count[e] / rows) * per tiles. Fills tile0[0..E]
+// (shared, E + 1 ints) and returns their number; all threads of the block call it.
+__device__ __forceinline__ int group_tiles(const QGemmArgs& a, int rows, int per, int* tile0) {
+  if (!a.counts) {
+    const int n = qceil(a.M, rows) * per;
+    if (threadIdx.x == 0) {
+      tile0[0] = 0;
+      tile0[1] = n;
+    }
+    __syncthreads();
+    return n;
+  }
+  if (threadIdx.x < 32) {
+    int base = 0;
+    for (int e0 = 0; e0 < a.E; e0 += 32) {
+      const int e = e0 + static_cast<int>(threadIdx.x);
+      int n = e < a.E ? qceil(__ldcg(a.counts + e), rows) * per : 0;
+      const int own = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, n, o);
+        if (static_cast<int>(threadIdx.x) >= o) n += v;
+      }
+      if (e < a.E) tile0[e] = base + n - own;
+      base += __shfl_sync(0xffffffffu, n, 31);
+    }
+    if (threadIdx.x == 0) tile0[a.E] = base;
+  }
+  __syncthreads();
+  return tile0[a.E];
+}
+
+// The group of a tile: the last e with tile0[e] <= t.
+__device__ __forceinline__ int group_of(const int* tile0, int E, int t) {
+  int lo = 0, hi = E;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (tile0[mid] <= t)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+// Limit of the kernels' waits, and of those in which a CTA that gives up lets its own copies and
+// products finish.
+constexpr uint64_t Q_WAIT_NS = 2000000000ull;
+constexpr uint64_t Q_DRAIN_NS = 1000000000ull;
+
+}  // namespace pop

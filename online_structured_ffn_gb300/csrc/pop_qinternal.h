@@ -81,10 +81,19 @@ struct QGemmArgs {
   void* y;
   long long ldy;
   int out_f32;
+  // thin products: parts of tiles that several CTAs share (qgemm_thin_parts floats) and a counter per
+  // tile, zero between calls
+  float* parts;
+  unsigned* done;
   unsigned* err;
   int num_sms;
 };
-cudaError_t launch_qgemm(const QGemmArgs& a, bool gated, cudaStream_t st);
+// few rows per group (G = 16): the matrix streams once (pop_qthin.cu). max_rows: the most rows that a group
+// is expected to have; more are right too.
+cudaError_t launch_qgemm_thin(const QGemmArgs& a, bool gated, int max_rows, cudaStream_t st);
+size_t qgemm_thin_parts(int num_sms, bool gated);
+// many rows per group (G = 128): 128 x 256 tiles (pop_qwide.cu)
+cudaError_t launch_qgemm_wide(const QGemmArgs& a, bool gated, cudaStream_t st);
 
 enum : unsigned {
   QERR_EXPERT = 1u << 0,   // an expert index outside [-1, n_experts)

@@ -1,43 +1,9 @@
 // Rows and matrices in e4m3 with a scale per block of 128: quantising, operand images, the grouping of
 // tokens by expert and the weighted sum of the experts' outputs (include/pop_quant.h, pop_qinternal.h).
-#include <cuda_fp8.h>
-
-#include "pop_device.cuh"
-#include "pop_qinternal.h"
+#include "pop_qdevice.cuh"
 
 namespace pop {
 namespace {
-
-// e4m3(512 * ((0.875 * x) / a)) of two values. y = 1 / a, correctly rounded. The quotient is q0 = t y
-// corrected once by its exact remainder (Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000 processor", 1990): a quotient that is an fp32 number, as every tie between two e4m3
-// values is, comes out exactly. 1 / a must be a normal number: larger a take the division itself.
-__device__ __forceinline__ float q_ratio(float x, float a, float y, bool huge) {
-  const float t = 0.875f * x;
-  if (huge) return 512.f * __fdiv_rn(t, a);
-  const float q0 = t * y;
-  return 512.f * fmaf(fmaf(-q0, a, t), y, q0);
-}
-
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-}
-
-__device__ __forceinline__ uint4 e4m3x16(const float (&v)[16], float a) {
-  const bool huge = a > 0x1p120f;
-  const float y = huge ? 0.f : __frcp_rn(a);
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = e4m3x2(q_ratio(v[4 * i], a, y, huge), q_ratio(v[4 * i + 1], a, y, huge)) |
-           (e4m3x2(q_ratio(v[4 * i + 2], a, y, huge), q_ratio(v[4 * i + 3], a, y, huge)) << 16);
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
-// The bits of |x| are ordered as the numbers are, with NaN above infinity: a block with a NaN gets a
-// NaN for its largest value.
-__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
-constexpr uint32_t AMAX_MIN_BITS = 0x1f800000u;  // 2^-64
 
 __device__ __forceinline__ void unpack8(const void* p, int kind, float* v) {
   if (kind == 0) {

@@ -86,6 +86,8 @@ struct pop_qlinear {
   float* ws = nullptr;
   uint8_t* act = nullptr;  // image of a call's rows
   float* act_s = nullptr;
+  float* parts = nullptr;
+  unsigned* done = nullptr;
   unsigned* err = nullptr;
   int num_sms = 1;
 };
@@ -99,25 +101,41 @@ struct pop_qmoe {
   uint8_t *act = nullptr, *h = nullptr;
   float *act_s = nullptr, *h_s = nullptr;
   float* o = nullptr;      // [rows][D] outputs of the experts
+  float* parts = nullptr;
+  unsigned* done = nullptr;
   unsigned* err = nullptr;
   int num_sms = 1;
 };
 
 namespace {
 
-// Rows of a run: see launch_qgemm.
-int granule(long long rows_per_group) { return rows_per_group >= 64 ? 128 : 16; }
+// Rows of a run, which says which kind of product a call takes: 128 (wide) or 16 (thin).
+constexpr int WIDE_ROWS = 64;
+int granule(long long rows_per_group) { return rows_per_group >= WIDE_ROWS ? 128 : 16; }
+
+// Counters of a thin product's tiles: token tiles (of 16 at least) of all groups, times output tiles.
+size_t thin_tiles(long long pairs, int E, size_t out_tiles) {
+  const long long most = static_cast<long long>(WIDE_ROWS) * E;
+  const long long n = pairs < most ? pairs : most;
+  return static_cast<size_t>(n / 16 + (n < E ? n : E)) * out_tiles;
+}
+
+cudaError_t launch_qgemm(const QGemmArgs& g, bool gated, int max_rows, cudaStream_t st) {
+  return g.G == 128 ? launch_qgemm_wide(g, gated, st) : launch_qgemm_thin(g, gated, max_rows, st);
+}
 
 void free_linear(pop_qlinear* h) {
   cudaFree(h->w);
   cudaFree(h->ws);
   cudaFree(h->act);
   cudaFree(h->act_s);
+  cudaFree(h->parts);
+  cudaFree(h->done);
   cudaFree(h->err);
 }
 
 void free_qmoe(pop_qmoe* m) {
-  void* p[] = {m->wgu, m->wdn, m->sgu, m->sdn, m->counts, m->run0, m->row_of, m->act, m->h, m->act_s, m->h_s, m->o, m->err};
+  void* p[] = {m->wgu, m->wdn, m->sgu, m->sdn, m->counts, m->run0, m->row_of, m->act, m->h, m->act_s, m->h_s, m->o, m->parts, m->done, m->err};
   for (void* q : p) cudaFree(q);
 }
 
@@ -152,9 +170,11 @@ pop_status linear_call(pop_qlinear* h, QRowsArgs in, size_t row_bytes, int M, vo
     g.y = static_cast<uint8_t*>(y) + static_cast<size_t>(m0) * ldy * (h->cfg.out_f32 ? 4 : 2);
     g.ldy = ldy;
     g.out_f32 = h->cfg.out_f32;
+    g.parts = h->parts;
+    g.done = h->done;
     g.err = h->err;
     g.num_sms = h->num_sms;
-    e = launch_qgemm(g, false, st);
+    e = launch_qgemm(g, false, n, st);
     if (e != cudaSuccess) return q_cuda(e, call);
   }
   return POP_OK;
@@ -215,8 +235,12 @@ pop_status pop_qlinear_create(const pop_qlinear_config* cfg, const void* W, cons
   if (e == cudaSuccess) e = dalloc(&h->ws, NT * KB);
   if (e == cudaSuccess) e = dalloc(&h->act, static_cast<size_t>(h->rows) * KB * QB);
   if (e == cudaSuccess) e = dalloc(&h->act_s, static_cast<size_t>(h->rows) * KB);
+  const size_t thin = thin_tiles(cfg->max_tokens, 1, NT);
+  if (e == cudaSuccess) e = dalloc(&h->parts, qgemm_thin_parts(h->num_sms, false));
+  if (e == cudaSuccess) e = dalloc(&h->done, thin);
   if (e == cudaSuccess) e = dalloc(&h->err, 1);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (e == cudaSuccess) e = cudaMemsetAsync(h->done, 0, thin * sizeof(unsigned), st);
   if (e == cudaSuccess) e = cudaMemsetAsync(h->err, 0, sizeof(unsigned), st);
   if (e == cudaSuccess) e = launch_pack_matrix(W, W_s, cfg->N, cfg->K, h->w, h->ws, 1, 0, st);
   // later calls may come on other streams
@@ -325,8 +349,12 @@ pop_status pop_qmoe_create(const pop_qmoe_config* cfg, const void* const* Wg, co
   if (e == cudaSuccess) e = dalloc(&m->h, rows * NT * QB);
   if (e == cudaSuccess) e = dalloc(&m->h_s, rows * NT);
   if (e == cudaSuccess) e = dalloc(&m->o, static_cast<size_t>(rows) * cfg->D);
+  const size_t thin = thin_tiles(pairs, E, NT > DT ? NT : DT);
+  if (e == cudaSuccess) e = dalloc(&m->parts, qgemm_thin_parts(m->num_sms, true));
+  if (e == cudaSuccess) e = dalloc(&m->done, thin);
   if (e == cudaSuccess) e = dalloc(&m->err, 1);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (e == cudaSuccess) e = cudaMemsetAsync(m->done, 0, thin * sizeof(unsigned), st);
   if (e == cudaSuccess) e = cudaMemsetAsync(m->err, 0, sizeof(unsigned), st);
   for (int x = 0; x < E && e == cudaSuccess; ++x) {
     uint8_t* gu = m->wgu + x * NT * DT * 2 * QTILE;
@@ -403,9 +431,11 @@ pop_status pop_qmoe_forward(pop_qmoe_t m, const void* x, long long ldx, const in
     g.M = pairs;
     g.h = m->h;
     g.h_s = m->h_s;
+    g.parts = m->parts;
+    g.done = m->done;
     g.err = m->err;
     g.num_sms = m->num_sms;
-    e = launch_qgemm(g, true, st);
+    e = launch_qgemm(g, true, n, st);
     if (e != cudaSuccess) return q_cuda(e, call);
     g.act = m->h;
     g.act_s = m->h_s;
@@ -420,7 +450,7 @@ pop_status pop_qmoe_forward(pop_qmoe_t m, const void* x, long long ldx, const in
     g.y = m->o;
     g.ldy = c.D;
     g.out_f32 = 1;
-    e = launch_qgemm(g, false, st);
+    e = launch_qgemm(g, false, n, st);
     if (e != cudaSuccess) return q_cuda(e, call);
     e = launch_combine(m->o, m->row_of, weights + static_cast<size_t>(t0) * c.top_k, n, c.top_k, c.D,
                        static_cast<uint8_t*>(y) + static_cast<size_t>(t0) * ldy * (c.out_f32 ? 4 : 2), ldy, c.out_f32, st);
