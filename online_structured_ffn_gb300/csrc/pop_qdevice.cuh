@@ -95,6 +95,92 @@ __device__ __forceinline__ void umma_block(uint32_t d_tmem, uint32_t a_smem, uin
   for (int k = 0; k < 4; ++k) umma_e4m3(d_tmem, ad + 2 * k, bd + 2 * k, idesc, k > 0 ? 1u : 0u);
 }
 
+// Waits until the phase with the given parity has completed; false after limit_ns, or once another role of the
+// CTA has given up. The timer is first read after 64 tries: reading it takes longer than most waits, and these
+// kernels wait several times per k-block.
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile int* abort_flag) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 63u) == 0u) {
+      if (*abort_flag) return false;
+      const uint64_t now = globaltimer_ns();
+      if (t0 == 0)
+        t0 = now;
+      else if (now - t0 > limit_ns)
+        return false;
+    }
+  }
+}
+
+// One lane of the warp (the same one every time). Code that only this lane runs inside a loop of the whole warp
+// keeps its operands in uniform registers, which the tensor-core instructions need them in.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// ------------------------------------------------------------------ pairs of CTAs (clusters of two)
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of a barrier at the same place in the first CTA of the cluster.
+__device__ __forceinline__ uint32_t first_cta(uint64_t* bar) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(bar)));
+  return a;
+}
+// Arrives there. Of this thread's operations it orders what the barrier's own kind orders: a copy that a
+// barrier of this CTA has reported, and tensor-memory loads that tcgen05.wait::ld and a fence have ended. A
+// release at cluster scope would also wait for every load still on its way.
+__device__ __forceinline__ void mbar_arrive_first(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* smem_result, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(smem_result)), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// One k-block on both CTAs' tensor cores: A's rows and B's rows lie half in each, at the same addresses. a_lo
+// and b_lo: the low words of the descriptors (address >> 4 | leading offset), which alone change from block to
+// block; built from 32-bit words here, as 64-bit sums in a thread's own registers took four times as long to
+// issue as the products take.
+constexpr uint32_t DESC_LO = 1u << 16;                                 // leading byte offset 16 (not used by the swizzle)
+constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride 1024, version 1, 128-byte swizzle
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return ((saddr >> 4) & 0x3FFFu) | DESC_LO; }
+__device__ __forceinline__ void umma_block_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %4};\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo + 2 * k), "r"(b_lo + 2 * k), "r"(idesc), "r"(DESC_HI), "r"(k > 0 ? 1u : 0u)
+        : "memory");
+}
+// Arrives on `bar` in both CTAs once all products issued so far by this thread have completed.
+__device__ __forceinline__ void umma_commit_pair(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .b16 m;\n\tmov.b16 m, 3;\n\t"
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(
+          smem_u32(bar))
+      : "memory");
+}
+
 // Waits for this thread's tensor-memory loads; r names what they fill, so that nothing reads it before.
 __device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -140,51 +226,68 @@ __device__ __forceinline__ void fma2(float2& a, float dx, float dy, float f) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(s));
 }
 
-// ------------------------------------------------------------------ groups
-// The tiles of every group, in order: group e has ceil(count[e] / rows) * per tiles. Fills tile0[0..E]
-// (shared, E + 1 ints) and returns their number; all threads of the block call it.
-__device__ __forceinline__ int group_tiles(const QGemmArgs& a, int rows, int per, int* tile0) {
-  if (!a.counts) {
-    const int n = qceil(a.M, rows) * per;
-    if (threadIdx.x == 0) {
-      tile0[0] = 0;
-      tile0[1] = n;
-    }
-    __syncthreads();
-    return n;
-  }
-  if (threadIdx.x < 32) {
-    int base = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 32) {
-      const int e = e0 + static_cast<int>(threadIdx.x);
-      int n = e < a.E ? qceil(__ldcg(a.counts + e), rows) * per : 0;
-      const int own = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, n, o);
-        if (static_cast<int>(threadIdx.x) >= o) n += v;
-      }
-      if (e < a.E) tile0[e] = base + n - own;
-      base += __shfl_sync(0xffffffffu, n, 31);
-    }
-    if (threadIdx.x == 0) tile0[a.E] = base;
-  }
-  __syncthreads();
-  return tile0[a.E];
+// 32 bytes, aligned to 32, in one store.
+__device__ __forceinline__ void st_sector(void* p, uint4 lo, uint4 hi) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w),
+               "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
+               : "memory");
 }
 
-// The group of a tile: the last e with tile0[e] <= t.
-__device__ __forceinline__ int group_of(const int* tile0, int E, int t) {
-  int lo = 0, hi = E;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (tile0[mid] <= t)
-      lo = mid;
-    else
-      hi = mid;
+// ------------------------------------------------------------------ groups
+// The groups of a product, in shared memory.
+struct Groups {
+  int tile0[POP_QMOE_MAX_EXPERTS + 1];  // first tile of each
+  int count[POP_QMOE_MAX_EXPERTS];      // rows
+  int run0[POP_QMOE_MAX_EXPERTS];       // first run of G rows
+
+  // Group e has ceil(count[e] / rows) * per tiles. Returns their number; all threads of the block call it.
+  __device__ __forceinline__ int fill(const QGemmArgs& a, int rows, int per) {
+    if (!a.counts) {
+      if (threadIdx.x == 0) {
+        tile0[0] = 0;
+        tile0[1] = qceil(a.M, rows) * per;
+        count[0] = a.M;
+        run0[0] = 0;
+      }
+    } else if (threadIdx.x < 32) {
+      const int lane = threadIdx.x;
+      int base = 0;
+      for (int e0 = 0; e0 < a.E; e0 += 32) {
+        const int e = e0 + lane;
+        const int c = e < a.E ? __ldcg(a.counts + e) : 0;
+        const int own = qceil(c, rows) * per;
+        int n = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, n, o);
+          if (lane >= o) n += v;
+        }
+        if (e < a.E) {
+          tile0[e] = base + n - own;
+          count[e] = c;
+          run0[e] = __ldcg(a.run0 + e);
+        }
+        base += __shfl_sync(0xffffffffu, n, 31);
+      }
+      if (lane == 0) tile0[a.E] = base;
+    }
+    __syncthreads();
+    return tile0[a.E];
   }
-  return lo;
-}
+
+  // The group of a tile: the last e with tile0[e] <= t (the ones without tiles come before it).
+  __device__ __forceinline__ int of(int E, int t) const {
+    int lo = 0, hi = E;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (tile0[mid] <= t)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    return lo;
+  }
+};
 
 // Limit of the kernels' waits, and of those in which a CTA that gives up lets its own copies and
 // products finish.

@@ -4,8 +4,9 @@
 // of k) of a run of rows is `rows` x 128 bytes in the 128-byte swizzle (row r's 16-byte chunk c lies at
 // chunk c ^ (r % 8)), one contiguous piece of memory that a bulk copy brings into place as it is.
 //   - a matrix [N, K]: tiles of 128 rows, [ceil(N/128)][ceil(K/128)][16 KB]; rows past N and bytes past K
-//     are zero. Its scales are [ceil(N/128)][ceil(K/128)] float32. The gate and up matrices of a gated MLP
-//     share one image, [tile][k-block][gate 16 KB | up 16 KB], and their scales [tile][k-block][2].
+//     are zero. Its scales are float32, a tile's ceil(K/128) in order, tiles scale_stride apart. The gate and
+//     up matrices of a gated MLP share one image, [tile][k-block][gate 16 KB | up 16 KB], and their scales
+//     [tile][k-block][2].
 //   - rows (tokens): runs of G rows (G = 16 or 128), [run][k-block][G x 128 bytes]; scales
 //     [k-block][row]. Bytes past K are zero; what rows without a token hold is not used.
 // Tokens of an expert stand together: expert e's rows are the runs [run0[e], run0[e + 1]).
@@ -23,6 +24,8 @@ pop_status device_supported();
 constexpr int QB = 128;              // block of a scale, and of an operand image in k
 constexpr int QTILE = QB * QB;       // bytes of a 128 x 128 image
 __host__ __device__ constexpr int qceil(int a, int b) { return (a + b - 1) / b; }
+// Floats from one tile's scales to the next one's: whole runs of eight k-blocks, which bulk copies bring in.
+__host__ __device__ constexpr int scale_stride(int KB, int step) { return qceil(KB, 8) * 8 * step; }
 
 // Byte of (row, k) within an image of 128-byte rows.
 __host__ __device__ constexpr uint32_t image_at(uint32_t row, uint32_t k) {
@@ -49,7 +52,8 @@ struct QRowsOut {
 cudaError_t launch_quantize_rows(const QRowsArgs& in, const QRowsOut& out, cudaStream_t st);
 
 // One matrix [N, K] (e4m3 with scales Ws, or bf16 with Ws NULL) into its place in an image: tile t,
-// k-block b goes to img + ((t * KB + b) * step + part) * QTILE, its scale to s[(t * KB + b) * step + part].
+// k-block b goes to img + ((t * KB + b) * step + part) * QTILE, its scale to
+// s[t * scale_stride(KB, step) + b * step + part].
 cudaError_t launch_pack_matrix(const void* W, const float* Ws, int N, int K, uint8_t* img, float* s, int step,
                                int part, cudaStream_t st);
 

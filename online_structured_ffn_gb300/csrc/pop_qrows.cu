@@ -85,6 +85,7 @@ __global__ void __launch_bounds__(256) k_pack_matrix(const void* __restrict__ W,
   const int KB = qceil(K, QB);
   const int t = blockIdx.y, b = blockIdx.x;
   const size_t slot = (static_cast<size_t>(t) * KB + b) * step + part;
+  float* scale = sc + static_cast<size_t>(t) * scale_stride(KB, step) + b * step + part;
   const int c = threadIdx.x & 7, r0 = threadIdx.x >> 3;
   const int k0 = b * QB + c * 16;
   const int n8 = min(max((K - k0) >> 3, 0), 2);
@@ -105,7 +106,7 @@ __global__ void __launch_bounds__(256) k_pack_matrix(const void* __restrict__ W,
       }
       dst[image_at(r, c * 16) >> 4] = q;
     }
-    if (threadIdx.x == 0) sc[slot] = Ws[static_cast<size_t>(t) * KB + b];
+    if (threadIdx.x == 0) *scale = Ws[static_cast<size_t>(t) * KB + b];
     return;
   }
   if (threadIdx.x == 0) s_max = AMAX_MIN_BITS;
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(256) k_pack_matrix(const void* __restrict__ W,
   const float a = __uint_as_float(s_max);
 #pragma unroll
   for (int i = 0; i < 4; ++i) dst[image_at(r0 + 32 * i, c * 16) >> 4] = e4m3x16(v[i], a);
-  if (threadIdx.x == 0) sc[slot] = __fdiv_rn(a, 448.f);
+  if (threadIdx.x == 0) *scale = __fdiv_rn(a, 448.f);
 }
 
 // One CTA. Warp w numbers the pairs of experts w, w + 32, ... in ascending order, a ballot per 32 pairs;

@@ -43,7 +43,7 @@ struct Ctl {
   uint32_t tmem_base;
   int abort_flag;
   int last;
-  int tile0[POP_QMOE_MAX_EXPERTS + 1];
+  Groups groups;
   uint32_t amax[4][64];
 };
 
@@ -55,19 +55,19 @@ struct Seg {
 };
 
 template <int NT>
-__device__ __forceinline__ Seg segment(const QGemmArgs& a, const int* tile0, int KB, int NTILES, long long x, long long x1) {
+__device__ __forceinline__ Seg segment(const Groups& gr, int E, int KB, long long x, long long x1) {
   Seg s;
   s.tile = static_cast<int>(x / KB);
   s.kb0 = static_cast<int>(x - static_cast<long long>(s.tile) * KB);
   s.kb1 = static_cast<int>(min(static_cast<long long>(KB), s.kb0 + (x1 - x)));
-  s.e = group_of(tile0, a.E, s.tile);
-  const int cnt = a.counts ? __ldcg(a.counts + s.e) : a.M;
+  s.e = gr.of(E, s.tile);
+  const int cnt = gr.count[s.e];
   const int tts = qceil(cnt, NT);
-  const int local = s.tile - tile0[s.e];
+  const int local = s.tile - gr.tile0[s.e];
   s.t = local / tts;  // the token tiles of one output tile side by side: the matrix tile is in L2 for the others
   s.n0 = (local - s.t * tts) * NT;
   s.n = min(NT, cnt - s.n0);
-  s.row0 = (a.run0 ? __ldcg(a.run0 + s.e) : 0) * a.G + s.n0;
+  s.row0 = gr.run0[s.e] * 16 + s.n0;
   return s;
 }
 
@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
   const uint32_t tmem_base = ctl.tmem_base;
   pdl_wait();  // the rows, the groups, and what an earlier call's kernels still use
   pdl_trigger();
-  const int tiles = group_tiles(a, NT, NTILES, ctl.tile0);
+  const int tiles = ctl.groups.fill(a, NT, NTILES);
   const long long work = static_cast<long long>(tiles) * KB;
   const long long G = min(static_cast<long long>(gridDim.x), work);  // CTAs that have a unit
   const bool on = static_cast<long long>(blockIdx.x) < G;
@@ -126,14 +126,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
       uint32_t issued = 0;
       bool ok = true;
       for (long long x = x0; x < x1 && ok;) {
-        const Seg g = segment<NT>(a, ctl.tile0, KB, NTILES, x, x1);
+        const Seg g = segment<NT>(ctl.groups, a.E, KB, x, x1);
         const int runs = qceil(g.n, 16);
         const uint8_t* w = a.w + g.e * a.w_stride + static_cast<size_t>(g.t) * KB * C::W_BYTES;
         const uint8_t* xr = a.act + static_cast<size_t>(g.row0 / 16) * KB * 2048;
         const uint32_t bytes = C::W_BYTES + runs * (2048 + 64);
         for (int kb = g.kb0; kb < g.kb1; ++kb, ++issued) {
           const int s = issued % C::STAGES;
-          if (!mbar_wait_bounded(&ctl.empty[s], ((issued / C::STAGES) & 1u) ^ 1u, Q_WAIT_NS, abort_flag)) {
+          if (!mbar_wait(&ctl.empty[s], ((issued / C::STAGES) & 1u) ^ 1u, Q_WAIT_NS, abort_flag)) {
             fail();
             ok = false;
             break;
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
       const uint32_t lo = issued > C::STAGES ? issued - C::STAGES : 0;
       for (uint32_t i = lo; i < issued; ++i) {
         volatile int never = 0;
-        if (!mbar_wait_bounded(&ctl.full[i % C::STAGES], (i / C::STAGES) & 1u, Q_DRAIN_NS, &never)) fail();
+        if (!mbar_wait(&ctl.full[i % C::STAGES], (i / C::STAGES) & 1u, Q_DRAIN_NS, &never)) fail();
       }
     }
     __syncwarp();
@@ -162,12 +162,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
       uint32_t it = 0;
       bool ok = true;
       for (long long x = x0; x < x1 && ok;) {
-        const Seg g = segment<NT>(a, ctl.tile0, KB, NTILES, x, x1);
+        const Seg g = segment<NT>(ctl.groups, a.E, KB, x, x1);
         const uint32_t idesc = idesc_e4m3_f32(128, qceil(g.n, 16) * 16);
         for (int kb = g.kb0; kb < g.kb1; ++kb, ++it) {
           const int s = it % C::STAGES, b = it % C::BUFS;
-          if (!mbar_wait_bounded(&ctl.full[s], (it / C::STAGES) & 1u, Q_WAIT_NS, abort_flag) ||
-              !mbar_wait_bounded(&ctl.tempty[b], ((it / C::BUFS) & 1u) ^ 1u, Q_WAIT_NS, abort_flag)) {
+          if (!mbar_wait(&ctl.full[s], (it / C::STAGES) & 1u, Q_WAIT_NS, abort_flag) ||
+              !mbar_wait(&ctl.tempty[b], ((it / C::BUFS) & 1u) ^ 1u, Q_WAIT_NS, abort_flag)) {
             fail();
             ok = false;
             break;
@@ -184,7 +184,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
       }
       umma_commit(&ctl.drain);
       volatile int never = 0;
-      if (!mbar_wait_bounded(&ctl.drain, 0, Q_DRAIN_NS, &never)) fail();
+      if (!mbar_wait(&ctl.drain, 0, Q_DRAIN_NS, &never)) fail();
     }
     __syncwarp();
   } else {
@@ -194,8 +194,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
     const int et = threadIdx.x - 64;
     uint32_t it = 0;
     for (long long x = x0; x < x1;) {
-      const Seg g = segment<NT>(a, ctl.tile0, KB, NTILES, x, x1);
-      const float* ws = a.ws + g.e * a.ws_stride + static_cast<size_t>(g.t) * KB * P;
+      const Seg g = segment<NT>(ctl.groups, a.E, KB, x, x1);
+      const float* ws = a.ws + g.e * a.ws_stride + static_cast<size_t>(g.t) * scale_stride(KB, P);
       float acc[P][NT];
 #pragma unroll
       for (int p = 0; p < P; ++p)
@@ -207,8 +207,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
         const int i = (kb - g.kb0) * P;
         if ((i & 31) == 0) sw = i + lane < (g.kb1 - g.kb0) * P ? __ldg(ws + static_cast<size_t>(g.kb0) * P + i + lane) : 0.f;
         const int s = it % C::STAGES, b = it % C::BUFS;
-        ok = mbar_wait_bounded(&ctl.full[s], (it / C::STAGES) & 1u, Q_WAIT_NS, abort_flag) &&
-             mbar_wait_bounded(&ctl.tfull[b], (it / C::BUFS) & 1u, Q_WAIT_NS, abort_flag);
+        ok = mbar_wait(&ctl.full[s], (it / C::STAGES) & 1u, Q_WAIT_NS, abort_flag) &&
+             mbar_wait(&ctl.tfull[b], (it / C::BUFS) & 1u, Q_WAIT_NS, abort_flag);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -334,7 +334,7 @@ template <bool GATED, int NT>
 cudaError_t launch(const QGemmArgs& a, cudaStream_t st) {
   using C = Thin<GATED, NT>;
   const size_t smem = C::STAGES * C::STAGE + 1024;
-  cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(&k_qgemm_thin<GATED, NT>), smem + sizeof(Ctl));
+  cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(&k_qgemm_thin<GATED, NT>), smem);
   if (e != cudaSuccess) return e;
   return launch_q(k_qgemm_thin<GATED, NT>, dim3(a.num_sms), THREADS, smem, st, a);
 }

@@ -232,7 +232,7 @@ pop_status pop_qlinear_create(const pop_qlinear_config* cfg, const void* W, cons
   h->rows = qceil(cfg->max_tokens, 128) * 128;
   const size_t NT = qceil(cfg->N, QB), KB = qceil(cfg->K, QB);
   cudaError_t e = dalloc(&h->w, NT * KB * QTILE);
-  if (e == cudaSuccess) e = dalloc(&h->ws, NT * KB);
+  if (e == cudaSuccess) e = dalloc(&h->ws, NT * scale_stride(KB, 1));
   if (e == cudaSuccess) e = dalloc(&h->act, static_cast<size_t>(h->rows) * KB * QB);
   if (e == cudaSuccess) e = dalloc(&h->act_s, static_cast<size_t>(h->rows) * KB);
   const size_t thin = thin_tiles(cfg->max_tokens, 1, NT);
@@ -339,8 +339,9 @@ pop_status pop_qmoe_create(const pop_qmoe_config* cfg, const void* const* Wg, co
   const size_t NT = qceil(cfg->D_FF, QB), DT = qceil(cfg->D, QB);
   cudaError_t e = dalloc(&m->wgu, E * NT * DT * 2 * QTILE);
   if (e == cudaSuccess) e = dalloc(&m->wdn, E * DT * NT * QTILE);
-  if (e == cudaSuccess) e = dalloc(&m->sgu, E * NT * DT * 2);
-  if (e == cudaSuccess) e = dalloc(&m->sdn, E * NT * DT);
+  const size_t gu_scales = NT * scale_stride(DT, 2), dn_scales = DT * scale_stride(NT, 1);
+  if (e == cudaSuccess) e = dalloc(&m->sgu, E * gu_scales);
+  if (e == cudaSuccess) e = dalloc(&m->sdn, E * dn_scales);
   if (e == cudaSuccess) e = dalloc(&m->counts, E);
   if (e == cudaSuccess) e = dalloc(&m->run0, E + 1);
   if (e == cudaSuccess) e = dalloc(&m->row_of, pairs);
@@ -358,12 +359,12 @@ pop_status pop_qmoe_create(const pop_qmoe_config* cfg, const void* const* Wg, co
   if (e == cudaSuccess) e = cudaMemsetAsync(m->err, 0, sizeof(unsigned), st);
   for (int x = 0; x < E && e == cudaSuccess; ++x) {
     uint8_t* gu = m->wgu + x * NT * DT * 2 * QTILE;
-    float* sgu = m->sgu + x * NT * DT * 2;
+    float* sgu = m->sgu + x * gu_scales;
     e = launch_pack_matrix(Wg[x], scaled ? Sg[x] : nullptr, cfg->D_FF, cfg->D, gu, sgu, 2, 0, st);
     if (e == cudaSuccess) e = launch_pack_matrix(W1[x], scaled ? S1[x] : nullptr, cfg->D_FF, cfg->D, gu, sgu, 2, 1, st);
     if (e == cudaSuccess)
       e = launch_pack_matrix(W2[x], scaled ? S2[x] : nullptr, cfg->D, cfg->D_FF, m->wdn + x * DT * NT * QTILE,
-                             m->sdn + x * DT * NT, 1, 0, st);
+                             m->sdn + x * dn_scales, 1, 0, st);
   }
   // later calls may come on other streams
   if (e == cudaSuccess) e = cudaStreamSynchronize(st);
@@ -422,7 +423,7 @@ pop_status pop_qmoe_forward(pop_qmoe_t m, const void* x, long long ldx, const in
     g.w = m->wgu;
     g.ws = m->sgu;
     g.w_stride = NT * DT * 2 * QTILE;
-    g.ws_stride = NT * DT * 2;
+    g.ws_stride = NT * scale_stride(DT, 2);
     g.N = c.D_FF;
     g.K = c.D;
     g.E = c.n_experts;
@@ -442,7 +443,7 @@ pop_status pop_qmoe_forward(pop_qmoe_t m, const void* x, long long ldx, const in
     g.w = m->wdn;
     g.ws = m->sdn;
     g.w_stride = NT * DT * QTILE;
-    g.ws_stride = NT * DT;
+    g.ws_stride = DT * scale_stride(NT, 1);
     g.N = c.D;
     g.K = c.D_FF;
     g.h = nullptr;

@@ -1,17 +1,22 @@
 // Products of many rows (tokens) and a matrix in e4m3 with block scales, on 128 x 256 tiles.
 //
-// Rows are the M operand (128 per tile), the matrix the N operand: 256 outputs, or the gate and the up
-// rows of 128 channels. A block of 128 in k has scales of its own, so its product cannot be added to the
-// next one's in tensor memory: each k-block is one tcgen05 product of 128 x 256 x 128 into one of two
-// TMEM buffers, which eight epilogue warps add to fp32 registers, times the row's scale (one per thread: a
-// thread has one row) and the matrix's (one per 128 columns), while the tensor core fills the other.
-// A k-block takes the tensor core 512 cycles; reading 256 columns of TMEM and 128 x 256 fused
-// multiply-adds (two per instruction) about 300, so the products are what bounds it.
+// Rows are the M operand, the matrix the N operand: 256 outputs, or the gate and the up rows of 128
+// channels. Two CTAs of a cluster work as a pair on 256 rows by 256 outputs (cta_group::2): each brings its own
+// 128 rows and half of the matrix tile, 32 KB a k-block instead of the 48 KB of a CTA alone. An SM takes in
+// 64 bytes a cycle from L2 at most, which is 512 cycles for 32 KB, as long as the product takes (a CTA alone
+// ran at 53 bytes a cycle, 2.0 PFLOP/s, whatever its epilogue did).
 //
-// Persistent, one CTA per SM. Warp 0: copies (operand images: bulk copies of 16 KB). Warp 1: products.
-// Warps 2..9: epilogue, TMEM lane quarter warp % 4, two warps to a quarter that share its columns. Every wait
-// has a limit; a CTA that gives up records QERR_TIMEOUT, lets its copies and products finish, frees TMEM
-// and returns.
+// A block of 128 in k has scales of its own, so its product cannot be added to the next one's in tensor
+// memory: the epilogue adds each k-block's product to fp32 registers, times the row's scale (a thread has one
+// row) and the matrix's. Tensor memory holds two k-blocks. Each is in halves, of 64 rows of either CTA's part
+// of the matrix tile; a half has its own four epilogue warps, its own issuing thread and its own barriers, so
+// that one is read while the other is being filled and half the latency from product to epilogue and back
+// (some 600 cycles) is out of the way.
+//
+// Persistent, one CTA per SM. Warp 0: copies (operand images: bulk copies of 16 KB). Warps 1 and 3: of the first
+// CTA the products of both CTAs, a half each; warp 1 of the second the news that its operands have landed.
+// Warp 2: scales. Warps 4..11: epilogue, TMEM lane quarter warp % 4. Every wait has a limit; a CTA that gives
+// up records QERR_TIMEOUT, lets its copies and products finish, frees TMEM and returns.
 #include "pop_qdevice.cuh"
 
 namespace pop {
@@ -20,74 +25,96 @@ cudaError_t ensure_dyn_smem(const void* kernel, size_t bytes);
 
 namespace {
 
-constexpr int THREADS = 320;
+constexpr int THREADS = 384;
+// Registers a thread: the launch has 168 (65,536 / 384, in eights); the epilogue's two warpgroups hold 128
+// sums and up to 64 columns on their way, which at 168 spilled seven words a k-block.
+constexpr int REGS = 168, REGS_COPY = 88, REGS_EPI = 208;
+static_assert(REGS_COPY + 2 * REGS_EPI <= 3 * REGS, "the shares come out of the launch's registers");
 constexpr int BM = 128;
-constexpr int STAGES = 4;
-constexpr uint32_t A_BYTES = QTILE, B_BYTES = 2 * QTILE, STAGE = A_BYTES + B_BYTES;
+constexpr int STAGES = 6;
+constexpr uint32_t A_BYTES = QTILE, B_BYTES = QTILE, STAGE = A_BYTES + B_BYTES;
 constexpr uint32_t TMEM_COLS = 512;
 
+// Scales of eight k-blocks: the rows', and the matrix's of either half of the columns (gated: the gate's and the
+// up's of each k-block, in turn).
+constexpr int SB = 8, SRING = 4;
+struct alignas(16) Scales {
+  float x[SB][BM];
+  float w[2 * SB];
+};
+
 struct Ctl {
+  Scales scales[SRING];
+  uint64_t sfull[SRING], sempty[SRING];
   uint64_t full[STAGES], empty[STAGES];
-  uint64_t tfull[2], tempty[2];
-  uint64_t drain;
+  uint64_t tfull[2][2], tempty[2][2];  // [half][buffer]
+  uint64_t drain[2];
   uint32_t tmem_base;
   int abort_flag;
-  int tile0[POP_QMOE_MAX_EXPERTS + 1];
+  Groups groups;
   uint32_t amax[2][2][BM];  // gated: [tile parity][column half][row]
 };
 
 struct Tile {
-  int e, n, m0, rows;  // group, tile of the matrix, first row within the group, rows of this tile
-  int row0;            // first row
+  int e, n, m0, rows;  // group, tile of the matrix, first row within the group, rows of this CTA (may be none)
+  int row0;            // first row; one that exists if there are none
 };
 
-__device__ __forceinline__ Tile tile_at(const QGemmArgs& a, const int* tile0, int per, int tile) {
+__device__ __forceinline__ Tile tile_at(const Groups& g, int E, int tile, int rank) {
   Tile t;
-  t.e = group_of(tile0, a.E, tile);
-  const int cnt = a.counts ? __ldcg(a.counts + t.e) : a.M;
-  const int mts = qceil(cnt, BM);
-  const int local = tile - tile0[t.e];
+  t.e = g.of(E, tile);
+  const int cnt = g.count[t.e];
+  const int mts = qceil(cnt, 2 * BM);
+  const int local = tile - g.tile0[t.e];
   t.n = local / mts;  // the row tiles of one matrix tile side by side: it is in L2 for all of them
-  t.m0 = (local - t.n * mts) * BM;
-  t.rows = min(BM, cnt - t.m0);
-  t.row0 = (a.run0 ? __ldcg(a.run0 + t.e) : 0) * BM + t.m0;
+  t.m0 = (local - t.n * mts) * 2 * BM;
+  t.rows = min(BM, cnt - t.m0 - rank * BM);
+  if (t.rows > 0) t.m0 += rank * BM;
+  t.row0 = g.run0[t.e] * BM + t.m0;
   return t;
 }
 
 template <bool GATED>
-__global__ void __launch_bounds__(THREADS, 1) k_qgemm_wide(const __grid_constant__ QGemmArgs a) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_wide(const __grid_constant__ QGemmArgs a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Ctl ctl;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int KB = qceil(a.K, QB), NT = qceil(a.N, QB);
   const int per = GATED ? NT : qceil(NT, 2);  // tiles of the matrix
   volatile int* abort_flag = &ctl.abort_flag;
+  const int rank = static_cast<int>(cluster_rank());
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&ctl.full[s], 1);
-      mbar_init(&ctl.empty[s], 1);
+      mbar_init(&ctl.full[s], rank == 0 ? 2 : 1);  // the first CTA's: its own operands, and word of the second's
+      mbar_init(&ctl.empty[s], 2);
+    }
+    for (int g = 0; g < SRING; ++g) {
+      mbar_init(&ctl.sfull[g], 1);
+      mbar_init(&ctl.sempty[g], 8);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(&ctl.tfull[b], 1);
-      mbar_init(&ctl.tempty[b], 8);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&ctl.tfull[h][b], 1);
+        mbar_init(&ctl.tempty[h][b], 8);  // the first CTA's: the half's epilogue warps of both
+      }
+      mbar_init(&ctl.drain[b], 1);
     }
-    mbar_init(&ctl.drain, 1);
     ctl.abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(&ctl.tmem_base, TMEM_COLS);
-    tmem_relinquish();
+    tmem_alloc_pair(&ctl.tmem_base, TMEM_COLS);
   }
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = ctl.tmem_base;
   pdl_wait();  // the rows, the groups, and what an earlier call's kernels still use
   pdl_trigger();
-  const int tiles = group_tiles(a, BM, per, ctl.tile0);
+  const int tiles = ctl.groups.fill(a, 2 * BM, per);
 
   auto fail = [&]() {
     if (!*abort_flag) {
@@ -96,128 +123,188 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_wide(const __grid_constant
     }
   };
 
-  if (warp == 0) {
-    if (lane == 0) {
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS_COPY));
+    if (warp == 0 && lane == 0) {
       // ---------------------------------------------------------- copies (one thread)
-      uint32_t issued = 0;
+      // (lean loops here and below: one thread's instructions follow one another at its latencies, and divisions
+      // and 64-bit products once made these take longer than the products)
+      uint32_t issued = 0, s = 0, phase = 1;
       bool ok = true;
-      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-        const Tile t = tile_at(a, ctl.tile0, per, tile);
+      for (int tile = pair; tile < tiles && ok; tile += pairs) {
+        const Tile t = tile_at(ctl.groups, a.E, tile, rank);
         const uint8_t* xr = a.act + static_cast<size_t>(t.row0 / BM) * KB * A_BYTES;
-        // gated: [tile][k-block][gate | up]; else tiles 2 n and 2 n + 1 (which may lie past the last)
-        const uint8_t* w = a.w + t.e * a.w_stride + static_cast<size_t>(t.n) * KB * B_BYTES;
-        const bool both = GATED || 2 * t.n + 1 < NT;
-        for (int kb = 0; kb < KB; ++kb, ++issued) {
-          const int s = issued % STAGES;
-          if (!mbar_wait_bounded(&ctl.empty[s], ((issued / STAGES) & 1u) ^ 1u, Q_WAIT_NS, abort_flag)) {
+        // this CTA's half of the matrix tile. Gated: [tile][k-block][gate | up]; else tile 2 n + rank, or the
+        // last one again
+        const uint8_t* w = a.w + t.e * a.w_stride +
+                           (GATED ? (static_cast<size_t>(t.n) * KB * 2 + rank) : static_cast<size_t>(min(2 * t.n + rank, NT - 1)) * KB) * QTILE;
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!mbar_wait(&ctl.empty[s], phase, Q_WAIT_NS, abort_flag)) {
             fail();
             ok = false;
             break;
           }
           uint8_t* st = smem + s * STAGE;
-          mbar_arrive_expect_tx(&ctl.full[s], A_BYTES + (both ? B_BYTES : QTILE));
-          bulk_load(st, xr + static_cast<size_t>(kb) * A_BYTES, A_BYTES, &ctl.full[s]);
-          if (GATED) {
-            bulk_load(st + A_BYTES, w + static_cast<size_t>(kb) * B_BYTES, B_BYTES, &ctl.full[s]);
-          } else {
-            bulk_load(st + A_BYTES, w + static_cast<size_t>(kb) * QTILE, QTILE, &ctl.full[s]);
-            if (both) bulk_load(st + A_BYTES + QTILE, w + static_cast<size_t>(KB + kb) * QTILE, QTILE, &ctl.full[s]);
-          }
+          mbar_arrive_expect_tx(&ctl.full[s], STAGE);
+          bulk_load(st, xr, A_BYTES, &ctl.full[s]);
+          bulk_load(st + A_BYTES, w, QTILE, &ctl.full[s]);
+          xr += A_BYTES;
+          w += GATED ? 2 * QTILE : QTILE;
+          ++issued;
+          if (++s == STAGES) s = 0, phase ^= 1;
         }
       }
-      // no copy of this CTA may be in flight when it exits
+      // no copy of this CTA may be in flight when it exits. (The first CTA's barriers also wait for the second;
+      // one that gave up before its last copies' news is covered by its own limit.)
       const uint32_t lo = issued > STAGES ? issued - STAGES : 0;
       for (uint32_t i = lo; i < issued; ++i) {
         volatile int never = 0;
-        if (!mbar_wait_bounded(&ctl.full[i % STAGES], (i / STAGES) & 1u, Q_DRAIN_NS, &never)) fail();
+        if (!mbar_wait(&ctl.full[i % STAGES], (i / STAGES) & 1u, Q_DRAIN_NS, &never)) fail();
       }
     }
-    __syncwarp();
-  } else if (warp == 1) {
-    if (lane == 0) {
-      // ---------------------------------------------------------- products (one thread)
-      constexpr uint32_t IDESC = idesc_e4m3_f32(BM, 256);
-      uint32_t it = 0;
+    if (warp & 1) {
+      const uint32_t total = pair < tiles ? static_cast<uint32_t>((tiles - 1 - pair) / pairs + 1) * static_cast<uint32_t>(KB) : 0u;
+      const bool leader = elect_one();
+      uint32_t s = 0, phase = 0;
+      if (rank == 0) {
+        // -------------------------------------------------------- products (a warp for either half)
+        constexpr uint32_t IDESC = idesc_e4m3_f32(2 * BM, 128);
+        const uint32_t h = static_cast<uint32_t>(warp >> 1);
+        const uint32_t a0 = desc_lo(smem_u32(smem)), b0 = desc_lo(smem_u32(smem) + A_BYTES + h * (QTILE / 2));
+        for (uint32_t it = 0; it < total; ++it) {
+          const uint32_t b = it & 1u;
+          if (!mbar_wait(&ctl.full[s], phase, Q_WAIT_NS, abort_flag) ||
+              !mbar_wait(&ctl.tempty[h][b], ((it >> 1) & 1u) ^ 1u, Q_WAIT_NS, abort_flag)) {
+            if (leader) fail();
+            break;
+          }
+          tc_fence_after();
+          if (leader) {
+            umma_block_pair(tmem_base + b * 256u + h * 128u, a0 + s * (STAGE >> 4), b0 + s * (STAGE >> 4), IDESC);
+            umma_commit_pair(&ctl.tfull[h][b]);
+            umma_commit_pair(&ctl.empty[s]);
+          }
+          __syncwarp();
+          if (++s == STAGES) s = 0, phase ^= 1;
+        }
+        if (leader) umma_commit_pair(&ctl.drain[h]);
+        volatile int never = 0;
+        if (!mbar_wait(&ctl.drain[h], 0, Q_DRAIN_NS, &never) && leader) fail();
+      } else if (warp == 1) {
+        // -------------------------------------------------------- word of this CTA's operands
+        for (uint32_t it = 0; it < total; ++it) {
+          if (!mbar_wait(&ctl.full[s], phase, Q_WAIT_NS, abort_flag)) {
+            if (leader) fail();
+            break;
+          }
+          if (leader) mbar_arrive_first(first_cta(&ctl.full[s]));
+          __syncwarp();
+          if (++s == STAGES) s = 0, phase ^= 1;
+        }
+      }
+    }
+    if (warp == 2 && lane == 0) {
+      // ---------------------------------------------------------- scales (one thread). Not loads of the
+      // epilogue's own: its arrival on tempty would wait for those that are on their way (250 cycles a
+      // k-block with four of them every fourth)
+      uint32_t issued = 0, g = 0, phase = 1;
       bool ok = true;
-      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-        for (int kb = 0; kb < KB; ++kb, ++it) {
-          const int s = it % STAGES, b = it & 1;
-          if (!mbar_wait_bounded(&ctl.full[s], (it / STAGES) & 1u, Q_WAIT_NS, abort_flag) ||
-              !mbar_wait_bounded(&ctl.tempty[b], ((it >> 1) & 1u) ^ 1u, Q_WAIT_NS, abort_flag)) {
+      for (int tile = pair; tile < tiles && ok; tile += pairs) {
+        const Tile t = tile_at(ctl.groups, a.E, tile, rank);
+        const float* xs = a.act_s + t.row0;
+        const float* ws = a.ws + t.e * a.ws_stride;
+        const float *w0, *w1;
+        if (GATED) {
+          w0 = w1 = ws + static_cast<size_t>(t.n) * scale_stride(KB, 2);
+        } else {
+          w0 = ws + static_cast<size_t>(2 * t.n) * scale_stride(KB, 1);
+          w1 = ws + static_cast<size_t>(min(2 * t.n + 1, NT - 1)) * scale_stride(KB, 1);
+        }
+        for (int kb = 0; kb < KB; kb += SB) {
+          if (!mbar_wait(&ctl.sempty[g], phase, Q_WAIT_NS, abort_flag)) {
             fail();
             ok = false;
             break;
           }
-          tc_fence_after();
-          const uint32_t st = smem_u32(smem + s * STAGE);
-          umma_block(tmem_base + static_cast<uint32_t>(b * 256), st, st + A_BYTES, IDESC);
-          umma_commit(&ctl.empty[s]);
-          umma_commit(&ctl.tfull[b]);
+          const int n = min(SB, KB - kb);
+          Scales& sc = ctl.scales[g];
+          mbar_arrive_expect_tx(&ctl.sfull[g], n * BM * 4 + 2 * SB * 4);
+          for (int j = 0; j < n; ++j, xs += a.rows) bulk_load(sc.x[j], xs, BM * 4, &ctl.sfull[g]);
+          if (GATED) {
+            bulk_load(sc.w, w0 + 2 * kb, 2 * SB * 4, &ctl.sfull[g]);
+          } else {
+            bulk_load(sc.w, w0 + kb, SB * 4, &ctl.sfull[g]);
+            bulk_load(sc.w + SB, w1 + kb, SB * 4, &ctl.sfull[g]);
+          }
+          ++issued;
+          if (++g == SRING) g = 0, phase ^= 1;
         }
       }
-      umma_commit(&ctl.drain);
-      volatile int never = 0;
-      if (!mbar_wait_bounded(&ctl.drain, 0, Q_DRAIN_NS, &never)) fail();
+      const uint32_t lo = issued > SRING ? issued - SRING : 0;
+      for (uint32_t i = lo; i < issued; ++i) {
+        volatile int never = 0;
+        if (!mbar_wait(&ctl.sfull[i % SRING], (i / SRING) & 1u, Q_DRAIN_NS, &never)) fail();
+      }
     }
     __syncwarp();
   } else {
-    // ------------------------------------------------------------ epilogue (warps 2..9)
-    const int q = warp & 3, half = (warp - 2) >> 2;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_EPI));
+    // ------------------------------------------------------------ epilogue (warps 4..11)
+    const int q = warp & 3, half = (warp - 4) >> 2;
     const int r = 32 * q + lane;  // row of the tile
-    // this thread's columns: two runs of 64. Gated: gate and up of channels [64 half, 64 half + 64)
-    const uint32_t col0 = GATED ? 64u * half : 128u * half;
-    const uint32_t col1 = GATED ? 128u + 64u * half : 128u * half + 64u;
-    const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
-    uint32_t it = 0;
+    // this thread's columns: two runs of 64, of either CTA's part of the matrix tile. Gated: gate and up of
+    // channels [64 half, 64 half + 64); else outputs [64 half, 64 half + 64) of tiles 2 n and 2 n + 1
+    const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + 128u * half;
+    const uint32_t tempty0 = first_cta(&ctl.tempty[half][0]), tempty1 = first_cta(&ctl.tempty[half][1]);
+    uint32_t b = 0, tphase = 0, g = 0, gphase = 0;
     int parity = 0;
-    bool ok = true;
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, parity ^= 1) {
-      const Tile t = tile_at(a, ctl.tile0, per, tile);
-      const float* xs = a.act_s + t.row0 + r;
-      // scales of this thread's columns, k-block kb: ws[kb * step] (and ws[kb * step + 1] for up)
-      const int wt = GATED ? t.n : min(2 * t.n + half, NT - 1);
-      constexpr int STEP = GATED ? 2 : 1;
-      const float* ws = a.ws + t.e * a.ws_stride + static_cast<size_t>(wt) * KB * STEP;
+    bool ok = true;  // once a wait has run out the rest of the tile is gone through without waiting
+    for (int tile = pair; tile < tiles; tile += pairs, parity ^= 1) {
+      const Tile t = tile_at(ctl.groups, a.E, tile, rank);
       float2 acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
-      float sw = 0.f;                                                       // lane i: scale 32 j + i
-      float sx0 = __ldcg(xs), sx1 = KB > 1 ? __ldcg(xs + a.rows) : 0.f;  // two k-blocks ahead
-      for (int kb = 0; kb < KB; ++kb, ++it) {
-        const int i = kb * STEP;
-        if ((i & 31) == 0) sw = i + lane < KB * STEP ? __ldg(ws + i + lane) : 0.f;
-        const float sx = sx0;
-        sx0 = sx1;
-        if (kb + 2 < KB) sx1 = __ldcg(xs + static_cast<size_t>(kb + 2) * a.rows);
-        const float f0 = sx * __shfl_sync(0xffffffffu, sw, i & 31);
-        const float f1 = GATED ? sx * __shfl_sync(0xffffffffu, sw, (i + 1) & 31) : f0;
-        const int b = it & 1;
-        ok = mbar_wait_bounded(&ctl.tfull[b], (it >> 1) & 1u, Q_WAIT_NS, abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t taddr = lane_base + static_cast<uint32_t>(b * 256);
-        uint32_t d0[32], d1[32];
-        tmem_ld32(taddr + col0, d0);
-        tmem_wait32(d0);
-        tmem_ld32(taddr + col0 + 32, d1);
+      for (int kb = 0; kb < KB; kb += SB) {
+        ok = ok && mbar_wait(&ctl.sfull[g], gphase, Q_WAIT_NS, abort_flag);
+        const float* xg = &ctl.scales[g].x[0][r];
+        const float* wg = ctl.scales[g].w;
+        const int n = min(SB, KB - kb);
+        float f0 = xg[0] * wg[0], f1 = xg[0] * wg[GATED ? 1 : SB];
+#pragma unroll 1
+        for (int j = 1; j <= n; ++j) {
+          // the next k-block's scales are read before this one's product is waited for
+          const int jn = j & (SB - 1);
+          const float x = xg[jn * BM], w0 = wg[GATED ? 2 * jn : jn], w1 = wg[GATED ? 2 * jn + 1 : SB + jn];
+          ok = ok && mbar_wait(&ctl.tfull[half][b], tphase, Q_WAIT_NS, abort_flag);
+          tc_fence_after();
+          const uint32_t taddr = lane_base + b * 256u;
+          // sixteen columns on their way while the sixteen before are added: more in flight would not fit beside
+          // the 128 sums
+          uint32_t d[2][16];
+          tmem_ld16(taddr, d[0]);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) fma2(acc[j], __uint_as_float(d0[2 * j]), __uint_as_float(d0[2 * j + 1]), f0);
-        tmem_wait32(d1);
-        tmem_ld32(taddr + col1, d0);
+          for (int c = 0; c < 8; ++c) {
+            tmem_wait16(d[c & 1]);
+            if (c < 7) {
+              tmem_ld16(taddr + 16 * (c + 1), d[(c + 1) & 1]);
+            } else {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_first(b ? tempty1 : tempty0);
+            }
 #pragma unroll
-        for (int j = 0; j < 16; ++j) fma2(acc[16 + j], __uint_as_float(d1[2 * j]), __uint_as_float(d1[2 * j + 1]), f0);
-        tmem_wait32(d0);
-        tmem_ld32(taddr + col1 + 32, d1);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) fma2(acc[32 + j], __uint_as_float(d0[2 * j]), __uint_as_float(d0[2 * j + 1]), f1);
-        tmem_wait32(d1);
-        tc_fence_before();
+            for (int i = 0; i < 8; ++i)
+              fma2(acc[8 * c + i], __uint_as_float(d[c & 1][2 * i]), __uint_as_float(d[c & 1][2 * i + 1]), c < 4 ? f0 : f1);
+          }
+          f0 = x * w0, f1 = x * w1;
+          b ^= 1u;
+          tphase ^= b ^ 1u;
+        }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.tempty[b]);
-#pragma unroll
-        for (int j = 0; j < 16; ++j) fma2(acc[48 + j], __uint_as_float(d1[2 * j]), __uint_as_float(d1[2 * j + 1]), f1);
+        if (lane == 0) mbar_arrive(&ctl.sempty[g]);
+        if (++g == SRING) g = 0, gphase ^= 1;
       }
+      ok = __all_sync(0xffffffffu, ok);
       if (!ok && lane == 0) fail();
       if (!GATED && !ok) break;
       const bool valid = r < t.rows;
@@ -237,43 +324,56 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_wide(const __grid_constant
         if (valid) {
           const float am = __uint_as_float(m);
           uint8_t* hp = a.h + (static_cast<size_t>(row / BM) * NT + t.n) * A_BYTES;
+          // chunks 2 c and 2 c + 1 of a row lie in one 32-byte sector, in the order that the swizzle gives
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            *reinterpret_cast<uint4*>(hp + image_at(r, 64 * half + 16 * c)) =
-                e4m3x16(reinterpret_cast<const float*>(acc) + 16 * c, am);
+          for (int c = 0; c < 2; ++c) {
+            const uint4 lo = e4m3x16(reinterpret_cast<const float*>(acc) + 32 * c, am);
+            const uint4 hi = e4m3x16(reinterpret_cast<const float*>(acc) + 32 * c + 16, am);
+            st_sector(hp + (image_at(r, 64 * half + 32 * c) & ~31u), (r & 1) ? hi : lo, (r & 1) ? lo : hi);
+          }
           if (half == 0) a.h_s[static_cast<size_t>(t.n) * a.rows + row] = __fdiv_rn(am, 448.f);
         }
       } else if (valid) {
-        const int col = 256 * t.n + 128 * half;
-        const int cols = min(128, a.N - col);
-        const size_t o = static_cast<size_t>(row) * a.ldy + col;
-        if (a.out_f32) {
-          float* y = static_cast<float*>(a.y) + o;
-          if (cols == 128 && (reinterpret_cast<uintptr_t>(y) & 15) == 0) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              reinterpret_cast<float4*>(y)[j] = make_float4(acc[2 * j].x, acc[2 * j].y, acc[2 * j + 1].x, acc[2 * j + 1].y);
-          } else {
+        for (int part = 0; part < 2; ++part) {
+          const int col = 256 * t.n + 128 * part + 64 * half;
+          const int cols = min(64, a.N - col);
+          const size_t o = static_cast<size_t>(row) * a.ldy + col;
+          const float2* v = acc + 32 * part;
+          if (a.out_f32) {
+            float* y = static_cast<float*>(a.y) + o;
+            if (cols == 64 && (reinterpret_cast<uintptr_t>(y) & 31) == 0) {
 #pragma unroll
-            for (int j = 0; j < 64; ++j) {
-              if (2 * j < cols) y[2 * j] = acc[j].x;
-              if (2 * j + 1 < cols) y[2 * j + 1] = acc[j].y;
+              for (int j = 0; j < 8; ++j) {
+                const float2* w = v + 4 * j;
+                st_sector(y + 8 * j,
+                          make_uint4(__float_as_uint(w[0].x), __float_as_uint(w[0].y), __float_as_uint(w[1].x), __float_as_uint(w[1].y)),
+                          make_uint4(__float_as_uint(w[2].x), __float_as_uint(w[2].y), __float_as_uint(w[3].x), __float_as_uint(w[3].y)));
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                if (2 * j < cols) y[2 * j] = v[j].x;
+                if (2 * j + 1 < cols) y[2 * j + 1] = v[j].y;
+              }
             }
-          }
-        } else {
-          uint16_t* y = static_cast<uint16_t*>(a.y) + o;
-          if (cols == 128 && (reinterpret_cast<uintptr_t>(y) & 15) == 0) {
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              reinterpret_cast<uint4*>(y)[j] =
-                  make_uint4(pack_bf16x2(acc[4 * j].x, acc[4 * j].y), pack_bf16x2(acc[4 * j + 1].x, acc[4 * j + 1].y),
-                             pack_bf16x2(acc[4 * j + 2].x, acc[4 * j + 2].y), pack_bf16x2(acc[4 * j + 3].x, acc[4 * j + 3].y));
           } else {
+            uint16_t* y = static_cast<uint16_t*>(a.y) + o;
+            if (cols == 64 && (reinterpret_cast<uintptr_t>(y) & 31) == 0) {
 #pragma unroll
-            for (int j = 0; j < 64; ++j) {
-              const uint32_t v = pack_bf16x2(acc[j].x, acc[j].y);
-              if (2 * j < cols) y[2 * j] = static_cast<uint16_t>(v);
-              if (2 * j + 1 < cols) y[2 * j + 1] = static_cast<uint16_t>(v >> 16);
+              for (int j = 0; j < 4; ++j) {
+                uint32_t w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[8 * j + i].x, v[8 * j + i].y);
+                st_sector(y + 16 * j, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                const uint32_t w = pack_bf16x2(v[j].x, v[j].y);
+                if (2 * j < cols) y[2 * j] = static_cast<uint16_t>(w);
+                if (2 * j + 1 < cols) y[2 * j + 1] = static_cast<uint16_t>(w >> 16);
+              }
             }
           }
         }
@@ -282,10 +382,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_wide(const __grid_constant
   }
 
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();  // nothing of either CTA is still used by the other
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, TMEM_COLS);
+    tmem_dealloc_pair(tmem_base, TMEM_COLS);
   }
 }
 
@@ -294,10 +394,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_wide(const __grid_constant
 cudaError_t launch_qgemm_wide(const QGemmArgs& a, bool gated, cudaStream_t st) {
   const size_t smem = STAGES * STAGE + 1024;
   const void* k = gated ? reinterpret_cast<const void*>(&k_qgemm_wide<true>) : reinterpret_cast<const void*>(&k_qgemm_wide<false>);
-  const cudaError_t e = ensure_dyn_smem(k, smem + sizeof(Ctl));
+  const cudaError_t e = ensure_dyn_smem(k, smem);
   if (e != cudaSuccess) return e;
-  return gated ? launch_q(k_qgemm_wide<true>, dim3(a.num_sms), THREADS, smem, st, a)
-               : launch_q(k_qgemm_wide<false>, dim3(a.num_sms), THREADS, smem, st, a);
+  return gated ? launch_q(k_qgemm_wide<true>, dim3(a.num_sms & ~1), THREADS, smem, st, a)
+               : launch_q(k_qgemm_wide<false>, dim3(a.num_sms & ~1), THREADS, smem, st, a);
 }
 
 }  // namespace pop
