@@ -72,27 +72,28 @@ __device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint3
                : "memory");
 }
 
-// D[tmem] (+)= A[smem desc] * B[smem desc], kind::f8f6f4 (e4m3 inputs, fp32 accumulate), one CTA.
-__device__ __forceinline__ void umma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-      ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
 // Instruction descriptor, kind::f8f6f4 with e4m3 A and B (format 0), both K-major, and fp32 D.
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// One k-block (128 bytes of k: four products of 32) of A's and B's images.
-__device__ __forceinline__ void umma_block(uint32_t d_tmem, uint32_t a_smem, uint32_t b_smem, uint32_t idesc) {
-  const uint64_t ad = smem_desc_sw128(a_smem, 16u, 1024u), bd = smem_desc_sw128(b_smem, 16u, 1024u);
+// A k-block (128 bytes of k) is four products of 32. a_lo and b_lo: the low words of the operands' descriptors
+// (address >> 4 | leading offset), which alone change from block to block. The descriptors are put together
+// here from 32-bit words: as 64-bit sums in a thread's own registers they took about 70 cycles a product to
+// issue, as much as the product takes.
+constexpr uint32_t DESC_LO = 1u << 16;                                 // leading byte offset 16 (not used by the swizzle)
+constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride 1024, version 1, 128-byte swizzle
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return ((saddr >> 4) & 0x3FFFu) | DESC_LO; }
+__device__ __forceinline__ void umma_block(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) umma_e4m3(d_tmem, ad + 2 * k, bd + 2 * k, idesc, k > 0 ? 1u : 0u);
+  for (int k = 0; k < 4; ++k)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo + 2 * k), "r"(b_lo + 2 * k), "r"(idesc), "r"(DESC_HI), "r"(k > 0 ? 1u : 0u)
+        : "memory");
 }
 
 // Waits until the phase with the given parity has completed; false after limit_ns, or once another role of the
@@ -154,13 +155,7 @@ __device__ __forceinline__ void tmem_alloc_pair(uint32_t* smem_result, uint32_t 
 __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
-// One k-block on both CTAs' tensor cores: A's rows and B's rows lie half in each, at the same addresses. a_lo
-// and b_lo: the low words of the descriptors (address >> 4 | leading offset), which alone change from block to
-// block; built from 32-bit words here, as 64-bit sums in a thread's own registers took four times as long to
-// issue as the products take.
-constexpr uint32_t DESC_LO = 1u << 16;                                 // leading byte offset 16 (not used by the swizzle)
-constexpr uint32_t DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);  // stride 1024, version 1, 128-byte swizzle
-__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return ((saddr >> 4) & 0x3FFFu) | DESC_LO; }
+// The same on both CTAs' tensor cores: A's rows and B's rows lie half in each, at the same addresses.
 __device__ __forceinline__ void umma_block_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc) {
 #pragma unroll
   for (int k = 0; k < 4; ++k)

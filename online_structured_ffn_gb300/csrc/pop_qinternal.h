@@ -7,8 +7,8 @@
 //     are zero. Its scales are float32, a tile's ceil(K/128) in order, tiles scale_stride apart. The gate and
 //     up matrices of a gated MLP share one image, [tile][k-block][gate 16 KB | up 16 KB], and their scales
 //     [tile][k-block][2].
-//   - rows (tokens): runs of G rows (G = 16 or 128), [run][k-block][G x 128 bytes]; scales
-//     [k-block][row]. Bytes past K are zero; what rows without a token hold is not used.
+//   - rows (tokens): runs of G rows (G = 16, 32, 64 or 128), [run][k-block][G x 128 bytes]; scales
+//     [run][k-block][G]. Bytes past K are zero; what rows without a token hold is not used.
 // Tokens of an expert stand together: expert e's rows are the runs [run0[e], run0[e + 1]).
 #pragma once
 #include <cuda_runtime.h>
@@ -42,9 +42,9 @@ struct QRowsArgs {       // rows to quantise, or in e4m3 already
 };
 struct QRowsOut {
   uint8_t* q;            // plain: [M][ldq]; image: runs of G rows
-  float* s;              // plain: [M][KB]; image: [KB][rows]
+  float* s;              // plain: [M][KB]; image: [run][KB][G]
   long long ldq;
-  int G, rows;           // G = 0: plain
+  int G;                 // 0: plain
   // image: rows of token t (NULL: row t itself): row_of[t * k + j] for j < k, < 0 for none
   const int* row_of;
   int k;
@@ -69,7 +69,7 @@ cudaError_t launch_combine(const float* o, const int* row_of, const float* weigh
 struct QGemmArgs {
   const uint8_t* act;    // rows
   const float* act_s;
-  int G, rows;           // rows: capacity (stride of act_s)
+  int G;
   const uint8_t* w;      // E matrices (gated: E gate/up images), w_stride bytes apart
   const float* ws;       // ws_stride floats apart
   size_t w_stride, ws_stride;
@@ -92,9 +92,8 @@ struct QGemmArgs {
   unsigned* err;
   int num_sms;
 };
-// few rows per group (G = 16): the matrix streams once (pop_qthin.cu). max_rows: the most rows that a group
-// is expected to have; more are right too.
-cudaError_t launch_qgemm_thin(const QGemmArgs& a, bool gated, int max_rows, cudaStream_t st);
+// few rows per group (G = 16, 32 or 64): the matrix streams once (pop_qthin.cu)
+cudaError_t launch_qgemm_thin(const QGemmArgs& a, bool gated, cudaStream_t st);
 size_t qgemm_thin_parts(int num_sms, bool gated);
 // many rows per group (G = 128): 128 x 256 tiles (pop_qwide.cu)
 cudaError_t launch_qgemm_wide(const QGemmArgs& a, bool gated, cudaStream_t st);

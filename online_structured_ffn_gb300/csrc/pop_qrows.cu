@@ -17,16 +17,19 @@ __device__ __forceinline__ void unpack8(const void* p, int kind, float* v) {
   }
 }
 
-// Eight lanes per block of 128, 16 values each.
-__global__ void __launch_bounds__(256) k_quantize_rows(QRowsArgs in, QRowsOut out) {
+// Eight lanes per block of 128, 16 values each. A CTA has 32 blocks at a time: of one row, or of the `per` whole
+// rows that they hold.
+__global__ void __launch_bounds__(256) k_quantize_rows(const __grid_constant__ QRowsArgs in, const __grid_constant__ QRowsOut out, int per) {
+  pdl_wait();  // the rows, their places, and what an earlier call's kernels still read
+  pdl_trigger();
   const int KB = qceil(in.K, QB);
-  const long long units = static_cast<long long>(in.M) * KB;
-  const int lane8 = threadIdx.x & 7;
-  for (long long u = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 3;
-       u - ((threadIdx.x & 31) >> 3) < units; u += (static_cast<long long>(gridDim.x) * blockDim.x) >> 3) {
-    const bool on = u < units;
-    const int row = on ? static_cast<int>(u / KB) : 0;
-    const int kb = on ? static_cast<int>(u - static_cast<long long>(row) * KB) : 0;
+  const int lane8 = threadIdx.x & 7, u = threadIdx.x >> 3;
+  const int row_in = per > 1 ? u / KB : 0;
+  const int row = blockIdx.x * per + row_in;
+  const bool mine = row_in < per && row < in.M;
+  // (a warp's lanes go round together: for several rows a CTA there is one round)
+  for (int kb = u - row_in * KB; kb - u % 4 < KB; kb += per > 1 ? 1 << 24 : 32) {
+    const bool on = mine && kb < KB;
     const int k0 = kb * QB + lane8 * 16;
     const int n8 = on ? min(max((in.K - k0) >> 3, 0), 2) : 0;  // runs of 8 values this lane has
     uint4 q = make_uint4(0u, 0u, 0u, 0u);
@@ -68,11 +71,12 @@ __global__ void __launch_bounds__(256) k_quantize_rows(QRowsArgs in, QRowsOut ou
       continue;
     }
     for (int j = 0; j < out.k; ++j) {
-      const int r = out.row_of ? out.row_of[static_cast<size_t>(row) * out.k + j] : row;
+      const int r = out.row_of ? __ldcg(out.row_of + static_cast<size_t>(row) * out.k + j) : row;
       if (r < 0) continue;
-      const size_t image = (static_cast<size_t>(r / out.G) * KB + kb) * out.G * QB;
-      *reinterpret_cast<uint4*>(out.q + image + image_at(r % out.G, lane8 * 16)) = q;
-      if (lane8 == 0) out.s[static_cast<size_t>(kb) * out.rows + r] = s;
+      const int run = r / out.G, in_run = r - run * out.G;
+      const size_t block = static_cast<size_t>(run) * KB + kb;
+      *reinterpret_cast<uint4*>(out.q + block * out.G * QB + image_at(in_run, lane8 * 16)) = q;
+      if (lane8 == 0) out.s[block * out.G + in_run] = s;
     }
   }
 }
@@ -135,46 +139,80 @@ __global__ void __launch_bounds__(256) k_pack_matrix(const void* __restrict__ W,
   if (threadIdx.x == 0) *scale = __fdiv_rn(a, 448.f);
 }
 
-// One CTA. Warp w numbers the pairs of experts w, w + 32, ... in ascending order, a ballot per 32 pairs;
-// then the runs' prefix sums; then every pair's row.
-__global__ void __launch_bounds__(1024) k_plan(const int* __restrict__ experts, int pairs, int E, int G,
-                                               int* __restrict__ counts, int* __restrict__ run0,
-                                               int* __restrict__ row_of, unsigned* __restrict__ err) {
-  __shared__ int s_run0[POP_QMOE_MAX_EXPERTS];
+// One CTA; warp w has the w-th part of the pairs. First every warp counts its pairs of each expert (lanes with the
+// same expert find each other with a match), then the counts become first places (over the warps, and over the
+// experts in whole runs), then every warp goes through its pairs again and numbers them, in ascending order.
+constexpr int PLAN_WARPS = 32;
+__global__ void __launch_bounds__(32 * PLAN_WARPS) k_plan(const int* __restrict__ experts, int pairs, int E, int G,
+                                                          int* __restrict__ counts, int* __restrict__ run0,
+                                                          int* __restrict__ row_of, unsigned* __restrict__ err) {
+  __shared__ int s_at[PLAN_WARPS][POP_QMOE_MAX_EXPERTS];
+  __shared__ int s_runs[POP_QMOE_MAX_EXPERTS];
+  constexpr unsigned ALL = 0xffffffffu;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const unsigned lt = (1u << lane) - 1u;
-  for (int p = threadIdx.x; p < pairs; p += blockDim.x) {
-    const int e = experts[p];
-    if (e < 0 || e >= E) {
-      row_of[p] = -1;
-      if (e != -1) atomicOr(err, QERR_EXPERT);
+  pdl_wait();  // the routing, and an earlier call's use of what is written here
+  pdl_trigger();
+  for (int i = threadIdx.x; i < PLAN_WARPS * POP_QMOE_MAX_EXPERTS; i += blockDim.x) (&s_at[0][0])[i] = 0;
+  __syncthreads();
+  const int part = qceil(qceil(pairs, PLAN_WARPS), 32) * 32;
+  const int p0 = warp * part, p1 = min(pairs, p0 + part);
+  // f(pair, its expert or -1, lanes of the same expert), 32 pairs at a time, four loads on their way
+  auto each = [&](auto f) {
+    for (int c = p0; c < p1; c += 128) {
+      int e[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) e[i] = c + 32 * i + lane < p1 ? __ldg(experts + c + 32 * i + lane) : -1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (c + 32 * i >= p1) break;
+        const int v = static_cast<unsigned>(e[i]) < static_cast<unsigned>(E) ? e[i] : -1;
+        f(c + 32 * i + lane, v, __match_any_sync(ALL, v));
+        if (v != e[i] && e[i] != -1) atomicOr(err, QERR_EXPERT);
+      }
     }
+  };
+  each([&](int, int e, unsigned same) {
+    if (e >= 0 && lane == __ffs(same) - 1) s_at[warp][e] += __popc(same);
+    __syncwarp();
+  });
+  __syncthreads();
+  if (threadIdx.x < POP_QMOE_MAX_EXPERTS) {
+    const int e = threadIdx.x;
+    int n = 0;
+    for (int w = 0; w < PLAN_WARPS; ++w) {
+      const int v = s_at[w][e];
+      s_at[w][e] = n;
+      n += v;
+    }
+    if (e < E) counts[e] = n;
+    s_runs[e] = qceil(n, G);
   }
-  for (int e = warp; e < E; e += blockDim.x >> 5) {
+  __syncthreads();
+  if (warp == 0) {
     int base = 0;
-    for (int c = 0; c < pairs; c += 32) {
-      const bool hit = c + lane < pairs && experts[c + lane] == e;
-      const unsigned m = __ballot_sync(0xffffffffu, hit);
-      if (hit) row_of[c + lane] = base + __popc(m & lt);
-      base += __popc(m);
+    for (int e = lane; e < POP_QMOE_MAX_EXPERTS; e += 32) {
+      const int own = s_runs[e];
+      int n = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(ALL, n, o);
+        if (lane >= o) n += v;
+      }
+      s_runs[e] = base + n - own;
+      if (e <= E) run0[e] = base + n - own;
+      base += __shfl_sync(ALL, n, 31);
     }
-    if (lane == 0) counts[e] = base;
+    if (E == POP_QMOE_MAX_EXPERTS && lane == 0) run0[E] = base;
   }
   __syncthreads();
-  if (threadIdx.x == 0) {
-    int s = 0;
-    for (int e = 0; e < E; ++e) {
-      s_run0[e] = s;
-      run0[e] = s;
-      s += qceil(counts[e], G);
-    }
-    run0[E] = s;
-  }
-  __syncthreads();
-  for (int p = threadIdx.x; p < pairs; p += blockDim.x) {
-    const int e = experts[p];
-    if (e >= 0 && e < E) row_of[p] += s_run0[e] * G;
-  }
+  each([&](int p, int e, unsigned same) {
+    int at = 0;
+    if (e >= 0) at = s_at[warp][e];
+    __syncwarp();
+    if (p < p1) row_of[p] = e < 0 ? -1 : s_runs[e] * G + at + __popc(same & ((1u << lane) - 1u));
+    if (e >= 0 && lane == __ffs(same) - 1) s_at[warp][e] = at + __popc(same);
+    __syncwarp();
+  });
 }
 
 // Four outputs per thread.
@@ -183,6 +221,8 @@ __global__ void __launch_bounds__(256) k_combine(const float* __restrict__ o, co
                                                  void* __restrict__ y, long long ldy, int out_f32) {
   const size_t t = blockIdx.x;
   const int d = 4 * (blockIdx.y * 256 + threadIdx.x);
+  pdl_wait();  // the experts' outputs
+  pdl_trigger();
   if (d >= D) return;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int j = 0; j < k; ++j) {
@@ -205,10 +245,9 @@ __global__ void __launch_bounds__(256) k_combine(const float* __restrict__ o, co
 }  // namespace
 
 cudaError_t launch_quantize_rows(const QRowsArgs& in, const QRowsOut& out, cudaStream_t st) {
-  const long long threads = static_cast<long long>(in.M) * qceil(in.K, QB) * 8;
-  const long long grid = (threads + 255) / 256;
-  k_quantize_rows<<<static_cast<unsigned>(grid < (1ll << 30) ? grid : (1ll << 30)), 256, 0, st>>>(in, out);
-  return cudaGetLastError();
+  const int KB = qceil(in.K, QB);
+  const int per = KB < 32 ? 32 / KB : 1;
+  return launch_q(k_quantize_rows, dim3(qceil(in.M, per)), 256, 0, st, in, out, per);
 }
 
 cudaError_t launch_pack_matrix(const void* W, const float* Ws, int N, int K, uint8_t* img, float* s, int step,
@@ -219,14 +258,12 @@ cudaError_t launch_pack_matrix(const void* W, const float* Ws, int N, int K, uin
 
 cudaError_t launch_plan(const int* experts, int pairs, int E, int G, int* counts, int* run0, int* row_of,
                         unsigned* err, cudaStream_t st) {
-  k_plan<<<1, 1024, 0, st>>>(experts, pairs, E, G, counts, run0, row_of, err);
-  return cudaGetLastError();
+  return launch_q(k_plan, dim3(1), 32 * PLAN_WARPS, 0, st, experts, pairs, E, G, counts, run0, row_of, err);
 }
 
 cudaError_t launch_combine(const float* o, const int* row_of, const float* weights, int T, int k, int D, void* y,
                            long long ldy, int out_f32, cudaStream_t st) {
-  k_combine<<<dim3(T, qceil(D, 1024)), 256, 0, st>>>(o, row_of, weights, k, D, y, ldy, out_f32);
-  return cudaGetLastError();
+  return launch_q(k_combine, dim3(T, qceil(D, 1024)), 256, 0, st, o, row_of, weights, k, D, y, ldy, out_f32);
 }
 
 }  // namespace pop

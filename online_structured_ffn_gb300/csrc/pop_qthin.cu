@@ -9,10 +9,11 @@
 // whichever of its CTAs comes last (a counter per tile; no CTA waits for another), so the bits do not
 // depend on the order in which CTAs run.
 //
-// Warp 0: copies (one bulk copy per stage for the matrix, its image being what shared memory needs; 2 KB
-// per 16 tokens; the tokens' scales). Warp 1: products. Warps 2..5: epilogue, TMEM lane quarter warp % 4.
-// Every wait has a limit; a CTA that gives up records QERR_TIMEOUT, lets its copies and products finish,
-// frees TMEM and returns.
+// Warp 0: copies. A stage is 32 KB of the matrix (one bulk copy: its image is what shared memory needs) and
+// the same k-blocks of the rows and of their scales (a copy each; a run of rows is one tile). The matrix does not depend on the
+// kernel before, so the first stages' copies of it go out before this one is waited for. Warp 1: products. Warps
+// 2..5: epilogue, TMEM lane quarter warp % 4. Every wait has a limit; a CTA that gives up records QERR_TIMEOUT,
+// lets its copies and products finish, frees TMEM and returns.
 #include "pop_qdevice.cuh"
 
 namespace pop {
@@ -22,17 +23,20 @@ cudaError_t ensure_dyn_smem(const void* kernel, size_t bytes);
 namespace {
 
 constexpr int THREADS = 192;
-constexpr uint32_t RING_BYTES = 200 * 1024;
+constexpr uint32_t RING_BYTES = 208 * 1024;
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int MAX_STAGES = 16, MAX_BUFS = 8;
+constexpr int MAX_STAGES = 8, MAX_BUFS = 8;
 
 template <bool GATED, int NT>
 struct Thin {
   static constexpr int P = GATED ? 2 : 1;
-  static constexpr uint32_t W_BYTES = P * QTILE;
-  static constexpr uint32_t X_BYTES = NT * QB;
-  static constexpr uint32_t STAGE = (W_BYTES + X_BYTES + NT * 4 + 1023) / 1024 * 1024;
-  static constexpr int STAGES = RING_BYTES / STAGE < MAX_STAGES ? RING_BYTES / STAGE : MAX_STAGES;
+  static constexpr int KS = GATED ? 1 : 2;          // k-blocks of a stage
+  static constexpr uint32_t W_BYTES = P * QTILE;    // of a k-block
+  static constexpr uint32_t X_BYTES = NT * QB;      // of a k-block's rows: one run of NT
+  static constexpr uint32_t S_BYTES = NT * 4;       // of their scales
+  static constexpr uint32_t X_OFF = KS * W_BYTES, S_OFF = X_OFF + KS * X_BYTES;
+  static constexpr uint32_t STAGE = (S_OFF + KS * S_BYTES + 1023) / 1024 * 1024;
+  static constexpr int STAGES = RING_BYTES / STAGE;
   static constexpr int BUFS = static_cast<int>(TMEM_COLS) / (P * NT) < MAX_BUFS ? static_cast<int>(TMEM_COLS) / (P * NT) : MAX_BUFS;
 };
 
@@ -50,8 +54,8 @@ struct Ctl {
 // One run of k-blocks of a tile.
 struct Seg {
   int tile, kb0, kb1;
-  int e, t, n0, n;  // group, output tile, first token and number of tokens of the tile
-  int row0;         // first row
+  int e, t, n;      // group, output tile, rows of the tile
+  int run;          // of rows
 };
 
 template <int NT>
@@ -65,9 +69,9 @@ __device__ __forceinline__ Seg segment(const Groups& gr, int E, int KB, long lon
   const int tts = qceil(cnt, NT);
   const int local = s.tile - gr.tile0[s.e];
   s.t = local / tts;  // the token tiles of one output tile side by side: the matrix tile is in L2 for the others
-  s.n0 = (local - s.t * tts) * NT;
-  s.n = min(NT, cnt - s.n0);
-  s.row0 = gr.run0[s.e] * 16 + s.n0;
+  const int i = local - s.t * tts;
+  s.n = min(NT, cnt - i * NT);
+  s.run = gr.run0[s.e] + i;
   return s;
 }
 
@@ -80,7 +84,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
   extern __shared__ uint8_t smem_raw[];
   __shared__ Ctl ctl;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int KB = qceil(a.K, QB), NTILES = qceil(a.N, QB);
   volatile int* abort_flag = &ctl.abort_flag;
 
@@ -105,7 +109,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = ctl.tmem_base;
-  pdl_wait();  // the rows, the groups, and what an earlier call's kernels still use
+  // The groups (of experts) are two kernels back: the one before this waited for them before it let this one
+  // start.
   pdl_trigger();
   const int tiles = ctl.groups.fill(a, NT, NTILES);
   const long long work = static_cast<long long>(tiles) * KB;
@@ -123,30 +128,60 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
   if (warp == 0) {
     if (lane == 0) {
       // ---------------------------------------------------------- copies (one thread)
-      uint32_t issued = 0;
-      bool ok = true;
+      // A stage's rows follow its part of the matrix; the first stages' all at once, after the wait.
+      struct Rows {
+        const uint8_t* x;
+        const float* s;
+        int n;  // k-blocks
+      } owed[C::STAGES];
+      auto load_rows = [&](const Rows& r, uint32_t s) {
+        uint8_t* st = smem + s * C::STAGE;
+        bulk_load(st + C::X_OFF, r.x, r.n * C::X_BYTES, &ctl.full[s]);
+        bulk_load(st + C::S_OFF, r.s, r.n * C::S_BYTES, &ctl.full[s]);
+      };
+      uint32_t issued = 0, s = 0, phase = 1;
+      bool ok = true, waited = false;
       for (long long x = x0; x < x1 && ok;) {
         const Seg g = segment<NT>(ctl.groups, a.E, KB, x, x1);
-        const int runs = qceil(g.n, 16);
-        const uint8_t* w = a.w + g.e * a.w_stride + static_cast<size_t>(g.t) * KB * C::W_BYTES;
-        const uint8_t* xr = a.act + static_cast<size_t>(g.row0 / 16) * KB * 2048;
-        const uint32_t bytes = C::W_BYTES + runs * (2048 + 64);
-        for (int kb = g.kb0; kb < g.kb1; ++kb, ++issued) {
-          const int s = issued % C::STAGES;
-          if (!mbar_wait(&ctl.empty[s], ((issued / C::STAGES) & 1u) ^ 1u, Q_WAIT_NS, abort_flag)) {
+        const uint8_t* w = a.w + g.e * a.w_stride + (static_cast<size_t>(g.t) * KB + g.kb0) * C::W_BYTES;
+        Rows r;
+        r.x = a.act + (static_cast<size_t>(g.run) * KB + g.kb0) * C::X_BYTES;
+        r.s = a.act_s + (static_cast<size_t>(g.run) * KB + g.kb0) * NT;
+        for (int kb = g.kb0; kb < g.kb1; kb += C::KS) {
+          if (!waited && issued == C::STAGES) {
+            pdl_wait();
+            waited = true;
+#pragma unroll
+            for (int i = 0; i < C::STAGES; ++i) load_rows(owed[i], i);
+          }
+          if (!mbar_wait(&ctl.empty[s], phase, Q_WAIT_NS, abort_flag)) {
             fail();
             ok = false;
             break;
           }
-          uint8_t* st = smem + s * C::STAGE;
-          mbar_arrive_expect_tx(&ctl.full[s], bytes);
-          bulk_load(st, w + static_cast<size_t>(kb) * C::W_BYTES, C::W_BYTES, &ctl.full[s]);
-          for (int r = 0; r < runs; ++r)
-            bulk_load(st + C::W_BYTES + r * 2048, xr + (static_cast<size_t>(r) * KB + kb) * 2048, 2048, &ctl.full[s]);
-          bulk_load(st + C::W_BYTES + C::X_BYTES, a.act_s + static_cast<size_t>(kb) * a.rows + g.row0, runs * 64,
-                    &ctl.full[s]);
+          r.n = min(C::KS, g.kb1 - kb);
+          mbar_arrive_expect_tx(&ctl.full[s], r.n * (C::W_BYTES + C::X_BYTES + C::S_BYTES));
+          bulk_load(smem + s * C::STAGE, w, r.n * C::W_BYTES, &ctl.full[s]);
+          if (waited) {
+            load_rows(r, s);
+          } else {
+#pragma unroll
+            for (int i = 0; i < C::STAGES; ++i)
+              if (i == static_cast<int>(s)) owed[i] = r;
+          }
+          w += C::KS * C::W_BYTES;
+          r.x += C::KS * C::X_BYTES;
+          r.s += C::KS * NT;
+          ++issued;
+          if (++s == C::STAGES) s = 0, phase ^= 1;
         }
         x += g.kb1 - g.kb0;
+      }
+      if (!waited) {  // a short run: every stage that was begun gets its rows
+        pdl_wait();
+#pragma unroll
+        for (int i = 0; i < C::STAGES; ++i)
+          if (i < static_cast<int>(issued)) load_rows(owed[i], i);
       }
       // no copy of this CTA may be in flight when it exits
       const uint32_t lo = issued > C::STAGES ? issued - C::STAGES : 0;
@@ -157,90 +192,111 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---------------------------------------------------------- products (one thread)
-      uint32_t it = 0;
-      bool ok = true;
-      for (long long x = x0; x < x1 && ok;) {
-        const Seg g = segment<NT>(ctl.groups, a.E, KB, x, x1);
-        const uint32_t idesc = idesc_e4m3_f32(128, qceil(g.n, 16) * 16);
-        for (int kb = g.kb0; kb < g.kb1; ++kb, ++it) {
-          const int s = it % C::STAGES, b = it % C::BUFS;
-          if (!mbar_wait(&ctl.full[s], (it / C::STAGES) & 1u, Q_WAIT_NS, abort_flag) ||
-              !mbar_wait(&ctl.tempty[b], ((it / C::BUFS) & 1u) ^ 1u, Q_WAIT_NS, abort_flag)) {
-            fail();
-            ok = false;
-            break;
+    // ------------------------------------------------------------ products (one warp, one lane of it issuing)
+    const bool leader = elect_one();
+    const uint32_t ring = desc_lo(smem_u32(smem));
+    uint32_t s = 0, phase = 0, b = 0, tphase = 1;
+    bool ok = true;
+    for (long long x = x0; x < x1 && ok;) {
+      const Seg g = segment<NT>(ctl.groups, a.E, KB, x, x1);
+      const uint32_t idesc = idesc_e4m3_f32(128, qceil(g.n, 16) * 16);
+      for (int kb = g.kb0; kb < g.kb1 && ok; kb += C::KS) {
+        ok = mbar_wait(&ctl.full[s], phase, Q_WAIT_NS, abort_flag);
+#pragma unroll
+        for (int u = 0; u < C::KS; ++u) {
+          if (kb + u < g.kb1) {
+            ok = ok && mbar_wait(&ctl.tempty[b], tphase, Q_WAIT_NS, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            if (leader) {
+              const uint32_t st = ring + s * (C::STAGE >> 4);
+              const uint32_t d = tmem_base + b * static_cast<uint32_t>(P * NT);
+              const uint32_t w = st + u * (C::W_BYTES >> 4), xr = st + ((C::X_OFF + u * C::X_BYTES) >> 4);
+              umma_block(d, w, xr, idesc);
+              if (GATED) umma_block(d + NT, w + (QTILE >> 4), xr, idesc);
+              umma_commit(&ctl.tfull[b]);
+              if (u == C::KS - 1 || kb + u == g.kb1 - 1) umma_commit(&ctl.empty[s]);
+            }
+            __syncwarp();
+            if (++b == C::BUFS) b = 0, tphase ^= 1;
           }
-          tc_fence_after();
-          const uint32_t st = smem_u32(smem + s * C::STAGE);
-          const uint32_t d = tmem_base + static_cast<uint32_t>(b * P * NT);
-          umma_block(d, st, st + C::W_BYTES, idesc);
-          if (GATED) umma_block(d + NT, st + QTILE, st + C::W_BYTES, idesc);
-          umma_commit(&ctl.empty[s]);
-          umma_commit(&ctl.tfull[b]);
         }
-        x += g.kb1 - g.kb0;
+        if (++s == C::STAGES) s = 0, phase ^= 1;
       }
-      umma_commit(&ctl.drain);
-      volatile int never = 0;
-      if (!mbar_wait(&ctl.drain, 0, Q_DRAIN_NS, &never)) fail();
+      x += g.kb1 - g.kb0;
     }
+    if (!ok && leader) fail();
+    if (leader) umma_commit(&ctl.drain);
+    volatile int never = 0;
+    if (!mbar_wait(&ctl.drain, 0, Q_DRAIN_NS, &never) && leader) fail();
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue (warps 2..5)
+    pdl_wait();  // what this kernel writes may still be read by the one before
     const int q = warp & 3;
     const int f = 32 * q + lane;  // output of the tile
     const int et = threadIdx.x - 64;
-    uint32_t it = 0;
+    const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
+    uint32_t s = 0, phase = 0, b = 0, tphase = 0;
     for (long long x = x0; x < x1;) {
       const Seg g = segment<NT>(ctl.groups, a.E, KB, x, x1);
-      const float* ws = a.ws + g.e * a.ws_stride + static_cast<size_t>(g.t) * scale_stride(KB, P);
+      // the matrix's scales of this run of k-blocks: lane i holds number 32 j + i, and the one after is on its way
+      const float* ws = a.ws + g.e * a.ws_stride + static_cast<size_t>(g.t) * scale_stride(KB, P) + g.kb0 * P;
+      const int nw = (g.kb1 - g.kb0) * P;
+      float sw = 0.f, sw_next = lane < nw ? __ldg(ws + lane) : 0.f;
       float acc[P][NT];
 #pragma unroll
       for (int p = 0; p < P; ++p)
 #pragma unroll
         for (int n = 0; n < NT; ++n) acc[p][n] = 0.f;
-      float sw = 0.f;  // lane i: the matrix's scale number 32 j + i of this run
-      bool ok = true;
-      for (int kb = g.kb0; kb < g.kb1; ++kb, ++it) {
-        const int i = (kb - g.kb0) * P;
-        if ((i & 31) == 0) sw = i + lane < (g.kb1 - g.kb0) * P ? __ldg(ws + static_cast<size_t>(g.kb0) * P + i + lane) : 0.f;
-        const int s = it % C::STAGES, b = it % C::BUFS;
-        ok = mbar_wait(&ctl.full[s], (it / C::STAGES) & 1u, Q_WAIT_NS, abort_flag) &&
-             mbar_wait(&ctl.tfull[b], (it / C::BUFS) & 1u, Q_WAIT_NS, abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        tc_fence_after();
-        const float4* sx = reinterpret_cast<const float4*>(smem + s * C::STAGE + C::W_BYTES + C::X_BYTES);
-        const uint32_t taddr = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + static_cast<uint32_t>(b * P * NT);
-        const float s0 = __shfl_sync(0xffffffffu, sw, i & 31), s1 = __shfl_sync(0xffffffffu, sw, (i + P - 1) & 31);
+      bool ok = true;  // once a wait has run out the rest of the run is gone through without waiting
+      int i = 0;
+      for (int kb = g.kb0; kb < g.kb1; kb += C::KS) {
+        ok = ok && mbar_wait(&ctl.full[s], phase, Q_WAIT_NS, abort_flag);
+        const uint8_t* st = smem + s * C::STAGE + C::S_OFF;
 #pragma unroll
-        for (int c = 0; c < NT; c += 16) {
-          if (c >= g.n) break;
-          uint32_t d0[16], d1[16];
-          tmem_ld16(taddr + c, d0);
-          if (GATED) tmem_ld16(taddr + NT + c, d1);
-          tmem_wait16(d0);
-          if (GATED) tmem_wait16(d1);
-#pragma unroll
-          for (int j = 0; j < 16; j += 4) {
-            const float4 v = sx[(c + j) >> 2];
-            const float vs[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              acc[0][c + j + r] = fmaf(s0 * vs[r], __uint_as_float(d0[j + r]), acc[0][c + j + r]);
-              if (GATED) acc[P - 1][c + j + r] = fmaf(s1 * vs[r], __uint_as_float(d1[j + r]), acc[P - 1][c + j + r]);
+        for (int u = 0; u < C::KS; ++u) {
+          if (kb + u < g.kb1) {
+            if ((i & 31) == 0) {
+              sw = sw_next;
+              sw_next = i + 32 + lane < nw ? __ldg(ws + i + 32 + lane) : 0.f;
             }
+            const float s0 = __shfl_sync(0xffffffffu, sw, i & 31), s1 = __shfl_sync(0xffffffffu, sw, (i + P - 1) & 31);
+            i += P;
+            const float4* sx = reinterpret_cast<const float4*>(st + u * C::S_BYTES);
+            const uint32_t taddr = lane_base + b * static_cast<uint32_t>(P * NT);
+            ok = ok && mbar_wait(&ctl.tfull[b], tphase, Q_WAIT_NS, abort_flag);
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < NT; c += 16) {
+              if (c >= g.n) break;
+              uint32_t d0[16], d1[16];
+              tmem_ld16(taddr + c, d0);
+              if (GATED) tmem_ld16(taddr + NT + c, d1);
+              tmem_wait16(d0);
+              if (GATED) tmem_wait16(d1);
+#pragma unroll
+              for (int j = 0; j < 16; j += 4) {
+                const float4 v = sx[(c + j) >> 2];
+                const float vs[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                  acc[0][c + j + r] = fmaf(s0 * vs[r], __uint_as_float(d0[j + r]), acc[0][c + j + r]);
+                  if (GATED) acc[P - 1][c + j + r] = fmaf(s1 * vs[r], __uint_as_float(d1[j + r]), acc[P - 1][c + j + r]);
+                }
+              }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.tempty[b]);
+            if (++b == C::BUFS) b = 0, tphase ^= 1;
           }
         }
-        tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&ctl.tempty[b]);
-          mbar_arrive(&ctl.empty[s]);
-        }
+        if (lane == 0) mbar_arrive(&ctl.empty[s]);
+        if (++s == C::STAGES) s = 0, phase ^= 1;
       }
+      ok = __all_sync(0xffffffffu, ok);
       if (!ok && lane == 0) fail();
       if (epi_any<128>(!ok)) break;  // all four warps go on, or none
       x += g.kb1 - g.kb0;
@@ -285,7 +341,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             if (n < g.n) {
-              const size_t o = static_cast<size_t>(g.row0 + n) * a.ldy + col;
+              const size_t o = (static_cast<size_t>(g.run) * NT + n) * a.ldy + col;
               if (a.out_f32)
                 static_cast<float*>(a.y)[o] = acc[0][n];
               else
@@ -311,10 +367,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
             const float am = __uint_as_float(m);
             const bool huge = q_huge(am);
             const float v = q_ratio(acc[0][n], am, q_recip(am, huge), huge);
-            const int r = g.row0 + n;
-            a.h[(static_cast<size_t>(r / 16) * NTILES + g.t) * 2048 + image_at(r % 16, f)] =
-                static_cast<uint8_t>(e4m3x2(v, 0.f));
-            if (f == 0) a.h_s[static_cast<size_t>(g.t) * a.rows + r] = __fdiv_rn(am, 448.f);
+            const size_t block = static_cast<size_t>(g.run) * NTILES + g.t;
+            a.h[block * C::X_BYTES + image_at(n, f)] = static_cast<uint8_t>(e4m3x2(v, 0.f));
+            if (f == 0) a.h_s[block * NT + n] = __fdiv_rn(am, 448.f);
           }
         }
         epi_sync();  // ctl.amax is free again
@@ -344,10 +399,9 @@ cudaError_t launch(const QGemmArgs& a, cudaStream_t st) {
 // Two slots per CTA of the widest kind of tile.
 size_t qgemm_thin_parts(int num_sms, bool gated) { return static_cast<size_t>(2) * num_sms * 128 * 64 * (gated ? 2 : 1); }
 
-cudaError_t launch_qgemm_thin(const QGemmArgs& a, bool gated, int max_rows, cudaStream_t st) {
-  const int nt = max_rows <= 16 ? 16 : max_rows <= 32 ? 32 : 64;
-  if (gated) return nt == 16 ? launch<true, 16>(a, st) : nt == 32 ? launch<true, 32>(a, st) : launch<true, 64>(a, st);
-  return nt == 16 ? launch<false, 16>(a, st) : nt == 32 ? launch<false, 32>(a, st) : launch<false, 64>(a, st);
+cudaError_t launch_qgemm_thin(const QGemmArgs& a, bool gated, cudaStream_t st) {
+  if (gated) return a.G == 16 ? launch<true, 16>(a, st) : a.G == 32 ? launch<true, 32>(a, st) : launch<true, 64>(a, st);
+  return a.G == 16 ? launch<false, 16>(a, st) : a.G == 32 ? launch<false, 32>(a, st) : launch<false, 64>(a, st);
 }
 
 }  // namespace pop

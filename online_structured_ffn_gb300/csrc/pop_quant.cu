@@ -109,9 +109,12 @@ struct pop_qmoe {
 
 namespace {
 
-// Rows of a run, which says which kind of product a call takes: 128 (wide) or 16 (thin).
+// Rows of a run, which says which kind of product a call takes: 128 (wide), else thin with tiles of as many
+// tokens as a group can have if a token is in it once, up to 64.
 constexpr int WIDE_ROWS = 64;
-int granule(long long rows_per_group) { return rows_per_group >= WIDE_ROWS ? 128 : 16; }
+int granule(long long rows_per_group, int tokens) {
+  return rows_per_group >= WIDE_ROWS ? 128 : tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64;
+}
 
 // Counters of a thin product's tiles: token tiles (of 16 at least) of all groups, times output tiles.
 size_t thin_tiles(long long pairs, int E, size_t out_tiles) {
@@ -120,8 +123,8 @@ size_t thin_tiles(long long pairs, int E, size_t out_tiles) {
   return static_cast<size_t>(n / 16 + (n < E ? n : E)) * out_tiles;
 }
 
-cudaError_t launch_qgemm(const QGemmArgs& g, bool gated, int max_rows, cudaStream_t st) {
-  return g.G == 128 ? launch_qgemm_wide(g, gated, st) : launch_qgemm_thin(g, gated, max_rows, st);
+cudaError_t launch_qgemm(const QGemmArgs& g, bool gated, cudaStream_t st) {
+  return g.G == 128 ? launch_qgemm_wide(g, gated, st) : launch_qgemm_thin(g, gated, st);
 }
 
 void free_linear(pop_qlinear* h) {
@@ -141,9 +144,9 @@ void free_qmoe(pop_qmoe* m) {
 
 pop_status linear_call(pop_qlinear* h, QRowsArgs in, size_t row_bytes, int M, void* y, long long ldy, cudaStream_t st,
                        const char* call) {
-  const int G = granule(M < h->cfg.max_tokens ? M : h->cfg.max_tokens);
-  for (int m0 = 0; m0 < M; m0 += h->cfg.max_tokens) {
+    for (int m0 = 0; m0 < M; m0 += h->cfg.max_tokens) {
     const int n = M - m0 < h->cfg.max_tokens ? M - m0 : h->cfg.max_tokens;
+    const int G = granule(n, n);
     QRowsArgs part = in;
     part.x = static_cast<const uint8_t*>(in.x) + static_cast<size_t>(m0) * in.ldx * row_bytes;
     if (in.xs) part.xs = in.xs + static_cast<size_t>(m0) * in.lds;
@@ -152,7 +155,6 @@ pop_status linear_call(pop_qlinear* h, QRowsArgs in, size_t row_bytes, int M, vo
     o.q = h->act;
     o.s = h->act_s;
     o.G = G;
-    o.rows = h->rows;
     o.k = 1;
     cudaError_t e = launch_quantize_rows(part, o, st);
     if (e != cudaSuccess) return q_cuda(e, call);
@@ -160,7 +162,6 @@ pop_status linear_call(pop_qlinear* h, QRowsArgs in, size_t row_bytes, int M, vo
     g.act = h->act;
     g.act_s = h->act_s;
     g.G = G;
-    g.rows = h->rows;
     g.w = h->w;
     g.ws = h->ws;
     g.N = h->cfg.N;
@@ -174,7 +175,7 @@ pop_status linear_call(pop_qlinear* h, QRowsArgs in, size_t row_bytes, int M, vo
     g.done = h->done;
     g.err = h->err;
     g.num_sms = h->num_sms;
-    e = launch_qgemm(g, false, n, st);
+    e = launch_qgemm(g, false, st);
     if (e != cudaSuccess) return q_cuda(e, call);
   }
   return POP_OK;
@@ -333,8 +334,8 @@ pop_status pop_qmoe_create(const pop_qmoe_config* cfg, const void* const* Wg, co
   m->num_sms = sm_count();
   const long long pairs = static_cast<long long>(cfg->max_tokens) * cfg->top_k;
   const long long used = pairs < E ? pairs : E;  // experts that can have rows
-  long long rows = (pairs / 16 + used) * 16;
-  if (granule(pairs / E) == 128 && (pairs / 128 + used) * 128 > rows) rows = (pairs / 128 + used) * 128;
+  const int most = granule(pairs / E, cfg->max_tokens);  // grows with the tokens, as the rows do
+  const long long rows = (pairs / most + used) * most;
   m->rows = static_cast<int>(rows);
   const size_t NT = qceil(cfg->D_FF, QB), DT = qceil(cfg->D, QB);
   cudaError_t e = dalloc(&m->wgu, E * NT * DT * 2 * QTILE);
@@ -401,7 +402,7 @@ pop_status pop_qmoe_forward(pop_qmoe_t m, const void* x, long long ldx, const in
   for (int t0 = 0; t0 < T; t0 += c.max_tokens) {
     const int n = T - t0 < c.max_tokens ? T - t0 : c.max_tokens;
     const int pairs = n * c.top_k;
-    const int G = granule(pairs / c.n_experts);
+    const int G = granule(pairs / c.n_experts, n);
     const int* ex = experts + static_cast<size_t>(t0) * c.top_k;
     cudaError_t e = launch_plan(ex, pairs, c.n_experts, G, m->counts, m->run0, m->row_of, m->err, st);
     if (e != cudaSuccess) return q_cuda(e, call);
@@ -410,7 +411,6 @@ pop_status pop_qmoe_forward(pop_qmoe_t m, const void* x, long long ldx, const in
     o.q = m->act;
     o.s = m->act_s;
     o.G = G;
-    o.rows = m->rows;
     o.row_of = m->row_of;
     o.k = c.top_k;
     e = launch_quantize_rows(in, o, st);
@@ -419,7 +419,6 @@ pop_status pop_qmoe_forward(pop_qmoe_t m, const void* x, long long ldx, const in
     g.act = m->act;
     g.act_s = m->act_s;
     g.G = G;
-    g.rows = m->rows;
     g.w = m->wgu;
     g.ws = m->sgu;
     g.w_stride = NT * DT * 2 * QTILE;
@@ -436,7 +435,7 @@ pop_status pop_qmoe_forward(pop_qmoe_t m, const void* x, long long ldx, const in
     g.done = m->done;
     g.err = m->err;
     g.num_sms = m->num_sms;
-    e = launch_qgemm(g, true, n, st);
+    e = launch_qgemm(g, true, st);
     if (e != cudaSuccess) return q_cuda(e, call);
     g.act = m->h;
     g.act_s = m->h_s;
@@ -451,7 +450,7 @@ pop_status pop_qmoe_forward(pop_qmoe_t m, const void* x, long long ldx, const in
     g.y = m->o;
     g.ldy = c.D;
     g.out_f32 = 1;
-    e = launch_qgemm(g, false, n, st);
+    e = launch_qgemm(g, false, st);
     if (e != cudaSuccess) return q_cuda(e, call);
     e = launch_combine(m->o, m->row_of, weights + static_cast<size_t>(t0) * c.top_k, n, c.top_k, c.D,
                        static_cast<uint8_t*>(y) + static_cast<size_t>(t0) * ldy * (c.out_f32 ? 4 : 2), ldy, c.out_f32, st);

@@ -211,7 +211,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
       bool ok = true;
       for (int tile = pair; tile < tiles && ok; tile += pairs) {
         const Tile t = tile_at(ctl.groups, a.E, tile, rank);
-        const float* xs = a.act_s + t.row0;
+        const float* xs = a.act_s + static_cast<size_t>(t.row0 / BM) * KB * BM;
         const float* ws = a.ws + t.e * a.ws_stride;
         const float *w0, *w1;
         if (GATED) {
@@ -229,7 +229,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
           const int n = min(SB, KB - kb);
           Scales& sc = ctl.scales[g];
           mbar_arrive_expect_tx(&ctl.sfull[g], n * BM * 4 + 2 * SB * 4);
-          for (int j = 0; j < n; ++j, xs += a.rows) bulk_load(sc.x[j], xs, BM * 4, &ctl.sfull[g]);
+          bulk_load(sc.x, xs, n * BM * 4, &ctl.sfull[g]);
+          xs += SB * BM;
           if (GATED) {
             bulk_load(sc.w, w0 + 2 * kb, 2 * SB * 4, &ctl.sfull[g]);
           } else {
@@ -331,7 +332,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
             const uint4 hi = e4m3x16(reinterpret_cast<const float*>(acc) + 32 * c + 16, am);
             st_sector(hp + (image_at(r, 64 * half + 32 * c) & ~31u), (r & 1) ? hi : lo, (r & 1) ? lo : hi);
           }
-          if (half == 0) a.h_s[static_cast<size_t>(t.n) * a.rows + row] = __fdiv_rn(am, 448.f);
+          if (half == 0) a.h_s[(static_cast<size_t>(row / BM) * NT + t.n) * BM + r] = __fdiv_rn(am, 448.f);
         }
       } else if (valid) {
 #pragma unroll
