@@ -12,7 +12,7 @@
 // Warp 0: copies. A stage is 32 KB of the matrix (one bulk copy: its image is what shared memory needs) and
 // the same k-blocks of the rows and of their scales (a copy each; a run of rows is one tile). The matrix does not depend on the
 // kernel before, so the first stages' copies of it go out before this one is waited for. Warp 1: products. Warps
-// 2..5: epilogue, TMEM lane quarter warp % 4. Every wait has a limit; a CTA that gives up records QERR_TIMEOUT,
+// 2..9: epilogue, TMEM lane quarter warp % 4, two warps to a quarter that share its columns. Every wait has a limit; a CTA that gives up records QERR_TIMEOUT,
 // lets its copies and products finish, frees TMEM and returns.
 #include "pop_qdevice.cuh"
 
@@ -22,7 +22,7 @@ cudaError_t ensure_dyn_smem(const void* kernel, size_t bytes);
 
 namespace {
 
-constexpr int THREADS = 192;
+constexpr int THREADS = 320, EPI = 256;
 constexpr uint32_t RING_BYTES = 208 * 1024;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int MAX_STAGES = 8, MAX_BUFS = 8;
@@ -36,7 +36,8 @@ struct Thin {
   static constexpr uint32_t S_BYTES = NT * 4;       // of their scales
   static constexpr uint32_t X_OFF = KS * W_BYTES, S_OFF = X_OFF + KS * X_BYTES;
   static constexpr uint32_t STAGE = (S_OFF + KS * S_BYTES + 1023) / 1024 * 1024;
-  static constexpr int STAGES = RING_BYTES / STAGE;
+  static constexpr uint32_t H_BYTES = GATED ? NT * QB * 4 : 0;  // a finished tile on its way to e4m3
+  static constexpr int STAGES = (RING_BYTES - H_BYTES) / STAGE;
   static constexpr int BUFS = static_cast<int>(TMEM_COLS) / (P * NT) < MAX_BUFS ? static_cast<int>(TMEM_COLS) / (P * NT) : MAX_BUFS;
 };
 
@@ -48,7 +49,6 @@ struct Ctl {
   int abort_flag;
   int last;
   Groups groups;
-  uint32_t amax[4][64];
 };
 
 // One run of k-blocks of a tile.
@@ -75,7 +75,7 @@ __device__ __forceinline__ Seg segment(const Groups& gr, int E, int KB, long lon
   return s;
 }
 
-__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(EPI) : "memory"); }
 
 template <bool GATED, int NT>
 __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant__ QGemmArgs a) {
@@ -91,11 +91,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&ctl.full[s], 1);
-      mbar_init(&ctl.empty[s], 1 + 4);  // the products and the epilogue's four warps (scales)
+      mbar_init(&ctl.empty[s], 1 + EPI / 32);  // the products and the epilogue's warps (scales)
     }
     for (int b = 0; b < C::BUFS; ++b) {
       mbar_init(&ctl.tfull[b], 1);
-      mbar_init(&ctl.tempty[b], 4);
+      mbar_init(&ctl.tempty[b], EPI / 32);
     }
     mbar_init(&ctl.drain, 1);
     ctl.abort_flag = 0;
@@ -231,12 +231,13 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
     if (!mbar_wait(&ctl.drain, 0, Q_DRAIN_NS, &never) && leader) fail();
     __syncwarp();
   } else {
-    // ------------------------------------------------------------ epilogue (warps 2..5)
+    // ------------------------------------------------------------ epilogue (warps 2..9)
     pdl_wait();  // what this kernel writes may still be read by the one before
-    const int q = warp & 3;
+    constexpr int CW = NT / 2, CH = CW < 16 ? CW : 16;  // rows of the tile that a thread has, and loads at a time
+    const int q = warp & 3, n0 = CW * ((warp - 2) >> 2);
     const int f = 32 * q + lane;  // output of the tile
     const int et = threadIdx.x - 64;
-    const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
+    const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + n0;
     uint32_t s = 0, phase = 0, b = 0, tphase = 0;
     for (long long x = x0; x < x1;) {
       const Seg g = segment<NT>(ctl.groups, a.E, KB, x, x1);
@@ -244,11 +245,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
       const float* ws = a.ws + g.e * a.ws_stride + static_cast<size_t>(g.t) * scale_stride(KB, P) + g.kb0 * P;
       const int nw = (g.kb1 - g.kb0) * P;
       float sw = 0.f, sw_next = lane < nw ? __ldg(ws + lane) : 0.f;
-      float acc[P][NT];
+      const int mine = g.n - n0;  // this thread's rows that there are: the first ones, if any
+      float acc[P][CW];
 #pragma unroll
       for (int p = 0; p < P; ++p)
 #pragma unroll
-        for (int n = 0; n < NT; ++n) acc[p][n] = 0.f;
+        for (int n = 0; n < CW; ++n) acc[p][n] = 0.f;
       bool ok = true;  // once a wait has run out the rest of the run is gone through without waiting
       int i = 0;
       for (int kb = g.kb0; kb < g.kb1; kb += C::KS) {
@@ -263,20 +265,20 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
             }
             const float s0 = __shfl_sync(0xffffffffu, sw, i & 31), s1 = __shfl_sync(0xffffffffu, sw, (i + P - 1) & 31);
             i += P;
-            const float4* sx = reinterpret_cast<const float4*>(st + u * C::S_BYTES);
+            const float4* sx = reinterpret_cast<const float4*>(st + u * C::S_BYTES + n0 * 4);
             const uint32_t taddr = lane_base + b * static_cast<uint32_t>(P * NT);
             ok = ok && mbar_wait(&ctl.tfull[b], tphase, Q_WAIT_NS, abort_flag);
             tc_fence_after();
 #pragma unroll
-            for (int c = 0; c < NT; c += 16) {
-              if (c >= g.n) break;
-              uint32_t d0[16], d1[16];
-              tmem_ld16(taddr + c, d0);
-              if (GATED) tmem_ld16(taddr + NT + c, d1);
-              tmem_wait16(d0);
-              if (GATED) tmem_wait16(d1);
+            for (int c = 0; c < CW; c += CH) {
+              if (c >= mine) break;
+              uint32_t d0[CH], d1[CH];
+              tmem_load(taddr + c, d0);
+              if (GATED) tmem_load(taddr + NT + c, d1);
+              tmem_wait(d0);
+              if (GATED) tmem_wait(d1);
 #pragma unroll
-              for (int j = 0; j < 16; j += 4) {
+              for (int j = 0; j < CH; j += 4) {
                 const float4 v = sx[(c + j) >> 2];
                 const float vs[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -298,18 +300,19 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
       }
       ok = __all_sync(0xffffffffu, ok);
       if (!ok && lane == 0) fail();
-      if (epi_any<128>(!ok)) break;  // all four warps go on, or none
+      if (epi_any<EPI>(!ok)) break;  // all warps go on, or none
       x += g.kb1 - g.kb0;
       if (g.kb1 - g.kb0 < KB) {
-        // a part of the tile. Slot 0 of this CTA holds one that starts within its tile, slot 1 one that
-        // starts it: a run has at most one of each.
-        const size_t slot_floats = static_cast<size_t>(P) * NT * 128;
-        float* mine = a.parts + (2 * static_cast<size_t>(blockIdx.x) + (g.kb0 == 0 ? 1 : 0)) * slot_floats + f;
+        // a part of the tile, [product][row][output]. Slot 0 of this CTA holds one that starts within its tile,
+        // slot 1 one that starts it: a run has at most one of each.
+        constexpr size_t slot = static_cast<size_t>(P) * NT * 128;
+        const size_t at = static_cast<size_t>(n0) * 128 + f;
+        float* part = a.parts + (2 * static_cast<size_t>(blockIdx.x) + (g.kb0 == 0 ? 1 : 0)) * slot + at;
 #pragma unroll
         for (int p = 0; p < P; ++p)
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
-            if (n < g.n) __stcg(mine + (p * NT + n) * 128, acc[p][n]);
+          for (int n = 0; n < CW; ++n)
+            if (n < mine) __stcg(part + (p * NT + n) * 128, acc[p][n]);
         const long long first = static_cast<long long>(g.tile) * KB, last = first + KB - 1;
         // CTA c holds [work c / G, work (c + 1) / G): the one of unit x is ((x + 1) G - 1) / work
         const int c0 = static_cast<int>(((first + 1) * G - 1) / work), c1 = static_cast<int>(((last + 1) * G - 1) / work);
@@ -317,62 +320,74 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
         epi_sync();
         if (et == 0) ctl.last = atomicAdd(a.done + g.tile, 1u) == static_cast<unsigned>(c1 - c0) ? 1 : 0;
         epi_sync();
-        const bool mine_last = ctl.last != 0;
+        const bool is_last = ctl.last != 0;
         epi_sync();  // ctl.last is free again
-        if (!mine_last) continue;
+        if (!is_last) continue;
         __threadfence();
         if (et == 0) a.done[g.tile] = 0;
 #pragma unroll
         for (int p = 0; p < P; ++p)
 #pragma unroll
-          for (int n = 0; n < NT; ++n) acc[p][n] = 0.f;
+          for (int n = 0; n < CW; ++n) acc[p][n] = 0.f;
+#pragma unroll 1
         for (int c = c0; c <= c1; ++c) {
-          const float* p0 = a.parts + (2 * static_cast<size_t>(c) + (work * c / G <= first ? 1 : 0)) * slot_floats + f;
+          const float* p0 = a.parts + (2 * static_cast<size_t>(c) + (work * c / G <= first ? 1 : 0)) * slot + at;
 #pragma unroll
           for (int p = 0; p < P; ++p)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-              if (n < g.n) acc[p][n] += __ldcg(p0 + (p * NT + n) * 128);
+            for (int n = 0; n < CW; ++n)
+              if (n < mine) acc[p][n] += __ldcg(p0 + (p * NT + n) * 128);
         }
       }
       if (!GATED) {
         const int col = g.t * QB + f;
         if (col < a.N) {
+          const size_t o = (static_cast<size_t>(g.run) * NT + n0) * a.ldy + col;
+          if (a.out_f32) {
+            float* y = static_cast<float*>(a.y) + o;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            if (n < g.n) {
-              const size_t o = (static_cast<size_t>(g.run) * NT + n) * a.ldy + col;
-              if (a.out_f32)
-                static_cast<float*>(a.y)[o] = acc[0][n];
-              else
-                static_cast<__nv_bfloat16*>(a.y)[o] = __float2bfloat16_rn(acc[0][n]);
-            }
+            for (int n = 0; n < CW; ++n)
+              if (n < mine) y[n * a.ldy] = acc[0][n];
+          } else {
+            __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + o;
+#pragma unroll
+            for (int n = 0; n < CW; ++n)
+              if (n < mine) y[n * a.ldy] = __float2bfloat16_rn(acc[0][n]);
           }
         }
       } else {
-        // the tile's 128 channels are one block of the next product's rows
+        // the tile's 128 channels are one block of the next product's rows: through shared memory, where eight
+        // lanes then have a row, 16 channels each (4 at a time, 32 apart)
+        float* hs = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          if (n < g.n) {
-            acc[0][n] = silu_mul(acc[0][n], acc[P - 1][n]);
-            const uint32_t m = __reduce_max_sync(0xffffffffu, abs_bits(acc[0][n]));
-            if (lane == 0) ctl.amax[q][n] = m;
-          }
-        }
+        for (int n = 0; n < CW; ++n)
+          if (n < mine) hs[(n0 + n) * QB + f] = silu_mul(acc[0][n], acc[P - 1][n]);
         epi_sync();
+#pragma unroll 1
+        for (int i = et; i < NT * 8; i += EPI) {
+          const int n = i >> 3, l8 = i & 7;
+          float v[16];
+          uint32_t m = AMAX_MIN_BITS;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+          for (int j = 0; j < 4; ++j) {
+            const float4 w = n < g.n ? *reinterpret_cast<const float4*>(hs + n * QB + 32 * j + 4 * l8) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[4 * j] = w.x, v[4 * j + 1] = w.y, v[4 * j + 2] = w.z, v[4 * j + 3] = w.w;
+            m = max(max(m, max(abs_bits(w.x), abs_bits(w.y))), max(abs_bits(w.z), abs_bits(w.w)));
+          }
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
           if (n < g.n) {
-            const uint32_t m = max(max(max(ctl.amax[0][n], ctl.amax[1][n]), max(ctl.amax[2][n], ctl.amax[3][n])), AMAX_MIN_BITS);
             const float am = __uint_as_float(m);
-            const bool huge = q_huge(am);
-            const float v = q_ratio(acc[0][n], am, q_recip(am, huge), huge);
+            const uint4 w = e4m3x16(v, am);
+            const uint32_t ws4[4] = {w.x, w.y, w.z, w.w};
             const size_t block = static_cast<size_t>(g.run) * NTILES + g.t;
-            a.h[block * C::X_BYTES + image_at(n, f)] = static_cast<uint8_t>(e4m3x2(v, 0.f));
-            if (f == 0) a.h_s[block * NT + n] = __fdiv_rn(am, 448.f);
+            uint8_t* hp = a.h + block * C::X_BYTES;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) *reinterpret_cast<uint32_t*>(hp + image_at(n, 32 * j + 4 * l8)) = ws4[j];
+            if (l8 == 0) a.h_s[block * NT + n] = __fdiv_rn(am, 448.f);
           }
         }
-        epi_sync();  // ctl.amax is free again
+        epi_sync();  // the buffer is free again
       }
     }
   }
@@ -388,7 +403,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
 template <bool GATED, int NT>
 cudaError_t launch(const QGemmArgs& a, cudaStream_t st) {
   using C = Thin<GATED, NT>;
-  const size_t smem = C::STAGES * C::STAGE + 1024;
+  const size_t smem = C::STAGES * C::STAGE + C::H_BYTES + 1024;
   cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(&k_qgemm_thin<GATED, NT>), smem);
   if (e != cudaSuccess) return e;
   return launch_q(k_qgemm_thin<GATED, NT>, dim3(a.num_sms), THREADS, smem, st, a);

@@ -282,12 +282,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
           // sixteen columns on their way while the sixteen before are added: more in flight would not fit beside
           // the 128 sums
           uint32_t d[2][16];
-          tmem_ld16(taddr, d[0]);
+          tmem_load(taddr, d[0]);
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            tmem_wait16(d[c & 1]);
+            tmem_wait(d[c & 1]);
             if (c < 7) {
-              tmem_ld16(taddr + 16 * (c + 1), d[(c + 1) & 1]);
+              tmem_load(taddr + 16 * (c + 1), d[(c + 1) & 1]);
             } else {
               tc_fence_before();
               __syncwarp();
