@@ -508,16 +508,20 @@ def _bad(what: str):
 
 def _rows_arg(t, name, dtypes, cols, align):
     """Checks a [rows, cols] CUDA tensor whose elements of a row are contiguous (the rows may lie
-    farther apart). Returns its row stride in elements."""
-    if t.dtype not in dtypes or t.dim() != 2 or t.shape[1] != cols or not t.is_cuda:
+    farther apart). Returns (rows, row stride in elements)."""
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != cols or t.dtype not in dtypes or not t.is_cuda:
         _bad(f"{name}: expected a CUDA tensor of shape (*, {cols}) and type {' or '.join(map(str, dtypes))}, got "
-             f"{t.dtype} {tuple(t.shape)} on {t.device}")
-    if (cols > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < cols):
+             f"{t.dtype} {tuple(shape)} on {t.device}")
+    rows = shape[0]
+    ld, step = t.stride()
+    if (cols > 1 and step != 1) or (rows > 1 and ld < cols):
         _bad(f"{name}: the elements of a row must be contiguous, its rows apart; strides are {tuple(t.stride())}")
-    ld = t.stride(0) if t.shape[0] > 1 else -(-cols // 8) * 8
-    if align > 1 and t.shape[0] > 0 and (t.data_ptr() % align or (ld * t.element_size()) % align):
+    if rows <= 1:
+        ld = -(-cols // 8) * 8
+    if align > 1 and rows > 0 and (t.data_ptr() % align or (ld * t.element_size()) % align):
         _bad(f"{name}: rows must start on {align}-byte boundaries")
-    return ld
+    return rows, ld
 
 
 def _whole_arg(t, name, dtype, shape):
@@ -526,28 +530,30 @@ def _whole_arg(t, name, dtype, shape):
              f"{tuple(t.shape)} on {t.device}")
 
 
-class _On:
-    """The stream of a call. New outputs belong to it, and inputs that another stream allocated are not
-    given to others before it is done with them."""
+def _on(stream, t, *others):
+    """The stream of a call on t's device: (raw handle, what new outputs are to be made under, or None for the
+    current stream). New outputs belong to the call's stream, and inputs that another stream allocated are
+    not given to others before it is done with them."""
+    import torch
+    raw = torch._C._cuda_getCurrentRawStream(t.get_device())
+    if stream is None:
+        return raw, None
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    if stream.cuda_stream == raw:
+        return raw, None
+    for x in (t, *others):
+        if x is not None:
+            x.record_stream(stream)
+    return stream.cuda_stream, stream
 
-    def __init__(self, stream, *inputs):
-        import torch
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
-        self.stream, here = stream, torch.cuda.current_stream()
-        self.other = stream is not None and stream.cuda_stream != here.cuda_stream
-        self.raw = here.cuda_stream if stream is None else stream.cuda_stream
-        if self.other:
-            for t in inputs:
-                if t is not None:
-                    t.record_stream(stream)
 
-    def empty(self, shape, dtype, device):
-        import torch
-        if not self.other:
-            return torch.empty(shape, dtype=dtype, device=device)
-        with torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device=device)
+def _empty(under, shape, dtype, device):
+    import torch
+    if under is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(under):
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 class PopRouter:
@@ -562,6 +568,7 @@ class PopRouter:
             _bad(f"score must be 'softmax' or 'sigmoid', got {score!r}")
         self.cfg = pop_route_config(n_experts=n_experts, top_k=top_k, score=kinds[score], n_groups=n_groups,
                                     top_groups=top_groups, group_sum=group_sum, renorm=1 if renorm else 0, scale=scale)
+        self._cfg_ref = ctypes.byref(self.cfg)
 
     def route(self, logits, bias=None, counts=None, stream=None):
         """logits: [T, n_experts] float32 or bf16 (rows may be strided); bias: float32 [n_experts];
@@ -569,18 +576,19 @@ class PopRouter:
         Returns (experts int32 [T, top_k], weights float32 [T, top_k])."""
         import torch
         E, k = self.cfg.n_experts, self.cfg.top_k
-        ld = _rows_arg(logits, "logits", (torch.float32, torch.bfloat16), E, 1)
+        T, ld = _rows_arg(logits, "logits", (torch.float32, torch.bfloat16), E, 1)
         if bias is not None:
             _whole_arg(bias, "bias", torch.float32, (E,))
         if counts is not None:
             _whole_arg(counts, "counts", torch.int32, (E,))
-        T = logits.shape[0]
-        on = _On(stream, logits, bias, counts)
-        experts = on.empty((T, k), torch.int32, logits.device)
-        weights = on.empty((T, k), torch.float32, logits.device)
-        _check_with("pop_route_last_error", load_library().pop_route(
-            ctypes.byref(self.cfg), _ptr(logits), 1 if logits.dtype == torch.bfloat16 else 0, ld, _ptr(bias), T,
-            _ptr(experts), _ptr(weights), _ptr(counts), on.raw))
+        raw, under = _on(stream, logits, bias, counts)
+        device = logits.device
+        experts = _empty(under, (T, k), torch.int32, device)
+        weights = _empty(under, (T, k), torch.float32, device)
+        st = _lib.pop_route(self._cfg_ref, logits.data_ptr(), 1 if logits.dtype == torch.bfloat16 else 0, ld, _ptr(bias),
+                            T, experts.data_ptr(), weights.data_ptr(), _ptr(counts), raw)
+        if st != POP_OK:
+            _check_with("pop_route_last_error", st)
         return experts, weights
 
 
@@ -600,13 +608,16 @@ def quantize_rows(x, stream=None):
     import torch
     if x.dim() != 2:
         _bad(f"x: expected two dimensions, got {tuple(x.shape)}")
-    M, K = x.shape
-    ld = _rows_arg(x, "x", (torch.bfloat16, torch.float32), K, 16)
-    on = _On(stream, x)
-    q = on.empty((M, K), torch.float8_e4m3fn, x.device)
-    s = on.empty((M, _blocks(K)), torch.float32, x.device)
-    _check_quant(load_library().pop_quantize_rows(_ptr(x), 1 if x.dtype == torch.float32 else 0, ld, M, K, _ptr(q), K,
-                                                  _ptr(s), on.raw))
+    K = x.shape[1]
+    M, ld = _rows_arg(x, "x", (torch.bfloat16, torch.float32), K, 16)
+    raw, under = _on(stream, x)
+    device = x.device
+    q = _empty(under, (M, K), torch.float8_e4m3fn, device)
+    s = _empty(under, (M, _blocks(K)), torch.float32, device)
+    st = _lib.pop_quantize_rows(x.data_ptr(), 1 if x.dtype == torch.float32 else 0, ld, M, K, q.data_ptr(), K,
+                                s.data_ptr(), raw)
+    if st != POP_OK:
+        _check_quant(st)
     return q, s
 
 
@@ -634,13 +645,14 @@ class _QHandle:
         """Syncs and raises the first device-side failure since the last check."""
         _check_quant(getattr(load_library(), self._checker)(self.handle))
 
-    def _output(self, y, rows, cols, device, on, align):
+    def _output(self, y, rows, cols, device, under, align):
         """(y, its row stride): a new [rows, cols] tensor, or the caller's, checked."""
         if y is None:
-            y = on.empty((rows, cols), self.out_dtype(), device)
-        if y.dim() != 2 or y.shape[0] != rows:
+            return _empty(under, (rows, cols), self.out_dtype(), device), cols
+        got, ld = _rows_arg(y, "y", (self.out_dtype(),), cols, align)
+        if got != rows:
             _bad(f"y: expected {rows} rows, got {tuple(y.shape)}")
-        return y, _rows_arg(y, "y", (self.out_dtype(),), cols, align)
+        return y, ld
 
 
 def _matrix_arg(W, S, name):
@@ -673,23 +685,27 @@ class PopQLinear(_QHandle):
     def forward(self, x, y=None, stream=None):
         """x: bf16 [M, K], quantised on the way. Returns y [M, N] of out_dtype()."""
         import torch
-        ld = _rows_arg(x, "x", (torch.bfloat16,), self.K, 16)
-        on = _On(stream, x, y)
-        y, ldy = self._output(y, x.shape[0], self.N, x.device, on, 1)
-        _check_quant(load_library().pop_qlinear_forward(self.handle, _ptr(x), ld, x.shape[0], _ptr(y), ldy, on.raw))
+        M, ld = _rows_arg(x, "x", (torch.bfloat16,), self.K, 16)
+        raw, under = _on(stream, x, y)
+        y, ldy = self._output(y, M, self.N, x.device, under, 1)
+        st = _lib.pop_qlinear_forward(self.handle, x.data_ptr(), ld, M, y.data_ptr(), ldy, raw)
+        if st != POP_OK:
+            _check_quant(st)
         return y
 
     def forward_q(self, xq, xs, y=None, stream=None):
         """The same for rows that quantize_rows gave: xq float8_e4m3fn [M, K], xs float32."""
         import torch
-        ldq = _rows_arg(xq, "xq", (torch.float8_e4m3fn,), self.K, 8)
-        lds = _rows_arg(xs, "xs", (torch.float32,), _blocks(self.K), 1)
-        if xs.shape[0] != xq.shape[0]:
-            _bad(f"xs: expected {xq.shape[0]} rows, got {xs.shape[0]}")
-        on = _On(stream, xq, xs, y)
-        y, ldy = self._output(y, xq.shape[0], self.N, xq.device, on, 1)
-        _check_quant(load_library().pop_qlinear_forward_quantized(self.handle, _ptr(xq), ldq, _ptr(xs), lds,
-                                                                  xq.shape[0], _ptr(y), ldy, on.raw))
+        M, ldq = _rows_arg(xq, "xq", (torch.float8_e4m3fn,), self.K, 8)
+        rows, lds = _rows_arg(xs, "xs", (torch.float32,), _blocks(self.K), 1)
+        if rows != M:
+            _bad(f"xs: expected {M} rows, got {rows}")
+        raw, under = _on(stream, xq, xs, y)
+        y, ldy = self._output(y, M, self.N, xq.device, under, 1)
+        st = _lib.pop_qlinear_forward_quantized(self.handle, xq.data_ptr(), ldq, xs.data_ptr(), lds, M, y.data_ptr(), ldy,
+                                                raw)
+        if st != POP_OK:
+            _check_quant(st)
         return y
 
 
@@ -729,14 +745,15 @@ class PopQMoE(_QHandle):
         """x: bf16 [T, D]; experts int32 and weights float32 [T, top_k], as PopRouter.route gives them.
         Returns y [T, D] of out_dtype()."""
         import torch
-        ld = _rows_arg(x, "x", (torch.bfloat16,), self.D, 16)
-        T = x.shape[0]
+        T, ld = _rows_arg(x, "x", (torch.bfloat16,), self.D, 16)
         _whole_arg(experts, "experts", torch.int32, (T, self.cfg.top_k))
         _whole_arg(weights, "weights", torch.float32, (T, self.cfg.top_k))
-        on = _On(stream, x, experts, weights, y)
-        y, ldy = self._output(y, T, self.D, x.device, on, 16)
-        _check_quant(load_library().pop_qmoe_forward(self.handle, _ptr(x), ld, _ptr(experts), _ptr(weights), T, _ptr(y),
-                                                     ldy, on.raw))
+        raw, under = _on(stream, x, experts, weights, y)
+        y, ldy = self._output(y, T, self.D, x.device, under, 16)
+        st = _lib.pop_qmoe_forward(self.handle, x.data_ptr(), ld, experts.data_ptr(), weights.data_ptr(), T, y.data_ptr(),
+                                   ldy, raw)
+        if st != POP_OK:
+            _check_quant(st)
         return y
 
 

@@ -17,8 +17,8 @@ __device__ __forceinline__ void unpack8(const void* p, int kind, float* v) {
   }
 }
 
-// Eight lanes per block of 128, 16 values each. A CTA has 32 blocks at a time: of one row, or of the `per` whole
-// rows that they hold.
+// Eight lanes per block of 128, 16 values each. A CTA has 32 blocks: of one row (the blockIdx.y-th 32), or of the
+// `per` whole rows that they hold.
 __global__ void __launch_bounds__(256) k_quantize_rows(const __grid_constant__ QRowsArgs in, const __grid_constant__ QRowsOut out, int per) {
   pdl_wait();  // the rows, their places, and what an earlier call's kernels still read
   pdl_trigger();
@@ -27,57 +27,55 @@ __global__ void __launch_bounds__(256) k_quantize_rows(const __grid_constant__ Q
   const int row_in = per > 1 ? u / KB : 0;
   const int row = blockIdx.x * per + row_in;
   const bool mine = row_in < per && row < in.M;
-  // (a warp's lanes go round together: for several rows a CTA there is one round)
-  for (int kb = u - row_in * KB; kb - u % 4 < KB; kb += per > 1 ? 1 << 24 : 32) {
-    const bool on = mine && kb < KB;
-    const int k0 = kb * QB + lane8 * 16;
-    const int n8 = on ? min(max((in.K - k0) >> 3, 0), 2) : 0;  // runs of 8 values this lane has
-    uint4 q = make_uint4(0u, 0u, 0u, 0u);
-    float s = 0.f;
-    if (in.kind == 2) {
-      const uint8_t* p = static_cast<const uint8_t*>(in.x) + static_cast<size_t>(row) * in.ldx + k0;
-      if (n8 > 0) {
-        const uint2 a = *reinterpret_cast<const uint2*>(p);
-        q.x = a.x, q.y = a.y;
-      }
-      if (n8 > 1) {
-        const uint2 b = *reinterpret_cast<const uint2*>(p + 8);
-        q.z = b.x, q.w = b.y;
-      }
-      if (on) s = in.xs[static_cast<size_t>(row) * in.lds + kb];
-    } else {
-      const int size = in.kind == 0 ? 2 : 4;
-      const uint8_t* p = static_cast<const uint8_t*>(in.x) + (static_cast<size_t>(row) * in.ldx + k0) * size;
-      float v[16];
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = 0.f;
-      if (n8 > 0) unpack8(p, in.kind, v);
-      if (n8 > 1) unpack8(p + 8 * size, in.kind, v + 8);
-      uint32_t m = AMAX_MIN_BITS;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) m = max(m, abs_bits(v[i]));
-#pragma unroll
-      for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const float a = __uint_as_float(m);
-      q = e4m3x16(v, a);
-      s = __fdiv_rn(a, 448.f);
+  const int kb = u - row_in * KB + 32 * blockIdx.y;
+  const bool on = mine && kb < KB;
+  const int k0 = kb * QB + lane8 * 16;
+  const int n8 = on ? min(max((in.K - k0) >> 3, 0), 2) : 0;  // runs of 8 values this lane has
+  uint4 q = make_uint4(0u, 0u, 0u, 0u);
+  float s = 0.f;
+  if (in.kind == 2) {
+    const uint8_t* p = static_cast<const uint8_t*>(in.x) + static_cast<size_t>(row) * in.ldx + k0;
+    if (n8 > 0) {
+      const uint2 a = *reinterpret_cast<const uint2*>(p);
+      q.x = a.x, q.y = a.y;
     }
-    if (!on) continue;
-    if (out.G == 0) {
-      uint8_t* p = out.q + static_cast<size_t>(row) * out.ldq + k0;
-      if (n8 > 0) *reinterpret_cast<uint2*>(p) = make_uint2(q.x, q.y);
-      if (n8 > 1) *reinterpret_cast<uint2*>(p + 8) = make_uint2(q.z, q.w);
-      if (lane8 == 0) out.s[static_cast<size_t>(row) * KB + kb] = s;
-      continue;
+    if (n8 > 1) {
+      const uint2 b = *reinterpret_cast<const uint2*>(p + 8);
+      q.z = b.x, q.w = b.y;
     }
-    for (int j = 0; j < out.k; ++j) {
-      const int r = out.row_of ? __ldcg(out.row_of + static_cast<size_t>(row) * out.k + j) : row;
-      if (r < 0) continue;
-      const int run = r / out.G, in_run = r - run * out.G;
-      const size_t block = static_cast<size_t>(run) * KB + kb;
-      *reinterpret_cast<uint4*>(out.q + block * out.G * QB + image_at(in_run, lane8 * 16)) = q;
-      if (lane8 == 0) out.s[block * out.G + in_run] = s;
-    }
+    if (on) s = in.xs[static_cast<size_t>(row) * in.lds + kb];
+  } else {
+    const int size = in.kind == 0 ? 2 : 4;
+    const uint8_t* p = static_cast<const uint8_t*>(in.x) + (static_cast<size_t>(row) * in.ldx + k0) * size;
+    float v[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = 0.f;
+    if (n8 > 0) unpack8(p, in.kind, v);
+    if (n8 > 1) unpack8(p + 8 * size, in.kind, v + 8);
+    uint32_t m = AMAX_MIN_BITS;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = max(m, abs_bits(v[i]));
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float a = __uint_as_float(m);
+    q = e4m3x16(v, a);
+    s = __fdiv_rn(a, 448.f);
+  }
+  if (!on) return;
+  if (out.G == 0) {
+    uint8_t* p = out.q + static_cast<size_t>(row) * out.ldq + k0;
+    if (n8 > 0) *reinterpret_cast<uint2*>(p) = make_uint2(q.x, q.y);
+    if (n8 > 1) *reinterpret_cast<uint2*>(p + 8) = make_uint2(q.z, q.w);
+    if (lane8 == 0) out.s[static_cast<size_t>(row) * KB + kb] = s;
+    return;
+  }
+  for (int j = 0; j < out.k; ++j) {
+    const int r = out.row_of ? __ldcg(out.row_of + static_cast<size_t>(row) * out.k + j) : row;
+    if (r < 0) continue;
+    const int run = r / out.G, in_run = r - run * out.G;
+    const size_t block = static_cast<size_t>(run) * KB + kb;
+    *reinterpret_cast<uint4*>(out.q + block * out.G * QB + image_at(in_run, lane8 * 16)) = q;
+    if (lane8 == 0) out.s[block * out.G + in_run] = s;
   }
 }
 
@@ -247,7 +245,7 @@ __global__ void __launch_bounds__(256) k_combine(const float* __restrict__ o, co
 cudaError_t launch_quantize_rows(const QRowsArgs& in, const QRowsOut& out, cudaStream_t st) {
   const int KB = qceil(in.K, QB);
   const int per = KB < 32 ? 32 / KB : 1;
-  return launch_q(k_quantize_rows, dim3(qceil(in.M, per)), 256, 0, st, in, out, per);
+  return launch_q(k_quantize_rows, dim3(qceil(in.M, per), qceil(KB, 32)), 256, 0, st, in, out, per);
 }
 
 cudaError_t launch_pack_matrix(const void* W, const float* Ws, int N, int K, uint8_t* img, float* s, int step,
