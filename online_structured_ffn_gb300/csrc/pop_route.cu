@@ -1,8 +1,11 @@
 // Routing of tokens to experts (include/pop_route.h): scores, bias, groups, the k best, weights.
 //
-// One warp per token; lane j holds experts j, j + 32, ... A choice value is kept as an unsigned key in
-// the order of the floats (0: not live), so that the best is a warp maximum and a tie's lower index a
-// warp minimum.
+// L lanes per token (1 to 16, a power of two) with V = 8 or 16 neighbouring experts each, so that among equal
+// values the lowest lane, and in it the lowest place, is the lower expert. A choice value is kept as an
+// unsigned key in the order of the floats (0: cannot be chosen). k times: the largest of the lanes' best keys, the
+// first lane that has it, which writes it down and looks for its next best. The chosen scores are computed
+// at the end, from the keys or (with a bias) the logits again, a lane each, so that the loop carries keys alone.
+// What bounds it is the instructions: some 200 a token for 100 experts and k = 6.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -16,9 +19,7 @@
 namespace pop {
 namespace {
 
-constexpr int RT_WARPS = 8;
-constexpr int RT_VALS = POP_ROUTE_MAX_EXPERTS / 32;
-
+constexpr int RT_WARPS = 4;
 struct RouteArgs {
   const void* logits;
   long long ld;
@@ -37,138 +38,252 @@ __device__ __forceinline__ float key_float(uint32_t key) {
 // Key of a choice value; 0 for one that cannot be chosen (NaN, -infinity). + 0: -0 and +0 tie.
 __device__ __forceinline__ uint32_t choice_key(float c) { return c >= -3.402823466e38f ? float_key(c + 0.f) : 0u; }
 
-template <bool BF16>
-__device__ __forceinline__ float load_logit(const void* p, long long i) {
-  if (BF16) return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t*>(p)[i]) << 16);
-  return static_cast<const float*>(p)[i];
-}
+// What a logit counts as: -infinity where it is not live.
+__device__ __forceinline__ float live_logit(float l) { return l == l ? fminf(l, 3.402823466e38f) : -INFINITY; }
 
 template <bool BF16>
-__global__ void __launch_bounds__(32 * RT_WARPS) k_route(RouteArgs a) {
-  __shared__ uint32_t s_key[RT_WARPS][POP_ROUTE_MAX_EXPERTS];
-  __shared__ uint32_t s_grp[RT_WARPS][POP_ROUTE_MAX_EXPERTS];
+__device__ __forceinline__ float load_logit(const void* p, long long at) {
+  if (BF16) return __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(p) + at)) << 16);
+  return __ldg(static_cast<const float*>(p) + at);
+}
+
+// A lane's V logits, n of which there are; the others are not live. VEC: four at a time.
+template <bool BF16, int V, bool VEC>
+__device__ __forceinline__ void load_logits(const void* p, long long at, int n, float (&l)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; i += VEC ? 4 : 1) {
+    if (VEC) {
+      float4 v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      if (i < n) {
+        if (BF16) {
+          const uint2 w = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at + i));
+          v = make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
+        } else {
+          v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + at + i));
+        }
+      }
+      l[i] = live_logit(v.x), l[i + 1] = live_logit(v.y), l[i + 2] = live_logit(v.z), l[i + 3] = live_logit(v.w);
+    } else {
+      l[i] = i < n ? live_logit(load_logit<BF16>(p, at + i)) : -INFINITY;
+    }
+  }
+}
+
+constexpr unsigned ALL = 0xffffffffu;
+
+template <int L>
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+  for (int o = L / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(ALL, v, o));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int o = L / 2; o; o >>= 1) v += __shfl_xor_sync(ALL, v, o);
+  return v;
+}
+template <int L>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+#pragma unroll
+  for (int o = L / 2; o; o >>= 1) v = max(v, __shfl_xor_sync(ALL, v, o));
+  return v;
+}
+template <int V>
+__device__ __forceinline__ uint32_t best_of(const uint32_t (&key)[V]) {
+  uint32_t m = key[0];
+#pragma unroll
+  for (int i = 1; i < V; ++i) m = max(m, key[i]);
+  return m;
+}
+
+// The two largest of (a1 >= a2) and (b1 >= b2).
+__device__ __forceinline__ void merge2(uint32_t& a1, uint32_t& a2, uint32_t b1, uint32_t b2) {
+  const uint32_t lo = min(a1, b1);
+  a1 = max(a1, b1);
+  a2 = max(lo, max(a2, b2));
+}
+
+template <bool BF16, int L, int V, bool VEC>
+__global__ void __launch_bounds__(32 * RT_WARPS) k_route(const __grid_constant__ RouteArgs a) {
+  constexpr int TOK = 32 / L;  // tokens of a warp
+  __shared__ uint32_t s_key[RT_WARPS][TOK][POP_ROUTE_MAX_TOP_K];  // the chosen: keys, then scores
+  __shared__ int s_e[RT_WARPS][TOK][POP_ROUTE_MAX_TOP_K];
+  __shared__ float s_top[RT_WARPS][TOK], s_sum[RT_WARPS][TOK];
+  __shared__ uint32_t s_all[RT_WARPS][TOK][L * V], s_grp[RT_WARPS][TOK][L * V];
+  __shared__ int s_count[POP_ROUTE_MAX_EXPERTS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int t = blockIdx.x * RT_WARPS + warp;
-  if (t >= a.T) return;
-  constexpr unsigned ALL = 0xffffffffu;
-  float s[RT_VALS];
-  uint32_t key[RT_VALS];
-  float top = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < RT_VALS; ++i) {
-    const int e = lane + 32 * i;
-    float l = -INFINITY;
-    if (e < a.E) l = load_logit<BF16>(a.logits, t * a.ld + e);
-    l = l == l ? fminf(l, 3.402823466e38f) : -INFINITY;
-    s[i] = l;
-    top = fmaxf(top, l);
+  const int sub = lane & (L - 1), tok = lane / L;
+  const int t0 = (blockIdx.x * RT_WARPS + warp) * TOK;
+  const int t = min(t0 + tok, a.T - 1);  // (the last warp's spare lanes do the last token again)
+  if (a.counts) {
+    for (int e = threadIdx.x; e < a.E; e += 32 * RT_WARPS) s_count[e] = 0;
+    __syncthreads();
   }
-  float sum = 0.f;
-  if (!a.sigmoid) {
+  const int e0 = sub * V;
+  uint32_t key[V];
+  float top = 0.f, sum = 1.f;
+  {
+    float l[V];
+    load_logits<BF16, V, VEC>(a.logits, t * a.ld + e0, a.E - e0, l);
+    if (a.sigmoid) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(ALL, top, o));
-  }
+      for (int i = 0; i < V; ++i) {
+        key[i] = 0u;
+        if (l[i] != -INFINITY) {
+          const float p = 1.f / (1.f + expf(-l[i]));
+          key[i] = choice_key(a.bias ? p + __ldg(a.bias + e0 + i) : p);
+        }
+      }
+    } else {
+      top = l[0];
 #pragma unroll
-  for (int i = 0; i < RT_VALS; ++i) {
-    const int e = lane + 32 * i;
-    const float l = s[i];
-    const bool live = l != -INFINITY;
-    key[i] = choice_key(l);
-    s[i] = 0.f;
-    if (live) s[i] = a.sigmoid ? 1.f / (1.f + expf(-l)) : expf(l - top);
-    sum += s[i];
-    if (a.sigmoid && live) key[i] = choice_key(a.bias ? s[i] + a.bias[e] : s[i]);
-  }
-  if (!a.sigmoid) {
+      for (int i = 1; i < V; ++i) top = fmaxf(top, l[i]);
+      top = lanes_max<L>(top);
+      sum = 0.f;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(ALL, sum, o);
+      for (int i = 0; i < V; ++i) {
+        key[i] = choice_key(l[i]);
+        l[i] = key[i] ? expf(l[i] - top) : 0.f;
+        sum += l[i];
+      }
+      sum = lanes_sum<L>(sum);
+      if (a.bias) {
 #pragma unroll
-    for (int i = 0; i < RT_VALS; ++i) {
-      s[i] = key[i] ? s[i] / sum : 0.f;
-      if (a.bias && key[i]) key[i] = choice_key(s[i] + a.bias[lane + 32 * i]);
+        for (int i = 0; i < V; ++i)
+          if (key[i]) key[i] = choice_key(l[i] / sum + __ldg(a.bias + e0 + i));
+      }
     }
   }
   if (a.G > 1) {
-    const int per = a.E / a.G;
+    const int per = a.E / a.G, lanes = per / V;
+    if (lanes * V == per && (lanes & (lanes - 1)) == 0) {
+      // a group is a power of two of whole lanes
+      uint32_t k1 = max(key[0], key[1]), k2 = min(key[0], key[1]);
 #pragma unroll
-    for (int i = 0; i < RT_VALS; ++i)
-      if (lane + 32 * i < a.E) s_key[warp][lane + 32 * i] = key[i];
-    __syncwarp();
-    for (int g = lane; g < a.G; g += 32) {
-      uint32_t k1 = 0, k2 = 0;
-      for (int j = 0; j < per; ++j) {
-        const uint32_t v = s_key[warp][g * per + j];
-        if (v > k1) {
-          k2 = k1;
-          k1 = v;
-        } else if (v > k2) {
-          k2 = v;
-        }
+      for (int i = 2; i < V; i += 2) merge2(k1, k2, max(key[i], key[i + 1]), min(key[i], key[i + 1]));
+      for (int o = 1; o < lanes; o <<= 1) {
+        const uint32_t b1 = __shfl_xor_sync(ALL, k1, o), b2 = __shfl_xor_sync(ALL, k2, o);
+        merge2(k1, k2, b1, b2);
       }
       if (a.group_sum == 2 && k2) k1 = float_key(key_float(k1) + key_float(k2) + 0.f);
-      s_grp[warp][g] = k1;
-    }
-    __syncwarp();
-    // rank of every group among the others: a group stays if fewer than top_groups come before it
-    uint32_t stay[RT_VALS];
+      const int g = e0 / per;
+      int before = 0;
+      for (int j = 0; j < a.G; ++j) {
+        const uint32_t u = __shfl_sync(ALL, k1, j * lanes, L);
+        before += (u > k1 || (u == k1 && j < g)) ? 1 : 0;
+      }
+      if (before >= a.top_groups) {
 #pragma unroll
-    for (int i = 0; i < RT_VALS; ++i) {
-      const int g = lane + 32 * i;
-      stay[i] = 0;
-      if (g < a.G) {
-        const uint32_t v = s_grp[warp][g];
+        for (int i = 0; i < V; ++i) key[i] = 0u;
+      }
+    } else {
+      uint32_t *sk = s_all[warp][tok], *sg = s_grp[warp][tok];
+#pragma unroll
+      for (int i = 0; i < V; ++i) sk[e0 + i] = key[i];
+      __syncwarp();
+      for (int g = sub; g < a.G; g += L) {
+        uint32_t k1 = 0, k2 = 0;
+        for (int j = 0; j < per; ++j) merge2(k1, k2, sk[g * per + j], 0u);
+        if (a.group_sum == 2 && k2) k1 = float_key(key_float(k1) + key_float(k2) + 0.f);
+        sg[g] = k1;
+      }
+      __syncwarp();
+#pragma unroll 1
+      for (int i = 0; i < V; ++i) {
+        const int g = min(e0 + i, a.E - 1) / per;
         int before = 0;
-        for (int j = 0; j < a.G; ++j) {
-          const uint32_t u = s_grp[warp][j];
-          before += (u > v || (u == v && j < g)) ? 1 : 0;
-        }
-        stay[i] = before < a.top_groups ? 1u : 0u;
+        for (int j = 0; j < a.G; ++j) before += (sg[j] > sg[g] || (sg[j] == sg[g] && j < g)) ? 1 : 0;
+        if (before >= a.top_groups) sk[e0 + i] = 0u;
       }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = sk[e0 + i];
     }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < RT_VALS; ++i)
-      if (lane + 32 * i < a.G) s_grp[warp][lane + 32 * i] = stay[i];
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < RT_VALS; ++i)
-      if (lane + 32 * i < a.E && !s_grp[warp][(lane + 32 * i) / per]) key[i] = 0u;
   }
-  int my_e = -1;      // slot `lane` of the token
-  float my_w = 0.f;
-  float total = 0.f;
+  uint32_t best = best_of(key);
+#pragma unroll 1
   for (int j = 0; j < a.k; ++j) {
-    uint32_t best = 0;
+    const uint32_t m = lanes_max<L>(best);
+    unsigned has = __ballot_sync(ALL, best == m);
+    if (L < 32) has &= ((1u << (L & 31)) - 1u) << (lane & ~(L - 1));
+    if (lane == __ffs(has) - 1) {
+      unsigned hits = 0;
 #pragma unroll
-    for (int i = 0; i < RT_VALS; ++i) best = max(best, key[i]);
-    best = __reduce_max_sync(ALL, best);
-    if (best == 0) break;
-    unsigned at = 0xffffffffu;
+      for (int i = 0; i < V; ++i)
+        if (key[i] == m) hits |= 1u << i, key[i] = 0u;
+      const int at = __ffs(hits) - 1;
+      hits &= hits - 1;
+      if (hits && m) {  // a tie within the lane: the others stay
 #pragma unroll
-    for (int i = RT_VALS - 1; i >= 0; --i)
-      if (key[i] == best) at = lane + 32 * i;
-    at = __reduce_min_sync(ALL, at);
-    float w = 0.f;
-#pragma unroll
-    for (int i = 0; i < RT_VALS; ++i)
-      if (static_cast<unsigned>(lane + 32 * i) == at) {
-        w = s[i];
-        key[i] = 0u;
+        for (int i = 0; i < V; ++i)
+          if (hits >> i & 1u) key[i] = m;
       }
-    w = __shfl_sync(ALL, w, at & 31u);
-    total += w;
-    if (lane == j) {
-      my_e = static_cast<int>(at);
-      my_w = w;
+      best = best_of(key);
+      s_key[warp][tok][j] = m;
+      s_e[warp][tok][j] = m ? e0 + at : -1;
     }
   }
-  if (a.renorm) my_w = total > 0.f ? my_w / total : 0.f;
-  if (lane < a.k) {
-    const size_t o = static_cast<size_t>(t) * a.k + lane;
-    a.experts[o] = my_e;
-    a.weights[o] = my_w * a.scale;
-    if (a.counts && my_e >= 0) atomicAdd(a.counts + my_e, 1);
+  if (sub == 0) s_top[warp][tok] = top, s_sum[warp][tok] = sum;
+  __syncwarp();
+  // the scores of the chosen, a lane each
+  const int n = min(TOK, a.T - t0) * a.k;
+  for (int o = lane; o < n; o += 32) {
+    const int u = o / a.k, j = o - u * a.k;
+    const uint32_t m = s_key[warp][u][j];
+    float w = 0.f;
+    if (m) {
+      float v = key_float(m);
+      if (a.bias) v = live_logit(load_logit<BF16>(a.logits, (t0 + u) * a.ld + s_e[warp][u][j]));
+      if (!a.sigmoid)
+        w = expf(v - s_top[warp][u]) / s_sum[warp][u];
+      else
+        w = a.bias ? 1.f / (1.f + expf(-v)) : v;
+    }
+    s_key[warp][u][j] = __float_as_uint(w);
   }
+  __syncwarp();
+  const size_t out = static_cast<size_t>(t0) * a.k;
+  for (int o = lane; o < n; o += 32) {
+    const int u = o / a.k, j = o - u * a.k;
+    const int e = s_e[warp][u][j];
+    float w = __uint_as_float(s_key[warp][u][j]);
+    if (a.renorm) {
+      float total = 0.f;
+      for (int i = 0; i < a.k; ++i) total += __uint_as_float(s_key[warp][u][i]);
+      w = total > 0.f ? w / total : 0.f;
+    }
+    a.experts[out + o] = e;
+    a.weights[out + o] = w * a.scale;
+    if (a.counts && e >= 0) atomicAdd(&s_count[e], 1);
+  }
+  if (a.counts) {
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += 32 * RT_WARPS)
+      if (s_count[e]) atomicAdd(a.counts + e, s_count[e]);
+  }
+}
+
+template <bool BF16, int L, int V>
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t st) {
+  const int grid = (a.T + 32 / L * RT_WARPS - 1) / (32 / L * RT_WARPS);
+  // four logits a load where rows and runs of four start on such a boundary and end with the experts
+  const bool vec = a.E % 4 == 0 && a.ld % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % (BF16 ? 8 : 16) == 0;
+  if (vec)
+    k_route<BF16, L, V, true><<<grid, 32 * RT_WARPS, 0, st>>>(a);
+  else
+    k_route<BF16, L, V, false><<<grid, 32 * RT_WARPS, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <bool BF16>
+cudaError_t launch_route(const RouteArgs& a, cudaStream_t st) {
+  if (a.E <= 8) return launch_route<BF16, 1, 8>(a, st);
+  if (a.E <= 16) return launch_route<BF16, 1, 16>(a, st);
+  if (a.E <= 32) return launch_route<BF16, 2, 16>(a, st);
+  if (a.E <= 64) return launch_route<BF16, 4, 16>(a, st);
+  if (a.E <= 128) return launch_route<BF16, 8, 16>(a, st);
+  return launch_route<BF16, 16, 16>(a, st);
 }
 
 thread_local std::string g_route_msg;
@@ -222,12 +337,7 @@ pop_status pop_route(const pop_route_config* cfg, const void* logits, int logits
   RouteArgs a{logits,       ld_logits,   bias,     T,       c.n_experts, c.top_k, c.score == POP_ROUTE_SIGMOID,
               c.n_groups,   c.top_groups, c.group_sum, c.renorm, c.scale,     experts, weights,
               counts};
-  const int grid = (T + RT_WARPS - 1) / RT_WARPS;
-  if (logits_bf16)
-    k_route<true><<<grid, 32 * RT_WARPS, 0, st>>>(a);
-  else
-    k_route<false><<<grid, 32 * RT_WARPS, 0, st>>>(a);
-  e = cudaGetLastError();
+  e = logits_bf16 ? launch_route<true>(a, st) : launch_route<false>(a, st);
   return e == cudaSuccess ? POP_OK : route_fail(POP_ERR_CUDA, cudaGetErrorString(e));
 }
 
