@@ -8,31 +8,35 @@
 namespace pop {
 
 // ------------------------------------------------------------------ e4m3
-// 512 * ((0.875 * x) / a), which e4m3x2 rounds. y = 1 / a, correctly rounded. The quotient is q0 = t y
-// corrected once by its exact remainder (Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000 processor", 1990): a quotient that is an fp32 number, as every tie between two e4m3
-// values is, comes out exactly. 1 / a must be a normal number: larger a take the division itself.
-__device__ __forceinline__ float q_ratio(float x, float a, float y, bool huge) {
-  const float t = 0.875f * x;
-  if (huge) return 512.f * __fdiv_rn(t, a);
-  const float q0 = t * y;
-  return 512.f * fmaf(fmaf(-q0, a, t), y, q0);
-}
-__device__ __forceinline__ bool q_huge(float a) { return a > 0x1p120f; }
-__device__ __forceinline__ float q_recip(float a, bool huge) { return huge ? 0.f : __frcp_rn(a); }
+// How the values of a block with largest magnitude a become (448 * x) / a, which e4m3x2 rounds: 448 = 0.875 * 512 is
+// e4m3's largest value, and the power of two of it changes no rounding (include/pop_quant.h has 0.875, whose
+// product does not overflow; here a block with a > 2^100 is scaled by 2^-64 first, which is as good). The quotient
+// is q0 = t * (1 / a) corrected once by its exact remainder (Markstein, "Computation of elementary functions on
+// the IBM RISC System/6000 processor", 1990): a quotient that is an fp32 number, as every tie between two e4m3
+// values is, comes out exactly.
+struct BlockRatio {
+  float k, a, y;
+  __device__ __forceinline__ explicit BlockRatio(float amax) {
+    const bool big = amax > 0x1p100f;
+    k = big ? 448.f * 0x1p-64f : 448.f;
+    a = big ? amax * 0x1p-64f : amax;
+    y = __frcp_rn(a);
+  }
+  __device__ __forceinline__ float operator()(float x) const {
+    const float t = k * x, q0 = t * y;
+    return fmaf(fmaf(-q0, a, t), y, q0);
+  }
+};
 
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
 
-__device__ __forceinline__ uint4 e4m3x16(const float* v, float a) {
-  const bool huge = q_huge(a);
-  const float y = q_recip(a, huge);
+__device__ __forceinline__ uint4 e4m3x16(const float* v, const BlockRatio& ratio) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    w[i] = e4m3x2(q_ratio(v[4 * i], a, y, huge), q_ratio(v[4 * i + 1], a, y, huge)) |
-           (e4m3x2(q_ratio(v[4 * i + 2], a, y, huge), q_ratio(v[4 * i + 3], a, y, huge)) << 16);
+    w[i] = e4m3x2(ratio(v[4 * i]), ratio(v[4 * i + 1])) | (e4m3x2(ratio(v[4 * i + 2]), ratio(v[4 * i + 3])) << 16);
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
@@ -40,6 +44,13 @@ __device__ __forceinline__ uint4 e4m3x16(const float* v, float a) {
 // NaN for its largest value.
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 constexpr uint32_t AMAX_MIN_BITS = 0x1f800000u;  // 2^-64
+
+// max(m, |a|, |b|), NaN if any is.
+__device__ __forceinline__ float max_abs(float m, float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
+}
 
 // SiLU(g) u. __expf and __fdividef are off by a few units of 2^-23, far less than the e4m3 rounding of
 // the result; the full-precision forms take about three times the instructions.

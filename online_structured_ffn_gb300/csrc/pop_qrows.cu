@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(256) k_quantize_rows(const __grid_constant__ Q
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float a = __uint_as_float(m);
-    q = e4m3x16(v, a);
+    q = e4m3x16(v, BlockRatio(a));
     s = __fdiv_rn(a, 448.f);
   }
   if (!on) return;
@@ -132,8 +132,9 @@ __global__ void __launch_bounds__(256) k_pack_matrix(const void* __restrict__ W,
   if ((threadIdx.x & 31) == 0) atomicMax(&s_max, m);
   __syncthreads();
   const float a = __uint_as_float(s_max);
+  const BlockRatio ratio(a);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) dst[image_at(r0 + 32 * i, c * 16) >> 4] = e4m3x16(v[i], a);
+  for (int i = 0; i < 4; ++i) dst[image_at(r0 + 32 * i, c * 16) >> 4] = e4m3x16(v[i], ratio);
   if (threadIdx.x == 0) *scale = __fdiv_rn(a, 448.f);
 }
 

@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
           for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
           if (n < g.n) {
             const float am = __uint_as_float(m);
-            const uint4 w = e4m3x16(v, am);
+            const uint4 w = e4m3x16(v, BlockRatio(am));
             const uint32_t ws4[4] = {w.x, w.y, w.z, w.w};
             const size_t block = static_cast<size_t>(g.run) * NTILES + g.t;
             uint8_t* hp = a.h + block * C::X_BYTES;

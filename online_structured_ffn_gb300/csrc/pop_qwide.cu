@@ -52,7 +52,7 @@ struct Ctl {
   uint32_t tmem_base;
   int abort_flag;
   Groups groups;
-  uint32_t amax[2][2][BM];  // gated: [tile parity][column half][row]
+  float amax[2][2][BM];  // gated: [tile parity][column half][row]
 };
 
 struct Tile {
@@ -311,25 +311,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
       const bool valid = r < t.rows;
       const int row = t.row0 + r;
       if (GATED) {
-        uint32_t m = AMAX_MIN_BITS;
+        float am = __uint_as_float(AMAX_MIN_BITS);
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
           acc[j].x = silu_mul(acc[j].x, acc[32 + j].x);
           acc[j].y = silu_mul(acc[j].y, acc[32 + j].y);
-          m = max(m, max(abs_bits(acc[j].x), abs_bits(acc[j].y)));
+          am = max_abs(am, acc[j].x, acc[j].y);
         }
         // the block of 128 channels is shared with the thread of the other half
-        ctl.amax[parity][half][r] = m;
+        ctl.amax[parity][half][r] = am;
         if (epi_any<256>(!ok)) break;  // all eight warps go on, or none
-        m = max(m, ctl.amax[parity][half ^ 1][r]);
+        am = max_abs(am, ctl.amax[parity][half ^ 1][r], 0.f);
         if (valid) {
-          const float am = __uint_as_float(m);
+          const BlockRatio ratio(am);
           uint8_t* hp = a.h + (static_cast<size_t>(row / BM) * NT + t.n) * A_BYTES;
           // chunks 2 c and 2 c + 1 of a row lie in one 32-byte sector, in the order that the swizzle gives
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const uint4 lo = e4m3x16(reinterpret_cast<const float*>(acc) + 32 * c, am);
-            const uint4 hi = e4m3x16(reinterpret_cast<const float*>(acc) + 32 * c + 16, am);
+            const uint4 lo = e4m3x16(reinterpret_cast<const float*>(acc) + 32 * c, ratio);
+            const uint4 hi = e4m3x16(reinterpret_cast<const float*>(acc) + 32 * c + 16, ratio);
             st_sector(hp + (image_at(r, 64 * half + 32 * c) & ~31u), (r & 1) ? hi : lo, (r & 1) ? lo : hi);
           }
           if (half == 0) a.h_s[(static_cast<size_t>(row / BM) * NT + t.n) * BM + r] = __fdiv_rn(am, 448.f);
