@@ -51,29 +51,54 @@ struct Ctl {
   Groups groups;
 };
 
-// One run of k-blocks of a tile.
-struct Seg {
-  int tile, kb0, kb1;
-  int e, t, n;      // group, output tile, rows of the tile
-  int run;          // of rows
-};
-
+// The tiles of one CTA's run of (tile, k-block) units [x0, x1), in order, each with its k-blocks.
 template <int NT>
-__device__ __forceinline__ Seg segment(const Groups& gr, int E, int KB, long long x, long long x1) {
-  Seg s;
-  s.tile = static_cast<int>(x / KB);
-  s.kb0 = static_cast<int>(x - static_cast<long long>(s.tile) * KB);
-  s.kb1 = static_cast<int>(min(static_cast<long long>(KB), s.kb0 + (x1 - x)));
-  s.e = gr.of(E, s.tile);
-  const int cnt = gr.count[s.e];
-  const int tts = qceil(cnt, NT);
-  const int local = s.tile - gr.tile0[s.e];
-  s.t = local / tts;  // the token tiles of one output tile side by side: the matrix tile is in L2 for the others
-  const int i = local - s.t * tts;
-  s.n = min(NT, cnt - i * NT);
-  s.run = gr.run0[s.e] + i;
-  return s;
-}
+struct Walk {
+  int tile, kb0, kb1;
+  int e, t, n;  // group, output tile, rows of the tile
+  int run;      // of rows
+  __device__ __forceinline__ Walk(const Groups& gr, int E, int KB, long long x0, long long x1) : gr_(gr), KB_(KB) {
+    tile = static_cast<int>(x0 / KB);
+    kb0 = static_cast<int>(x0 - static_cast<long long>(tile) * KB);
+    left_ = static_cast<int>(x1 - x0);
+    if (left_ <= 0) return;
+    e = gr.of(E, tile);
+    enter();
+    const int local = tile - gr.tile0[e];
+    t = local / tts_;  // the row tiles of one output tile side by side: the matrix tile is in L2 for the others
+    i_ = local - t * tts_;
+    place();
+  }
+  __device__ __forceinline__ bool more() const { return left_ > 0; }
+  __device__ __forceinline__ void next() {
+    left_ -= kb1 - kb0;
+    if (left_ <= 0) return;
+    kb0 = 0;
+    ++tile;
+    if (++i_ == tts_) i_ = 0, ++t;
+    if (tile == gr_.tile0[e + 1]) {
+      do ++e;
+      while (tile == gr_.tile0[e + 1]);  // groups without rows
+      enter();
+      t = i_ = 0;
+    }
+    place();
+  }
+
+ private:
+  const Groups& gr_;
+  int KB_, left_, tts_, i_, cnt_, run0_;
+  __device__ __forceinline__ void enter() {
+    cnt_ = gr_.count[e];
+    run0_ = gr_.run0[e];
+    tts_ = qceil(cnt_, NT);
+  }
+  __device__ __forceinline__ void place() {
+    kb1 = min(KB_, kb0 + left_);
+    n = min(NT, cnt_ - i_ * NT);
+    run = run0_ + i_;
+  }
+};
 
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(EPI) : "memory"); }
 
@@ -141,8 +166,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
       };
       uint32_t issued = 0, s = 0, phase = 1;
       bool ok = true, waited = false;
-      for (long long x = x0; x < x1 && ok;) {
-        const Seg g = segment<NT>(ctl.groups, a.E, KB, x, x1);
+      for (Walk<NT> g(ctl.groups, a.E, KB, x0, x1); g.more() && ok; g.next()) {
         const uint8_t* w = a.w + g.e * a.w_stride + (static_cast<size_t>(g.t) * KB + g.kb0) * C::W_BYTES;
         Rows r;
         r.x = a.act + (static_cast<size_t>(g.run) * KB + g.kb0) * C::X_BYTES;
@@ -175,7 +199,6 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
           ++issued;
           if (++s == C::STAGES) s = 0, phase ^= 1;
         }
-        x += g.kb1 - g.kb0;
       }
       if (!waited) {  // a short run: every stage that was begun gets its rows
         pdl_wait();
@@ -197,8 +220,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
     const uint32_t ring = desc_lo(smem_u32(smem));
     uint32_t s = 0, phase = 0, b = 0, tphase = 1;
     bool ok = true;
-    for (long long x = x0; x < x1 && ok;) {
-      const Seg g = segment<NT>(ctl.groups, a.E, KB, x, x1);
+    for (Walk<NT> g(ctl.groups, a.E, KB, x0, x1); g.more() && ok; g.next()) {
       const uint32_t idesc = idesc_e4m3_f32(128, qceil(g.n, 16) * 16);
       for (int kb = g.kb0; kb < g.kb1 && ok; kb += C::KS) {
         ok = mbar_wait(&ctl.full[s], phase, Q_WAIT_NS, abort_flag);
@@ -223,7 +245,6 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
         }
         if (++s == C::STAGES) s = 0, phase ^= 1;
       }
-      x += g.kb1 - g.kb0;
     }
     if (!ok && leader) fail();
     if (leader) umma_commit(&ctl.drain);
@@ -239,12 +260,20 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
     const int et = threadIdx.x - 64;
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + n0;
     uint32_t s = 0, phase = 0, b = 0, tphase = 0;
-    for (long long x = x0; x < x1;) {
-      const Seg g = segment<NT>(ctl.groups, a.E, KB, x, x1);
-      // the matrix's scales of this run of k-blocks: lane i holds number 32 j + i, and the one after is on its way
-      const float* ws = a.ws + g.e * a.ws_stride + static_cast<size_t>(g.t) * scale_stride(KB, P) + g.kb0 * P;
-      const int nw = (g.kb1 - g.kb0) * P;
-      float sw = 0.f, sw_next = lane < nw ? __ldg(ws + lane) : 0.f;
+    // The matrix's scales of a run of k-blocks: lane i holds number 32 j + i, and the one after is on its way; the
+    // next tile's first while this one is written out.
+    Walk<NT> g(ctl.groups, a.E, KB, x0, x1);
+    const float* ws = nullptr;
+    int nw = 0;
+    float sw_next = 0.f;
+    auto first_scales = [&]() {
+      ws = a.ws + g.e * a.ws_stride + static_cast<size_t>(g.t) * scale_stride(KB, P) + g.kb0 * P;
+      nw = (g.kb1 - g.kb0) * P;
+      sw_next = lane < nw ? __ldg(ws + lane) : 0.f;
+    };
+    if (g.more()) first_scales();
+    while (g.more()) {
+      float sw = 0.f;
       const int mine = g.n - n0;  // this thread's rows that there are: the first ones, if any
       float acc[P][CW];
 #pragma unroll
@@ -301,30 +330,34 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
       ok = __all_sync(0xffffffffu, ok);
       if (!ok && lane == 0) fail();
       if (epi_any<EPI>(!ok)) break;  // all warps go on, or none
-      x += g.kb1 - g.kb0;
-      if (g.kb1 - g.kb0 < KB) {
+      const int tile = g.tile, t = g.t, rows = g.n, kb0 = g.kb0;
+      const size_t run = g.run;
+      const bool part_only = g.kb1 - g.kb0 < KB;
+      g.next();
+      if (g.more()) first_scales();
+      if (part_only) {
         // a part of the tile, [product][row][output]. Slot 0 of this CTA holds one that starts within its tile,
         // slot 1 one that starts it: a run has at most one of each.
         constexpr size_t slot = static_cast<size_t>(P) * NT * 128;
         const size_t at = static_cast<size_t>(n0) * 128 + f;
-        float* part = a.parts + (2 * static_cast<size_t>(blockIdx.x) + (g.kb0 == 0 ? 1 : 0)) * slot + at;
+        float* part = a.parts + (2 * static_cast<size_t>(blockIdx.x) + (kb0 == 0 ? 1 : 0)) * slot + at;
 #pragma unroll
         for (int p = 0; p < P; ++p)
 #pragma unroll
           for (int n = 0; n < CW; ++n)
             if (n < mine) __stcg(part + (p * NT + n) * 128, acc[p][n]);
-        const long long first = static_cast<long long>(g.tile) * KB, last = first + KB - 1;
+        const long long first = static_cast<long long>(tile) * KB, last = first + KB - 1;
         // CTA c holds [work c / G, work (c + 1) / G): the one of unit x is ((x + 1) G - 1) / work
         const int c0 = static_cast<int>(((first + 1) * G - 1) / work), c1 = static_cast<int>(((last + 1) * G - 1) / work);
         __threadfence();
         epi_sync();
-        if (et == 0) ctl.last = atomicAdd(a.done + g.tile, 1u) == static_cast<unsigned>(c1 - c0) ? 1 : 0;
+        if (et == 0) ctl.last = atomicAdd(a.done + tile, 1u) == static_cast<unsigned>(c1 - c0) ? 1 : 0;
         epi_sync();
         const bool is_last = ctl.last != 0;
         epi_sync();  // ctl.last is free again
         if (!is_last) continue;
         __threadfence();
-        if (et == 0) a.done[g.tile] = 0;
+        if (et == 0) a.done[tile] = 0;
 #pragma unroll
         for (int p = 0; p < P; ++p)
 #pragma unroll
@@ -340,9 +373,9 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
         }
       }
       if (!GATED) {
-        const int col = g.t * QB + f;
+        const int col = t * QB + f;
         if (col < a.N) {
-          const size_t o = (static_cast<size_t>(g.run) * NT + n0) * a.ldy + col;
+          const size_t o = (run * NT + n0) * a.ldy + col;
           if (a.out_f32) {
             float* y = static_cast<float*>(a.y) + o;
 #pragma unroll
@@ -370,17 +403,17 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
           uint32_t m = AMAX_MIN_BITS;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float4 w = n < g.n ? *reinterpret_cast<const float4*>(hs + n * QB + 32 * j + 4 * l8) : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 w = n < rows ? *reinterpret_cast<const float4*>(hs + n * QB + 32 * j + 4 * l8) : make_float4(0.f, 0.f, 0.f, 0.f);
             v[4 * j] = w.x, v[4 * j + 1] = w.y, v[4 * j + 2] = w.z, v[4 * j + 3] = w.w;
             m = max(max(m, max(abs_bits(w.x), abs_bits(w.y))), max(abs_bits(w.z), abs_bits(w.w)));
           }
 #pragma unroll
           for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-          if (n < g.n) {
+          if (n < rows) {
             const float am = __uint_as_float(m);
             const uint4 w = e4m3x16(v, BlockRatio(am));
             const uint32_t ws4[4] = {w.x, w.y, w.z, w.w};
-            const size_t block = static_cast<size_t>(g.run) * NTILES + g.t;
+            const size_t block = run * NTILES + t;
             uint8_t* hp = a.h + block * C::X_BYTES;
 #pragma unroll
             for (int j = 0; j < 4; ++j) *reinterpret_cast<uint32_t*>(hp + image_at(n, 32 * j + 4 * l8)) = ws4[j];
