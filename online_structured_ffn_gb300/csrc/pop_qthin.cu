@@ -2,8 +2,9 @@
 //
 // y[n][f] = sum over k-blocks b of s_x[n][b] s_w[f/128][b] * (q_x[n] . q_w[f])_b. The matrix is the M operand
 // (128 outputs f per tile), the tokens the N operand (NT = 16, 32 or 64 per tile, as many as there are,
-// rounded up to 16). A k-block is one tcgen05 product of 128 x N x 128 into a TMEM buffer of its own,
-// which the epilogue adds to fp32 registers with the block's scales. Bound by the matrix's bytes, so the
+// rounded up to 16). A k-block is one tcgen05 product of 128 x N x 128 into TMEM columns of its own,
+// which the epilogue adds to fp32 registers with the block's scales; a stage's two products (two k-blocks, or the
+// gate's and the up's of one) make one TMEM buffer. Bound by the matrix's bytes, so the
 // split is one that keeps every SM streaming to the end: all (tile, k-block) pairs in order are cut into
 // one equal run per CTA. A tile that lies in several runs is summed from fp32 parts in the order of k by
 // whichever of its CTAs comes last (a counter per tile; no CTA waits for another), so the bits do not
@@ -36,9 +37,9 @@ struct Thin {
   static constexpr uint32_t S_BYTES = NT * 4;       // of their scales
   static constexpr uint32_t X_OFF = KS * W_BYTES, S_OFF = X_OFF + KS * X_BYTES;
   static constexpr uint32_t STAGE = (S_OFF + KS * S_BYTES + 1023) / 1024 * 1024;
-  static constexpr uint32_t H_BYTES = GATED ? NT * QB * 4 : 0;  // a finished tile on its way to e4m3
+  static constexpr uint32_t H_BYTES = NT * QB * 4;  // a finished tile on its way out
   static constexpr int STAGES = (RING_BYTES - H_BYTES) / STAGE;
-  static constexpr int BUFS = static_cast<int>(TMEM_COLS) / (P * NT) < MAX_BUFS ? static_cast<int>(TMEM_COLS) / (P * NT) : MAX_BUFS;
+  static constexpr int BUFS = static_cast<int>(TMEM_COLS) / (2 * NT) < MAX_BUFS ? static_cast<int>(TMEM_COLS) / (2 * NT) : MAX_BUFS;
 };
 
 struct Ctl {
@@ -223,26 +224,22 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
     for (Walk<NT> g(ctl.groups, a.E, KB, x0, x1); g.more() && ok; g.next()) {
       const uint32_t idesc = idesc_e4m3_f32(128, qceil(g.n, 16) * 16);
       for (int kb = g.kb0; kb < g.kb1 && ok; kb += C::KS) {
-        ok = mbar_wait(&ctl.full[s], phase, Q_WAIT_NS, abort_flag);
-#pragma unroll
-        for (int u = 0; u < C::KS; ++u) {
-          if (kb + u < g.kb1) {
-            ok = ok && mbar_wait(&ctl.tempty[b], tphase, Q_WAIT_NS, abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-            if (leader) {
-              const uint32_t st = ring + s * (C::STAGE >> 4);
-              const uint32_t d = tmem_base + b * static_cast<uint32_t>(P * NT);
-              const uint32_t w = st + u * (C::W_BYTES >> 4), xr = st + ((C::X_OFF + u * C::X_BYTES) >> 4);
-              umma_block(d, w, xr, idesc);
-              if (GATED) umma_block(d + NT, w + (QTILE >> 4), xr, idesc);
-              umma_commit(&ctl.tfull[b]);
-              if (u == C::KS - 1 || kb + u == g.kb1 - 1) umma_commit(&ctl.empty[s]);
-            }
-            __syncwarp();
-            if (++b == C::BUFS) b = 0, tphase ^= 1;
-          }
+        ok = mbar_wait(&ctl.full[s], phase, Q_WAIT_NS, abort_flag) && mbar_wait(&ctl.tempty[b], tphase, Q_WAIT_NS, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+          const uint32_t st = ring + s * (C::STAGE >> 4);
+          const uint32_t d = tmem_base + b * static_cast<uint32_t>(2 * NT);
+          umma_block(d, st, st + (C::X_OFF >> 4), idesc);
+          if (GATED)
+            umma_block(d + NT, st + (QTILE >> 4), st + (C::X_OFF >> 4), idesc);
+          else if (kb + 1 < g.kb1)
+            umma_block(d + NT, st + (QTILE >> 4), st + ((C::X_OFF + C::X_BYTES) >> 4), idesc);
+          umma_commit(&ctl.tfull[b]);
+          umma_commit(&ctl.empty[s]);
         }
+        __syncwarp();
+        if (++b == C::BUFS) b = 0, tphase ^= 1;
         if (++s == C::STAGES) s = 0, phase ^= 1;
       }
     }
@@ -283,48 +280,57 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
       bool ok = true;  // once a wait has run out the rest of the run is gone through without waiting
       int i = 0;
       for (int kb = g.kb0; kb < g.kb1; kb += C::KS) {
-        ok = ok && mbar_wait(&ctl.full[s], phase, Q_WAIT_NS, abort_flag);
-        const uint8_t* st = smem + s * C::STAGE + C::S_OFF;
+        if ((i & 31) == 0) {
+          sw = sw_next;
+          sw_next = i + 32 + lane < nw ? __ldg(ws + i + 32 + lane) : 0.f;
+        }
+        // the two products' scales; a k-block that is not there (the last of an odd number) gets 0 times what its
+        // columns hold, which is left out below
+        const float s0 = __shfl_sync(0xffffffffu, sw, i & 31), s1 = __shfl_sync(0xffffffffu, sw, (i + 1) & 31);
+        i += 2;
+        const bool two = GATED || kb + 1 < g.kb1;
+        const float4* sx0 = reinterpret_cast<const float4*>(smem + s * C::STAGE + C::S_OFF + n0 * 4);
+        const float4* sx1 = sx0 + (GATED ? 0 : C::S_BYTES / 16);
+        const uint32_t taddr = lane_base + b * static_cast<uint32_t>(2 * NT);
+        ok = ok && mbar_wait(&ctl.full[s], phase, Q_WAIT_NS, abort_flag) &&
+             mbar_wait(&ctl.tfull[b], tphase, Q_WAIT_NS, abort_flag);
+        tc_fence_after();
 #pragma unroll
-        for (int u = 0; u < C::KS; ++u) {
-          if (kb + u < g.kb1) {
-            if ((i & 31) == 0) {
-              sw = sw_next;
-              sw_next = i + 32 + lane < nw ? __ldg(ws + i + 32 + lane) : 0.f;
+        for (int c = 0; c < CW; c += CH) {
+          if (c >= mine) break;
+          uint32_t d0[CH], d1[CH];
+          tmem_load(taddr + c, d0);
+          if (two) tmem_load(taddr + NT + c, d1);
+          tmem_wait(d0);
+          tmem_wait(d1);
+#pragma unroll
+          for (int j = 0; j < CH; j += 4) {
+            const float4 v = sx0[(c + j) >> 2];
+            const float vs[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              acc[0][c + j + r] = fmaf(s0 * vs[r], __uint_as_float(d0[j + r]), acc[0][c + j + r]);
+              if (GATED) acc[P - 1][c + j + r] = fmaf(s1 * vs[r], __uint_as_float(d1[j + r]), acc[P - 1][c + j + r]);
             }
-            const float s0 = __shfl_sync(0xffffffffu, sw, i & 31), s1 = __shfl_sync(0xffffffffu, sw, (i + P - 1) & 31);
-            i += P;
-            const float4* sx = reinterpret_cast<const float4*>(st + u * C::S_BYTES + n0 * 4);
-            const uint32_t taddr = lane_base + b * static_cast<uint32_t>(P * NT);
-            ok = ok && mbar_wait(&ctl.tfull[b], tphase, Q_WAIT_NS, abort_flag);
-            tc_fence_after();
+          }
+          if (!GATED && two) {
 #pragma unroll
-            for (int c = 0; c < CW; c += CH) {
-              if (c >= mine) break;
-              uint32_t d0[CH], d1[CH];
-              tmem_load(taddr + c, d0);
-              if (GATED) tmem_load(taddr + NT + c, d1);
-              tmem_wait(d0);
-              if (GATED) tmem_wait(d1);
+            for (int j = 0; j < CH; j += 4) {
+              const float4 v = sx1[(c + j) >> 2];
+              const float vs[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-              for (int j = 0; j < CH; j += 4) {
-                const float4 v = sx[(c + j) >> 2];
-                const float vs[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                  acc[0][c + j + r] = fmaf(s0 * vs[r], __uint_as_float(d0[j + r]), acc[0][c + j + r]);
-                  if (GATED) acc[P - 1][c + j + r] = fmaf(s1 * vs[r], __uint_as_float(d1[j + r]), acc[P - 1][c + j + r]);
-                }
-              }
+              for (int r = 0; r < 4; ++r)
+                acc[0][c + j + r] = fmaf(s1 * vs[r], __uint_as_float(d1[j + r]), acc[0][c + j + r]);
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.tempty[b]);
-            if (++b == C::BUFS) b = 0, tphase ^= 1;
           }
         }
+        tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.empty[s]);
+        if (lane == 0) {
+          mbar_arrive(&ctl.tempty[b]);
+          mbar_arrive(&ctl.empty[s]);
+        }
+        if (++b == C::BUFS) b = 0, tphase ^= 1;
         if (++s == C::STAGES) s = 0, phase ^= 1;
       }
       ok = __all_sync(0xffffffffu, ok);
@@ -335,93 +341,111 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
       const bool part_only = g.kb1 - g.kb0 < KB;
       g.next();
       if (g.more()) first_scales();
-      if (part_only) {
+      // A finished tile goes through shared memory, hs[row][output], so that it leaves in whole 16-byte pieces by
+      // short loops: as unrolled stores of every thread's own column it took several thousand cycles a tile.
+      float* hs = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);
+      if (!part_only) {
+#pragma unroll
+        for (int n = 0; n < CW; ++n) hs[(n0 + n) * QB + f] = GATED ? silu_mul(acc[0][n], acc[P - 1][n]) : acc[0][n];
+        epi_sync();
+      } else {
         // a part of the tile, [product][row][output]. Slot 0 of this CTA holds one that starts within its tile,
         // slot 1 one that starts it: a run has at most one of each.
-        constexpr size_t slot = static_cast<size_t>(P) * NT * 128;
-        const size_t at = static_cast<size_t>(n0) * 128 + f;
-        float* part = a.parts + (2 * static_cast<size_t>(blockIdx.x) + (kb0 == 0 ? 1 : 0)) * slot + at;
+        constexpr size_t slot = static_cast<size_t>(P) * NT * QB;
+        float* part = a.parts + (2 * static_cast<size_t>(blockIdx.x) + (kb0 == 0 ? 1 : 0)) * slot + n0 * QB + f;
 #pragma unroll
         for (int p = 0; p < P; ++p)
 #pragma unroll
           for (int n = 0; n < CW; ++n)
-            if (n < mine) __stcg(part + (p * NT + n) * 128, acc[p][n]);
+            if (n < mine) __stcg(part + (p * NT + n) * QB, acc[p][n]);
         const long long first = static_cast<long long>(tile) * KB, last = first + KB - 1;
         // CTA c holds [work c / G, work (c + 1) / G): the one of unit x is ((x + 1) G - 1) / work
         const int c0 = static_cast<int>(((first + 1) * G - 1) / work), c1 = static_cast<int>(((last + 1) * G - 1) / work);
-        __threadfence();
         epi_sync();
-        if (et == 0) ctl.last = atomicAdd(a.done + tile, 1u) == static_cast<unsigned>(c1 - c0) ? 1 : 0;
-        epi_sync();
-        const bool is_last = ctl.last != 0;
-        epi_sync();  // ctl.last is free again
-        if (!is_last) continue;
-        __threadfence();
-        if (et == 0) a.done[tile] = 0;
-#pragma unroll
-        for (int p = 0; p < P; ++p)
-#pragma unroll
-          for (int n = 0; n < CW; ++n) acc[p][n] = 0.f;
-#pragma unroll 1
-        for (int c = c0; c <= c1; ++c) {
-          const float* p0 = a.parts + (2 * static_cast<size_t>(c) + (work * c / G <= first ? 1 : 0)) * slot + at;
-#pragma unroll
-          for (int p = 0; p < P; ++p)
-#pragma unroll
-            for (int n = 0; n < CW; ++n)
-              if (n < mine) acc[p][n] += __ldcg(p0 + (p * NT + n) * 128);
+        if (et == 0) {
+          __threadfence();  // of what all threads of the barrier have written
+          ctl.last = atomicAdd(a.done + tile, 1u) == static_cast<unsigned>(c1 - c0) ? 1 : 0;
+          __threadfence();
         }
+        epi_sync();
+        if (!ctl.last) continue;  // (the next write to it comes after another barrier)
+        if (et == 0) a.done[tile] = 0;
+        const bool whole0 = work * c0 / G <= first;  // the first CTA's part starts the tile; the others' lie within
+        for (int i = et; i < rows * (QB / 4); i += EPI) {
+          float4 v[P];
+#pragma unroll
+          for (int p = 0; p < P; ++p) v[p] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+          for (int c = c0; c <= c1; ++c) {
+            const float4* p0 =
+                reinterpret_cast<const float4*>(a.parts + (2 * static_cast<size_t>(c) + (c == c0 && whole0 ? 1 : 0)) * slot) + i;
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+              const float4 w = __ldcg(p0 + p * NT * (QB / 4));
+              v[p].x += w.x, v[p].y += w.y, v[p].z += w.z, v[p].w += w.w;
+            }
+          }
+          if (GATED) {
+            const float4 u = v[P - 1];
+            v[0] = make_float4(silu_mul(v[0].x, u.x), silu_mul(v[0].y, u.y), silu_mul(v[0].z, u.z), silu_mul(v[0].w, u.w));
+          }
+          reinterpret_cast<float4*>(hs)[i] = v[0];
+        }
+        epi_sync();
       }
       if (!GATED) {
-        const int col = t * QB + f;
-        if (col < a.N) {
-          const size_t o = (run * NT + n0) * a.ldy + col;
-          if (a.out_f32) {
-            float* y = static_cast<float*>(a.y) + o;
-#pragma unroll
-            for (int n = 0; n < CW; ++n)
-              if (n < mine) y[n * a.ldy] = acc[0][n];
+        const size_t o = run * NT * a.ldy + t * QB;
+        const size_t size = a.out_f32 ? 4 : 2;
+        const bool whole = t * QB + QB <= a.N && a.ldy % 4 == 0 && (o * size + reinterpret_cast<uintptr_t>(a.y)) % (4 * size) == 0;
+#pragma unroll 2
+        for (int i = et; i < rows * (QB / 4); i += EPI) {
+          const int n = i >> 5, c = (i & 31) * 4;
+          const float4 v = reinterpret_cast<const float4*>(hs)[i];
+          const size_t at = o + static_cast<size_t>(n) * a.ldy + c;
+          if (whole && a.out_f32) {
+            *reinterpret_cast<float4*>(static_cast<float*>(a.y) + at) = v;
+          } else if (whole) {
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + at) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
           } else {
-            __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y) + o;
+            const float vs[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int n = 0; n < CW; ++n)
-              if (n < mine) y[n * a.ldy] = __float2bfloat16_rn(acc[0][n]);
+            for (int j = 0; j < 4; ++j) {
+              if (t * QB + c + j >= a.N) break;
+              if (a.out_f32)
+                static_cast<float*>(a.y)[at + j] = vs[j];
+              else
+                static_cast<__nv_bfloat16*>(a.y)[at + j] = __float2bfloat16_rn(vs[j]);
+            }
           }
         }
       } else {
-        // the tile's 128 channels are one block of the next product's rows: through shared memory, where eight
-        // lanes then have a row, 16 channels each (4 at a time, 32 apart)
-        float* hs = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);
-#pragma unroll
-        for (int n = 0; n < CW; ++n)
-          if (n < mine) hs[(n0 + n) * QB + f] = silu_mul(acc[0][n], acc[P - 1][n]);
-        epi_sync();
+        // the tile's 128 channels are one block of the next product's rows: eight lanes to a row, 16 channels each
+        // (4 at a time, 32 apart)
+        const size_t block = run * NTILES + t;
+        uint8_t* hp = a.h + block * C::X_BYTES;
 #pragma unroll 1
-        for (int i = et; i < NT * 8; i += EPI) {
+        for (int i = et; i < (rows + 3) / 4 * 32; i += EPI) {
           const int n = i >> 3, l8 = i & 7;
           float v[16];
-          uint32_t m = AMAX_MIN_BITS;
+          float am = __uint_as_float(AMAX_MIN_BITS);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float4 w = n < rows ? *reinterpret_cast<const float4*>(hs + n * QB + 32 * j + 4 * l8) : make_float4(0.f, 0.f, 0.f, 0.f);
             v[4 * j] = w.x, v[4 * j + 1] = w.y, v[4 * j + 2] = w.z, v[4 * j + 3] = w.w;
-            m = max(max(m, max(abs_bits(w.x), abs_bits(w.y))), max(abs_bits(w.z), abs_bits(w.w)));
+            am = max_abs(max_abs(am, w.x, w.y), w.z, w.w);
           }
 #pragma unroll
-          for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+          for (int o = 1; o < 8; o <<= 1) am = max_abs(am, __shfl_xor_sync(0xffffffffu, am, o), 0.f);
           if (n < rows) {
-            const float am = __uint_as_float(m);
             const uint4 w = e4m3x16(v, BlockRatio(am));
             const uint32_t ws4[4] = {w.x, w.y, w.z, w.w};
-            const size_t block = run * NTILES + t;
-            uint8_t* hp = a.h + block * C::X_BYTES;
 #pragma unroll
             for (int j = 0; j < 4; ++j) *reinterpret_cast<uint32_t*>(hp + image_at(n, 32 * j + 4 * l8)) = ws4[j];
             if (l8 == 0) a.h_s[block * NT + n] = __fdiv_rn(am, 448.f);
           }
         }
-        epi_sync();  // the buffer is free again
       }
+      epi_sync();  // hs is free again
     }
   }
 
