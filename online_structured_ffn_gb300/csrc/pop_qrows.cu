@@ -20,8 +20,9 @@ __device__ __forceinline__ void unpack8(const void* p, int kind, float* v) {
 // Eight lanes per block of 128, 16 values each. A CTA has 32 blocks: of one row (the blockIdx.y-th 32), or of the
 // `per` whole rows that they hold.
 __global__ void __launch_bounds__(256) k_quantize_rows(const __grid_constant__ QRowsArgs in, const __grid_constant__ QRowsOut out, int per) {
-  pdl_wait();  // the rows, their places, and what an earlier call's kernels still read
-  pdl_trigger();
+  // Behind the kernel that places the rows (row_of) x is complete, as that one has waited for it: only the places, and
+  // what an earlier call's kernels may still read, are then waited for, after the arithmetic.
+  if (!out.row_of) pdl_wait();
   const int KB = qceil(in.K, QB);
   const int lane8 = threadIdx.x & 7, u = threadIdx.x >> 3;
   const int row_in = per > 1 ? u / KB : 0;
@@ -61,6 +62,8 @@ __global__ void __launch_bounds__(256) k_quantize_rows(const __grid_constant__ Q
     q = e4m3x16(v, BlockRatio(a));
     s = __fdiv_rn(a, 448.f);
   }
+  if (out.row_of) pdl_wait();
+  pdl_trigger();
   if (!on) return;
   if (out.G == 0) {
     uint8_t* p = out.q + static_cast<size_t>(row) * out.ldq + k0;
@@ -146,93 +149,122 @@ __global__ void __launch_bounds__(32 * PLAN_WARPS) k_plan(const int* __restrict_
                                                           int* __restrict__ counts, int* __restrict__ run0,
                                                           int* __restrict__ row_of, unsigned* __restrict__ err) {
   __shared__ int s_at[PLAN_WARPS][POP_QMOE_MAX_EXPERTS];
-  __shared__ int s_runs[POP_QMOE_MAX_EXPERTS];
+  __shared__ int s_base[POP_QMOE_MAX_EXPERTS / 32];
   constexpr unsigned ALL = 0xffffffffu;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = threadIdx.x; i < PLAN_WARPS * POP_QMOE_MAX_EXPERTS / 4; i += blockDim.x)
+    reinterpret_cast<int4*>(&s_at[0][0])[i] = make_int4(0, 0, 0, 0);
   pdl_wait();  // the routing, and an earlier call's use of what is written here
   pdl_trigger();
-  for (int i = threadIdx.x; i < PLAN_WARPS * POP_QMOE_MAX_EXPERTS; i += blockDim.x) (&s_at[0][0])[i] = 0;
-  __syncthreads();
   const int part = qceil(qceil(pairs, PLAN_WARPS), 32) * 32;
-  const int p0 = warp * part, p1 = min(pairs, p0 + part);
-  // f(pair, its expert or -1, lanes of the same expert), 32 pairs at a time, four loads on their way
-  auto each = [&](auto f) {
-    for (int c = p0; c < p1; c += 128) {
-      int e[4];
+  const int p0 = min(pairs, warp * part), p1 = min(pairs, p0 + part);
+  // 128 pairs at a time: the experts of four of them per lane, -1 for none
+  int e[4];
+  auto load = [&](int c, bool report) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) e[i] = c + 32 * i + lane < p1 ? __ldg(experts + c + 32 * i + lane) : -1;
+    for (int i = 0; i < 4; ++i) e[i] = c + 32 * i + lane < p1 ? __ldg(experts + c + 32 * i + lane) : -1;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (c + 32 * i >= p1) break;
-        const int v = static_cast<unsigned>(e[i]) < static_cast<unsigned>(E) ? e[i] : -1;
-        f(c + 32 * i + lane, v, __match_any_sync(ALL, v));
-        if (v != e[i] && e[i] != -1) atomicOr(err, QERR_EXPERT);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const bool is = static_cast<unsigned>(e[i]) < static_cast<unsigned>(E);
+      if (report && !is && e[i] != -1) atomicOr(err, QERR_EXPERT);
+      if (!is) e[i] = -1;
     }
   };
-  each([&](int, int e, unsigned same) {
-    if (e >= 0 && lane == __ffs(same) - 1) s_at[warp][e] += __popc(same);
-    __syncwarp();
-  });
+  if (p0 < p1) load(p0, true);
+  __syncthreads();
+  for (int c = p0; c < p1; c += 128) {
+    if (c > p0) load(c, true);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (c + 32 * i >= p1) break;
+      const unsigned same = __match_any_sync(ALL, e[i]);
+      if (e[i] >= 0 && lane == __ffs(same) - 1) s_at[warp][e[i]] += __popc(same);
+      __syncwarp();
+    }
+  }
+  __syncthreads();
+  int own = 0, before = 0;
+  if (threadIdx.x < POP_QMOE_MAX_EXPERTS) {
+    const int x = threadIdx.x;
+    int at[PLAN_WARPS];
+#pragma unroll
+    for (int w = 0; w < PLAN_WARPS; ++w) at[w] = s_at[w][x];
+    int n = 0;
+#pragma unroll
+    for (int w = 0; w < PLAN_WARPS; ++w) {
+      s_at[w][x] = n;
+      n += at[w];
+    }
+    if (x < E) counts[x] = n;
+    own = before = qceil(n, G);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(ALL, before, o);
+      if (lane >= o) before += v;
+    }
+    if (lane == 31) s_base[warp] = before;
+    before -= own;
+  }
   __syncthreads();
   if (threadIdx.x < POP_QMOE_MAX_EXPERTS) {
-    const int e = threadIdx.x;
-    int n = 0;
-    for (int w = 0; w < PLAN_WARPS; ++w) {
-      const int v = s_at[w][e];
-      s_at[w][e] = n;
-      n += v;
-    }
-    if (e < E) counts[e] = n;
-    s_runs[e] = qceil(n, G);
-  }
-  __syncthreads();
-  if (warp == 0) {
-    int base = 0;
-    for (int e = lane; e < POP_QMOE_MAX_EXPERTS; e += 32) {
-      const int own = s_runs[e];
-      int n = own;
+    const int x = threadIdx.x;
+    for (int w = 0; w < warp; ++w) before += s_base[w];
+    if (x < E) run0[x] = before;
+    if (x == E - 1) run0[E] = before + own;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(ALL, n, o);
-        if (lane >= o) n += v;
-      }
-      s_runs[e] = base + n - own;
-      if (e <= E) run0[e] = base + n - own;
-      base += __shfl_sync(ALL, n, 31);
-    }
-    if (E == POP_QMOE_MAX_EXPERTS && lane == 0) run0[E] = base;
+    for (int w = 0; w < PLAN_WARPS; ++w) s_at[w][x] += before * G;
   }
   __syncthreads();
-  each([&](int p, int e, unsigned same) {
-    int at = 0;
-    if (e >= 0) at = s_at[warp][e];
-    __syncwarp();
-    if (p < p1) row_of[p] = e < 0 ? -1 : s_runs[e] * G + at + __popc(same & ((1u << lane) - 1u));
-    if (e >= 0 && lane == __ffs(same) - 1) s_at[warp][e] = at + __popc(same);
-    __syncwarp();
-  });
+  for (int c = p0; c < p1; c += 128) {
+    if (p1 - p0 > 128) load(c, false);  // else they are still there
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (c + 32 * i >= p1) break;
+      const unsigned same = __match_any_sync(ALL, e[i]);
+      int at = 0;
+      if (e[i] >= 0) at = s_at[warp][e[i]];
+      __syncwarp();
+      const int p = c + 32 * i + lane;
+      if (p < p1) row_of[p] = e[i] < 0 ? -1 : at + __popc(same & ((1u << lane) - 1u));
+      if (e[i] >= 0 && lane == __ffs(same) - 1) s_at[warp][e[i]] = at + __popc(same);
+      __syncwarp();
+    }
+  }
 }
 
-// Four outputs per thread.
+// Four outputs per thread, up to K slots at a time so that their rows are on their way together.
+template <int K>
 __global__ void __launch_bounds__(256) k_combine(const float* __restrict__ o, const int* __restrict__ row_of,
                                                  const float* __restrict__ weights, int k, int D,
                                                  void* __restrict__ y, long long ldy, int out_f32) {
   const size_t t = blockIdx.x;
   const int d = 4 * (blockIdx.y * 256 + threadIdx.x);
-  pdl_wait();  // the experts' outputs
-  pdl_trigger();
-  if (d >= D) return;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int j = 0; j < k; ++j) {
-    const int r = row_of[t * k + j];
-    if (r < 0) continue;
-    const float w = weights[t * k + j];
-    const float4 v = *reinterpret_cast<const float4*>(o + static_cast<size_t>(r) * D + d);
-    acc.x = fmaf(w, v.x, acc.x);
-    acc.y = fmaf(w, v.y, acc.y);
-    acc.z = fmaf(w, v.z, acc.z);
-    acc.w = fmaf(w, v.w, acc.w);
+  for (int j0 = 0; j0 < k; j0 += K) {
+    int r[K];
+    float w[K];
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      r[j] = j0 + j < k ? __ldcg(row_of + t * k + j0 + j) : -1;
+      w[j] = r[j] >= 0 ? weights[t * k + j0 + j] : 0.f;
+    }
+    if (j0 == 0) {
+      pdl_wait();  // the experts' outputs (the places were there before they began)
+      pdl_trigger();
+      if (d >= D) return;
+    }
+    float4 v[K];
+#pragma unroll
+    for (int j = 0; j < K; ++j)
+      if (r[j] >= 0) v[j] = __ldcg(reinterpret_cast<const float4*>(o + static_cast<size_t>(r[j]) * D + d));
+#pragma unroll
+    for (int j = 0; j < K; ++j) {
+      if (r[j] < 0) continue;
+      acc.x = fmaf(w[j], v[j].x, acc.x);
+      acc.y = fmaf(w[j], v[j].y, acc.y);
+      acc.z = fmaf(w[j], v[j].z, acc.z);
+      acc.w = fmaf(w[j], v[j].w, acc.w);
+    }
   }
   if (out_f32)
     *reinterpret_cast<float4*>(static_cast<float*>(y) + t * ldy + d) = acc;
@@ -262,7 +294,9 @@ cudaError_t launch_plan(const int* experts, int pairs, int E, int G, int* counts
 
 cudaError_t launch_combine(const float* o, const int* row_of, const float* weights, int T, int k, int D, void* y,
                            long long ldy, int out_f32, cudaStream_t st) {
-  return launch_q(k_combine, dim3(T, qceil(D, 1024)), 256, 0, st, o, row_of, weights, k, D, y, ldy, out_f32);
+  const dim3 grid(T, qceil(D, 1024));
+  if (k <= 2) return launch_q(k_combine<2>, grid, 256, 0, st, o, row_of, weights, k, D, y, ldy, out_f32);
+  return launch_q(k_combine<4>, grid, 256, 0, st, o, row_of, weights, k, D, y, ldy, out_f32);
 }
 
 }  // namespace pop
