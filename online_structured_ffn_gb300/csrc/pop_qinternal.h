@@ -26,6 +26,8 @@ constexpr int QTILE = QB * QB;       // bytes of a 128 x 128 image
 __host__ __device__ constexpr int qceil(int a, int b) { return (a + b - 1) / b; }
 // Floats from one tile's scales to the next one's: whole runs of eight k-blocks, which bulk copies bring in.
 __host__ __device__ constexpr int scale_stride(int KB, int step) { return qceil(KB, 8) * 8 * step; }
+// Floats that a copy of eight k-blocks' scales may reach past the last tile's.
+constexpr int SCALE_PAD = 16;
 
 // Byte of (row, k) within an image of 128-byte rows.
 __host__ __device__ constexpr uint32_t image_at(uint32_t row, uint32_t k) {
@@ -85,8 +87,8 @@ struct QGemmArgs {
   void* y;
   long long ldy;
   int out_f32;
-  // thin products: parts of tiles that several CTAs share (qgemm_thin_parts floats) and a counter per
-  // tile, zero between calls
+  // parts of tiles that several CTAs share (qgemm_thin_parts or qgemm_wide_parts floats), and a counter per tile
+  // (thin; wide: per SM), zero between calls
   float* parts;
   unsigned* done;
   unsigned* err;
@@ -97,6 +99,7 @@ cudaError_t launch_qgemm_thin(const QGemmArgs& a, bool gated, cudaStream_t st);
 size_t qgemm_thin_parts(int num_sms, bool gated);
 // many rows per group (G = 128): 128 x 256 tiles (pop_qwide.cu)
 cudaError_t launch_qgemm_wide(const QGemmArgs& a, bool gated, cudaStream_t st);
+size_t qgemm_wide_parts(int num_sms);
 
 enum : unsigned {
   QERR_EXPERT = 1u << 0,   // an expert index outside [-1, n_experts)

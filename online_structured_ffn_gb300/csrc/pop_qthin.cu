@@ -140,7 +140,15 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
   pdl_trigger();
   const int tiles = ctl.groups.fill(a, NT, NTILES);
   const long long work = static_cast<long long>(tiles) * KB;
-  const long long G = min(static_cast<long long>(gridDim.x), work);  // CTAs that have a unit
+  // CTAs that have a run, G: all, but with few tiles a run is at least sqrt(NT KB / 28) units, as each more CTA of a
+  // tile costs its last one the reading of a part (NT = 64: some 0.8 us; a unit takes 0.35 us). Runs that are whole
+  // fractions of a tile have one part to hand in instead of two, which is worth some six units. (64 rows by 1000 x
+  // 8000: 29 us over all 152 CTAs, 19 to a tile, 18 by the square root alone.)
+  const int least = max(1, static_cast<int>(sqrtf(NT * KB / 28.f)));
+  const int spread = static_cast<int>(min(static_cast<long long>(gridDim.x), max(work / least, min(work, 1ll))));
+  const int each = tiles > 0 ? min(static_cast<int>(gridDim.x) / tiles, max(1, KB / least)) : 0;  // CTAs to a tile
+  const bool aligned = each > 0 && qceil(KB, each) <= work / spread + 6;
+  const long long G = aligned ? static_cast<long long>(tiles) * each : spread;
   const bool on = static_cast<long long>(blockIdx.x) < G;
   const long long x0 = on ? work * blockIdx.x / G : 0, x1 = on ? work * (blockIdx.x + 1) / G : 0;
 

@@ -2,6 +2,7 @@
 #include "pop_quant.h"
 
 #include <atomic>
+#include <initializer_list>
 #include <mutex>
 #include <new>
 #include <string>
@@ -81,7 +82,6 @@ using namespace pop;
 
 struct pop_qlinear {
   pop_qlinear_config cfg;
-  int rows = 0;            // row capacity of the workspace
   uint8_t* w = nullptr;    // matrix image
   float* ws = nullptr;
   uint8_t* act = nullptr;  // image of a call's rows
@@ -94,7 +94,6 @@ struct pop_qlinear {
 
 struct pop_qmoe {
   pop_qmoe_config cfg;
-  int rows = 0;
   uint8_t *wgu = nullptr, *wdn = nullptr;
   float *sgu = nullptr, *sdn = nullptr;
   int *counts = nullptr, *run0 = nullptr, *row_of = nullptr;
@@ -109,18 +108,55 @@ struct pop_qmoe {
 
 namespace {
 
-// Rows of a run, which says which kind of product a call takes: 128 (wide), else thin with tiles of as many
-// tokens as a group can have if a token is in it once, up to 64.
-constexpr int WIDE_ROWS = 64;
-int granule(long long rows_per_group, int tokens) {
-  return rows_per_group >= WIDE_ROWS ? 128 : tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64;
+// One product of the experts or of a matrix, for the choice between its two kernels: `groups` groups of about `rows`
+// rows, NT tiles of 128 outputs (gated: of channels), KB k-blocks.
+struct Shape {
+  long long groups, rows;
+  int NT, KB;
+  bool gated;
+};
+
+// Times of the two kernels, in 0.05 us. Wide: rounds of 256 x 256 tiles over pairs of SMs, a k-block 0.35 us, or 0.5
+// where a matrix tile serves one row tile only and comes from memory. Thin: tiles of 64 rows by 128 outputs over all SMs, a
+// k-block 0.36 us (gated: two products, 0.8 us) and a little more, as the matrix is read again for every further
+// tile of rows. Measured, rows per group, thin against wide in us: 8 experts of 2 x 14336 x 4096 64: 149/187, 96: 279/188;
+// 11008 x 4096 64: 19/18, 96: 22/19; 1000 x 8000 96: 20/28; 64 experts of 2048 x 1000 64: 43/49, 96: 61/55.
+double wide_time(const Shape& s, int sms) {
+  const long long tiles = s.groups * ((s.rows + 255) / 256) * (s.gated ? s.NT : qceil(s.NT, 2));
+  return static_cast<double>((tiles + sms / 2 - 1) / (sms / 2)) * s.KB * (s.rows <= 256 ? 10 : 7);
+}
+double thin_time(const Shape& s, int sms) {
+  return static_cast<double>(s.groups * ((s.rows + 63) / 64) * s.NT) * s.KB * (s.gated ? 20 : 10) / sms;
 }
 
-// Counters of a thin product's tiles: token tiles (of 16 at least) of all groups, times output tiles.
-size_t thin_tiles(long long pairs, int E, size_t out_tiles) {
-  const long long most = static_cast<long long>(WIDE_ROWS) * E;
-  const long long n = pairs < most ? pairs : most;
-  return static_cast<size_t>(n / 16 + (n < E ? n : E)) * out_tiles;
+constexpr long long THIN_MOST = 1024;  // rows of a group
+
+// Rows of a run, which says which kernel a call takes: 128 (wide), else thin with tiles of as many rows as a group can
+// have if a token is in it once, up to 64.
+int granule(std::initializer_list<Shape> products, int tokens, int sms) {
+  double wide = 0, thin = 0;
+  bool few = true;
+  for (const Shape& s : products) {
+    wide += wide_time(s, sms);
+    thin += thin_time(s, sms);
+    few = few && s.rows <= THIN_MOST;
+  }
+  return !few || thin > wide ? 128 : tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64;
+}
+
+// Counters of the tiles that CTAs share. Thin: row tiles (of 16 at least; of 64 with more than 32 tokens) of all groups,
+// times output tiles. Wide: one per SM.
+size_t tile_counters(long long pairs, long long few_pairs, int E, size_t out_tiles, int num_sms) {
+  const long long most = THIN_MOST * E < pairs ? THIN_MOST * E : pairs;
+  const long long used = most < E ? most : E;
+  const long long many = most / 64 + used, few = few_pairs / 16 + used;
+  const size_t thin = static_cast<size_t>(many > few ? many : few) * out_tiles;
+  return thin > static_cast<size_t>(num_sms) ? thin : num_sms;
+}
+// Floats of their parts.
+size_t part_floats(bool wide, bool gated, int num_sms) {
+  const size_t t = qgemm_thin_parts(num_sms, gated), w = wide ? qgemm_wide_parts(num_sms) : 0;
+  return t > w ? t : w;
 }
 
 cudaError_t launch_qgemm(const QGemmArgs& g, bool gated, cudaStream_t st) {
@@ -142,11 +178,24 @@ void free_qmoe(pop_qmoe* m) {
   for (void* q : p) cudaFree(q);
 }
 
+int linear_granule(const pop_qlinear_config& c, int rows, int sms) {
+  return granule({{1, rows, qceil(c.N, QB), qceil(c.K, QB), false}}, rows, sms);
+}
+
+// The experts' rows spread about their mean, as routers do: some pass 64 when the mean is at 56.
+int qmoe_granule(const pop_qmoe_config& c, int tokens, int sms) {
+  const long long pairs = static_cast<long long>(tokens) * c.top_k;
+  const long long groups = pairs < c.n_experts ? pairs : c.n_experts;
+  const long long rows = c.n_experts > 1 ? pairs * 8 / (groups * 7) + 1 : pairs;
+  const int NT = qceil(c.D_FF, QB), DT = qceil(c.D, QB);
+  return granule({{groups, rows, NT, DT, true}, {groups, rows, DT, NT, false}}, tokens, sms);
+}
+
 pop_status linear_call(pop_qlinear* h, QRowsArgs in, size_t row_bytes, int M, void* y, long long ldy, cudaStream_t st,
                        const char* call) {
     for (int m0 = 0; m0 < M; m0 += h->cfg.max_tokens) {
     const int n = M - m0 < h->cfg.max_tokens ? M - m0 : h->cfg.max_tokens;
-    const int G = granule(n, n);
+    const int G = linear_granule(h->cfg, n, h->num_sms);
     QRowsArgs part = in;
     part.x = static_cast<const uint8_t*>(in.x) + static_cast<size_t>(m0) * in.ldx * row_bytes;
     if (in.xs) part.xs = in.xs + static_cast<size_t>(m0) * in.lds;
@@ -230,18 +279,20 @@ pop_status pop_qlinear_create(const pop_qlinear_config* cfg, const void* W, cons
   if (!h) return q_fail(POP_ERR_OOM, call, "out of host memory");
   h->cfg = *cfg;
   h->num_sms = sm_count();
-  h->rows = qceil(cfg->max_tokens, 128) * 128;
+  const size_t rows = static_cast<size_t>(qceil(cfg->max_tokens, 128)) * 128;
   const size_t NT = qceil(cfg->N, QB), KB = qceil(cfg->K, QB);
   cudaError_t e = dalloc(&h->w, NT * KB * QTILE);
-  if (e == cudaSuccess) e = dalloc(&h->ws, NT * scale_stride(KB, 1));
-  if (e == cudaSuccess) e = dalloc(&h->act, static_cast<size_t>(h->rows) * KB * QB);
-  if (e == cudaSuccess) e = dalloc(&h->act_s, static_cast<size_t>(h->rows) * KB);
-  const size_t thin = thin_tiles(cfg->max_tokens, 1, NT);
-  if (e == cudaSuccess) e = dalloc(&h->parts, qgemm_thin_parts(h->num_sms, false));
-  if (e == cudaSuccess) e = dalloc(&h->done, thin);
+  if (e == cudaSuccess) e = dalloc(&h->ws, NT * scale_stride(KB, 1) + SCALE_PAD);
+  if (e == cudaSuccess) e = dalloc(&h->act, rows * KB * QB);
+  if (e == cudaSuccess) e = dalloc(&h->act_s, rows * KB);
+  const size_t counters = tile_counters(cfg->max_tokens, cfg->max_tokens < 32 ? cfg->max_tokens : 32, 1, NT, h->num_sms);
+  bool wide = false;
+  for (int m = 1; m <= cfg->max_tokens && !wide; ++m) wide = linear_granule(*cfg, m, h->num_sms) == 128;
+  if (e == cudaSuccess) e = dalloc(&h->parts, part_floats(wide, false, h->num_sms));
+  if (e == cudaSuccess) e = dalloc(&h->done, counters);
   if (e == cudaSuccess) e = dalloc(&h->err, 1);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (e == cudaSuccess) e = cudaMemsetAsync(h->done, 0, thin * sizeof(unsigned), st);
+  if (e == cudaSuccess) e = cudaMemsetAsync(h->done, 0, counters * sizeof(unsigned), st);
   if (e == cudaSuccess) e = cudaMemsetAsync(h->err, 0, sizeof(unsigned), st);
   if (e == cudaSuccess) e = launch_pack_matrix(W, W_s, cfg->N, cfg->K, h->w, h->ws, 1, 0, st);
   // later calls may come on other streams
@@ -334,15 +385,16 @@ pop_status pop_qmoe_create(const pop_qmoe_config* cfg, const void* const* Wg, co
   m->num_sms = sm_count();
   const long long pairs = static_cast<long long>(cfg->max_tokens) * cfg->top_k;
   const long long used = pairs < E ? pairs : E;  // experts that can have rows
-  const int most = granule(pairs / E, cfg->max_tokens);  // grows with the tokens, as the rows do
+  bool wide = false;
+  for (int t = 1; t <= cfg->max_tokens && !wide; ++t) wide = qmoe_granule(*cfg, t, m->num_sms) == 128;
+  const int most = wide ? 128 : cfg->max_tokens <= 16 ? 16 : cfg->max_tokens <= 32 ? 32 : 64;
   const long long rows = (pairs / most + used) * most;
-  m->rows = static_cast<int>(rows);
   const size_t NT = qceil(cfg->D_FF, QB), DT = qceil(cfg->D, QB);
   cudaError_t e = dalloc(&m->wgu, E * NT * DT * 2 * QTILE);
   if (e == cudaSuccess) e = dalloc(&m->wdn, E * DT * NT * QTILE);
   const size_t gu_scales = NT * scale_stride(DT, 2), dn_scales = DT * scale_stride(NT, 1);
-  if (e == cudaSuccess) e = dalloc(&m->sgu, E * gu_scales);
-  if (e == cudaSuccess) e = dalloc(&m->sdn, E * dn_scales);
+  if (e == cudaSuccess) e = dalloc(&m->sgu, E * gu_scales + SCALE_PAD);
+  if (e == cudaSuccess) e = dalloc(&m->sdn, E * dn_scales + SCALE_PAD);
   if (e == cudaSuccess) e = dalloc(&m->counts, E);
   if (e == cudaSuccess) e = dalloc(&m->run0, E + 1);
   if (e == cudaSuccess) e = dalloc(&m->row_of, pairs);
@@ -351,12 +403,13 @@ pop_status pop_qmoe_create(const pop_qmoe_config* cfg, const void* const* Wg, co
   if (e == cudaSuccess) e = dalloc(&m->h, rows * NT * QB);
   if (e == cudaSuccess) e = dalloc(&m->h_s, rows * NT);
   if (e == cudaSuccess) e = dalloc(&m->o, static_cast<size_t>(rows) * cfg->D);
-  const size_t thin = thin_tiles(pairs, E, NT > DT ? NT : DT);
-  if (e == cudaSuccess) e = dalloc(&m->parts, qgemm_thin_parts(m->num_sms, true));
-  if (e == cudaSuccess) e = dalloc(&m->done, thin);
+  const long long few = static_cast<long long>(cfg->max_tokens < 32 ? cfg->max_tokens : 32) * cfg->top_k;
+  const size_t counters = tile_counters(pairs, few, E, NT > DT ? NT : DT, m->num_sms);
+  if (e == cudaSuccess) e = dalloc(&m->parts, part_floats(wide, true, m->num_sms));
+  if (e == cudaSuccess) e = dalloc(&m->done, counters);
   if (e == cudaSuccess) e = dalloc(&m->err, 1);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (e == cudaSuccess) e = cudaMemsetAsync(m->done, 0, thin * sizeof(unsigned), st);
+  if (e == cudaSuccess) e = cudaMemsetAsync(m->done, 0, counters * sizeof(unsigned), st);
   if (e == cudaSuccess) e = cudaMemsetAsync(m->err, 0, sizeof(unsigned), st);
   for (int x = 0; x < E && e == cudaSuccess; ++x) {
     uint8_t* gu = m->wgu + x * NT * DT * 2 * QTILE;
@@ -402,7 +455,7 @@ pop_status pop_qmoe_forward(pop_qmoe_t m, const void* x, long long ldx, const in
   for (int t0 = 0; t0 < T; t0 += c.max_tokens) {
     const int n = T - t0 < c.max_tokens ? T - t0 : c.max_tokens;
     const int pairs = n * c.top_k;
-    const int G = granule(pairs / c.n_experts, n);
+    const int G = qmoe_granule(c, n, m->num_sms);
     const int* ex = experts + static_cast<size_t>(t0) * c.top_k;
     cudaError_t e = launch_plan(ex, pairs, c.n_experts, G, m->counts, m->run0, m->row_of, m->err, st);
     if (e != cudaSuccess) return q_cuda(e, call);

@@ -13,6 +13,10 @@
 // that one is read while the other is being filled and half the latency from product to epilogue and back
 // (some 600 cycles) is out of the way.
 //
+// The tiles go round the pairs, neighbours at the same time, so that what is in L2 serves many. Those that are left
+// for a last round that would not be full are cut into one equal run of k-blocks per pair; a tile in several runs is
+// summed from fp32 parts in the order of k by whichever of its pairs comes last (a counter per tile and CTA).
+//
 // Persistent, one CTA per SM. Warp 0: copies (operand images: bulk copies of 16 KB). Warps 1 and 3: of the first
 // CTA the products of both CTAs, a half each; warp 1 of the second the news that its operands have landed.
 // Warp 2: scales. Warps 4..11: epilogue, TMEM lane quarter warp % 4. Every wait has a limit; a CTA that gives
@@ -51,6 +55,7 @@ struct Ctl {
   uint64_t drain[2];
   uint32_t tmem_base;
   int abort_flag;
+  int last;
   Groups groups;
   float amax[2][2][BM];  // gated: [tile parity][column half][row]
 };
@@ -73,6 +78,60 @@ __device__ __forceinline__ Tile tile_at(const Groups& g, int E, int tile, int ra
   t.row0 = g.run0[t.e] * BM + t.m0;
   return t;
 }
+
+// The tiles of one pair, in order, each with its k-blocks: whole ones, then its run of the last round's.
+constexpr int SPLIT = 4;  // k-blocks of a run's unit: the scales of four begin on 16 bytes
+struct Walk {
+  int tile, kb0, kb1;
+  // the split tiles: `units` units in all, over `sharers` pairs
+  int first_split, units, sharers, KG;
+
+  __device__ __forceinline__ Walk(int tiles, int pair, int pairs, int KB) : KB_(KB), pairs_(pairs) {
+    const int rest = tiles % pairs;
+    KG = qceil(KB, SPLIT);
+    // A round takes KB k-blocks of 0.35 us or so. The split one takes KB * rest / pairs of them and some 20 us for the
+    // parts, 128 KB of them per run and CTA written and read again (96 rows by 8192 x 28672: 32 tiles of 224 k-blocks, 83
+    // us whole, 64 split; by 28672 x 8192, 36 tiles of 64 left: 59 whole, 65 split).
+    const bool split = rest > 0 && KB * (pairs - rest) >= 72 * pairs;
+    first_split = split ? tiles - rest : tiles;
+    units = split ? rest * KG : 0;
+    sharers = min(pairs, units);
+    u_ = start(pair);
+    u1_ = pair < sharers ? start(pair + 1) : u_;
+    tile = pair - pairs;
+    next();
+  }
+  __device__ __forceinline__ int start(int p) const {
+    return p < sharers ? static_cast<int>(static_cast<long long>(units) * p / sharers) : units;
+  }
+  // the pair that holds unit u
+  __device__ __forceinline__ int holder(int u) const {
+    return static_cast<int>(((static_cast<long long>(u) + 1) * sharers - 1) / units);
+  }
+  __device__ __forceinline__ bool more() const { return kb1 > kb0; }
+  __device__ __forceinline__ void next() {
+    tile += pairs_;
+    kb0 = 0;
+    kb1 = KB_;
+    if (tile < first_split) return;
+    const int t = units > 0 ? u_ / KG : 0, k = u_ - t * KG;
+    const int n = min(KG - k, u1_ - u_);
+    tile = first_split + t - pairs_;
+    kb0 = k * SPLIT;
+    kb1 = n > 0 ? min(KB_, (k + n) * SPLIT) : kb0;
+    tile += pairs_;
+    u_ += n;
+    at_tail_ = true;
+  }
+  __device__ __forceinline__ void advance() {
+    if (at_tail_) tile = first_split - pairs_;  // the units say where to go on
+    next();
+  }
+
+ private:
+  int KB_, pairs_, u_, u1_;
+  bool at_tail_ = false;
+};
 
 template <bool GATED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_wide(const __grid_constant__ QGemmArgs a) {
@@ -131,14 +190,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
       // and 64-bit products once made these take longer than the products)
       uint32_t issued = 0, s = 0, phase = 1;
       bool ok = true;
-      for (int tile = pair; tile < tiles && ok; tile += pairs) {
-        const Tile t = tile_at(ctl.groups, a.E, tile, rank);
-        const uint8_t* xr = a.act + static_cast<size_t>(t.row0 / BM) * KB * A_BYTES;
+      for (Walk v(tiles, pair, pairs, KB); v.more() && ok; v.advance()) {
+        const Tile t = tile_at(ctl.groups, a.E, v.tile, rank);
+        const uint8_t* xr = a.act + (static_cast<size_t>(t.row0 / BM) * KB + v.kb0) * A_BYTES;
         // this CTA's half of the matrix tile. Gated: [tile][k-block][gate | up]; else tile 2 n + rank, or the
         // last one again
         const uint8_t* w = a.w + t.e * a.w_stride +
-                           (GATED ? (static_cast<size_t>(t.n) * KB * 2 + rank) : static_cast<size_t>(min(2 * t.n + rank, NT - 1)) * KB) * QTILE;
-        for (int kb = 0; kb < KB; ++kb) {
+                           (GATED ? ((static_cast<size_t>(t.n) * KB + v.kb0) * 2 + rank)
+                                  : static_cast<size_t>(min(2 * t.n + rank, NT - 1)) * KB + v.kb0) * QTILE;
+        for (int kb = v.kb0; kb < v.kb1; ++kb) {
           if (!mbar_wait(&ctl.empty[s], phase, Q_WAIT_NS, abort_flag)) {
             fail();
             ok = false;
@@ -163,7 +223,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
       }
     }
     if (warp & 1) {
-      const uint32_t total = pair < tiles ? static_cast<uint32_t>((tiles - 1 - pair) / pairs + 1) * static_cast<uint32_t>(KB) : 0u;
+      uint32_t total = 0;  // k-blocks
+      for (Walk v(tiles, pair, pairs, KB); v.more(); v.advance()) total += v.kb1 - v.kb0;
       const bool leader = elect_one();
       uint32_t s = 0, phase = 0;
       if (rank == 0) {
@@ -209,9 +270,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
       // k-block with four of them every fourth)
       uint32_t issued = 0, g = 0, phase = 1;
       bool ok = true;
-      for (int tile = pair; tile < tiles && ok; tile += pairs) {
-        const Tile t = tile_at(ctl.groups, a.E, tile, rank);
-        const float* xs = a.act_s + static_cast<size_t>(t.row0 / BM) * KB * BM;
+      for (Walk v(tiles, pair, pairs, KB); v.more() && ok; v.advance()) {
+        const Tile t = tile_at(ctl.groups, a.E, v.tile, rank);
+        const float* xs = a.act_s + (static_cast<size_t>(t.row0 / BM) * KB + v.kb0) * BM;
         const float* ws = a.ws + t.e * a.ws_stride;
         const float *w0, *w1;
         if (GATED) {
@@ -220,13 +281,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
           w0 = ws + static_cast<size_t>(2 * t.n) * scale_stride(KB, 1);
           w1 = ws + static_cast<size_t>(min(2 * t.n + 1, NT - 1)) * scale_stride(KB, 1);
         }
-        for (int kb = 0; kb < KB; kb += SB) {
+        for (int kb = v.kb0; kb < v.kb1; kb += SB) {
           if (!mbar_wait(&ctl.sempty[g], phase, Q_WAIT_NS, abort_flag)) {
             fail();
             ok = false;
             break;
           }
-          const int n = min(SB, KB - kb);
+          const int n = min(SB, v.kb1 - kb);
           Scales& sc = ctl.scales[g];
           mbar_arrive_expect_tx(&ctl.sfull[g], n * BM * 4 + 2 * SB * 4);
           bulk_load(sc.x, xs, n * BM * 4, &ctl.sfull[g]);
@@ -260,16 +321,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
     uint32_t b = 0, tphase = 0, g = 0, gphase = 0;
     int parity = 0;
     bool ok = true;  // once a wait has run out the rest of the tile is gone through without waiting
-    for (int tile = pair; tile < tiles; tile += pairs, parity ^= 1) {
-      const Tile t = tile_at(ctl.groups, a.E, tile, rank);
+    for (Walk v(tiles, pair, pairs, KB); v.more(); v.advance(), parity ^= 1) {
+      const Tile t = tile_at(ctl.groups, a.E, v.tile, rank);
       float2 acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
-      for (int kb = 0; kb < KB; kb += SB) {
+      for (int kb = v.kb0; kb < v.kb1; kb += SB) {
         ok = ok && mbar_wait(&ctl.sfull[g], gphase, Q_WAIT_NS, abort_flag);
         const float* xg = &ctl.scales[g].x[0][r];
         const float* wg = ctl.scales[g].w;
-        const int n = min(SB, KB - kb);
+        const int n = min(SB, v.kb1 - kb);
         float f0 = xg[0] * wg[0], f1 = xg[0] * wg[GATED ? 1 : SB];
 #pragma unroll 1
         for (int j = 1; j <= n; ++j) {
@@ -307,7 +368,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
       }
       ok = __all_sync(0xffffffffu, ok);
       if (!ok && lane == 0) fail();
-      if (!GATED && !ok) break;
+      if (v.kb1 - v.kb0 < KB) {
+        // a part of the tile, [half][column][row]. Slot 0 of this CTA holds one that starts within its tile, slot 1
+        // one that starts it: a run has at most one of each.
+        if (epi_any<256>(!ok)) break;  // all eight warps go on, or none
+        constexpr size_t slot = 256 * BM;
+        const size_t at = static_cast<size_t>(half) * 128 * BM + r;
+        float* part = a.parts + (2 * static_cast<size_t>(blockIdx.x) + (v.kb0 == 0 ? 1 : 0)) * slot + at;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) {
+          __stcg(part + 2 * i * BM, acc[i].x);
+          __stcg(part + (2 * i + 1) * BM, acc[i].y);
+        }
+        const int first = (v.tile - v.first_split) * v.KG;  // the tile's first unit
+        const int c0 = v.holder(first), c1 = v.holder(first + v.KG - 1);
+        unsigned* done = a.done + 2 * (v.tile - v.first_split) + rank;
+        epi_any<256>(false);
+        if (threadIdx.x == 128) {
+          __threadfence();  // of what all threads of the barrier have written
+          ctl.last = atomicAdd(done, 1u) == static_cast<unsigned>(c1 - c0) ? 1 : 0;
+          __threadfence();
+        }
+        epi_any<256>(false);
+        if (!ctl.last) continue;  // (the next write to it comes after another barrier)
+        if (threadIdx.x == 128) *done = 0;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
+#pragma unroll 1
+        for (int c = c0; c <= c1; ++c) {
+          const float* p = a.parts + (2 * static_cast<size_t>(2 * c + rank) + (v.start(c) <= first ? 1 : 0)) * slot + at;
+#pragma unroll
+          for (int i = 0; i < 64; ++i) {
+            acc[i].x += __ldcg(p + 2 * i * BM);
+            acc[i].y += __ldcg(p + (2 * i + 1) * BM);
+          }
+        }
+      } else if (!GATED && !ok) {
+        break;
+      }
       const bool valid = r < t.rows;
       const int row = t.row0 + r;
       if (GATED) {
@@ -391,6 +489,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
 }
 
 }  // namespace
+
+size_t qgemm_wide_parts(int num_sms) { return static_cast<size_t>(2) * num_sms * 256 * BM; }
 
 cudaError_t launch_qgemm_wide(const QGemmArgs& a, bool gated, cudaStream_t st) {
   const size_t smem = STAGES * STAGE + 1024;
