@@ -52,6 +52,13 @@ __device__ __forceinline__ float max_abs(float m, float a, float b) {
   return r;
 }
 
+// a / 448, rounded once: the product with 1 / 448 corrected by its exact remainder, as above.
+__device__ __forceinline__ float block_scale(float a) {
+  constexpr float y = 1.f / 448.f;
+  const float q = a * y;
+  return a == INFINITY ? a : fmaf(fmaf(-q, 448.f, a), y, q);
+}
+
 // SiLU(g) u. __expf and __fdividef are off by a few units of 2^-23, far less than the e4m3 rounding of
 // the result; the full-precision forms take about three times the instructions.
 __device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }

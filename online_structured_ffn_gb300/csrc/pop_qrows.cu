@@ -18,23 +18,28 @@ __device__ __forceinline__ void unpack8(const void* p, int kind, float* v) {
 }
 
 // Eight lanes per block of 128, 16 values each. A CTA has 32 blocks: of one row (the blockIdx.y-th 32), or of the
-// `per` whole rows that they hold.
+// `per` whole rows that they hold. Bound by memory and nearly so by its instructions, of which every one counts:
+// 16 values take 4 each for the quotient, half a rounding, one for bf16's unpacking.
+template <int KIND>
 __global__ void __launch_bounds__(256) k_quantize_rows(const __grid_constant__ QRowsArgs in, const __grid_constant__ QRowsOut out, int per) {
   // Behind the kernel that places the rows (row_of) x is complete, as that one has waited for it: only the places, and
   // what an earlier call's kernels may still read, are then waited for, after the arithmetic.
   if (!out.row_of) pdl_wait();
   const int KB = qceil(in.K, QB);
   const int lane8 = threadIdx.x & 7, u = threadIdx.x >> 3;
-  const int row_in = per > 1 ? u / KB : 0;
-  const int row = blockIdx.x * per + row_in;
-  const bool mine = row_in < per && row < in.M;
-  const int kb = u - row_in * KB + 32 * blockIdx.y;
-  const bool on = mine && kb < KB;
+  int row = blockIdx.x, kb = u + 32 * blockIdx.y;
+  bool on = kb < KB;
+  if (per > 1) {
+    const int row_in = u / KB;
+    row = blockIdx.x * per + row_in;
+    kb = u - row_in * KB;
+    on = row_in < per && row < in.M;
+  }
   const int k0 = kb * QB + lane8 * 16;
   const int n8 = on ? min(max((in.K - k0) >> 3, 0), 2) : 0;  // runs of 8 values this lane has
   uint4 q = make_uint4(0u, 0u, 0u, 0u);
   float s = 0.f;
-  if (in.kind == 2) {
+  if (KIND == 2) {
     const uint8_t* p = static_cast<const uint8_t*>(in.x) + static_cast<size_t>(row) * in.ldx + k0;
     if (n8 > 0) {
       const uint2 a = *reinterpret_cast<const uint2*>(p);
@@ -46,39 +51,43 @@ __global__ void __launch_bounds__(256) k_quantize_rows(const __grid_constant__ Q
     }
     if (on) s = in.xs[static_cast<size_t>(row) * in.lds + kb];
   } else {
-    const int size = in.kind == 0 ? 2 : 4;
-    const uint8_t* p = static_cast<const uint8_t*>(in.x) + (static_cast<size_t>(row) * in.ldx + k0) * size;
+    constexpr int SIZE = KIND == 0 ? 2 : 4;
+    const uint8_t* p = static_cast<const uint8_t*>(in.x) + (static_cast<size_t>(row) * in.ldx + k0) * SIZE;
     float v[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = 0.f;
-    if (n8 > 0) unpack8(p, in.kind, v);
-    if (n8 > 1) unpack8(p + 8 * size, in.kind, v + 8);
-    uint32_t m = AMAX_MIN_BITS;
+    if (n8 > 0) unpack8(p, KIND, v);
+    if (n8 > 1) unpack8(p + 8 * SIZE, KIND, v + 8);
+    float a = __uint_as_float(AMAX_MIN_BITS);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) m = max(m, abs_bits(v[i]));
+    for (int i = 0; i < 16; i += 2) a = max_abs(a, v[i], v[i + 1]);
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float a = __uint_as_float(m);
+    for (int o = 1; o < 8; o <<= 1) a = max_abs(a, __shfl_xor_sync(0xffffffffu, a, o), 0.f);
     q = e4m3x16(v, BlockRatio(a));
-    s = __fdiv_rn(a, 448.f);
+    s = block_scale(a);
   }
   if (out.row_of) pdl_wait();
   pdl_trigger();
   if (!on) return;
   if (out.G == 0) {
     uint8_t* p = out.q + static_cast<size_t>(row) * out.ldq + k0;
-    if (n8 > 0) *reinterpret_cast<uint2*>(p) = make_uint2(q.x, q.y);
-    if (n8 > 1) *reinterpret_cast<uint2*>(p + 8) = make_uint2(q.z, q.w);
+    if (n8 > 1 && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+      *reinterpret_cast<uint4*>(p) = q;
+    } else {
+      if (n8 > 0) *reinterpret_cast<uint2*>(p) = make_uint2(q.x, q.y);
+      if (n8 > 1) *reinterpret_cast<uint2*>(p + 8) = make_uint2(q.z, q.w);
+    }
     if (lane8 == 0) out.s[static_cast<size_t>(row) * KB + kb] = s;
     return;
   }
+  const int log_g = 31 - __clz(out.G);
   for (int j = 0; j < out.k; ++j) {
     const int r = out.row_of ? __ldcg(out.row_of + static_cast<size_t>(row) * out.k + j) : row;
     if (r < 0) continue;
-    const int run = r / out.G, in_run = r - run * out.G;
-    const size_t block = static_cast<size_t>(run) * KB + kb;
-    *reinterpret_cast<uint4*>(out.q + block * out.G * QB + image_at(in_run, lane8 * 16)) = q;
-    if (lane8 == 0) out.s[block * out.G + in_run] = s;
+    const int in_run = r & (out.G - 1);
+    const size_t block = static_cast<size_t>(r >> log_g) * KB + kb;
+    *reinterpret_cast<uint4*>(out.q + ((block * QB) << log_g) + image_at(in_run, lane8 * 16)) = q;
+    if (lane8 == 0) out.s[(block << log_g) + in_run] = s;
   }
 }
 
@@ -138,7 +147,7 @@ __global__ void __launch_bounds__(256) k_pack_matrix(const void* __restrict__ W,
   const BlockRatio ratio(a);
 #pragma unroll
   for (int i = 0; i < 4; ++i) dst[image_at(r0 + 32 * i, c * 16) >> 4] = e4m3x16(v[i], ratio);
-  if (threadIdx.x == 0) *scale = __fdiv_rn(a, 448.f);
+  if (threadIdx.x == 0) *scale = block_scale(a);
 }
 
 // One CTA; warp w has the w-th part of the pairs. First every warp counts its pairs of each expert (lanes with the
@@ -278,7 +287,10 @@ __global__ void __launch_bounds__(256) k_combine(const float* __restrict__ o, co
 cudaError_t launch_quantize_rows(const QRowsArgs& in, const QRowsOut& out, cudaStream_t st) {
   const int KB = qceil(in.K, QB);
   const int per = KB < 32 ? 32 / KB : 1;
-  return launch_q(k_quantize_rows, dim3(qceil(in.M, per), qceil(KB, 32)), 256, 0, st, in, out, per);
+  const dim3 grid(qceil(in.M, per), qceil(KB, 32));
+  if (in.kind == 0) return launch_q(k_quantize_rows<0>, grid, 256, 0, st, in, out, per);
+  if (in.kind == 1) return launch_q(k_quantize_rows<1>, grid, 256, 0, st, in, out, per);
+  return launch_q(k_quantize_rows<2>, grid, 256, 0, st, in, out, per);
 }
 
 cudaError_t launch_pack_matrix(const void* W, const float* Ws, int N, int K, uint8_t* img, float* s, int step,

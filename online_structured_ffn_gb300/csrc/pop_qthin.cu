@@ -449,7 +449,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
             const uint32_t ws4[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) *reinterpret_cast<uint32_t*>(hp + image_at(n, 32 * j + 4 * l8)) = ws4[j];
-            if (l8 == 0) a.h_s[block * NT + n] = __fdiv_rn(am, 448.f);
+            if (l8 == 0) a.h_s[block * NT + n] = block_scale(am);
           }
         }
       }

@@ -430,7 +430,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
             const uint4 hi = e4m3x16(reinterpret_cast<const float*>(acc) + 32 * c + 16, ratio);
             st_sector(hp + (image_at(r, 64 * half + 32 * c) & ~31u), (r & 1) ? hi : lo, (r & 1) ? lo : hi);
           }
-          if (half == 0) a.h_s[(static_cast<size_t>(row / BM) * NT + t.n) * BM + r] = __fdiv_rn(am, 448.f);
+          if (half == 0) a.h_s[(static_cast<size_t>(row / BM) * NT + t.n) * BM + r] = block_scale(am);
         }
       } else if (valid) {
 #pragma unroll

@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(32 * RT_WARPS) k_route(const __grid_constant__
       for (int i = 0; i < V; ++i) {
         key[i] = 0u;
         if (l[i] != -INFINITY) {
-          const float p = 1.f / (1.f + expf(-l[i]));
+          const float p = __frcp_rn(1.f + expf(-l[i]));
           key[i] = choice_key(a.bias ? p + __ldg(a.bias + e0 + i) : p);
         }
       }
@@ -140,14 +140,17 @@ __global__ void __launch_bounds__(32 * RT_WARPS) k_route(const __grid_constant__
 #pragma unroll
       for (int i = 1; i < V; ++i) top = fmaxf(top, l[i]);
       top = lanes_max<L>(top);
-      sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        key[i] = choice_key(l[i]);
-        l[i] = key[i] ? expf(l[i] - top) : 0.f;
-        sum += l[i];
+      for (int i = 0; i < V; ++i) key[i] = choice_key(l[i]);
+      if (a.bias || !a.renorm) {  // (renormalised weights do not depend on the sum)
+        sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          l[i] = key[i] ? expf(l[i] - top) : 0.f;
+          sum += l[i];
+        }
+        sum = lanes_sum<L>(sum);
       }
-      sum = lanes_sum<L>(sum);
       if (a.bias) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
@@ -238,7 +241,7 @@ __global__ void __launch_bounds__(32 * RT_WARPS) k_route(const __grid_constant__
       if (!a.sigmoid)
         w = expf(v - s_top[warp][u]) / s_sum[warp][u];
       else
-        w = a.bias ? 1.f / (1.f + expf(-v)) : v;
+        w = a.bias ? __frcp_rn(1.f + expf(-v)) : v;
     }
     s_key[warp][u][j] = __float_as_uint(w);
   }
