@@ -81,6 +81,8 @@ struct QGemmArgs {
   const int* run0;       // device [E + 1] first run of each group (NULL: 0)
   int M;                 // rows in all, as far as the host knows: the exact number without counts, else
                          // the number of pairs
+  const QRowsArgs* rows; // thin, one group of up to 16 rows: the rows themselves (kind 0 or 2), which the kernel
+                         // quantises on the way instead of taking act and act_s; or NULL
   // outputs. gated: rows in e4m3 for the next product (same G and rows); else y
   uint8_t* h;
   float* h_s;

@@ -10,6 +10,11 @@
 // whichever of its CTAs comes last (a counter per tile; no CTA waits for another), so the bits do not
 // depend on the order in which CTAs run.
 //
+// Up to 16 rows of one group need no kernel before this one: with ROWS, warps 10..17 bring each stage's rows from
+// bf16 (or e4m3) into their image themselves. Every CTA does so for the k-blocks of its run, which is little beside
+// the matrix's bytes (16 rows: 4 KB of 20 a k-block, from L2), and saves the quantiser's launch (one row by 11008 x
+// 4096: 17 us a call with it, 13 without).
+//
 // Warp 0: copies. A stage is 32 KB of the matrix (one bulk copy: its image is what shared memory needs) and
 // the same k-blocks of the rows and of their scales (a copy each; a run of rows is one tile). The matrix does not depend on the
 // kernel before, so the first stages' copies of it go out before this one is waited for. Warp 1: products. Warps
@@ -103,8 +108,11 @@ struct Walk {
 
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(EPI) : "memory"); }
 
-template <bool GATED, int NT>
-__global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant__ QGemmArgs a) {
+constexpr int ROW_TEAM = 128, ROW_TEAMS = 2, ROW_THREADS = ROW_TEAM * ROW_TEAMS;  // beside the others, with ROWS
+
+template <bool GATED, int NT, bool ROWS>
+__global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0), 1)
+    k_qgemm_thin(const __grid_constant__ QGemmArgs a, const __grid_constant__ QRowsArgs in) {
   using C = Thin<GATED, NT>;
   constexpr int P = C::P;
   extern __shared__ uint8_t smem_raw[];
@@ -116,7 +124,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(&ctl.full[s], 1);
+      mbar_init(&ctl.full[s], 1 + (ROWS ? ROW_TEAM / 32 : 0));
       mbar_init(&ctl.empty[s], 1 + EPI / 32);  // the products and the epilogue's warps (scales)
     }
     for (int b = 0; b < C::BUFS; ++b) {
@@ -174,7 +182,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
         bulk_load(st + C::S_OFF, r.s, r.n * C::S_BYTES, &ctl.full[s]);
       };
       uint32_t issued = 0, s = 0, phase = 1;
-      bool ok = true, waited = false;
+      bool ok = true, waited = ROWS;
       for (Walk<NT> g(ctl.groups, a.E, KB, x0, x1); g.more() && ok; g.next()) {
         const uint8_t* w = a.w + g.e * a.w_stride + (static_cast<size_t>(g.t) * KB + g.kb0) * C::W_BYTES;
         Rows r;
@@ -193,10 +201,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
             break;
           }
           r.n = min(C::KS, g.kb1 - kb);
-          mbar_arrive_expect_tx(&ctl.full[s], r.n * (C::W_BYTES + C::X_BYTES + C::S_BYTES));
+          mbar_arrive_expect_tx(&ctl.full[s], r.n * (C::W_BYTES + (ROWS ? 0 : C::X_BYTES + C::S_BYTES)));
           bulk_load(smem + s * C::STAGE, w, r.n * C::W_BYTES, &ctl.full[s]);
           if (waited) {
-            load_rows(r, s);
+            if (!ROWS) load_rows(r, s);
           } else {
 #pragma unroll
             for (int i = 0; i < C::STAGES; ++i)
@@ -256,6 +264,101 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
     volatile int never = 0;
     if (!mbar_wait(&ctl.drain, 0, Q_DRAIN_NS, &never) && leader) fail();
     __syncwarp();
+  } else if (ROWS && warp >= 10) {
+    // ------------------------------------------------------------ rows (warps 10..17): eight lanes to a row, two teams
+    // in turn: a stage takes a team about 1900 cycles from its loads to its arrival, and the matrix comes in 1400
+    pdl_wait();
+    const int team = (threadIdx.x - THREADS) / ROW_TEAM;
+    const int row = ((threadIdx.x - THREADS) & (ROW_TEAM - 1)) >> 3, lane8 = threadIdx.x & 7;
+    const bool mine = row < in.M;
+    // A stage's values: of its two k-blocks, 16 of bf16 each, or of e4m3 in the first half.
+    struct Raw {
+      uint4 v[2][2];
+      float scale[2];
+    };
+    auto load = [&](Raw& raw, int kb, int n) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int k0 = (kb + u) * QB + lane8 * 16;
+        const int n8 = mine && u < n ? min(max((in.K - k0) >> 3, 0), 2) : 0;
+        raw.v[u][0] = raw.v[u][1] = make_uint4(0u, 0u, 0u, 0u);
+        raw.scale[u] = 0.f;
+        if (in.kind == 0) {
+          const uint16_t* p = static_cast<const uint16_t*>(in.x) + static_cast<size_t>(row) * in.ldx + k0;
+          if (n8 > 0) raw.v[u][0] = __ldg(reinterpret_cast<const uint4*>(p));
+          if (n8 > 1) raw.v[u][1] = __ldg(reinterpret_cast<const uint4*>(p + 8));
+        } else {
+          const uint8_t* p = static_cast<const uint8_t*>(in.x) + static_cast<size_t>(row) * in.ldx + k0;
+          if (n8 > 0) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+            raw.v[u][0].x = v.x, raw.v[u][0].y = v.y;
+          }
+          if (n8 > 1) {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(p + 8));
+            raw.v[u][0].z = v.x, raw.v[u][0].w = v.y;
+          }
+          if (mine && u < n) raw.scale[u] = __ldg(in.xs + static_cast<size_t>(row) * in.lds + kb + u);
+        }
+      }
+    };
+    auto write = [&](const Raw& raw, uint8_t* st) {
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint4 q = raw.v[u][0];
+        float sc = raw.scale[u];
+        if (in.kind == 0) {
+          const uint4 a0 = raw.v[u][0], a1 = raw.v[u][1];
+          const uint32_t w[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+          float v[16];
+          float am = __uint_as_float(AMAX_MIN_BITS);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            v[2 * i] = bf16lo(w[i]), v[2 * i + 1] = bf16hi(w[i]);
+            am = max_abs(am, v[2 * i], v[2 * i + 1]);
+          }
+#pragma unroll
+          for (int o = 1; o < 8; o <<= 1) am = max_abs(am, __shfl_xor_sync(0xffffffffu, am, o), 0.f);
+          q = e4m3x16(v, BlockRatio(am));
+          sc = block_scale(am);
+        }
+        if (mine) {
+          *reinterpret_cast<uint4*>(st + C::X_OFF + u * C::X_BYTES + image_at(row, lane8 * 16)) = q;
+          if (lane8 == 0) *reinterpret_cast<float*>(st + C::S_OFF + u * C::S_BYTES + row * 4) = sc;
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the products read what was written here
+    };
+    Raw raw;
+    Walk<NT> g(ctl.groups, a.E, KB, x0, x1);
+    int kb = g.kb0;
+    auto step = [&]() {  // to the next stage
+      kb += C::KS;
+      if (kb >= g.kb1) {
+        g.next();
+        kb = g.kb0;
+      }
+    };
+    uint32_t s = 0, phase = 1;
+    auto ring_step = [&]() {
+      if (++s == C::STAGES) s = 0, phase ^= 1;
+    };
+    bool ok = true;
+    for (int i = 0; i < team && g.more(); ++i) step(), ring_step();
+    if (g.more()) load(raw, kb, g.kb1 - kb);
+    while (g.more()) {
+      ok = __all_sync(0xffffffffu, mbar_wait(&ctl.empty[s], phase, Q_WAIT_NS, abort_flag));
+      if (!ok) break;
+      write(raw, smem + s * C::STAGE);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.full[s]);
+#pragma unroll
+      for (int i = 0; i < ROW_TEAMS; ++i) {
+        ring_step();
+        if (g.more()) step();
+      }
+      if (g.more()) load(raw, kb, g.kb1 - kb);
+    }
+    if (!ok && lane == 0) fail();
   } else {
     // ------------------------------------------------------------ epilogue (warps 2..9)
     pdl_wait();  // what this kernel writes may still be read by the one before
@@ -465,13 +568,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_qgemm_thin(const __grid_constant
   }
 }
 
-template <bool GATED, int NT>
+template <bool GATED, int NT, bool ROWS = false>
 cudaError_t launch(const QGemmArgs& a, cudaStream_t st) {
   using C = Thin<GATED, NT>;
   const size_t smem = C::STAGES * C::STAGE + C::H_BYTES + 1024;
-  cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(&k_qgemm_thin<GATED, NT>), smem);
+  const cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(&k_qgemm_thin<GATED, NT, ROWS>), smem);
   if (e != cudaSuccess) return e;
-  return launch_q(k_qgemm_thin<GATED, NT>, dim3(a.num_sms), THREADS, smem, st, a);
+  return launch_q(k_qgemm_thin<GATED, NT, ROWS>, dim3(a.num_sms), THREADS + (ROWS ? ROW_THREADS : 0), smem, st, a,
+                  ROWS ? *a.rows : QRowsArgs{});
 }
 
 }  // namespace
@@ -480,6 +584,7 @@ cudaError_t launch(const QGemmArgs& a, cudaStream_t st) {
 size_t qgemm_thin_parts(int num_sms, bool gated) { return static_cast<size_t>(2) * num_sms * 128 * 64 * (gated ? 2 : 1); }
 
 cudaError_t launch_qgemm_thin(const QGemmArgs& a, bool gated, cudaStream_t st) {
+  if (a.rows) return launch<false, 16, true>(a, st);
   if (gated) return a.G == 16 ? launch<true, 16>(a, st) : a.G == 32 ? launch<true, 32>(a, st) : launch<true, 64>(a, st);
   return a.G == 16 ? launch<false, 16>(a, st) : a.G == 32 ? launch<false, 32>(a, st) : launch<false, 64>(a, st);
 }

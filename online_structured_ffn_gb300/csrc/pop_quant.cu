@@ -200,14 +200,19 @@ pop_status linear_call(pop_qlinear* h, QRowsArgs in, size_t row_bytes, int M, vo
     part.x = static_cast<const uint8_t*>(in.x) + static_cast<size_t>(m0) * in.ldx * row_bytes;
     if (in.xs) part.xs = in.xs + static_cast<size_t>(m0) * in.lds;
     part.M = n;
-    QRowsOut o{};
-    o.q = h->act;
-    o.s = h->act_s;
-    o.G = G;
-    o.k = 1;
-    cudaError_t e = launch_quantize_rows(part, o, st);
-    if (e != cudaSuccess) return q_cuda(e, call);
     QGemmArgs g{};
+    cudaError_t e = cudaSuccess;
+    if (n <= 16 && G == 16) {
+      g.rows = &part;  // quantised on the way into the product
+    } else {
+      QRowsOut o{};
+      o.q = h->act;
+      o.s = h->act_s;
+      o.G = G;
+      o.k = 1;
+      e = launch_quantize_rows(part, o, st);
+      if (e != cudaSuccess) return q_cuda(e, call);
+    }
     g.act = h->act;
     g.act_s = h->act_s;
     g.G = G;
