@@ -257,9 +257,19 @@ struct Groups {
   int count[POP_QMOE_MAX_EXPERTS];      // rows
   int run0[POP_QMOE_MAX_EXPERTS];       // first run of G rows
 
-  // Group e has ceil(count[e] / rows) * per tiles. Returns their number; all threads of the block call it.
+  // Group e has ceil(count[e] / rows) * per tiles. Returns their number; all threads of the block call it. The rows of
+  // each group are given (counts, run0), or counted here from the experts of all pairs.
   __device__ __forceinline__ int fill(const QGemmArgs& a, int rows, int per) {
-    if (!a.counts) {
+    if (a.experts) {
+      for (int e = threadIdx.x; e < a.E; e += blockDim.x) count[e] = 0;
+      __syncthreads();
+      for (int p = threadIdx.x; p < a.M; p += blockDim.x) {
+        const int e = __ldg(a.experts + p);
+        if (static_cast<unsigned>(e) < static_cast<unsigned>(a.E)) atomicAdd(&count[e], 1);
+      }
+      __syncthreads();
+    }
+    if (!a.counts && !a.experts) {
       if (threadIdx.x == 0) {
         tile0[0] = 0;
         tile0[1] = qceil(a.M, rows) * per;
@@ -268,25 +278,26 @@ struct Groups {
       }
     } else if (threadIdx.x < 32) {
       const int lane = threadIdx.x;
-      int base = 0;
+      int tiles = 0, runs = 0;
       for (int e0 = 0; e0 < a.E; e0 += 32) {
         const int e = e0 + lane;
-        const int c = e < a.E ? __ldcg(a.counts + e) : 0;
-        const int own = qceil(c, rows) * per;
-        int n = own;
+        const int c = e >= a.E ? 0 : a.experts ? count[e] : __ldcg(a.counts + e);
+        const int own_t = qceil(c, rows) * per, own_r = qceil(c, a.G);
+        int t = own_t, r = own_r;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const int v = __shfl_up_sync(0xffffffffu, n, o);
-          if (lane >= o) n += v;
+          const int u = __shfl_up_sync(0xffffffffu, t, o), v = __shfl_up_sync(0xffffffffu, r, o);
+          if (lane >= o) t += u, r += v;
         }
         if (e < a.E) {
-          tile0[e] = base + n - own;
+          tile0[e] = tiles + t - own_t;
           count[e] = c;
-          run0[e] = __ldcg(a.run0 + e);
+          run0[e] = runs + r - own_r;
         }
-        base += __shfl_sync(0xffffffffu, n, 31);
+        tiles += __shfl_sync(0xffffffffu, t, 31);
+        runs += __shfl_sync(0xffffffffu, r, 31);
       }
-      if (lane == 0) tile0[a.E] = base;
+      if (lane == 0) tile0[a.E] = tiles;
     }
     __syncthreads();
     return tile0[a.E];

@@ -50,6 +50,11 @@ struct QRowsOut {
   // image: rows of token t (NULL: row t itself): row_of[t * k + j] for j < k, < 0 for none
   const int* row_of;
   int k;
+  // few pairs: the places are found on the way, from the experts of all pairs, and written to places
+  const int* experts;
+  int E;
+  int* places;
+  unsigned* err;
 };
 cudaError_t launch_quantize_rows(const QRowsArgs& in, const QRowsOut& out, cudaStream_t st);
 
@@ -59,10 +64,12 @@ cudaError_t launch_quantize_rows(const QRowsArgs& in, const QRowsOut& out, cudaS
 cudaError_t launch_pack_matrix(const void* W, const float* Ws, int N, int K, uint8_t* img, float* s, int step,
                                int part, cudaStream_t st);
 
-// Groups the pairs (token, slot) by expert: counts[e], run0[e] (of runs of G rows) and every pair's row,
-// in ascending pair order within an expert; -1 for a pair without an expert.
-cudaError_t launch_plan(const int* experts, int pairs, int E, int G, int* counts, int* run0, int* row_of,
-                        unsigned* err, cudaStream_t st);
+// Groups the pairs (token, slot) by expert: counts[e] and every pair's row, in ascending pair order within an expert,
+// each expert beginning a run of G rows; -1 for a pair without an expert. For up to FEW_PAIRS pairs no kernel of its
+// own is needed: the quantiser finds the places and the products count (a launch and some 4 us less).
+constexpr int FEW_PAIRS = 1024;
+cudaError_t launch_plan(const int* experts, int pairs, int E, int G, int* counts, int* row_of, unsigned* err,
+                        cudaStream_t st);
 
 // y[t] = sum over j of weights[t, j] * o[row_of[t, j]]
 cudaError_t launch_combine(const float* o, const int* row_of, const float* weights, int T, int k, int D, void* y,
@@ -77,10 +84,9 @@ struct QGemmArgs {
   size_t w_stride, ws_stride;
   int N, K;
   int E;                 // groups: experts, or 1
-  const int* counts;     // device [E] rows of each group, or NULL: one group of M rows
-  const int* run0;       // device [E + 1] first run of each group (NULL: 0)
-  int M;                 // rows in all, as far as the host knows: the exact number without counts, else
-                         // the number of pairs
+  const int* counts;     // device [E] rows of each group; or
+  const int* experts;    // device [M] experts of all pairs, which are counted here; both NULL: one group of M rows
+  int M;                 // rows in all, as far as the host knows: the exact number, or the number of pairs
   const QRowsArgs* rows; // thin, one group of up to 16 rows: the rows themselves (kind 0 or 2), which the kernel
                          // quantises on the way instead of taking act and act_s; or NULL
   // outputs. gated: rows in e4m3 for the next product (same G and rows); else y

@@ -20,6 +20,53 @@ __device__ __forceinline__ void unpack8(const void* p, int kind, float* v) {
 // Eight lanes per block of 128, 16 values each. A CTA has 32 blocks: of one row (the blockIdx.y-th 32), or of the
 // `per` whole rows that they hold. Bound by memory and nearly so by its instructions, of which every one counts:
 // 16 values take 4 each for the quotient, half a rounding, one for bf16's unpacking.
+// The places of a CTA's own pairs, [p0, p0 + n) of all, found from the experts of all of them: how many pairs of the
+// same expert come before, and where the expert's rows begin. row[i] is that of pair p0 + i.
+struct Places {
+  int total[POP_QMOE_MAX_EXPERTS], before[POP_QMOE_MAX_EXPERTS];
+  int own[32 * POP_QMOE_MAX_TOP_K], row[32 * POP_QMOE_MAX_TOP_K];
+
+  __device__ __forceinline__ void find(const QRowsOut& out, int pairs, int p0, int n, bool report) {
+    for (int e = threadIdx.x; e < out.E; e += 256) total[e] = before[e] = 0;
+    __syncthreads();
+    for (int p = threadIdx.x; p < pairs; p += 256) {
+      const int e = __ldg(out.experts + p);
+      const bool is = static_cast<unsigned>(e) < static_cast<unsigned>(out.E);
+      if (is) atomicAdd(&total[e], 1);
+      if (is && p < p0) atomicAdd(&before[e], 1);
+      if (p >= p0 && p < p0 + n) own[p - p0] = is ? e : -1;
+      if (report && !is && e != -1) atomicOr(out.err, QERR_EXPERT);
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+      int base = 0;
+      for (int e0 = 0; e0 < out.E; e0 += 32) {
+        const int e = e0 + static_cast<int>(threadIdx.x);
+        const int rows = e < out.E ? qceil(total[e], out.G) * out.G : 0;
+        int s = rows;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, s, o);
+          if (static_cast<int>(threadIdx.x) >= o) s += v;
+        }
+        if (e < out.E) before[e] += base + s - rows;
+        base += __shfl_sync(0xffffffffu, s, 31);
+      }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += 256) {
+      const int e = own[i];
+      int r = -1;
+      if (e >= 0) {
+        r = before[e];
+        for (int j = 0; j < i; ++j) r += own[j] == e ? 1 : 0;
+      }
+      row[i] = r;
+    }
+    __syncthreads();
+  }
+};
+
 template <int KIND>
 __global__ void __launch_bounds__(256) k_quantize_rows(const __grid_constant__ QRowsArgs in, const __grid_constant__ QRowsOut out, int per) {
   // Behind the kernel that places the rows (row_of) x is complete, as that one has waited for it: only the places, and
@@ -68,6 +115,13 @@ __global__ void __launch_bounds__(256) k_quantize_rows(const __grid_constant__ Q
   }
   if (out.row_of) pdl_wait();
   pdl_trigger();
+  __shared__ Places places;
+  if (out.experts) {
+    const int t0 = blockIdx.x * per, n = min(per, in.M - t0) * out.k;
+    places.find(out, in.M * out.k, t0 * out.k, n, blockIdx.x == 0 && blockIdx.y == 0);
+    if (blockIdx.y == 0)
+      for (int i = threadIdx.x; i < n; i += 256) out.places[t0 * out.k + i] = places.row[i];
+  }
   if (!on) return;
   if (out.G == 0) {
     uint8_t* p = out.q + static_cast<size_t>(row) * out.ldq + k0;
@@ -82,7 +136,9 @@ __global__ void __launch_bounds__(256) k_quantize_rows(const __grid_constant__ Q
   }
   const int log_g = 31 - __clz(out.G);
   for (int j = 0; j < out.k; ++j) {
-    const int r = out.row_of ? __ldcg(out.row_of + static_cast<size_t>(row) * out.k + j) : row;
+    const int r = out.experts  ? places.row[(row - blockIdx.x * per) * out.k + j]
+                  : out.row_of ? __ldcg(out.row_of + static_cast<size_t>(row) * out.k + j)
+                               : row;
     if (r < 0) continue;
     const int in_run = r & (out.G - 1);
     const size_t block = static_cast<size_t>(r >> log_g) * KB + kb;
@@ -155,8 +211,8 @@ __global__ void __launch_bounds__(256) k_pack_matrix(const void* __restrict__ W,
 // experts in whole runs), then every warp goes through its pairs again and numbers them, in ascending order.
 constexpr int PLAN_WARPS = 32;
 __global__ void __launch_bounds__(32 * PLAN_WARPS) k_plan(const int* __restrict__ experts, int pairs, int E, int G,
-                                                          int* __restrict__ counts, int* __restrict__ run0,
-                                                          int* __restrict__ row_of, unsigned* __restrict__ err) {
+                                                          int* __restrict__ counts, int* __restrict__ row_of,
+                                                          unsigned* __restrict__ err) {
   __shared__ int s_at[PLAN_WARPS][POP_QMOE_MAX_EXPERTS];
   __shared__ int s_base[POP_QMOE_MAX_EXPERTS / 32];
   constexpr unsigned ALL = 0xffffffffu;
@@ -218,8 +274,6 @@ __global__ void __launch_bounds__(32 * PLAN_WARPS) k_plan(const int* __restrict_
   if (threadIdx.x < POP_QMOE_MAX_EXPERTS) {
     const int x = threadIdx.x;
     for (int w = 0; w < warp; ++w) before += s_base[w];
-    if (x < E) run0[x] = before;
-    if (x == E - 1) run0[E] = before + own;
 #pragma unroll
     for (int w = 0; w < PLAN_WARPS; ++w) s_at[w][x] += before * G;
   }
@@ -299,9 +353,9 @@ cudaError_t launch_pack_matrix(const void* W, const float* Ws, int N, int K, uin
   return cudaGetLastError();
 }
 
-cudaError_t launch_plan(const int* experts, int pairs, int E, int G, int* counts, int* run0, int* row_of,
-                        unsigned* err, cudaStream_t st) {
-  return launch_q(k_plan, dim3(1), 32 * PLAN_WARPS, 0, st, experts, pairs, E, G, counts, run0, row_of, err);
+cudaError_t launch_plan(const int* experts, int pairs, int E, int G, int* counts, int* row_of, unsigned* err,
+                        cudaStream_t st) {
+  return launch_q(k_plan, dim3(1), 32 * PLAN_WARPS, 0, st, experts, pairs, E, G, counts, row_of, err);
 }
 
 cudaError_t launch_combine(const float* o, const int* row_of, const float* weights, int T, int k, int D, void* y,

@@ -143,8 +143,8 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0), 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = ctl.tmem_base;
-  // The groups (of experts) are two kernels back: the one before this waited for them before it let this one
-  // start.
+  // The groups' numbers, or the experts that they are counted from, are two kernels back or more: the kernel before this
+  // waited for them before it let this one start.
   pdl_trigger();
   const int tiles = ctl.groups.fill(a, NT, NTILES);
   const long long work = static_cast<long long>(tiles) * KB;

@@ -96,7 +96,7 @@ struct pop_qmoe {
   pop_qmoe_config cfg;
   uint8_t *wgu = nullptr, *wdn = nullptr;
   float *sgu = nullptr, *sdn = nullptr;
-  int *counts = nullptr, *run0 = nullptr, *row_of = nullptr;
+  int *counts = nullptr, *row_of = nullptr;
   uint8_t *act = nullptr, *h = nullptr;
   float *act_s = nullptr, *h_s = nullptr;
   float* o = nullptr;      // [rows][D] outputs of the experts
@@ -174,7 +174,7 @@ void free_linear(pop_qlinear* h) {
 }
 
 void free_qmoe(pop_qmoe* m) {
-  void* p[] = {m->wgu, m->wdn, m->sgu, m->sdn, m->counts, m->run0, m->row_of, m->act, m->h, m->act_s, m->h_s, m->o, m->parts, m->done, m->err};
+  void* p[] = {m->wgu, m->wdn, m->sgu, m->sdn, m->counts, m->row_of, m->act, m->h, m->act_s, m->h_s, m->o, m->parts, m->done, m->err};
   for (void* q : p) cudaFree(q);
 }
 
@@ -401,7 +401,6 @@ pop_status pop_qmoe_create(const pop_qmoe_config* cfg, const void* const* Wg, co
   if (e == cudaSuccess) e = dalloc(&m->sgu, E * gu_scales + SCALE_PAD);
   if (e == cudaSuccess) e = dalloc(&m->sdn, E * dn_scales + SCALE_PAD);
   if (e == cudaSuccess) e = dalloc(&m->counts, E);
-  if (e == cudaSuccess) e = dalloc(&m->run0, E + 1);
   if (e == cudaSuccess) e = dalloc(&m->row_of, pairs);
   if (e == cudaSuccess) e = dalloc(&m->act, rows * DT * QB);
   if (e == cudaSuccess) e = dalloc(&m->act_s, rows * DT);
@@ -462,15 +461,23 @@ pop_status pop_qmoe_forward(pop_qmoe_t m, const void* x, long long ldx, const in
     const int pairs = n * c.top_k;
     const int G = qmoe_granule(c, n, m->num_sms);
     const int* ex = experts + static_cast<size_t>(t0) * c.top_k;
-    cudaError_t e = launch_plan(ex, pairs, c.n_experts, G, m->counts, m->run0, m->row_of, m->err, st);
+    const bool few = pairs <= FEW_PAIRS;
+    cudaError_t e = few ? cudaSuccess : launch_plan(ex, pairs, c.n_experts, G, m->counts, m->row_of, m->err, st);
     if (e != cudaSuccess) return q_cuda(e, call);
     QRowsArgs in{static_cast<const uint16_t*>(x) + static_cast<size_t>(t0) * ldx, ldx, 0, nullptr, 0, n, c.D};
     QRowsOut o{};
     o.q = m->act;
     o.s = m->act_s;
     o.G = G;
-    o.row_of = m->row_of;
     o.k = c.top_k;
+    if (few) {
+      o.experts = ex;
+      o.E = c.n_experts;
+      o.places = m->row_of;
+      o.err = m->err;
+    } else {
+      o.row_of = m->row_of;
+    }
     e = launch_quantize_rows(in, o, st);
     if (e != cudaSuccess) return q_cuda(e, call);
     QGemmArgs g{};
@@ -484,8 +491,8 @@ pop_status pop_qmoe_forward(pop_qmoe_t m, const void* x, long long ldx, const in
     g.N = c.D_FF;
     g.K = c.D;
     g.E = c.n_experts;
-    g.counts = m->counts;
-    g.run0 = m->run0;
+    g.counts = few ? nullptr : m->counts;
+    g.experts = few ? ex : nullptr;
     g.M = pairs;
     g.h = m->h;
     g.h_s = m->h_s;
