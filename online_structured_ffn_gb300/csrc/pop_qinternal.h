@@ -66,8 +66,10 @@ cudaError_t launch_pack_matrix(const void* W, const float* Ws, int N, int K, uin
 
 // Groups the pairs (token, slot) by expert: counts[e] and every pair's row, in ascending pair order within an expert,
 // each expert beginning a run of G rows; -1 for a pair without an expert. For up to FEW_PAIRS pairs no kernel of its
-// own is needed: the quantiser finds the places and the products count (a launch and some 4 us less).
-constexpr int FEW_PAIRS = 1024;
+// own is needed: the quantiser finds the places and the products count, every CTA for itself (calls of a graph with and
+// without the kernel: one token through 8 experts 70.6 and 66.0 us, 1998 pairs over 64 experts 110.9 and 108.0, 4096
+// over 8 46.8 and 50.3).
+constexpr int FEW_PAIRS = 2048;
 cudaError_t launch_plan(const int* experts, int pairs, int E, int G, int* counts, int* row_of, unsigned* err,
                         cudaStream_t st);
 

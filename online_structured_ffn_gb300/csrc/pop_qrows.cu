@@ -29,13 +29,19 @@ struct Places {
   __device__ __forceinline__ void find(const QRowsOut& out, int pairs, int p0, int n, bool report) {
     for (int e = threadIdx.x; e < out.E; e += 256) total[e] = before[e] = 0;
     __syncthreads();
-    for (int p = threadIdx.x; p < pairs; p += 256) {
-      const int e = __ldg(out.experts + p);
-      const bool is = static_cast<unsigned>(e) < static_cast<unsigned>(out.E);
-      if (is) atomicAdd(&total[e], 1);
-      if (is && p < p0) atomicAdd(&before[e], 1);
-      if (p >= p0 && p < p0 + n) own[p - p0] = is ? e : -1;
-      if (report && !is && e != -1) atomicOr(out.err, QERR_EXPERT);
+    for (int c = threadIdx.x; c < pairs; c += 4 * 256) {
+      int es[4];  // four loads on their way
+#pragma unroll
+      for (int i = 0; i < 4; ++i) es[i] = c + 256 * i < pairs ? __ldg(out.experts + c + 256 * i) : -1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int p = c + 256 * i, e = es[i];
+        const bool is = static_cast<unsigned>(e) < static_cast<unsigned>(out.E);
+        if (is) atomicAdd(&total[e], 1);
+        if (is && p < p0) atomicAdd(&before[e], 1);
+        if (p >= p0 && p < p0 + n) own[p - p0] = is ? e : -1;
+        if (report && !is && e != -1) atomicOr(out.err, QERR_EXPERT);
+      }
     }
     __syncthreads();
     if (threadIdx.x < 32) {

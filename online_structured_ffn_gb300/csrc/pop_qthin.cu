@@ -144,8 +144,7 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0), 1)
   tc_fence_after();
   const uint32_t tmem_base = ctl.tmem_base;
   // The groups' numbers, or the experts that they are counted from, are two kernels back or more: the kernel before this
-  // waited for them before it let this one start.
-  pdl_trigger();
+  // waited for them before it let this one start (as this one does: pdl_trigger comes after a pdl_wait).
   const int tiles = ctl.groups.fill(a, NT, NTILES);
   const long long work = static_cast<long long>(tiles) * KB;
   // CTAs that have a run, G: all, but with few tiles a run is at least sqrt(NT KB / 28) units, as each more CTA of a
@@ -362,6 +361,7 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0), 1)
   } else {
     // ------------------------------------------------------------ epilogue (warps 2..9)
     pdl_wait();  // what this kernel writes may still be read by the one before
+    pdl_trigger();
     constexpr int CW = NT / 2, CH = CW < 16 ? CW : 16;  // rows of the tile that a thread has, and loads at a time
     const int q = warp & 3, n0 = CW * ((warp - 2) >> 2);
     const int f = 32 * q + lane;  // output of the tile

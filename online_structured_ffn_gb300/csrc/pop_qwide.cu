@@ -35,7 +35,7 @@ constexpr int THREADS = 384;
 constexpr int REGS = 168, REGS_COPY = 88, REGS_EPI = 208;
 static_assert(REGS_COPY + 2 * REGS_EPI <= 3 * REGS, "the shares come out of the launch's registers");
 constexpr int BM = 128;
-constexpr int STAGES = 6;
+constexpr int STAGES = 5;
 constexpr uint32_t A_BYTES = QTILE, B_BYTES = QTILE, STAGE = A_BYTES + B_BYTES;
 constexpr uint32_t TMEM_COLS = 512;
 
@@ -46,6 +46,9 @@ struct alignas(16) Scales {
   float x[SB][BM];
   float w[2 * SB];
 };
+
+// Plain: 128 bytes of 32 rows on their way out, of each epilogue warp, behind the ring.
+constexpr uint32_t OUT_BYTES = 8 * 32 * 128;
 
 struct Ctl {
   Scales scales[SRING];
@@ -171,8 +174,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem_base = ctl.tmem_base;
-  pdl_wait();  // the rows, the groups, and what an earlier call's kernels still use
-  pdl_trigger();
+  // The groups' numbers, or the experts that they are counted from, are two kernels back or more: the kernel before this
+  // waited for them before it let this one start (as this one does: pdl_trigger comes after a pdl_wait).
   const int tiles = ctl.groups.fill(a, 2 * BM, per);
 
   auto fail = [&]() {
@@ -189,7 +192,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
       // (lean loops here and below: one thread's instructions follow one another at its latencies, and divisions
       // and 64-bit products once made these take longer than the products)
       uint32_t issued = 0, s = 0, phase = 1;
-      bool ok = true;
+      bool ok = true, waited = false;
       for (Walk v(tiles, pair, pairs, KB); v.more() && ok; v.advance()) {
         const Tile t = tile_at(ctl.groups, a.E, v.tile, rank);
         const uint8_t* xr = a.act + (static_cast<size_t>(t.row0 / BM) * KB + v.kb0) * A_BYTES;
@@ -198,7 +201,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
         const uint8_t* w = a.w + t.e * a.w_stride +
                            (GATED ? ((static_cast<size_t>(t.n) * KB + v.kb0) * 2 + rank)
                                   : static_cast<size_t>(min(2 * t.n + rank, NT - 1)) * KB + v.kb0) * QTILE;
-        for (int kb = v.kb0; kb < v.kb1; ++kb) {
+        int kb = v.kb0;
+        if (!waited) {
+          // the matrix does not depend on the kernel before: the first stages' part of it goes out ahead of the rows
+          const int ahead = min(STAGES, v.kb1 - v.kb0);
+          for (int i = 0; i < ahead; ++i) {
+            mbar_arrive_expect_tx(&ctl.full[i], STAGE);
+            bulk_load(smem + i * STAGE + A_BYTES, w + static_cast<size_t>(i) * (GATED ? 2 * QTILE : QTILE), QTILE, &ctl.full[i]);
+          }
+          pdl_wait();
+          waited = true;
+          for (int i = 0; i < ahead; ++i) bulk_load(smem + i * STAGE, xr + static_cast<size_t>(i) * A_BYTES, A_BYTES, &ctl.full[i]);
+          kb += ahead;
+          xr += static_cast<size_t>(ahead) * A_BYTES;
+          w += static_cast<size_t>(ahead) * (GATED ? 2 * QTILE : QTILE);
+          issued = ahead;
+          s = ahead;
+          if (s == STAGES) s = 0, phase ^= 1;
+        }
+        for (; kb < v.kb1; ++kb) {
           if (!mbar_wait(&ctl.empty[s], phase, Q_WAIT_NS, abort_flag)) {
             fail();
             ok = false;
@@ -268,6 +289,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
       // ---------------------------------------------------------- scales (one thread). Not loads of the
       // epilogue's own: its arrival on tempty would wait for those that are on their way (250 cycles a
       // k-block with four of them every fourth)
+      pdl_wait();  // the rows' scales
       uint32_t issued = 0, g = 0, phase = 1;
       bool ok = true;
       for (Walk v(tiles, pair, pairs, KB); v.more() && ok; v.advance()) {
@@ -312,6 +334,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS_EPI));
     // ------------------------------------------------------------ epilogue (warps 4..11)
+    pdl_wait();  // what this kernel writes may still be read by the one before
+    pdl_trigger();
     const int q = warp & 3, half = (warp - 4) >> 2;
     const int r = 32 * q + lane;  // row of the tile
     // this thread's columns: two runs of 64, of either CTA's part of the matrix tile. Gated: gate and up of
@@ -432,43 +456,57 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
           }
           if (half == 0) a.h_s[(static_cast<size_t>(row / BM) * NT + t.n) * BM + r] = block_scale(am);
         }
-      } else if (valid) {
+      } else {
+        // Through shared memory, 128 bytes of each of the warp's 32 rows at a time: then eight lanes have a row's, and a
+        // store is four whole lines. As 32 bytes of every lane's own row it was 32 pieces of lines (256 fp32 columns,
+        // 3.1 us a tile).
+        uint4(*buf)[8] = reinterpret_cast<uint4(*)[8]>(smem + STAGES * STAGE + (warp - 4) * (32 * 128));
+        const int size = a.out_f32 ? 4 : 2, n16 = a.out_f32 ? 2 : 1;  // bytes of a value, 128-byte pieces of 64 columns
+        const bool even = a.ldy * size % 16 == 0 && reinterpret_cast<uintptr_t>(a.y) % 16 == 0;
 #pragma unroll
         for (int part = 0; part < 2; ++part) {
           const int col = 256 * t.n + 128 * part + 64 * half;
           const int cols = min(64, a.N - col);
-          const size_t o = static_cast<size_t>(row) * a.ldy + col;
+          if (cols <= 0) break;
           const float2* v = acc + 32 * part;
-          if (a.out_f32) {
-            float* y = static_cast<float*>(a.y) + o;
-            if (cols == 64 && (reinterpret_cast<uintptr_t>(y) & 31) == 0) {
+          if (even && cols == 64) {
+            uint8_t* y = static_cast<uint8_t*>(a.y) + (static_cast<size_t>(t.row0 + 32 * q) * a.ldy + col) * size;
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const float2* w = v + 4 * j;
-                st_sector(y + 8 * j,
-                          make_uint4(__float_as_uint(w[0].x), __float_as_uint(w[0].y), __float_as_uint(w[1].x), __float_as_uint(w[1].y)),
-                          make_uint4(__float_as_uint(w[2].x), __float_as_uint(w[2].y), __float_as_uint(w[3].x), __float_as_uint(w[3].y)));
+            for (int c = 0; c < 2; ++c) {
+              if (c >= n16) break;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                uint4 w;
+                if (a.out_f32) {
+                  const float2 p0 = v[16 * c + 2 * i], p1 = v[16 * c + 2 * i + 1];
+                  w = make_uint4(__float_as_uint(p0.x), __float_as_uint(p0.y), __float_as_uint(p1.x), __float_as_uint(p1.y));
+                } else {
+                  const float2* p = v + 4 * i;
+                  w = make_uint4(pack_bf16x2(p[0].x, p[0].y), pack_bf16x2(p[1].x, p[1].y), pack_bf16x2(p[2].x, p[2].y),
+                                 pack_bf16x2(p[3].x, p[3].y));
+                }
+                buf[lane][i ^ (lane & 7)] = w;
               }
-            } else {
+              __syncwarp();
 #pragma unroll
-              for (int j = 0; j < 32; ++j) {
+              for (int i = 0; i < 8; ++i) {
+                const int row = 4 * i + (lane >> 3), piece = lane & 7;
+                if (32 * q + row < t.rows)
+                  *reinterpret_cast<uint4*>(y + static_cast<size_t>(row) * a.ldy * size + 128 * c + 16 * piece) =
+                      buf[row][piece ^ (row & 7)];
+              }
+              __syncwarp();
+            }
+          } else if (valid) {
+            const size_t o = static_cast<size_t>(row) * a.ldy + col;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              if (a.out_f32) {
+                float* y = static_cast<float*>(a.y) + o;
                 if (2 * j < cols) y[2 * j] = v[j].x;
                 if (2 * j + 1 < cols) y[2 * j + 1] = v[j].y;
-              }
-            }
-          } else {
-            uint16_t* y = static_cast<uint16_t*>(a.y) + o;
-            if (cols == 64 && (reinterpret_cast<uintptr_t>(y) & 31) == 0) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                uint32_t w[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(v[8 * j + i].x, v[8 * j + i].y);
-                st_sector(y + 16 * j, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]));
-              }
-            } else {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) {
+              } else {
+                uint16_t* y = static_cast<uint16_t*>(a.y) + o;
                 const uint32_t w = pack_bf16x2(v[j].x, v[j].y);
                 if (2 * j < cols) y[2 * j] = static_cast<uint16_t>(w);
                 if (2 * j + 1 < cols) y[2 * j + 1] = static_cast<uint16_t>(w >> 16);
@@ -493,7 +531,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
 size_t qgemm_wide_parts(int num_sms) { return static_cast<size_t>(2) * num_sms * 256 * BM; }
 
 cudaError_t launch_qgemm_wide(const QGemmArgs& a, bool gated, cudaStream_t st) {
-  const size_t smem = STAGES * STAGE + 1024;
+  const size_t smem = STAGES * STAGE + (gated ? 0 : OUT_BYTES) + 1024;
   const void* k = gated ? reinterpret_cast<const void*>(&k_qgemm_wide<true>) : reinterpret_cast<const void*>(&k_qgemm_wide<false>);
   const cudaError_t e = ensure_dyn_smem(k, smem);
   if (e != cudaSuccess) return e;
