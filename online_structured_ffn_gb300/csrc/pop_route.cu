@@ -1,11 +1,23 @@
 // Routing of tokens to experts (include/pop_route.h): scores, bias, groups, the k best, weights.
 //
-// L lanes per token (1 to 16, a power of two) with V = 8 or 16 neighbouring experts each, so that among equal
-// values the lowest lane, and in it the lowest place, is the lower expert. A choice value is kept as an
-// unsigned key in the order of the floats (0: cannot be chosen). k times: the largest of the lanes' best keys, the
-// first lane that has it, which writes it down and looks for its next best. The chosen scores are computed
-// at the end, from the keys or (with a bias) the logits again, a lane each, so that the loop carries keys alone.
-// What bounds it is the instructions: some 200 a token for 100 experts and k = 6.
+// L lanes per token (1 to 32, a power of two) with V neighbouring experts each, so that among equal values the
+// lowest lane, and in it the lowest place, is the lower expert. A choice value is kept as an unsigned key in
+// the order of the floats (0: cannot be chosen). A lane sorts its keys in fours. k times: the largest of the
+// lanes' first keys; the first lane that has it writes it down and moves up what stands behind it. At the end the
+// chosen have a lane each, which finds the place of its key among all (they stand in shared memory) and computes the
+// score, from the key or (with a bias) the logit again, so that the loop carries keys alone.
+//
+// UNIQUE: a bf16 logit fills half a key, and where the logits are the order (softmax without a bias) the other half
+// holds the expert, from the top down. Then no two keys are equal and the largest key names its expert: there is no
+// first lane and no place to find.
+//
+// What bounds it: few tokens, the k dependent steps (32 tokens, 256 experts in 8 groups, k = 8: 3.9 us; 8 experts,
+// k = 2: 2.1); many, the instructions. 65,536 tokens, k = 6: 100 experts 11.6 us from bf16 (1.4 TB/s; 25 with keys of
+// the other kind), 19.3 from float32 (1.5 TB/s); 64 experts 12.4. 256 experts in 8 groups, sigmoid and bias, k = 8: 4096
+// tokens 7.0 us, 65,536 tokens 70 us. From 129 experts on a token has a whole warp, which finds its
+// largest key in one instruction (16 lanes with 16 experts: 8.7 us for 4096 tokens); below that a warp has
+// several tokens (a warp each: 65,536 x 100 from bf16 20.1 us instead of 11.6, float32 35 instead of 19, and less than 1 us
+// gained for 64 tokens).
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -69,14 +81,22 @@ __device__ __forceinline__ void load_logits(const void* p, long long at, int n, 
   }
 }
 
+// The bias of a lane's experts.
+template <int V, bool VEC>
+__device__ __forceinline__ void load_bias(const float* p, int n, float (&b)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; i += VEC ? 4 : 1) {
+    if (VEC) {
+      const float4 v = i < n ? __ldg(reinterpret_cast<const float4*>(p + i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      b[i] = v.x, b[i + 1] = v.y, b[i + 2] = v.z, b[i + 3] = v.w;
+    } else {
+      b[i] = i < n ? __ldg(p + i) : 0.f;
+    }
+  }
+}
+
 constexpr unsigned ALL = 0xffffffffu;
 
-template <int L>
-__device__ __forceinline__ float lanes_max(float v) {
-#pragma unroll
-  for (int o = L / 2; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(ALL, v, o));
-  return v;
-}
 template <int L>
 __device__ __forceinline__ float lanes_sum(float v) {
 #pragma unroll
@@ -85,9 +105,13 @@ __device__ __forceinline__ float lanes_sum(float v) {
 }
 template <int L>
 __device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  if constexpr (L == 32) {
+    return __reduce_max_sync(ALL, v);
+  } else {
 #pragma unroll
-  for (int o = L / 2; o; o >>= 1) v = max(v, __shfl_xor_sync(ALL, v, o));
-  return v;
+    for (int o = L / 2; o; o >>= 1) v = max(v, __shfl_xor_sync(ALL, v, o));
+    return v;
+  }
 }
 template <int V>
 __device__ __forceinline__ uint32_t best_of(const uint32_t (&key)[V]) {
@@ -104,13 +128,57 @@ __device__ __forceinline__ void merge2(uint32_t& a1, uint32_t& a2, uint32_t b1, 
   a2 = max(lo, max(a2, b2));
 }
 
-template <bool BF16, int L, int V, bool VEC>
+// Larger first.
+__device__ __forceinline__ void order(uint32_t& a, uint32_t& b) {
+  const uint32_t lo = min(a, b);
+  a = max(a, b);
+  b = lo;
+}
+
+// Unique keys: the logit's bits, in order, above 0xffff - expert. Smaller ones than this cannot be chosen (NaN
+// counts as -infinity, and -infinity's bits become 0x007f).
+constexpr uint32_t UNIQUE_LIVE = 0x00800000u;
+
+__device__ __forceinline__ float unique_float(uint32_t key) {
+  return fminf(key_float(key >= 0x80000000u ? key & 0xffff0000u : key | 0xffffu), 3.402823466e38f);
+}
+
+// The keys of a lane's V logits, of experts from e0 on, n of which there are.
+template <int V, bool VEC>
+__device__ __forceinline__ void unique_keys(const void* p, long long at, int e0, int n, uint32_t (&key)[V]) {
+  const uint16_t* l = static_cast<const uint16_t*>(p) + at;
+#pragma unroll
+  for (int i = 0; i < V; i += 4) {
+    uint32_t w[2] = {0xff80ff80u, 0xff80ff80u};  // -infinity
+    if (VEC) {
+      if (i < n) {
+        const uint2 u = __ldg(reinterpret_cast<const uint2*>(l + i));
+        w[0] = u.x, w[1] = u.y;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i + j < n) w[j / 2] = __byte_perm(w[j / 2], __ldg(l + i + j), j % 2 ? 0x5410 : 0x3254);
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      // NaN to -infinity, -0 to 0
+      asm("max.bf16x2 %0, %0, %1;\n\tadd.rn.bf16x2 %0, %0, %2;" : "+r"(w[j]) : "r"(0xff80ff80u), "r"(0u));
+      const uint32_t u = w[j] ^ 0x80008000u ^ ((w[j] >> 15 & 0x00010001u) * 0x7fffu);
+      const uint32_t x = 0xffffu - static_cast<uint32_t>(e0 + i + 2 * j);
+      key[i + 2 * j] = __byte_perm(u, x, 0x1054);
+      key[i + 2 * j + 1] = __byte_perm(u, x - 1u, 0x3254);
+    }
+  }
+}
+
+template <bool BF16, bool UNIQUE, int L, int V, bool VEC>
 __global__ void __launch_bounds__(32 * RT_WARPS) k_route(const __grid_constant__ RouteArgs a) {
   constexpr int TOK = 32 / L;  // tokens of a warp
-  __shared__ uint32_t s_key[RT_WARPS][TOK][POP_ROUTE_MAX_TOP_K];  // the chosen: keys, then scores
-  __shared__ int s_e[RT_WARPS][TOK][POP_ROUTE_MAX_TOP_K];
-  __shared__ float s_top[RT_WARPS][TOK], s_sum[RT_WARPS][TOK];
-  __shared__ uint32_t s_all[RT_WARPS][TOK][L * V], s_grp[RT_WARPS][TOK][L * V];
+  constexpr int K = L * V < POP_ROUTE_MAX_TOP_K ? L * V : POP_ROUTE_MAX_TOP_K;
+  __shared__ uint32_t s_key[RT_WARPS][TOK][K];  // the chosen: keys, then scores
+  __shared__ int s_e[RT_WARPS][TOK][K];         // lanes and which of equal keys, then experts
+  __shared__ uint32_t s_all[RT_WARPS][V][32], s_grp[RT_WARPS][TOK][L * V];  // (all keys: place, lane)
   __shared__ int s_count[POP_ROUTE_MAX_EXPERTS];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane & (L - 1), tok = lane / L;
@@ -123,26 +191,35 @@ __global__ void __launch_bounds__(32 * RT_WARPS) k_route(const __grid_constant__
   const int e0 = sub * V;
   uint32_t key[V];
   float top = 0.f, sum = 1.f;
-  {
+  if (UNIQUE) {
+    unique_keys<V, VEC>(a.logits, t * a.ld + e0, e0, a.E - e0, key);
+    if (!a.renorm) {  // (renormalised weights do not depend on the sum)
+      top = unique_float(lanes_max<L>(best_of(key)));
+      sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum += key[i] >= UNIQUE_LIVE ? expf(unique_float(key[i]) - top) : 0.f;
+      sum = lanes_sum<L>(sum);
+    }
+  } else {
     float l[V];
     load_logits<BF16, V, VEC>(a.logits, t * a.ld + e0, a.E - e0, l);
+    float bias[V];
+    if (a.bias) load_bias<V, VEC>(a.bias + e0, a.E - e0, bias);
     if (a.sigmoid) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         key[i] = 0u;
         if (l[i] != -INFINITY) {
           const float p = __frcp_rn(1.f + expf(-l[i]));
-          key[i] = choice_key(a.bias ? p + __ldg(a.bias + e0 + i) : p);
+          key[i] = choice_key(a.bias ? p + bias[i] : p);
         }
       }
     } else {
-      top = l[0];
-#pragma unroll
-      for (int i = 1; i < V; ++i) top = fmaxf(top, l[i]);
-      top = lanes_max<L>(top);
 #pragma unroll
       for (int i = 0; i < V; ++i) key[i] = choice_key(l[i]);
-      if (a.bias || !a.renorm) {  // (renormalised weights do not depend on the sum)
+      const uint32_t m = lanes_max<L>(best_of(key));
+      top = m ? key_float(m) : 0.f;
+      if (a.bias || !a.renorm) {
         sum = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -154,7 +231,7 @@ __global__ void __launch_bounds__(32 * RT_WARPS) k_route(const __grid_constant__
       if (a.bias) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-          if (key[i]) key[i] = choice_key(l[i] / sum + __ldg(a.bias + e0 + i));
+          if (key[i]) key[i] = choice_key(l[i] / sum + bias[i]);
       }
     }
   }
@@ -181,13 +258,14 @@ __global__ void __launch_bounds__(32 * RT_WARPS) k_route(const __grid_constant__
         for (int i = 0; i < V; ++i) key[i] = 0u;
       }
     } else {
-      uint32_t *sk = s_all[warp][tok], *sg = s_grp[warp][tok];
+      uint32_t(*sk)[32] = s_all[warp], *sg = s_grp[warp][tok];
+      const int l0 = lane - sub;
 #pragma unroll
-      for (int i = 0; i < V; ++i) sk[e0 + i] = key[i];
+      for (int i = 0; i < V; ++i) sk[i][lane] = key[i];
       __syncwarp();
       for (int g = sub; g < a.G; g += L) {
         uint32_t k1 = 0, k2 = 0;
-        for (int j = 0; j < per; ++j) merge2(k1, k2, sk[g * per + j], 0u);
+        for (int e = g * per; e < (g + 1) * per; ++e) merge2(k1, k2, sk[e % V][l0 + e / V], 0u);
         if (a.group_sum == 2 && k2) k1 = float_key(key_float(k1) + key_float(k2) + 0.f);
         sg[g] = k1;
       }
@@ -197,67 +275,91 @@ __global__ void __launch_bounds__(32 * RT_WARPS) k_route(const __grid_constant__
         const int g = min(e0 + i, a.E - 1) / per;
         int before = 0;
         for (int j = 0; j < a.G; ++j) before += (sg[j] > sg[g] || (sg[j] == sg[g] && j < g)) ? 1 : 0;
-        if (before >= a.top_groups) sk[e0 + i] = 0u;
+        if (before >= a.top_groups) sk[i][lane] = 0u;
       }
-      __syncwarp();
 #pragma unroll
-      for (int i = 0; i < V; ++i) key[i] = sk[e0 + i];
+      for (int i = 0; i < V; ++i) key[i] = sk[i][lane];
     }
   }
-  uint32_t best = best_of(key);
+  if (!UNIQUE) {  // for the places of the chosen
+#pragma unroll
+    for (int i = 0; i < V; ++i) s_all[warp][i][lane] = key[i];
+  }
+#pragma unroll
+  for (int i = 0; i < V; i += 4) {
+    order(key[i], key[i + 1]), order(key[i + 2], key[i + 3]);
+    order(key[i], key[i + 2]), order(key[i + 1], key[i + 3]);
+    order(key[i + 1], key[i + 2]);
+  }
+  uint32_t last = 0;
+  int equal = 0;  // keys equal to the one a lane gave last that it had given before
 #pragma unroll 1
   for (int j = 0; j < a.k; ++j) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int i = 4; i < V; i += 4) best = max(best, key[i]);
     const uint32_t m = lanes_max<L>(best);
-    unsigned has = __ballot_sync(ALL, best == m);
-    if (L < 32) has &= ((1u << (L & 31)) - 1u) << (lane & ~(L - 1));
-    if (lane == __ffs(has) - 1) {
-      unsigned hits = 0;
+    bool mine = UNIQUE;
+    if (!UNIQUE) {
+      unsigned has = __ballot_sync(ALL, best == m);
+      if (L < 32) has &= ((1u << (L & 31)) - 1u) << (lane & ~(L - 1));
+      mine = lane == __ffs(has) - 1;
+    }
+    if (UNIQUE ? sub == 0 : mine) s_key[warp][tok][j] = m;
+    if (!UNIQUE && mine) {
+      equal = m == last ? equal + 1 : 0;
+      last = m;
+      s_e[warp][tok][j] = lane | equal << 8;
+    }
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (key[i] == m) hits |= 1u << i, key[i] = 0u;
-      const int at = __ffs(hits) - 1;
-      hits &= hits - 1;
-      if (hits && m) {  // a tie within the lane: the others stay
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (hits >> i & 1u) key[i] = m;
+    for (int i = 0; i < V; i += 4) {
+      if (mine && key[i] == m) {
+        key[i] = key[i + 1], key[i + 1] = key[i + 2], key[i + 2] = key[i + 3], key[i + 3] = 0u;
+        if (!UNIQUE) mine = false;
       }
-      best = best_of(key);
-      s_key[warp][tok][j] = m;
-      s_e[warp][tok][j] = m ? e0 + at : -1;
     }
   }
-  if (sub == 0) s_top[warp][tok] = top, s_sum[warp][tok] = sum;
   __syncwarp();
-  // the scores of the chosen, a lane each
-  const int n = min(TOK, a.T - t0) * a.k;
-  for (int o = lane; o < n; o += 32) {
-    const int u = o / a.k, j = o - u * a.k;
-    const uint32_t m = s_key[warp][u][j];
+  // the chosen, a lane each: scores, then weights
+  const bool live = t0 + tok < a.T;
+  if (UNIQUE) top = unique_float(s_key[warp][tok][0]);
+  __syncwarp();  // (the first one's key becomes a score)
+  float total = 0.f;
+  for (int j = sub; j < a.k; j += L) {
+    const uint32_t m = s_key[warp][tok][j];
     float w = 0.f;
-    if (m) {
-      float v = key_float(m);
-      if (a.bias) v = live_logit(load_logit<BF16>(a.logits, (t0 + u) * a.ld + s_e[warp][u][j]));
-      if (!a.sigmoid)
-        w = expf(v - s_top[warp][u]) / s_sum[warp][u];
-      else
-        w = a.bias ? __frcp_rn(1.f + expf(-v)) : v;
+    if (UNIQUE) {
+      if (m >= UNIQUE_LIVE) w = expf(unique_float(m) - top) / sum;
+      s_e[warp][tok][j] = m >= UNIQUE_LIVE ? static_cast<int>(0xffffu - (m & 0xffffu)) : -1;
+    } else {
+      int e = -1;
+      if (m) {
+        const int from = s_e[warp][tok][j];
+        unsigned hits = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) hits |= s_all[warp][i][from & 31] == m ? 1u << i : 0u;
+        for (int i = from >> 8; i; --i) hits &= hits - 1;
+        e = (from & (L - 1)) * V + __ffs(hits) - 1;
+        float v = key_float(m);
+        if (a.bias) v = live_logit(load_logit<BF16>(a.logits, t * a.ld + e));
+        if (!a.sigmoid)
+          w = expf(v - top) / sum;
+        else
+          w = a.bias ? __frcp_rn(1.f + expf(-v)) : v;
+      }
+      s_e[warp][tok][j] = e;
     }
-    s_key[warp][u][j] = __float_as_uint(w);
+    s_key[warp][tok][j] = __float_as_uint(w);
+    total += w;
   }
-  __syncwarp();
-  const size_t out = static_cast<size_t>(t0) * a.k;
-  for (int o = lane; o < n; o += 32) {
-    const int u = o / a.k, j = o - u * a.k;
-    const int e = s_e[warp][u][j];
-    float w = __uint_as_float(s_key[warp][u][j]);
-    if (a.renorm) {
-      float total = 0.f;
-      for (int i = 0; i < a.k; ++i) total += __uint_as_float(s_key[warp][u][i]);
-      w = total > 0.f ? w / total : 0.f;
-    }
-    a.experts[out + o] = e;
-    a.weights[out + o] = w * a.scale;
+  total = lanes_sum<L>(total);
+  for (int j = sub; j < a.k && live; j += L) {
+    const int e = s_e[warp][tok][j];
+    float w = __uint_as_float(s_key[warp][tok][j]);
+    if (a.renorm) w = total > 0.f ? w / total : 0.f;
+    const size_t at = static_cast<size_t>(t) * a.k + j;
+    a.experts[at] = e;
+    a.weights[at] = w * a.scale;
     if (a.counts && e >= 0) atomicAdd(&s_count[e], 1);
   }
   if (a.counts) {
@@ -267,26 +369,27 @@ __global__ void __launch_bounds__(32 * RT_WARPS) k_route(const __grid_constant__
   }
 }
 
-template <bool BF16, int L, int V>
+template <bool BF16, bool UNIQUE, int L, int V>
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t st) {
   const int grid = (a.T + 32 / L * RT_WARPS - 1) / (32 / L * RT_WARPS);
-  // four logits a load where rows and runs of four start on such a boundary and end with the experts
-  const bool vec = a.E % 4 == 0 && a.ld % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % (BF16 ? 8 : 16) == 0;
+  // four values a load where rows and runs of four start on such a boundary and end with the experts
+  const bool vec = a.E % 4 == 0 && a.ld % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % (BF16 ? 8 : 16) == 0 &&
+                   reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
   if (vec)
-    k_route<BF16, L, V, true><<<grid, 32 * RT_WARPS, 0, st>>>(a);
+    k_route<BF16, UNIQUE, L, V, true><<<grid, 32 * RT_WARPS, 0, st>>>(a);
   else
-    k_route<BF16, L, V, false><<<grid, 32 * RT_WARPS, 0, st>>>(a);
+    k_route<BF16, UNIQUE, L, V, false><<<grid, 32 * RT_WARPS, 0, st>>>(a);
   return cudaGetLastError();
 }
 
-template <bool BF16>
+template <bool BF16, bool UNIQUE>
 cudaError_t launch_route(const RouteArgs& a, cudaStream_t st) {
-  if (a.E <= 8) return launch_route<BF16, 1, 8>(a, st);
-  if (a.E <= 16) return launch_route<BF16, 1, 16>(a, st);
-  if (a.E <= 32) return launch_route<BF16, 2, 16>(a, st);
-  if (a.E <= 64) return launch_route<BF16, 4, 16>(a, st);
-  if (a.E <= 128) return launch_route<BF16, 8, 16>(a, st);
-  return launch_route<BF16, 16, 16>(a, st);
+  if (a.E <= 8) return launch_route<BF16, UNIQUE, 1, 8>(a, st);
+  if (a.E <= 16) return launch_route<BF16, UNIQUE, 1, 16>(a, st);
+  if (a.E <= 32) return launch_route<BF16, UNIQUE, 2, 16>(a, st);
+  if (a.E <= 64) return launch_route<BF16, UNIQUE, 4, 16>(a, st);
+  if (a.E <= 128) return launch_route<BF16, UNIQUE, 8, 16>(a, st);
+  return launch_route<BF16, UNIQUE, 32, 8>(a, st);
 }
 
 thread_local std::string g_route_msg;
@@ -340,7 +443,12 @@ pop_status pop_route(const pop_route_config* cfg, const void* logits, int logits
   RouteArgs a{logits,       ld_logits,   bias,     T,       c.n_experts, c.top_k, c.score == POP_ROUTE_SIGMOID,
               c.n_groups,   c.top_groups, c.group_sum, c.renorm, c.scale,     experts, weights,
               counts};
-  e = logits_bf16 ? launch_route<true>(a, st) : launch_route<false>(a, st);
+  if (!logits_bf16)
+    e = launch_route<false, false>(a, st);
+  else if (a.sigmoid || a.bias)
+    e = launch_route<true, false>(a, st);
+  else
+    e = launch_route<true, true>(a, st);
   return e == cudaSuccess ? POP_OK : route_fail(POP_ERR_CUDA, cudaGetErrorString(e));
 }
 
