@@ -243,6 +243,22 @@ __device__ __forceinline__ void fma2(float2& a, float dx, float dy, float f) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(s));
 }
 
+// ... with a factor for each, of float bits: a += d * f; and such factors, s times (x, y).
+__device__ __forceinline__ void fma2(float2& a, uint32_t dx, uint32_t dy, uint64_t f) {
+  uint64_t v, s;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(dx), "r"(dy));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(s) : "f"(a.x), "f"(a.y));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(s) : "l"(v), "l"(f));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(s));
+}
+__device__ __forceinline__ uint64_t mul2(float s, float x, float y) {
+  uint64_t v, w;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(w) : "f"(s));
+  asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(v) : "l"(w));
+  return v;
+}
+
 // 32 bytes, aligned to 32, in one store.
 __device__ __forceinline__ void st_sector(void* p, uint4 lo, uint4 hi) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(lo.x), "r"(lo.y), "r"(lo.z), "r"(lo.w),

@@ -28,10 +28,12 @@ cudaError_t ensure_dyn_smem(const void* kernel, size_t bytes);
 
 namespace {
 
-constexpr int THREADS = 320, EPI = 256;
-constexpr uint32_t RING_BYTES = 208 * 1024;
+constexpr int THREADS = 320, EPI = 256, HAND = 32;
+constexpr uint32_t RING_BYTES = 220 * 1024;
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int MAX_STAGES = 8, MAX_BUFS = 8;
+// More in flight is slower, not faster (8 x 2 x 14336 x 4096: 132 us with 4 stages, 135 with 5, 134 with 3; 64 x 2 x 1000 x
+// 2048 with 64 rows 50.3, 50.3 and 49.7).
+constexpr int MAX_STAGES = 4, MAX_BUFS = 8;
 
 template <bool GATED, int NT>
 struct Thin {
@@ -40,20 +42,31 @@ struct Thin {
   static constexpr uint32_t W_BYTES = P * QTILE;    // of a k-block
   static constexpr uint32_t X_BYTES = NT * QB;      // of a k-block's rows: one run of NT
   static constexpr uint32_t S_BYTES = NT * 4;       // of their scales
-  static constexpr uint32_t X_OFF = KS * W_BYTES, S_OFF = X_OFF + KS * X_BYTES;
-  static constexpr uint32_t STAGE = (S_OFF + KS * S_BYTES + 1023) / 1024 * 1024;
+  static constexpr uint32_t X_OFF = KS * W_BYTES;
+  static constexpr uint32_t STAGE = X_OFF + KS * X_BYTES;
   static constexpr uint32_t H_BYTES = NT * QB * 4;  // a finished tile on its way out
-  static constexpr int STAGES = (RING_BYTES - H_BYTES) / STAGE;
+  static constexpr int FIT = (RING_BYTES - H_BYTES) / STAGE;
+  static constexpr int STAGES = FIT < MAX_STAGES ? FIT : MAX_STAGES;
   static constexpr int BUFS = static_cast<int>(TMEM_COLS) / (2 * NT) < MAX_BUFS ? static_cast<int>(TMEM_COLS) / (2 * NT) : MAX_BUFS;
+  // The rows' scales have a ring of their own, as the epilogue needs them for longer than the products need a stage.
+  // A stage's products wait for the buffer BUFS before, and its copies for the products STAGES before, so what a slot
+  // held SLOTS stages ago has been read.
+  static constexpr int SLOTS = STAGES + BUFS;
+  static constexpr uint32_t SLOT = KS * S_BYTES;
+  static constexpr uint32_t S_OFF = STAGES * STAGE + H_BYTES;  // of the slots, behind the ring and the tile
+  static constexpr uint32_t SMEM = S_OFF + SLOTS * SLOT + 1024;
+  static_assert(STAGE % 1024 == 0 && STAGES <= MAX_STAGES, "images start on 1 KB");
 };
 
 struct Ctl {
   uint64_t full[MAX_STAGES], empty[MAX_STAGES];
+  uint64_t sfull[MAX_STAGES + MAX_BUFS];
   uint64_t tfull[MAX_BUFS], tempty[MAX_BUFS];
   uint64_t drain;
   uint32_t tmem_base;
   int abort_flag;
   int last;
+  int late, late_tile, late_t, late_rows, late_run;  // a first part: whether it was its tile's last, and the tile
   Groups groups;
 };
 
@@ -108,13 +121,33 @@ struct Walk {
 
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(EPI) : "memory"); }
 
+// Barriers 2 (a first part is written) and 3 (it is handed in) of the epilogue's warps and the one that hands it in.
+template <int B>
+__device__ __forceinline__ void hand_sync() { asm volatile("bar.sync %0, %1;" ::"n"(B), "n"(EPI + 32) : "memory"); }
+template <int B>
+__device__ __forceinline__ void hand_arrive() { asm volatile("bar.arrive %0, %1;" ::"n"(B), "n"(EPI + 32) : "memory"); }
+
+// The quotient of two numbers that are not negative, b > 0: by 32 bits where those hold them.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+}
+
+// One more part of a tile is there, written by threads that have met at a barrier. Whether it was the last of `parts`.
+__device__ __forceinline__ bool hand_in(unsigned* done, int parts) {
+  __threadfence();
+  const bool last = atomicAdd(done, 1u) == static_cast<unsigned>(parts - 1);
+  __threadfence();
+  if (last) *done = 0;
+  return last;
+}
+
 constexpr int ROW_TEAM = 128, ROW_TEAMS = 2, ROW_THREADS = ROW_TEAM * ROW_TEAMS;  // beside the others, with ROWS
 
 template <bool GATED, int NT, bool ROWS>
-__global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0), 1)
+__global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0) + HAND, 1)
     k_qgemm_thin(const __grid_constant__ QGemmArgs a, const __grid_constant__ QRowsArgs in) {
   using C = Thin<GATED, NT>;
-  constexpr int P = C::P;
+  constexpr int P = C::P, HAND_WARP = (THREADS + (ROWS ? ROW_THREADS : 0)) / 32;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Ctl ctl;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -125,8 +158,9 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0), 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&ctl.full[s], 1 + (ROWS ? ROW_TEAM / 32 : 0));
-      mbar_init(&ctl.empty[s], 1 + EPI / 32);  // the products and the epilogue's warps (scales)
+      mbar_init(&ctl.empty[s], 1);
     }
+    for (int i = 0; i < C::SLOTS; ++i) mbar_init(&ctl.sfull[i], ROWS ? ROW_TEAM / 32 : 1);
     for (int b = 0; b < C::BUFS; ++b) {
       mbar_init(&ctl.tfull[b], 1);
       mbar_init(&ctl.tempty[b], EPI / 32);
@@ -159,6 +193,15 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0), 1)
   const bool on = static_cast<long long>(blockIdx.x) < G;
   const long long x0 = on ? work * blockIdx.x / G : 0, x1 = on ? work * (blockIdx.x + 1) / G : 0;
 
+  // The first tile of this run is in others too, and there are more tiles: its part is handed in by a warp of its own.
+  const auto hand = [&]() {
+    const long long tile = quotient(x0, KB);
+    return x0 < x1 && tile * KB != x0 && (tile + 1) * KB < x1;
+  };
+  // The CTAs that share a tile. CTA c holds [work c / G, work (c + 1) / G): the one of unit x is ((x + 1) G - 1) / work.
+  const auto first_cta_of = [&](int tile) { return static_cast<int>(quotient((static_cast<long long>(tile) * KB + 1) * G - 1, work)); };
+  const auto last_cta_of = [&](int tile) { return static_cast<int>(quotient((static_cast<long long>(tile) + 1) * KB * G - 1, work)); };
+
   auto fail = [&]() {
     if (!*abort_flag) {
       *abort_flag = 1;
@@ -175,12 +218,12 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0), 1)
         const float* s;
         int n;  // k-blocks
       } owed[C::STAGES];
-      auto load_rows = [&](const Rows& r, uint32_t s) {
-        uint8_t* st = smem + s * C::STAGE;
-        bulk_load(st + C::X_OFF, r.x, r.n * C::X_BYTES, &ctl.full[s]);
-        bulk_load(st + C::S_OFF, r.s, r.n * C::S_BYTES, &ctl.full[s]);
+      auto load_rows = [&](const Rows& r, uint32_t s, uint32_t slot) {
+        bulk_load(smem + s * C::STAGE + C::X_OFF, r.x, r.n * C::X_BYTES, &ctl.full[s]);
+        mbar_arrive_expect_tx(&ctl.sfull[slot], r.n * C::S_BYTES);
+        bulk_load(smem + C::S_OFF + slot * C::SLOT, r.s, r.n * C::S_BYTES, &ctl.sfull[slot]);
       };
-      uint32_t issued = 0, s = 0, phase = 1;
+      uint32_t issued = 0, s = 0, phase = 1, slot = 0;
       bool ok = true, waited = ROWS;
       for (Walk<NT> g(ctl.groups, a.E, KB, x0, x1); g.more() && ok; g.next()) {
         const uint8_t* w = a.w + g.e * a.w_stride + (static_cast<size_t>(g.t) * KB + g.kb0) * C::W_BYTES;
@@ -192,7 +235,7 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0), 1)
             pdl_wait();
             waited = true;
 #pragma unroll
-            for (int i = 0; i < C::STAGES; ++i) load_rows(owed[i], i);
+            for (int i = 0; i < C::STAGES; ++i) load_rows(owed[i], i, i);
           }
           if (!mbar_wait(&ctl.empty[s], phase, Q_WAIT_NS, abort_flag)) {
             fail();
@@ -200,10 +243,10 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0), 1)
             break;
           }
           r.n = min(C::KS, g.kb1 - kb);
-          mbar_arrive_expect_tx(&ctl.full[s], r.n * (C::W_BYTES + (ROWS ? 0 : C::X_BYTES + C::S_BYTES)));
+          mbar_arrive_expect_tx(&ctl.full[s], r.n * (C::W_BYTES + (ROWS ? 0 : C::X_BYTES)));
           bulk_load(smem + s * C::STAGE, w, r.n * C::W_BYTES, &ctl.full[s]);
           if (waited) {
-            if (!ROWS) load_rows(r, s);
+            if (!ROWS) load_rows(r, s, slot);
           } else {
 #pragma unroll
             for (int i = 0; i < C::STAGES; ++i)
@@ -214,19 +257,24 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0), 1)
           r.s += C::KS * NT;
           ++issued;
           if (++s == C::STAGES) s = 0, phase ^= 1;
+          if (++slot == C::SLOTS) slot = 0;
         }
       }
       if (!waited) {  // a short run: every stage that was begun gets its rows
         pdl_wait();
 #pragma unroll
         for (int i = 0; i < C::STAGES; ++i)
-          if (i < static_cast<int>(issued)) load_rows(owed[i], i);
+          if (i < static_cast<int>(issued)) load_rows(owed[i], i, i);
       }
       // no copy of this CTA may be in flight when it exits
       const uint32_t lo = issued > C::STAGES ? issued - C::STAGES : 0;
       for (uint32_t i = lo; i < issued; ++i) {
         volatile int never = 0;
         if (!mbar_wait(&ctl.full[i % C::STAGES], (i / C::STAGES) & 1u, Q_DRAIN_NS, &never)) fail();
+      }
+      for (uint32_t i = ROWS ? issued : issued > C::SLOTS ? issued - C::SLOTS : 0; i < issued; ++i) {
+        volatile int never = 0;
+        if (!mbar_wait(&ctl.sfull[i % C::SLOTS], (i / C::SLOTS) & 1u, Q_DRAIN_NS, &never)) fail();
       }
     }
     __syncwarp();
@@ -263,7 +311,7 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0), 1)
     volatile int never = 0;
     if (!mbar_wait(&ctl.drain, 0, Q_DRAIN_NS, &never) && leader) fail();
     __syncwarp();
-  } else if (ROWS && warp >= 10) {
+  } else if (ROWS && warp >= 10 && warp < HAND_WARP) {
     // ------------------------------------------------------------ rows (warps 10..17): eight lanes to a row, two teams
     // in turn: a stage takes a team about 1900 cycles from its loads to its arrival, and the matrix comes in 1400
     pdl_wait();
@@ -300,7 +348,7 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0), 1)
         }
       }
     };
-    auto write = [&](const Raw& raw, uint8_t* st) {
+    auto write = [&](const Raw& raw, uint8_t* st, uint8_t* scales) {
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         uint4 q = raw.v[u][0];
@@ -322,7 +370,7 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0), 1)
         }
         if (mine) {
           *reinterpret_cast<uint4*>(st + C::X_OFF + u * C::X_BYTES + image_at(row, lane8 * 16)) = q;
-          if (lane8 == 0) *reinterpret_cast<float*>(st + C::S_OFF + u * C::S_BYTES + row * 4) = sc;
+          if (lane8 == 0) *reinterpret_cast<float*>(scales + u * C::S_BYTES + row * 4) = sc;
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the products read what was written here
@@ -337,9 +385,10 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0), 1)
         kb = g.kb0;
       }
     };
-    uint32_t s = 0, phase = 1;
+    uint32_t s = 0, phase = 1, slot = 0;
     auto ring_step = [&]() {
       if (++s == C::STAGES) s = 0, phase ^= 1;
+      if (++slot == C::SLOTS) slot = 0;
     };
     bool ok = true;
     for (int i = 0; i < team && g.more(); ++i) step(), ring_step();
@@ -347,9 +396,12 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0), 1)
     while (g.more()) {
       ok = __all_sync(0xffffffffu, mbar_wait(&ctl.empty[s], phase, Q_WAIT_NS, abort_flag));
       if (!ok) break;
-      write(raw, smem + s * C::STAGE);
+      write(raw, smem + s * C::STAGE, smem + C::S_OFF + slot * C::SLOT);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl.full[s]);
+      if (lane == 0) {
+        mbar_arrive(&ctl.full[s]);
+        mbar_arrive(&ctl.sfull[slot]);
+      }
 #pragma unroll
       for (int i = 0; i < ROW_TEAMS; ++i) {
         ring_step();
@@ -358,16 +410,29 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0), 1)
       if (g.more()) load(raw, kb, g.kb1 - kb);
     }
     if (!ok && lane == 0) fail();
+  } else if (warp == HAND_WARP) {
+    // ------------------------------------------------------------ a first part is handed in
+    if (hand()) {
+      const int tile = static_cast<int>(quotient(x0, KB));
+      const int parts = last_cta_of(tile) - first_cta_of(tile) + 1;
+      pdl_wait();
+      hand_sync<2>();
+      if (lane == 0) ctl.late = !*abort_flag && hand_in(a.done + tile, parts) ? 1 : 0;
+      __syncwarp();
+      hand_arrive<3>();
+    }
   } else {
     // ------------------------------------------------------------ epilogue (warps 2..9)
     pdl_wait();  // what this kernel writes may still be read by the one before
     pdl_trigger();
-    constexpr int CW = NT / 2, CH = CW < 16 ? CW : 16;  // rows of the tile that a thread has, and loads at a time
-    const int q = warp & 3, n0 = CW * ((warp - 2) >> 2);
+    // The tile's rows are in chunks of CH that the two warps of a quarter have in turn (so that both have some where
+    // a tile is half empty); chunk c of a thread begins at row n0 + 2 CH c.
+    constexpr int CW = NT / 2, CH = NT == 64 ? 16 : 8, NC = CW / CH;
+    const int q = warp & 3, n0 = CH * ((warp - 2) >> 2);
     const int f = 32 * q + lane;  // output of the tile
     const int et = threadIdx.x - 64;
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + n0;
-    uint32_t s = 0, phase = 0, b = 0, tphase = 0;
+    uint32_t slot = 0, sphase = 0, b = 0, tphase = 0;
     // The matrix's scales of a run of k-blocks: lane i holds number 32 j + i, and the one after is on its way; the
     // next tile's first while this one is written out.
     Walk<NT> g(ctl.groups, a.E, KB, x0, x1);
@@ -380,127 +445,191 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0), 1)
       sw_next = lane < nw ? __ldg(ws + lane) : 0.f;
     };
     if (g.more()) first_scales();
-    while (g.more()) {
-      float sw = 0.f;
-      const int mine = g.n - n0;  // this thread's rows that there are: the first ones, if any
-      float acc[P][CW];
-#pragma unroll
-      for (int p = 0; p < P; ++p)
-#pragma unroll
-        for (int n = 0; n < CW; ++n) acc[p][n] = 0.f;
-      bool ok = true;  // once a wait has run out the rest of the run is gone through without waiting
-      int i = 0;
-      for (int kb = g.kb0; kb < g.kb1; kb += C::KS) {
-        if ((i & 31) == 0) {
-          sw = sw_next;
-          sw_next = i + 32 + lane < nw ? __ldg(ws + i + 32 + lane) : 0.f;
-        }
-        // the two products' scales; a k-block that is not there (the last of an odd number) gets 0 times what its
-        // columns hold, which is left out below
-        const float s0 = __shfl_sync(0xffffffffu, sw, i & 31), s1 = __shfl_sync(0xffffffffu, sw, (i + 1) & 31);
-        i += 2;
-        const bool two = GATED || kb + 1 < g.kb1;
-        const float4* sx0 = reinterpret_cast<const float4*>(smem + s * C::STAGE + C::S_OFF + n0 * 4);
-        const float4* sx1 = sx0 + (GATED ? 0 : C::S_BYTES / 16);
-        const uint32_t taddr = lane_base + b * static_cast<uint32_t>(2 * NT);
-        ok = ok && mbar_wait(&ctl.full[s], phase, Q_WAIT_NS, abort_flag) &&
-             mbar_wait(&ctl.tfull[b], tphase, Q_WAIT_NS, abort_flag);
-        tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < CW; c += CH) {
-          if (c >= mine) break;
-          uint32_t d0[CH], d1[CH];
-          tmem_load(taddr + c, d0);
-          if (two) tmem_load(taddr + NT + c, d1);
-          tmem_wait(d0);
-          tmem_wait(d1);
-#pragma unroll
-          for (int j = 0; j < CH; j += 4) {
-            const float4 v = sx0[(c + j) >> 2];
-            const float vs[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              acc[0][c + j + r] = fmaf(s0 * vs[r], __uint_as_float(d0[j + r]), acc[0][c + j + r]);
-              if (GATED) acc[P - 1][c + j + r] = fmaf(s1 * vs[r], __uint_as_float(d1[j + r]), acc[P - 1][c + j + r]);
-            }
-          }
-          if (!GATED && two) {
-#pragma unroll
-            for (int j = 0; j < CH; j += 4) {
-              const float4 v = sx1[(c + j) >> 2];
-              const float vs[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-              for (int r = 0; r < 4; ++r)
-                acc[0][c + j + r] = fmaf(s1 * vs[r], __uint_as_float(d1[j + r]), acc[0][c + j + r]);
-            }
-          }
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&ctl.tempty[b]);
-          mbar_arrive(&ctl.empty[s]);
-        }
-        if (++b == C::BUFS) b = 0, tphase ^= 1;
-        if (++s == C::STAGES) s = 0, phase ^= 1;
-      }
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok && lane == 0) fail();
-      if (epi_any<EPI>(!ok)) break;  // all warps go on, or none
-      const int tile = g.tile, t = g.t, rows = g.n, kb0 = g.kb0;
-      const size_t run = g.run;
-      const bool part_only = g.kb1 - g.kb0 < KB;
-      g.next();
-      if (g.more()) first_scales();
-      // A finished tile goes through shared memory, hs[row][output], so that it leaves in whole 16-byte pieces by
-      // short loops: as unrolled stores of every thread's own column it took several thousand cycles a tile.
-      float* hs = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);
-      if (!part_only) {
-#pragma unroll
-        for (int n = 0; n < CW; ++n) hs[(n0 + n) * QB + f] = GATED ? silu_mul(acc[0][n], acc[P - 1][n]) : acc[0][n];
-        epi_sync();
-      } else {
-        // a part of the tile, [product][row][output]. Slot 0 of this CTA holds one that starts within its tile,
-        // slot 1 one that starts it: a run has at most one of each.
-        constexpr size_t slot = static_cast<size_t>(P) * NT * QB;
-        float* part = a.parts + (2 * static_cast<size_t>(blockIdx.x) + (kb0 == 0 ? 1 : 0)) * slot + n0 * QB + f;
+    bool owed = hand(), handed = false;  // the first part: still to be written; handed in, and not seen after yet
+    // A finished tile goes through shared memory, hs[row][output], so that it leaves in whole 16-byte pieces by
+    // short loops: as unrolled stores of every thread's own column it took several thousand cycles a tile.
+    float* hs = reinterpret_cast<float*>(smem + C::STAGES * C::STAGE);
+    // A part of a tile is [product][row][output]. Slot 0 of a CTA holds one that starts within its tile, slot 1
+    // one that starts it: a run has at most one of each.
+    constexpr size_t PART = static_cast<size_t>(P) * NT * QB;
+    // The CTAs that share a tile, and whether the first one's part starts it (the others' lie within).
+    int c0 = 0, c1 = 0;
+    bool whole0 = false;
+    auto sharers = [&](int tile) {
+      c0 = first_cta_of(tile), c1 = last_cta_of(tile);
+      whole0 = quotient(work * c0, G) <= static_cast<long long>(tile) * KB;
+    };
+    while (true) {
+      int tile, t, rows;
+      size_t run;
+      bool join;
+      if (g.more()) {
+        float sw = 0.f;
+        const int nc = min(NC, qceil(max(g.n - n0, 0), 2 * CH));  // chunks with rows
+        float2 acc[P][NC][CH / 2];
 #pragma unroll
         for (int p = 0; p < P; ++p)
 #pragma unroll
-          for (int n = 0; n < CW; ++n)
-            if (n < mine) __stcg(part + (p * NT + n) * QB, acc[p][n]);
-        const long long first = static_cast<long long>(tile) * KB, last = first + KB - 1;
-        // CTA c holds [work c / G, work (c + 1) / G): the one of unit x is ((x + 1) G - 1) / work
-        const int c0 = static_cast<int>(((first + 1) * G - 1) / work), c1 = static_cast<int>(((last + 1) * G - 1) / work);
-        epi_sync();
-        if (et == 0) {
-          __threadfence();  // of what all threads of the barrier have written
-          ctl.last = atomicAdd(a.done + tile, 1u) == static_cast<unsigned>(c1 - c0) ? 1 : 0;
-          __threadfence();
-        }
-        epi_sync();
-        if (!ctl.last) continue;  // (the next write to it comes after another barrier)
-        if (et == 0) a.done[tile] = 0;
-        const bool whole0 = work * c0 / G <= first;  // the first CTA's part starts the tile; the others' lie within
-        for (int i = et; i < rows * (QB / 4); i += EPI) {
-          float4 v[P];
+          for (int c = 0; c < NC; ++c)
 #pragma unroll
-          for (int p = 0; p < P; ++p) v[p] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int j = 0; j < CH / 2; ++j) acc[p][c][j] = make_float2(0.f, 0.f);
+        bool ok = true;  // once a wait has run out the rest of the run is gone through without waiting
+        int i = 0;
+        for (int kb = g.kb0; kb < g.kb1; kb += C::KS) {
+          if ((i & 31) == 0) {
+            sw = sw_next;
+            sw_next = i + 32 + lane < nw ? __ldg(ws + i + 32 + lane) : 0.f;
+          }
+          // the two products' scales; a k-block that is not there (the last of an odd number) gets 0 times what its
+          // columns hold, which is left out below
+          const float s0 = __shfl_sync(0xffffffffu, sw, i & 31), s1 = __shfl_sync(0xffffffffu, sw, (i + 1) & 31);
+          i += 2;
+          const bool two = GATED || kb + 1 < g.kb1;
+          const float4* sx0 = reinterpret_cast<const float4*>(smem + C::S_OFF + slot * C::SLOT + n0 * 4);
+          const float4* sx1 = sx0 + (GATED ? 0 : C::S_BYTES / 16);
+          const uint32_t taddr = lane_base + b * static_cast<uint32_t>(2 * NT);
+          ok = ok && mbar_wait(&ctl.sfull[slot], sphase, Q_WAIT_NS, abort_flag) &&
+               mbar_wait(&ctl.tfull[b], tphase, Q_WAIT_NS, abort_flag);
+          tc_fence_after();
+          // (all chunks on their way together where the registers hold them)
+          constexpr int LC = GATED && NT == 64 ? 1 : NC;
+#pragma unroll
+          for (int l0 = 0; l0 < NC; l0 += LC) {
+            uint32_t d0[LC][CH], d1[LC][CH];
+#pragma unroll
+            for (int l = 0; l < LC; ++l) {
+              if (l0 + l >= nc) break;
+              tmem_load(taddr + 2 * CH * (l0 + l), d0[l]);
+              if (two) tmem_load(taddr + NT + 2 * CH * (l0 + l), d1[l]);
+            }
+#pragma unroll
+            for (int l = 0; l < LC; ++l) tmem_wait(d0[l]), tmem_wait(d1[l]);
+#pragma unroll
+            for (int l = 0; l < LC; ++l) {
+              const int c = l0 + l;
+              if (c >= nc) break;
+#pragma unroll
+              for (int j = 0; j < CH / 2; j += 2) {
+                const float4 v = sx0[(2 * CH * c + 2 * j) >> 2];
+                fma2(acc[0][c][j], d0[l][2 * j], d0[l][2 * j + 1], mul2(s0, v.x, v.y));
+                fma2(acc[0][c][j + 1], d0[l][2 * j + 2], d0[l][2 * j + 3], mul2(s0, v.z, v.w));
+                if (GATED) {
+                  fma2(acc[P - 1][c][j], d1[l][2 * j], d1[l][2 * j + 1], mul2(s1, v.x, v.y));
+                  fma2(acc[P - 1][c][j + 1], d1[l][2 * j + 2], d1[l][2 * j + 3], mul2(s1, v.z, v.w));
+                }
+              }
+              if (!GATED && two) {
+#pragma unroll
+                for (int j = 0; j < CH / 2; j += 2) {
+                  const float4 v = sx1[(2 * CH * c + 2 * j) >> 2];
+                  fma2(acc[0][c][j], d1[l][2 * j], d1[l][2 * j + 1], mul2(s1, v.x, v.y));
+                  fma2(acc[0][c][j + 1], d1[l][2 * j + 2], d1[l][2 * j + 3], mul2(s1, v.z, v.w));
+                }
+              }
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl.tempty[b]);  // (and the slot of the scales has been read)
+          if (++b == C::BUFS) b = 0, tphase ^= 1;
+          if (++slot == C::SLOTS) slot = 0, sphase ^= 1;
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok && lane == 0) fail();
+        if (epi_any<EPI>(!ok)) break;  // all warps go on, or none
+        tile = g.tile, t = g.t, rows = g.n, run = g.run;
+        const int kb0 = g.kb0;
+        join = g.kb1 - g.kb0 < KB;
+        g.next();
+        if (g.more()) first_scales();
+        if (!join) {
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            if (c >= nc) break;
+#pragma unroll
+            for (int j = 0; j < CH / 2; ++j) {
+              const float2 v = acc[0][c][j], u = acc[P - 1][c][j];
+              float* h = hs + (n0 + 2 * CH * c + 2 * j) * QB + f;
+              h[0] = GATED ? silu_mul(v.x, u.x) : v.x;
+              h[QB] = GATED ? silu_mul(v.y, u.y) : v.y;
+            }
+          }
+          epi_sync();
+        } else {
+          float* part = a.parts + (2 * static_cast<size_t>(blockIdx.x) + (kb0 == 0 ? 1 : 0)) * PART + n0 * QB + f;
+#pragma unroll
+          for (int c = 0; c < NC; ++c) {
+            if (c >= nc) break;
+#pragma unroll
+            for (int p = 0; p < P; ++p)
+#pragma unroll
+              for (int j = 0; j < CH / 2; ++j) {
+                float* at = part + (p * NT + 2 * CH * c + 2 * j) * QB;
+                const int left = rows - (n0 + 2 * CH * c + 2 * j);  // (what waits below waits for every store)
+                if (left > 0) __stcg(at, acc[p][c][j].x);
+                if (left > 1) __stcg(at + QB, acc[p][c][j].y);
+              }
+          }
+          if (owed) {
+            // Nobody waits for its tile here: the CTA before this one will mostly be the last one there. If this one was,
+            // it has seen to the tile after its others.
+            if (et == 0) ctl.late_tile = tile, ctl.late_t = t, ctl.late_rows = rows, ctl.late_run = static_cast<int>(run);
+            hand_arrive<2>();
+            owed = false, handed = true;
+            continue;
+          }
+          sharers(tile);  // (while the part is on its way out)
+          epi_sync();
+          if (et == 0) ctl.last = hand_in(a.done + tile, c1 - c0 + 1) ? 1 : 0;
+          epi_sync();
+          if (!ctl.last) continue;  // (the next write to it comes after another barrier)
+        }
+      } else if (handed) {
+        handed = false;
+        hand_sync<3>();
+        if (!ctl.late) break;
+        tile = ctl.late_tile, t = ctl.late_t, rows = ctl.late_rows, run = ctl.late_run;
+        sharers(tile);
+        join = true;
+      } else {
+        break;
+      }
+      if (join) {
+        // all of a part's loads on their way together, as far as the registers hold them: one after the other they
+        // took some 1500 cycles each (31 rows, gated: 7000 a tile)
+        constexpr int U = NT == 16 ? 1 : GATED ? 2 : 4;
+        for (int i0 = et; i0 < rows * (QB / 4); i0 += U * EPI) {
+          float4 v[U][P];
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int p = 0; p < P; ++p) v[u][p] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
           for (int c = c0; c <= c1; ++c) {
             const float4* p0 =
-                reinterpret_cast<const float4*>(a.parts + (2 * static_cast<size_t>(c) + (c == c0 && whole0 ? 1 : 0)) * slot) + i;
+                reinterpret_cast<const float4*>(a.parts + (2 * static_cast<size_t>(c) + (c == c0 && whole0 ? 1 : 0)) * PART);
+            float4 w[U][P];
 #pragma unroll
-            for (int p = 0; p < P; ++p) {
-              const float4 w = __ldcg(p0 + p * NT * (QB / 4));
-              v[p].x += w.x, v[p].y += w.y, v[p].z += w.z, v[p].w += w.w;
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+              for (int p = 0; p < P; ++p)
+                if (i0 + u * EPI < rows * (QB / 4)) w[u][p] = __ldcg(p0 + p * NT * (QB / 4) + i0 + u * EPI);
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+              for (int p = 0; p < P; ++p)
+                if (i0 + u * EPI < rows * (QB / 4))
+                  v[u][p].x += w[u][p].x, v[u][p].y += w[u][p].y, v[u][p].z += w[u][p].z, v[u][p].w += w[u][p].w;
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            if (i0 + u * EPI >= rows * (QB / 4)) break;
+            if (GATED) {
+              const float4 g = v[u][0], h = v[u][P - 1];
+              v[u][0] = make_float4(silu_mul(g.x, h.x), silu_mul(g.y, h.y), silu_mul(g.z, h.z), silu_mul(g.w, h.w));
             }
+            reinterpret_cast<float4*>(hs)[i0 + u * EPI] = v[u][0];
           }
-          if (GATED) {
-            const float4 u = v[P - 1];
-            v[0] = make_float4(silu_mul(v[0].x, u.x), silu_mul(v[0].y, u.y), silu_mul(v[0].z, u.z), silu_mul(v[0].w, u.w));
-          }
-          reinterpret_cast<float4*>(hs)[i] = v[0];
         }
         epi_sync();
       }
@@ -556,8 +685,13 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0), 1)
           }
         }
       }
-      epi_sync();  // hs is free again
+      // (hs is written again after another barrier)
     }
+    if (owed) {  // given up
+      hand_arrive<2>();
+      handed = true;
+    }
+    if (handed) hand_sync<3>();
   }
 
   tc_fence_before();
@@ -571,10 +705,10 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0), 1)
 template <bool GATED, int NT, bool ROWS = false>
 cudaError_t launch(const QGemmArgs& a, cudaStream_t st) {
   using C = Thin<GATED, NT>;
-  const size_t smem = C::STAGES * C::STAGE + C::H_BYTES + 1024;
+  const size_t smem = C::SMEM;
   const cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(&k_qgemm_thin<GATED, NT, ROWS>), smem);
   if (e != cudaSuccess) return e;
-  return launch_q(k_qgemm_thin<GATED, NT, ROWS>, dim3(a.num_sms), THREADS + (ROWS ? ROW_THREADS : 0), smem, st, a,
+  return launch_q(k_qgemm_thin<GATED, NT, ROWS>, dim3(a.num_sms), THREADS + (ROWS ? ROW_THREADS : 0) + HAND, smem, st, a,
                   ROWS ? *a.rows : QRowsArgs{});
 }
 
