@@ -9,7 +9,7 @@
 //     [tile][k-block][2].
 //   - rows (tokens): runs of G rows (G = 16, 32, 64 or 128), [run][k-block][G x 128 bytes]; scales
 //     [run][k-block][G]. Bytes past K are zero; what rows without a token hold is not used.
-// Tokens of an expert stand together: expert e's rows are the runs [run0[e], run0[e + 1]).
+// Tokens of an expert stand together, in ascending order, and every expert's begin a run.
 #pragma once
 #include <cuda_runtime.h>
 #include <stdint.h>

@@ -13,13 +13,21 @@
 // Up to 16 rows of one group need no kernel before this one: with ROWS, warps 10..17 bring each stage's rows from
 // bf16 (or e4m3) into their image themselves. Every CTA does so for the k-blocks of its run, which is little beside
 // the matrix's bytes (16 rows: 4 KB of 20 a k-block, from L2), and saves the quantiser's launch (one row by 11008 x
-// 4096: 17 us a call with it, 13 without).
+// 4096: 17 us a call with it, 12.3 without).
 //
-// Warp 0: copies. A stage is 32 KB of the matrix (one bulk copy: its image is what shared memory needs) and
-// the same k-blocks of the rows and of their scales (a copy each; a run of rows is one tile). The matrix does not depend on the
-// kernel before, so the first stages' copies of it go out before this one is waited for. Warp 1: products. Warps
-// 2..9: epilogue, TMEM lane quarter warp % 4, two warps to a quarter that share its columns. Every wait has a limit; a CTA that gives up records QERR_TIMEOUT,
-// lets its copies and products finish, frees TMEM and returns.
+// Warp 0: copies. A stage is 32 KB of the matrix (one bulk copy: its image is what shared memory needs) and the same
+// k-blocks of the rows and of their scales (a copy each; a run of rows is one tile). The matrix does not depend on
+// the kernel before, so the first stages' copies of it go out before this one is waited for. Warp 1: products. Warps
+// 2..9: epilogue, TMEM lane quarter warp % 4, two warps to a quarter that have its rows in turn. The last warp hands in
+// the part of a CTA's first tile, so that the epilogue goes on meanwhile: a part's end costs 6 to 7 thousand cycles,
+// of which 2.5 are the fence and the counter (one row by 11008 x 4096: 11.0 us with it, 12.0 without; 64 experts'
+// 2048 x 1000 with 31 rows 30.5 and 31.0). Every wait has a limit; a CTA that gives up records QERR_TIMEOUT, lets its
+// copies and products finish, frees TMEM and returns.
+//
+// Measured, back to back: 8 x (2 x 14336 x 4096) with 8 rows each 133 us (7.0 TB/s of the matrices' bytes), 8 x 4096 x
+// 14336 70.5 (6.7), 8192 x 28672 with 16 rows 39 (6.0), 2 x (2 x 14336 x 4096) with one row 38 (6.2), 11008 x 4096 with one
+// row 10.6 (4.3); 64 x (2 x 1000 x 2048) with 31 rows 50.5 (5.3) and 64 x 2048 x 1000 30.2 (4.4), where a tile's end comes
+// every 16 or 8 k-blocks and takes some 2000 cycles of the epilogue.
 #include "pop_qdevice.cuh"
 
 namespace pop {
@@ -121,7 +129,7 @@ struct Walk {
 
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(EPI) : "memory"); }
 
-// Barriers 2 (a first part is written) and 3 (it is handed in) of the epilogue's warps and the one that hands it in.
+// Barriers 2 (the first part is written) and 3 (it is handed in) of the epilogue's warps and the one that hands it in.
 template <int B>
 __device__ __forceinline__ void hand_sync() { asm volatile("bar.sync %0, %1;" ::"n"(B), "n"(EPI + 32) : "memory"); }
 template <int B>
