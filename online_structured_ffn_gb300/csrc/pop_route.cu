@@ -13,7 +13,7 @@
 //
 // What bounds it: few tokens, the k dependent steps (32 tokens, 256 experts in 8 groups, k = 8: 3.9 us; 8 experts,
 // k = 2: 2.1); many, the instructions. 65,536 tokens, k = 6: 100 experts 11.6 us from bf16 (1.4 TB/s; 25 with keys of
-// the other kind), 19.3 from float32 (1.5 TB/s); 64 experts 12.4. 256 experts in 8 groups, sigmoid and bias, k = 8: 4096
+// the other kind; 13.8 where the weights need the sum), 19.3 from float32 (1.5 TB/s); 64 experts 12.4. 256 experts in 8 groups, sigmoid and bias, k = 8: 4096
 // tokens 7.0 us, 65,536 tokens 70 us. From 129 experts on a token has a whole warp, which finds its
 // largest key in one instruction (16 lanes with 16 experts: 8.7 us for 4096 tokens); below that a warp has
 // several tokens (a warp each: 65,536 x 100 from bf16 20.1 us instead of 11.6, float32 35 instead of 19, and less than 1 us
@@ -143,13 +143,16 @@ __device__ __forceinline__ float unique_float(uint32_t key) {
   return fminf(key_float(key >= 0x80000000u ? key & 0xffff0000u : key | 0xffffu), 3.402823466e38f);
 }
 
-// The keys of a lane's V logits, of experts from e0 on, n of which there are.
+// The keys of a lane's V logits, of experts from e0 on, n of which there are; and the logits, two to a word, -infinity
+// where they are not live.
 template <int V, bool VEC>
-__device__ __forceinline__ void unique_keys(const void* p, long long at, int e0, int n, uint32_t (&key)[V]) {
+__device__ __forceinline__ void unique_keys(const void* p, long long at, int e0, int n, uint32_t (&key)[V],
+                                            uint32_t (&both)[V / 2]) {
   const uint16_t* l = static_cast<const uint16_t*>(p) + at;
 #pragma unroll
   for (int i = 0; i < V; i += 4) {
-    uint32_t w[2] = {0xff80ff80u, 0xff80ff80u};  // -infinity
+    uint32_t* w = both + i / 2;
+    w[0] = w[1] = 0xff80ff80u;  // -infinity
     if (VEC) {
       if (i < n) {
         const uint2 u = __ldg(reinterpret_cast<const uint2*>(l + i));
@@ -192,12 +195,14 @@ __global__ void __launch_bounds__(32 * RT_WARPS) k_route(const __grid_constant__
   uint32_t key[V];
   float top = 0.f, sum = 1.f;
   if (UNIQUE) {
-    unique_keys<V, VEC>(a.logits, t * a.ld + e0, e0, a.E - e0, key);
+    uint32_t both[V / 2];
+    unique_keys<V, VEC>(a.logits, t * a.ld + e0, e0, a.E - e0, key, both);
     if (!a.renorm) {  // (renormalised weights do not depend on the sum)
       top = unique_float(lanes_max<L>(best_of(key)));
       sum = 0.f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) sum += key[i] >= UNIQUE_LIVE ? expf(unique_float(key[i]) - top) : 0.f;
+      for (int i = 0; i < V; ++i)
+        sum += expf(fminf(i % 2 ? bf16hi(both[i / 2]) : bf16lo(both[i / 2]), 3.402823466e38f) - top);
       sum = lanes_sum<L>(sum);
     }
   } else {
