@@ -5,16 +5,9 @@
 namespace pop {
 namespace {
 
-__device__ __forceinline__ void unpack8(const void* p, int kind, float* v) {
-  if (kind == 0) {
-    const uint4 w = ldg_stream(p);
-    v[0] = bf16lo(w.x), v[1] = bf16hi(w.x), v[2] = bf16lo(w.y), v[3] = bf16hi(w.y);
-    v[4] = bf16lo(w.z), v[5] = bf16hi(w.z), v[6] = bf16lo(w.w), v[7] = bf16hi(w.w);
-  } else {
-    const uint4 a = ldg_stream(p), b = ldg_stream(static_cast<const uint8_t*>(p) + 16);
-    v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y), v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
-    v[4] = __uint_as_float(b.x), v[5] = __uint_as_float(b.y), v[6] = __uint_as_float(b.z), v[7] = __uint_as_float(b.w);
-  }
+__device__ __forceinline__ void unpack8(const uint4& w, float* v) {
+  v[0] = bf16lo(w.x), v[1] = bf16hi(w.x), v[2] = bf16lo(w.y), v[3] = bf16hi(w.y);
+  v[4] = bf16lo(w.z), v[5] = bf16hi(w.z), v[6] = bf16lo(w.w), v[7] = bf16hi(w.w);
 }
 
 // The places of a CTA's own pairs, [p0, p0 + n) of all, found from the experts of all of them: how many pairs of the
@@ -26,12 +19,12 @@ struct Places {
   __device__ __forceinline__ void find(const QRowsOut& out, int pairs, int p0, int n, bool report) {
     for (int e = threadIdx.x; e < out.E; e += 256) total[e] = before[e] = 0;
     __syncthreads();
-    for (int c = threadIdx.x; c < pairs; c += 4 * 256) {
-      int es[4];  // four loads on their way
+    for (int c = threadIdx.x; c < pairs; c += 8 * 256) {
+      int es[8];  // eight loads on their way
 #pragma unroll
-      for (int i = 0; i < 4; ++i) es[i] = c + 256 * i < pairs ? __ldg(out.experts + c + 256 * i) : -1;
+      for (int i = 0; i < 8; ++i) es[i] = c + 256 * i < pairs ? __ldg(out.experts + c + 256 * i) : -1;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 8; ++i) {
         const int p = c + 256 * i, e = es[i];
         const bool is = static_cast<unsigned>(e) < static_cast<unsigned>(out.E);
         if (is) atomicAdd(&total[e], 1);
@@ -78,7 +71,10 @@ template <int KIND>
 __global__ void __launch_bounds__(256) k_quantize_rows(const __grid_constant__ QRowsArgs in, const __grid_constant__ QRowsOut out, int per) {
   // Behind the kernel that places the rows (row_of) x is complete, as that one has waited for it: only the places, and
   // what an earlier call's kernels may still read, are then waited for, after the arithmetic.
-  if (!out.row_of) pdl_wait();
+  if (!out.row_of) {
+    pdl_wait();
+    pdl_trigger();
+  }
   const int KB = qceil(in.K, QB);
   const int lane8 = threadIdx.x & 7, u = threadIdx.x >> 3;
   int row = blockIdx.x, kb = u + 32 * blockIdx.y;
@@ -91,27 +87,51 @@ __global__ void __launch_bounds__(256) k_quantize_rows(const __grid_constant__ Q
   }
   const int k0 = kb * QB + lane8 * 16;
   const int n8 = on ? min(max((in.K - k0) >> 3, 0), 2) : 0;  // runs of 8 values this lane has
-  uint4 q = make_uint4(0u, 0u, 0u, 0u);
+  // The values, as they stand in memory: on their way while the places are looked for.
+  uint4 raw[KIND == 1 ? 4 : 2];
+#pragma unroll
+  for (int i = 0; i < (KIND == 1 ? 4 : 2); ++i) raw[i] = make_uint4(0u, 0u, 0u, 0u);
   float s = 0.f;
   if (KIND == 2) {
     const uint8_t* p = static_cast<const uint8_t*>(in.x) + static_cast<size_t>(row) * in.ldx + k0;
     if (n8 > 0) {
       const uint2 a = *reinterpret_cast<const uint2*>(p);
-      q.x = a.x, q.y = a.y;
+      raw[0].x = a.x, raw[0].y = a.y;
     }
     if (n8 > 1) {
       const uint2 b = *reinterpret_cast<const uint2*>(p + 8);
-      q.z = b.x, q.w = b.y;
+      raw[0].z = b.x, raw[0].w = b.y;
     }
     if (on) s = in.xs[static_cast<size_t>(row) * in.lds + kb];
   } else {
-    constexpr int SIZE = KIND == 0 ? 2 : 4;
+    constexpr int SIZE = KIND == 0 ? 2 : 4, N16 = SIZE / 2;  // 16-byte loads of eight values
     const uint8_t* p = static_cast<const uint8_t*>(in.x) + (static_cast<size_t>(row) * in.ldx + k0) * SIZE;
-    float v[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = 0.f;
-    if (n8 > 0) unpack8(p, KIND, v);
-    if (n8 > 1) unpack8(p + 8 * SIZE, KIND, v + 8);
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < N16; ++j)
+        if (n8 > i) raw[i * N16 + j] = ldg_stream(p + (i * N16 + j) * 16);
+  }
+  __shared__ Places places;
+  if (out.experts) {
+    const int t0 = blockIdx.x * per, n = min(per, in.M - t0) * out.k;
+    places.find(out, in.M * out.k, t0 * out.k, n, blockIdx.x == 0 && blockIdx.y == 0);
+    if (blockIdx.y == 0)
+      for (int i = threadIdx.x; i < n; i += 256) out.places[t0 * out.k + i] = places.row[i];
+  }
+  uint4 q = raw[0];
+  if (KIND != 2) {
+    float v[16];
+    if (KIND == 0) {
+      unpack8(raw[0], v);
+      unpack8(raw[1], v + 8);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        const uint4 w = raw[KIND == 1 ? i / 4 : 0];
+        v[i] = __uint_as_float(w.x), v[i + 1] = __uint_as_float(w.y), v[i + 2] = __uint_as_float(w.z), v[i + 3] = __uint_as_float(w.w);
+      }
+    }
     float a = __uint_as_float(AMAX_MIN_BITS);
 #pragma unroll
     for (int i = 0; i < 16; i += 2) a = max_abs(a, v[i], v[i + 1]);
@@ -120,14 +140,9 @@ __global__ void __launch_bounds__(256) k_quantize_rows(const __grid_constant__ Q
     q = e4m3x16(v, BlockRatio(a));
     s = block_scale(a);
   }
-  if (out.row_of) pdl_wait();
-  pdl_trigger();
-  __shared__ Places places;
-  if (out.experts) {
-    const int t0 = blockIdx.x * per, n = min(per, in.M - t0) * out.k;
-    places.find(out, in.M * out.k, t0 * out.k, n, blockIdx.x == 0 && blockIdx.y == 0);
-    if (blockIdx.y == 0)
-      for (int i = threadIdx.x; i < n; i += 256) out.places[t0 * out.k + i] = places.row[i];
+  if (out.row_of) {
+    pdl_wait();
+    pdl_trigger();
   }
   if (!on) return;
   if (out.G == 0) {
@@ -197,8 +212,8 @@ __global__ void __launch_bounds__(256) k_pack_matrix(const void* __restrict__ W,
     for (int j = 0; j < 16; ++j) v[i][j] = 0.f;
     if (t * QB + r < N) {
       const uint8_t* p = static_cast<const uint8_t*>(W) + (static_cast<size_t>(t * QB + r) * K + k0) * 2;
-      if (n8 > 0) unpack8(p, 0, v[i]);
-      if (n8 > 1) unpack8(p + 16, 0, v[i] + 8);
+      if (n8 > 0) unpack8(ldg_stream(p), v[i]);
+      if (n8 > 1) unpack8(ldg_stream(p + 16), v[i] + 8);
     }
 #pragma unroll
     for (int j = 0; j < 16; ++j) m = max(m, abs_bits(v[i][j]));
