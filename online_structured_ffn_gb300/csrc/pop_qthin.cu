@@ -18,16 +18,19 @@
 // Warp 0: copies. A stage is 32 KB of the matrix (one bulk copy: its image is what shared memory needs) and the same
 // k-blocks of the rows and of their scales (a copy each; a run of rows is one tile). The matrix does not depend on
 // the kernel before, so the first stages' copies of it go out before this one is waited for. Warp 1: products. Warps
-// 2..9: epilogue, TMEM lane quarter warp % 4, two warps to a quarter that have its rows in turn. The last warp hands in
-// the part of a CTA's first tile, so that the epilogue goes on meanwhile: a part's end costs 6 to 7 thousand cycles,
-// of which 2.5 are the fence and the counter (one row by 11008 x 4096: 11.0 us with it, 12.0 without; 64 experts'
-// 2048 x 1000 with 31 rows 30.5 and 31.0). Every wait has a limit; a CTA that gives up records QERR_TIMEOUT, lets its
-// copies and products finish, frees TMEM and returns.
+// 2..9: epilogue, TMEM lane quarter warp % 4, two warps to a quarter that have its rows in turn. Every wait has a limit;
+// a CTA that gives up records QERR_TIMEOUT, lets its copies and products finish, frees TMEM and returns.
 //
-// Measured, back to back: 8 x (2 x 14336 x 4096) with 8 rows each 133 us (7.0 TB/s of the matrices' bytes), 8 x 4096 x
-// 14336 70.5 (6.7), 8192 x 28672 with 16 rows 39 (6.0), 2 x (2 x 14336 x 4096) with one row 38 (6.2), 11008 x 4096 with one
-// row 10.6 (4.3); 64 x (2 x 1000 x 2048) with 31 rows 50.5 (5.3) and 64 x 2048 x 1000 30.2 (4.4), where a tile's end comes
-// every 16 or 8 k-blocks and takes some 2000 cycles of the epilogue.
+// A tile in several runs costs its CTA 6 to 10 thousand cycles: the part on its way out, a fence and the counter 2500,
+// the sum 2000 to 5000. So the part of a run's first tile is handed in by a warp of its own, the last, while the
+// epilogue goes on (11008 x 4096 with one row 12.0 -> 11.0 us), and that warp then looks out for the others' parts of the
+// run's last tile: where they are all there in time, as they mostly are, the epilogue adds them to its registers
+// and hands nothing in (64 x (2 x 1000 x 2048) with 31 rows each 50.4 -> 46.9 us).
+//
+// Measured, back to back: 8 x (2 x 14336 x 4096) with 8 rows each 132 us (7.1 TB/s of the matrices' bytes), 8 x 4096 x
+// 14336 68.7 (6.8), 8192 x 28672 with 16 rows 39 (6.0), 2 x (2 x 14336 x 4096) with one row 36.6 (6.4), 11008 x 4096 with
+// one row 10.8 (4.2); 64 x (2 x 1000 x 2048) with 31 rows 46.9 (5.7) and 64 x 2048 x 1000 28.8 (4.7), where a tile's end
+// comes every 16 or 8 k-blocks and takes some 2000 cycles of the epilogue.
 #include "pop_qdevice.cuh"
 
 namespace pop {
@@ -75,6 +78,8 @@ struct Ctl {
   int abort_flag;
   int last;
   int late, late_tile, late_t, late_rows, late_run;  // a first part: whether it was its tile's last, and the tile
+  int others, alone;  // the last tile: whether the others' parts are there; as the epilogue saw it
+  int over;           // the epilogue needs no news of it any more
   Groups groups;
 };
 
@@ -140,6 +145,13 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
   return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
 }
 
+constexpr int LOOKS = 1 << 17;  // for others' parts, 0.3 us or more apart
+__device__ __forceinline__ unsigned ld_acquire(const unsigned* p) {
+  unsigned v;
+  asm volatile("ld.acquire.gpu.u32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+
 // One more part of a tile is there, written by threads that have met at a barrier. Whether it was the last of `parts`.
 __device__ __forceinline__ bool hand_in(unsigned* done, int parts) {
   __threadfence();
@@ -174,7 +186,7 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0) + HAND, 1)
       mbar_init(&ctl.tempty[b], EPI / 32);
     }
     mbar_init(&ctl.drain, 1);
-    ctl.abort_flag = 0;
+    ctl.abort_flag = ctl.others = ctl.over = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -429,6 +441,24 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0) + HAND, 1)
       __syncwarp();
       hand_arrive<3>();
     }
+    // The last tile, if this CTA has its beginning and others the rest: looks out for their parts, so that the
+    // epilogue, where all are there when it is done, adds them to its own registers and hands nothing in.
+    const long long end = quotient(x1, KB);
+    if (x0 <= end * KB && end * KB < x1) {
+      const int tile = static_cast<int>(end), others = last_cta_of(tile) - static_cast<int>(blockIdx.x);
+      pdl_wait();
+      if (lane == 0) {
+        for (int i = 0; i < LOOKS && !*static_cast<volatile int*>(&ctl.over); ++i) {
+          if (ld_acquire(a.done + tile) == static_cast<unsigned>(others)) {
+            __threadfence_block();
+            *static_cast<volatile int*>(&ctl.others) = 1;
+            break;
+          }
+          __nanosleep(300);
+        }
+      }
+      __syncwarp();
+    }
   } else {
     // ------------------------------------------------------------ epilogue (warps 2..9)
     pdl_wait();  // what this kernel writes may still be read by the one before
@@ -544,12 +574,43 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0) + HAND, 1)
         }
         ok = __all_sync(0xffffffffu, ok);
         if (!ok && lane == 0) fail();
+        const bool begins = g.kb0 == 0 && g.kb1 < KB;
+        if (begins && et == 0) {
+          ctl.alone = *static_cast<volatile int*>(&ctl.others);
+          *static_cast<volatile int*>(&ctl.over) = 1;
+          __threadfence_block();
+        }
         if (epi_any<EPI>(!ok)) break;  // all warps go on, or none
         tile = g.tile, t = g.t, rows = g.n, run = g.run;
         const int kb0 = g.kb0;
         join = g.kb1 - g.kb0 < KB;
         g.next();
         if (g.more()) first_scales();
+        if (begins && ctl.alone) {
+          // this CTA's part comes first; the others' are added in the order of k, as below (and to 0 first, as there)
+          if (et == 0) a.done[tile] = 0;
+          join = false;
+          const int end = last_cta_of(tile);
+          for (int c = blockIdx.x + 1; c <= end; ++c) {
+            const float* part = a.parts + 2 * static_cast<size_t>(c) * PART + n0 * QB + f;
+#pragma unroll
+            for (int l = 0; l < NC; ++l) {
+              if (l >= nc) break;
+#pragma unroll
+              for (int p = 0; p < P; ++p) {
+                float w[CH];
+#pragma unroll
+                for (int j = 0; j < CH; ++j)
+                  w[j] = n0 + 2 * CH * l + j < rows ? __ldcg(part + (p * NT + 2 * CH * l + j) * QB) : 0.f;
+#pragma unroll
+                for (int j = 0; j < CH; j += 2) {
+                  float2& v = acc[p][l][j / 2];
+                  v = make_float2((v.x + 0.f) + w[j], (v.y + 0.f) + w[j + 1]);
+                }
+              }
+            }
+          }
+        }
         if (!join) {
 #pragma unroll
           for (int c = 0; c < NC; ++c) {
@@ -695,6 +756,7 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0) + HAND, 1)
       }
       // (hs is written again after another barrier)
     }
+    if (et == 0) *static_cast<volatile int*>(&ctl.over) = 1;
     if (owed) {  // given up
       hand_arrive<2>();
       handed = true;
