@@ -193,13 +193,14 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0) + HAND, 1)
     tmem_alloc(&ctl.tmem_base, TMEM_COLS);
     tmem_relinquish();
   }
+  ctl.groups.zero(a);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = ctl.tmem_base;
   // The groups' numbers, or the experts that they are counted from, are two kernels back or more: the kernel before this
   // waited for them before it let this one start (as this one does: pdl_trigger comes after a pdl_wait).
-  const int tiles = ctl.groups.fill(a, NT, NTILES);
+  const int tiles = ctl.groups.fill<true>(a, NT, NTILES);
   const long long work = static_cast<long long>(tiles) * KB;
   // CTAs that have a run, G: all, but with few tiles a run is at least sqrt(NT KB / 28) units, as each more CTA of a
   // tile costs its last one the reading of a part (NT = 64: some 0.8 us; a unit takes 0.35 us). Runs that are whole

@@ -178,7 +178,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
   const uint32_t tmem_base = ctl.tmem_base;
   // The groups' numbers, or the experts that they are counted from, are two kernels back or more: the kernel before this
   // waited for them before it let this one start (as this one does: pdl_trigger comes after a pdl_wait).
-  const int tiles = ctl.groups.fill(a, 2 * BM, per);
+  const int tiles = ctl.groups.fill<false>(a, 2 * BM, per);
 
   auto fail = [&]() {
     if (!*abort_flag) {
