@@ -2,6 +2,7 @@
 #include "pop_quant.h"
 
 #include <atomic>
+#include <cmath>
 #include <initializer_list>
 #include <mutex>
 #include <new>
@@ -119,8 +120,9 @@ struct Shape {
 // Times of the two kernels, in 0.05 us. Wide: rounds of 256 x 256 tiles over pairs of SMs, a k-block 0.35 us, or 0.5
 // where a matrix tile serves one row tile only and comes from memory. Thin: tiles of 64 rows by 128 outputs over all SMs, a
 // k-block 0.36 us (gated: two products, 0.8 us) and a little more, as the matrix is read again for every further
-// tile of rows. Measured, rows per group, thin against wide in us: 8 experts of 2 x 14336 x 4096 64: 149/187, 96: 279/188;
-// 11008 x 4096 64: 19/18, 96: 22/19; 1000 x 8000 96: 20/28; 64 experts of 2048 x 1000 64: 43/49, 96: 61/55.
+// tile of rows. Measured, rows per group, thin against wide in us: 8 experts of 2 x 14336 x 4096 64: 143/183, 80: 274/183;
+// 28672 x 8192 64: 43/56, 80: 76/56; 11008 x 4096 64: 16/17, 80: 19/17; 1000 x 8000 64: 13/27, 256: 14/29; 64 experts of
+// 2 x 1000 x 2048 64: 52/61, 80: 77/62, of 2048 x 1000 64: 36/44, 80: 49/45.
 double wide_time(const Shape& s, int sms) {
   const long long tiles = s.groups * ((s.rows + 255) / 256) * (s.gated ? s.NT : qceil(s.NT, 2));
   return static_cast<double>((tiles + sms / 2 - 1) / (sms / 2)) * s.KB * (s.rows <= 256 ? 10 : 7);
@@ -182,11 +184,14 @@ int linear_granule(const pop_qlinear_config& c, int rows, int sms) {
   return granule({{1, rows, qceil(c.N, QB), qceil(c.K, QB), false}}, rows, sms);
 }
 
-// The experts' rows spread about their mean, as routers do: some pass 64 when the mean is at 56.
+// The experts' rows spread about their mean, by two deviations of a random routing: some pass 64 when the mean is at 50.
+// (Mean rows per expert, thin against wide, both products of a call, in us: 8 experts of 4096 x 14336 48: 280/273, 52: 306/275;
+// 64 of 2048 x 1000 48: 116/128, 52: 123/129, 60: 133/132; 16 of 1024 x 1024 52: 34/29.)
 int qmoe_granule(const pop_qmoe_config& c, int tokens, int sms) {
   const long long pairs = static_cast<long long>(tokens) * c.top_k;
   const long long groups = pairs < c.n_experts ? pairs : c.n_experts;
-  const long long rows = c.n_experts > 1 ? pairs * 8 / (groups * 7) + 1 : pairs;
+  const long long mean = groups ? (pairs + groups - 1) / groups : 0;
+  const long long rows = c.n_experts > 1 ? mean + static_cast<long long>(2 * std::sqrt(static_cast<double>(mean))) : pairs;
   const int NT = qceil(c.D_FF, QB), DT = qceil(c.D, QB);
   return granule({{groups, rows, NT, DT, true}, {groups, rows, DT, NT, false}}, tokens, sms);
 }
