@@ -22,21 +22,26 @@ struct BlockRatio {
     a = big ? amax * 0x1p-64f : amax;
     y = __frcp_rn(a);
   }
-  __device__ __forceinline__ float operator()(float x) const {
-    const float t = k * x, q0 = t * y;
-    return fmaf(fmaf(-q0, a, t), y, q0);
+  // of two values at a time
+  __device__ __forceinline__ float2 operator()(float x0, float x1) const {
+    float2 q;
+    asm("{\n\t.reg .b64 x, k, a, y, t, q, r;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 k, {%4, %4};\n\tmov.b64 a, {%5, %5};\n\tmov.b64 y, {%6, %6};\n\t"
+        "mul.rn.f32x2 t, x, k;\n\tmul.rn.f32x2 q, t, y;\n\tfma.rn.f32x2 r, q, a, t;\n\tfma.rn.f32x2 q, r, y, q;\n\t"
+        "mov.b64 {%0, %1}, q;\n\t}"
+        : "=f"(q.x), "=f"(q.y)
+        : "f"(x0), "f"(x1), "f"(k), "f"(-a), "f"(y));
+    return q;
   }
 };
 
-__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
-}
+__device__ __forceinline__ uint32_t e4m3x2(float2 v) { return __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3); }
 
 __device__ __forceinline__ uint4 e4m3x16(const float* v, const BlockRatio& ratio) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    w[i] = e4m3x2(ratio(v[4 * i]), ratio(v[4 * i + 1])) | (e4m3x2(ratio(v[4 * i + 2]), ratio(v[4 * i + 3])) << 16);
+    w[i] = e4m3x2(ratio(v[4 * i], v[4 * i + 1])) | (e4m3x2(ratio(v[4 * i + 2], v[4 * i + 3])) << 16);
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 

@@ -10,6 +10,13 @@ __device__ __forceinline__ void unpack8(const uint4& w, float* v) {
   v[4] = bf16lo(w.z), v[5] = bf16hi(w.z), v[6] = bf16lo(w.w), v[7] = bf16hi(w.w);
 }
 
+// 32 bytes, aligned to 32, in one load: a lane's values are whole sectors, which two loads of 16 bytes each fetched twice.
+__device__ __forceinline__ void ldg_sector(const void* p, uint4& a, uint4& b) {
+  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+               : "l"(p));
+}
+
 // The places of a CTA's own pairs, [p0, p0 + n) of all, found from the experts of all of them: how many pairs of the
 // same expert come before, and where the expert's rows begin. row[i] is that of pair p0 + i.
 struct Places {
@@ -65,8 +72,9 @@ struct Places {
 
 // Eight lanes per block of 128, 16 values each. A CTA has 32 blocks: of one row (the blockIdx.y-th 32), or of the
 // `per` whole rows that they hold. Bound by memory and nearly so by its instructions, of which every one counts:
-// 16 values take 4 each for the quotient, half a rounding, one for bf16's unpacking. 4096 x 4096 of bf16: 9.9 us (5.1
-// TB/s read and written), 16,384 x 4096 38.6 (5.2; issue slots 73 % busy); 1001 x 11008 of float32 9.8 (5.7).
+// 16 values take two each for the quotient (packed; four, and 9.8 us, without), half a rounding, one for bf16's
+// unpacking. 4096 x 4096 of bf16: 8.9 us (5.7 TB/s read and written), 16,384 x 4096 33.8 (6.0); 1001 x 11008 of float32
+// 8.5 (6.6; 9.4 with loads of 16 bytes).
 template <int KIND>
 __global__ void __launch_bounds__(256) k_quantize_rows(const __grid_constant__ QRowsArgs in, const __grid_constant__ QRowsOut out, int per) {
   // Behind the kernel that places the rows (row_of) x is complete, as that one has waited for it: only the places, and
@@ -106,11 +114,16 @@ __global__ void __launch_bounds__(256) k_quantize_rows(const __grid_constant__ Q
   } else {
     constexpr int SIZE = KIND == 0 ? 2 : 4, N16 = SIZE / 2;  // 16-byte loads of eight values
     const uint8_t* p = static_cast<const uint8_t*>(in.x) + (static_cast<size_t>(row) * in.ldx + k0) * SIZE;
+    if (n8 > 1 && (reinterpret_cast<uintptr_t>(p) & 31) == 0) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < N16; ++i) ldg_sector(p + 32 * i, raw[2 * i], raw[2 * i + 1]);
+    } else {
 #pragma unroll
-      for (int j = 0; j < N16; ++j)
-        if (n8 > i) raw[i * N16 + j] = ldg_stream(p + (i * N16 + j) * 16);
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < N16; ++j)
+          if (n8 > i) raw[i * N16 + j] = ldg_stream(p + (i * N16 + j) * 16);
+    }
   }
   __shared__ Places places;
   if (out.experts) {
