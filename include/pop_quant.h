@@ -76,6 +76,11 @@ pop_status pop_qlinear_forward(pop_qlinear_t h, const void* x, long long ldx, in
 pop_status pop_qlinear_forward_quantized(pop_qlinear_t h, const void* xq, long long ldq, const float* xs,
                                          long long lds, int M, void* y, long long ldy, void* stream);
 
+/* Limit, in nanoseconds, for every device-side wait of this handle's products (default 2 s). A wait that runs
+ * out is recorded (POP_ERR_TIMEOUT from the check below) and the kernel returns; the call's output is then
+ * not valid. ns >= 1. */
+pop_status pop_qlinear_set_wait_limit(pop_qlinear_t h, uint64_t ns);
+
 /* Synchronizes the device and returns the first recorded device-side failure, or POP_OK; clears it. */
 pop_status pop_qlinear_check(pop_qlinear_t h);
 
@@ -107,6 +112,9 @@ void pop_qmoe_destroy(pop_qmoe_t m);
  * token's slots. y: device [T, D]. No allocation, no host synchronization. */
 pop_status pop_qmoe_forward(pop_qmoe_t m, const void* x, long long ldx, const int* experts, const float* weights,
                             int T, void* y, long long ldy, void* stream);
+
+/* As pop_qlinear_set_wait_limit. */
+pop_status pop_qmoe_set_wait_limit(pop_qmoe_t m, uint64_t ns);
 
 /* Synchronizes the device and returns the first recorded device-side failure, or POP_OK; clears it. */
 pop_status pop_qmoe_check(pop_qmoe_t m);

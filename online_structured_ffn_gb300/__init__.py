@@ -108,10 +108,12 @@ SIGNATURES = {
     "pop_qlinear_destroy": (None, [_vp]),
     "pop_qlinear_forward": (_i32, [_vp, _vp, _i64, _i32, _vp, _i64, _vp]),
     "pop_qlinear_forward_quantized": (_i32, [_vp, _vp, _i64, _vp, _i64, _i32, _vp, _i64, _vp]),
+    "pop_qlinear_set_wait_limit": (_i32, [_vp, _u64]),
     "pop_qlinear_check": (_i32, [_vp]),
     "pop_qmoe_create": (_i32, [ctypes.POINTER(pop_qmoe_config)] + [ctypes.POINTER(_vp)] * 6 + [_vp, ctypes.POINTER(_vp)]),
     "pop_qmoe_destroy": (None, [_vp]),
     "pop_qmoe_forward": (_i32, [_vp, _vp, _i64, _vp, _vp, _i32, _vp, _i64, _vp]),
+    "pop_qmoe_set_wait_limit": (_i32, [_vp, _u64]),
     "pop_qmoe_check": (_i32, [_vp]),
     "pop_quant_last_error": (ctypes.c_char_p, []),
 }
@@ -623,7 +625,7 @@ def quantize_rows(x, stream=None):
 
 class _QHandle:
     """Owns a handle of include/pop_quant.h."""
-    _destroy = _checker = ""
+    _destroy = _checker = _limiter = ""
     handle = None
 
     def close(self):
@@ -640,6 +642,10 @@ class _QHandle:
     def out_dtype(self):
         import torch
         return torch.float32 if self.cfg.out_f32 else torch.bfloat16
+
+    def set_wait_limit(self, ns: int):
+        """Limit of every device-side wait of the handle's products, in nanoseconds (2 s unless set)."""
+        _check_quant(getattr(load_library(), self._limiter)(self.handle, ns))
 
     def check(self):
         """Syncs and raises the first device-side failure since the last check."""
@@ -671,7 +677,7 @@ class PopQLinear(_QHandle):
     W: torch bf16 [N, K], quantised here, or float8_e4m3fn [N, K] with float32 scales S
     [ceil(N/128), ceil(K/128)]. The handle keeps its own copy. max_tokens: rows that the workspace is
     made for; longer calls run in chunks."""
-    _destroy, _checker = "pop_qlinear_destroy", "pop_qlinear_check"
+    _destroy, _checker, _limiter = "pop_qlinear_destroy", "pop_qlinear_check", "pop_qlinear_set_wait_limit"
 
     def __init__(self, W, S=None, max_tokens: int = 2048, out_f32: bool = False, stream=None):
         _matrix_arg(W, S, "W")
@@ -715,7 +721,7 @@ class PopQMoE(_QHandle):
 
     Wg, W1: [D_FF, D] per expert, W2: [D, D_FF] per expert. Each is a sequence (or a stacked tensor) of
     bf16 matrices, quantised here, or a pair of such sequences: float8_e4m3fn matrices and their scales."""
-    _destroy, _checker = "pop_qmoe_destroy", "pop_qmoe_check"
+    _destroy, _checker, _limiter = "pop_qmoe_destroy", "pop_qmoe_check", "pop_qmoe_set_wait_limit"
 
     def __init__(self, Wg, W1, W2, top_k: int, max_tokens: int = 2048, out_f32: bool = False, stream=None):
         scaled = [isinstance(w, tuple) and len(w) == 2 and w[0][0].dim() == 2 for w in (Wg, W1, W2)]

@@ -119,19 +119,18 @@ __device__ __forceinline__ void umma_block(uint32_t d_tmem, uint32_t a_lo, uint3
         : "memory");
 }
 
-// Waits until the phase with the given parity has completed; false after limit_ns, or once another role of the
-// CTA has given up. The timer is first read after 64 tries: reading it takes longer than most waits, and these
-// kernels wait several times per k-block.
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns, volatile int* abort_flag) {
+// Waits until the phase with the given parity has completed; false after the limit, or once another role of the
+// CTA has given up. These kernels wait several times per k-block: the timer is first read after a number of tries.
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, QWait limit, volatile int* abort_flag) {
   uint64_t t0 = 0;
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 63u) == 0u) {
+    if ((it & limit.more) == 0u) {
       if (*abort_flag) return false;
       const uint64_t now = globaltimer_ns();
       if (t0 == 0)
         t0 = now;
-      else if (now - t0 > limit_ns)
+      else if (now - t0 > limit.ns)
         return false;
     }
   }
@@ -358,9 +357,8 @@ struct Groups {
   }
 };
 
-// Limit of the kernels' waits, and of those in which a CTA that gives up lets its own copies and
-// products finish.
-constexpr uint64_t Q_WAIT_NS = 2000000000ull;
-constexpr uint64_t Q_DRAIN_NS = 1000000000ull;
+// Limit of the waits in which a CTA that gives up lets its own copies and products finish (the others' is the
+// handle's, QGemmArgs::wait).
+constexpr QWait Q_DRAIN(1000000000ull);
 
 }  // namespace pop

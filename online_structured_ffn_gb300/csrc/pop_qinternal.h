@@ -77,6 +77,14 @@ cudaError_t launch_plan(const int* experts, int pairs, int E, int G, int* counts
 cudaError_t launch_combine(const float* o, const int* row_of, const float* weights, int T, int k, int D, void* y,
                            long long ldy, int out_f32, cudaStream_t st);
 
+// Limit of a wait: the timer is read after 64 tries, as reading it takes longer than most waits; after every one if
+// the limit is shorter than some hundred tries.
+struct QWait {
+  uint64_t ns;
+  uint32_t more;  // tries between two looks, less one: 2^n - 1
+  __host__ __device__ constexpr QWait(uint64_t limit = 2000000000ull) : ns(limit), more(limit < 100000u ? 0u : 63u) {}
+};
+
 struct QGemmArgs {
   const uint8_t* act;    // rows
   const float* act_s;
@@ -102,6 +110,7 @@ struct QGemmArgs {
   float* parts;
   unsigned* done;
   unsigned* err;
+  QWait wait;            // limit of the kernel's waits
   int num_sms;
 };
 // few rows per group (G = 16, 32 or 64): the matrix streams once (pop_qthin.cu)

@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0) + HAND, 1)
 #pragma unroll
             for (int i = 0; i < C::STAGES; ++i) load_rows(owed[i], i, i);
           }
-          if (!mbar_wait(&ctl.empty[s], phase, Q_WAIT_NS, abort_flag)) {
+          if (!mbar_wait(&ctl.empty[s], phase, a.wait, abort_flag)) {
             fail();
             ok = false;
             break;
@@ -291,11 +291,17 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0) + HAND, 1)
       const uint32_t lo = issued > C::STAGES ? issued - C::STAGES : 0;
       for (uint32_t i = lo; i < issued; ++i) {
         volatile int never = 0;
-        if (!mbar_wait(&ctl.full[i % C::STAGES], (i / C::STAGES) & 1u, Q_DRAIN_NS, &never)) fail();
+        if (!mbar_wait(&ctl.full[i % C::STAGES], (i / C::STAGES) & 1u, Q_DRAIN, &never)) {
+          fail();
+          break;  // (with ROWS it waits for rows that nobody brings; the copies have had their time)
+        }
       }
       for (uint32_t i = ROWS ? issued : issued > C::SLOTS ? issued - C::SLOTS : 0; i < issued; ++i) {
         volatile int never = 0;
-        if (!mbar_wait(&ctl.sfull[i % C::SLOTS], (i / C::SLOTS) & 1u, Q_DRAIN_NS, &never)) fail();
+        if (!mbar_wait(&ctl.sfull[i % C::SLOTS], (i / C::SLOTS) & 1u, Q_DRAIN, &never)) {
+          fail();
+          break;
+        }
       }
     }
     __syncwarp();
@@ -308,7 +314,7 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0) + HAND, 1)
     for (Walk<NT> g(ctl.groups, a.E, KB, x0, x1); g.more() && ok; g.next()) {
       const uint32_t idesc = idesc_e4m3_f32(128, qceil(g.n, 16) * 16);
       for (int kb = g.kb0; kb < g.kb1 && ok; kb += C::KS) {
-        ok = mbar_wait(&ctl.full[s], phase, Q_WAIT_NS, abort_flag) && mbar_wait(&ctl.tempty[b], tphase, Q_WAIT_NS, abort_flag);
+        ok = mbar_wait(&ctl.full[s], phase, a.wait, abort_flag) && mbar_wait(&ctl.tempty[b], tphase, a.wait, abort_flag);
         if (!ok) break;
         tc_fence_after();
         if (leader) {
@@ -330,7 +336,7 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0) + HAND, 1)
     if (!ok && leader) fail();
     if (leader) umma_commit(&ctl.drain);
     volatile int never = 0;
-    if (!mbar_wait(&ctl.drain, 0, Q_DRAIN_NS, &never) && leader) fail();
+    if (!mbar_wait(&ctl.drain, 0, Q_DRAIN, &never) && leader) fail();
     __syncwarp();
   } else if (ROWS && warp >= 10 && warp < HAND_WARP) {
     // ------------------------------------------------------------ rows (warps 10..17): eight lanes to a row, two teams
@@ -415,7 +421,7 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0) + HAND, 1)
     for (int i = 0; i < team && g.more(); ++i) step(), ring_step();
     if (g.more()) load(raw, kb, g.kb1 - kb);
     while (g.more()) {
-      ok = __all_sync(0xffffffffu, mbar_wait(&ctl.empty[s], phase, Q_WAIT_NS, abort_flag));
+      ok = __all_sync(0xffffffffu, mbar_wait(&ctl.empty[s], phase, a.wait, abort_flag));
       if (!ok) break;
       write(raw, smem + s * C::STAGE, smem + C::S_OFF + slot * C::SLOT);
       __syncwarp();
@@ -512,7 +518,9 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0) + HAND, 1)
           for (int c = 0; c < NC; ++c)
 #pragma unroll
             for (int j = 0; j < CH / 2; ++j) acc[p][c][j] = make_float2(0.f, 0.f);
-        bool ok = true;  // once a wait has run out the rest of the run is gone through without waiting
+        // once a wait has run out the rest of the run is gone through without waiting, and nobody is told that a
+        // buffer has been read
+        bool ok = true;
         int i = 0;
         for (int kb = g.kb0; kb < g.kb1; kb += C::KS) {
           if ((i & 31) == 0) {
@@ -527,8 +535,8 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0) + HAND, 1)
           const float4* sx0 = reinterpret_cast<const float4*>(smem + C::S_OFF + slot * C::SLOT + n0 * 4);
           const float4* sx1 = sx0 + (GATED ? 0 : C::S_BYTES / 16);
           const uint32_t taddr = lane_base + b * static_cast<uint32_t>(2 * NT);
-          ok = ok && mbar_wait(&ctl.sfull[slot], sphase, Q_WAIT_NS, abort_flag) &&
-               mbar_wait(&ctl.tfull[b], tphase, Q_WAIT_NS, abort_flag);
+          ok = ok && mbar_wait(&ctl.sfull[slot], sphase, a.wait, abort_flag) &&
+               mbar_wait(&ctl.tfull[b], tphase, a.wait, abort_flag);
           tc_fence_after();
           // (all chunks on their way together where the registers hold them)
           constexpr int LC = GATED && NT == 64 ? 1 : NC;
@@ -569,7 +577,7 @@ __global__ void __launch_bounds__(THREADS + (ROWS ? ROW_THREADS : 0) + HAND, 1)
           }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl.tempty[b]);  // (and the slot of the scales has been read)
+          if (ok && lane == 0) mbar_arrive(&ctl.tempty[b]);  // (and the slot of the scales has been read)
           if (++b == C::BUFS) b = 0, tphase ^= 1;
           if (++slot == C::SLOTS) slot = 0, sphase ^= 1;
         }

@@ -90,6 +90,7 @@ struct pop_qlinear {
   float* parts = nullptr;
   unsigned* done = nullptr;
   unsigned* err = nullptr;
+  QWait wait;
   int num_sms = 1;
 };
 
@@ -104,6 +105,7 @@ struct pop_qmoe {
   float* parts = nullptr;
   unsigned* done = nullptr;
   unsigned* err = nullptr;
+  QWait wait;
   int num_sms = 1;
 };
 
@@ -233,6 +235,7 @@ pop_status linear_call(pop_qlinear* h, QRowsArgs in, size_t row_bytes, int M, vo
     g.parts = h->parts;
     g.done = h->done;
     g.err = h->err;
+    g.wait = h->wait;
     g.num_sms = h->num_sms;
     e = launch_qgemm(g, false, st);
     if (e != cudaSuccess) return q_cuda(e, call);
@@ -357,6 +360,12 @@ pop_status pop_qlinear_forward_quantized(pop_qlinear_t h, const void* xq, long l
     return q_fail(POP_ERR_INVALID_ARG, call, "xq must be 8-byte aligned, ldq >= K a multiple of 8");
   QRowsArgs in{xq, ldq, 2, xs, lds, M, h->cfg.K};
   return linear_call(h, in, 1, M, y, ldy, static_cast<cudaStream_t>(stream), call);
+}
+
+pop_status pop_qlinear_set_wait_limit(pop_qlinear_t h, uint64_t ns) {
+  if (!h || ns == 0) return q_fail(POP_ERR_INVALID_ARG, "pop_qlinear_set_wait_limit", "NULL handle or zero limit");
+  h->wait = QWait(ns);
+  return POP_OK;
 }
 
 pop_status pop_qlinear_check(pop_qlinear_t h) {
@@ -504,6 +513,7 @@ pop_status pop_qmoe_forward(pop_qmoe_t m, const void* x, long long ldx, const in
     g.parts = m->parts;
     g.done = m->done;
     g.err = m->err;
+    g.wait = m->wait;
     g.num_sms = m->num_sms;
     e = launch_qgemm(g, true, st);
     if (e != cudaSuccess) return q_cuda(e, call);
@@ -526,6 +536,12 @@ pop_status pop_qmoe_forward(pop_qmoe_t m, const void* x, long long ldx, const in
                        static_cast<uint8_t*>(y) + static_cast<size_t>(t0) * ldy * (c.out_f32 ? 4 : 2), ldy, c.out_f32, st);
     if (e != cudaSuccess) return q_cuda(e, call);
   }
+  return POP_OK;
+}
+
+pop_status pop_qmoe_set_wait_limit(pop_qmoe_t m, uint64_t ns) {
+  if (!m || ns == 0) return q_fail(POP_ERR_INVALID_ARG, "pop_qmoe_set_wait_limit", "NULL handle or zero limit");
+  m->wait = QWait(ns);
   return POP_OK;
 }
 

@@ -225,7 +225,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
           if (s == STAGES) s = 0, phase ^= 1;
         }
         for (; kb < v.kb1; ++kb) {
-          if (!mbar_wait(&ctl.empty[s], phase, Q_WAIT_NS, abort_flag)) {
+          if (!mbar_wait(&ctl.empty[s], phase, a.wait, abort_flag)) {
             fail();
             ok = false;
             break;
@@ -240,12 +240,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
           if (++s == STAGES) s = 0, phase ^= 1;
         }
       }
-      // no copy of this CTA may be in flight when it exits. (The first CTA's barriers also wait for the second;
-      // one that gave up before its last copies' news is covered by its own limit.)
+      // no copy of this CTA may be in flight when it exits. (The first CTA's barriers also wait for word of the second,
+      // which does not come if that one has given up; the copies have had their time when one such wait has run out.)
       const uint32_t lo = issued > STAGES ? issued - STAGES : 0;
       for (uint32_t i = lo; i < issued; ++i) {
         volatile int never = 0;
-        if (!mbar_wait(&ctl.full[i % STAGES], (i / STAGES) & 1u, Q_DRAIN_NS, &never)) fail();
+        if (!mbar_wait(&ctl.full[i % STAGES], (i / STAGES) & 1u, Q_DRAIN, &never)) {
+          fail();
+          break;
+        }
       }
     }
     if (warp & 1) {
@@ -260,8 +263,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
         const uint32_t a0 = desc_lo(smem_u32(smem)), b0 = desc_lo(smem_u32(smem) + A_BYTES + h * (QTILE / 2));
         for (uint32_t it = 0; it < total; ++it) {
           const uint32_t b = it & 1u;
-          if (!mbar_wait(&ctl.full[s], phase, Q_WAIT_NS, abort_flag) ||
-              !mbar_wait(&ctl.tempty[h][b], ((it >> 1) & 1u) ^ 1u, Q_WAIT_NS, abort_flag)) {
+          if (!mbar_wait(&ctl.full[s], phase, a.wait, abort_flag) ||
+              !mbar_wait(&ctl.tempty[h][b], ((it >> 1) & 1u) ^ 1u, a.wait, abort_flag)) {
             if (leader) fail();
             break;
           }
@@ -276,11 +279,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
         }
         if (leader) umma_commit_pair(&ctl.drain[h]);
         volatile int never = 0;
-        if (!mbar_wait(&ctl.drain[h], 0, Q_DRAIN_NS, &never) && leader) fail();
+        if (!mbar_wait(&ctl.drain[h], 0, Q_DRAIN, &never) && leader) fail();
       } else if (warp == 1) {
         // -------------------------------------------------------- word of this CTA's operands
         for (uint32_t it = 0; it < total; ++it) {
-          if (!mbar_wait(&ctl.full[s], phase, Q_WAIT_NS, abort_flag)) {
+          if (!mbar_wait(&ctl.full[s], phase, a.wait, abort_flag)) {
             if (leader) fail();
             break;
           }
@@ -309,7 +312,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
           w1 = ws + static_cast<size_t>(min(2 * t.n + 1, NT - 1)) * scale_stride(KB, 1);
         }
         for (int kb = v.kb0; kb < v.kb1; kb += SB) {
-          if (!mbar_wait(&ctl.sempty[g], phase, Q_WAIT_NS, abort_flag)) {
+          if (!mbar_wait(&ctl.sempty[g], phase, a.wait, abort_flag)) {
             fail();
             ok = false;
             break;
@@ -332,7 +335,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
       const uint32_t lo = issued > SRING ? issued - SRING : 0;
       for (uint32_t i = lo; i < issued; ++i) {
         volatile int never = 0;
-        if (!mbar_wait(&ctl.sfull[i % SRING], (i / SRING) & 1u, Q_DRAIN_NS, &never)) fail();
+        if (!mbar_wait(&ctl.sfull[i % SRING], (i / SRING) & 1u, Q_DRAIN, &never)) {
+          fail();
+          break;
+        }
       }
     }
     __syncwarp();
@@ -349,14 +355,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
     const uint32_t tempty0 = first_cta(&ctl.tempty[half][0]), tempty1 = first_cta(&ctl.tempty[half][1]);
     uint32_t b = 0, tphase = 0, g = 0, gphase = 0;
     int parity = 0;
-    bool ok = true;  // once a wait has run out the rest of the tile is gone through without waiting
+    // once a wait has run out the rest of the tile is gone through without waiting, and nobody is told that a buffer or
+    // scales have been read
+    bool ok = true;
     for (Walk v(tiles, pair, pairs, KB); v.more(); v.advance(), parity ^= 1) {
       const Tile t = tile_at(ctl.groups, a.E, v.tile, rank);
       float2 acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = make_float2(0.f, 0.f);
       for (int kb = v.kb0; kb < v.kb1; kb += SB) {
-        ok = ok && mbar_wait(&ctl.sfull[g], gphase, Q_WAIT_NS, abort_flag);
+        ok = ok && mbar_wait(&ctl.sfull[g], gphase, a.wait, abort_flag);
         const float* xg = &ctl.scales[g].x[0][r];
         const float* wg = ctl.scales[g].w;
         const int n = min(SB, v.kb1 - kb);
@@ -366,7 +374,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
           // the next k-block's scales are read before this one's product is waited for
           const int jn = j & (SB - 1);
           const float x = xg[jn * BM], w0 = wg[GATED ? 2 * jn : jn], w1 = wg[GATED ? 2 * jn + 1 : SB + jn];
-          ok = ok && mbar_wait(&ctl.tfull[half][b], tphase, Q_WAIT_NS, abort_flag);
+          ok = ok && mbar_wait(&ctl.tfull[half][b], tphase, a.wait, abort_flag);
           tc_fence_after();
           const uint32_t taddr = lane_base + b * 256u;
           // sixteen columns on their way while the sixteen before are added: more in flight would not fit beside
@@ -381,7 +389,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
             } else {
               tc_fence_before();
               __syncwarp();
-              if (lane == 0) mbar_arrive_first(b ? tempty1 : tempty0);
+              if (ok && lane == 0) mbar_arrive_first(b ? tempty1 : tempty0);
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -392,7 +400,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
           tphase ^= b ^ 1u;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.sempty[g]);
+        if (ok && lane == 0) mbar_arrive(&ctl.sempty[g]);
         if (++g == SRING) g = 0, gphase ^= 1;
       }
       ok = __all_sync(0xffffffffu, ok);
