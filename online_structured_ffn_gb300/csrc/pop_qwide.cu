@@ -355,8 +355,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
     const uint32_t tempty0 = first_cta(&ctl.tempty[half][0]), tempty1 = first_cta(&ctl.tempty[half][1]);
     uint32_t b = 0, tphase = 0, g = 0, gphase = 0;
     int parity = 0;
-    // once a wait has run out the rest of the tile is gone through without waiting, and nobody is told that a buffer or
-    // scales have been read
+    // Once a wait has run out the rest of the tile is gone through without waiting, and nobody is told that a buffer or
+    // scales have been read. Where the eight warps meet at a barrier anyway, all leave together; a whole plain tile has
+    // none, so there a warp goes on without storing, to where a split tile's barriers count on it.
     bool ok = true;
     for (Walk v(tiles, pair, pairs, KB); v.more(); v.advance(), parity ^= 1) {
       const Tile t = tile_at(ctl.groups, a.E, v.tile, rank);
@@ -441,7 +442,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_qgemm_
           }
         }
       } else if (!GATED && !ok) {
-        break;
+        continue;
       }
       const bool valid = r < t.rows;
       const int row = t.row0 + r;

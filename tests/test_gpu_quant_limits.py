@@ -1,5 +1,5 @@
 """Waits of the 8-bit products that run out: with a limit of 1 ns every wait that is not over within its first tries
-does. The kernels record it and return, well within the seconds that each of their other waits may take, and the check
+does (which needs more than a few k-blocks: with one or two of them none is that long). The kernels record it and return, well within the seconds that each of their other waits may take, and the check
 reports it once."""
 import time
 
@@ -59,3 +59,15 @@ def test_a_limit_of_nothing_is_refused(env):
     with pytest.raises(pop.PopError) as e:
         h.set_wait_limit(0)
     assert e.value.status == pop.POP_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("M,N,K", [(2560, 2048, 9728), (2560, 2304, 4096)])
+def test_product_of_many_rows_gives_up(env, M, N, K):
+    """The wide plain product. 80 tiles over 76 pairs: of 76 k-blocks, so that a pair's whole tile, where its eight
+    epilogue warps do not meet, is followed by a run of the four that are split, where they do; and 90 whole ones of 32."""
+    pop, torch, dev = env
+    h = pop.PopQLinear((rows(env, 5, N, K, "f32") * 0.05).to(torch.bfloat16), max_tokens=M, out_f32=True)
+    x = rows(env, 6, M, K)
+    for _ in range(3):
+        give_up(env, h, lambda: h.forward(x))
+    h.close()
