@@ -77,11 +77,12 @@ pop_status pop_qlinear_forward_quantized(pop_qlinear_t h, const void* xq, long l
                                          long long lds, int M, void* y, long long ldy, void* stream);
 
 /* Limit, in nanoseconds, for every device-side wait of this handle's products (default 2 s). A wait that runs
- * out is recorded (POP_ERR_TIMEOUT from the check below) and the kernel returns; the call's output is then
- * not valid. ns >= 1. */
+ * out is recorded (POP_ERR_TIMEOUT from the check below) and the kernel returns. The outputs of that call
+ * and of the calls after it are not valid until the check has reported it; then the handle is as new. ns >= 1. */
 pop_status pop_qlinear_set_wait_limit(pop_qlinear_t h, uint64_t ns);
 
-/* Synchronizes the device and returns the first recorded device-side failure, or POP_OK; clears it. */
+/* Synchronizes the device and returns the first recorded device-side failure, or POP_OK; clears it, with
+ * what a wait that ran out has left in the handle. */
 pop_status pop_qlinear_check(pop_qlinear_t h);
 
 /* ---- gated-MLP experts: y_t = sum over j of w[t, j] * W2_e (quantised(SiLU(Wg_e x_t) (.) W1_e x_t)),
@@ -116,7 +117,7 @@ pop_status pop_qmoe_forward(pop_qmoe_t m, const void* x, long long ldx, const in
 /* As pop_qlinear_set_wait_limit. */
 pop_status pop_qmoe_set_wait_limit(pop_qmoe_t m, uint64_t ns);
 
-/* Synchronizes the device and returns the first recorded device-side failure, or POP_OK; clears it. */
+/* As pop_qlinear_check. */
 pop_status pop_qmoe_check(pop_qmoe_t m);
 
 #ifdef __cplusplus

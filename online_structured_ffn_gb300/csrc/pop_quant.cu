@@ -43,14 +43,17 @@ int sm_count() {
 
 constexpr long long MAX_ROWS = 1ll << 27;
 
-// The device error word's first failure.
-pop_status check_word(unsigned* err, const char* call) {
+// The device error word's first failure. After a wait that ran out the tiles' counters hold what the CTAs that gave up
+// left unfinished: they are cleared with it, or later calls would sum parts that are not there yet.
+pop_status check_word(unsigned* err, unsigned* done, size_t counters, const char* call) {
   cudaError_t e = cudaDeviceSynchronize();
   unsigned w = 0;
   if (e == cudaSuccess) e = cudaMemcpy(&w, err, sizeof(w), cudaMemcpyDeviceToHost);
   if (e != cudaSuccess) return q_cuda(e, call);
   if (!w) return POP_OK;
-  e = cudaMemset(err, 0, sizeof(w));
+  if (w & pop::QERR_TIMEOUT) e = cudaMemset(done, 0, counters * sizeof(unsigned));
+  if (e == cudaSuccess) e = cudaMemset(err, 0, sizeof(w));
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();  // later calls may come on streams that do not wait for this one
   if (e != cudaSuccess) return q_cuda(e, call);
   if (w & pop::QERR_TIMEOUT) return q_fail(POP_ERR_TIMEOUT, call, "a wait of a product ran out");
   return q_fail(POP_ERR_DEVICE, call, "an expert index outside [-1, n_experts)");
@@ -89,6 +92,7 @@ struct pop_qlinear {
   float* act_s = nullptr;
   float* parts = nullptr;
   unsigned* done = nullptr;
+  size_t counters = 0;     // of done
   unsigned* err = nullptr;
   QWait wait;
   int num_sms = 1;
@@ -104,6 +108,7 @@ struct pop_qmoe {
   float* o = nullptr;      // [rows][D] outputs of the experts
   float* parts = nullptr;
   unsigned* done = nullptr;
+  size_t counters = 0;     // of done
   unsigned* err = nullptr;
   QWait wait;
   int num_sms = 1;
@@ -298,7 +303,7 @@ pop_status pop_qlinear_create(const pop_qlinear_config* cfg, const void* W, cons
   if (e == cudaSuccess) e = dalloc(&h->ws, NT * scale_stride(KB, 1) + SCALE_PAD);
   if (e == cudaSuccess) e = dalloc(&h->act, rows * KB * QB);
   if (e == cudaSuccess) e = dalloc(&h->act_s, rows * KB);
-  const size_t counters = tile_counters(cfg->max_tokens, cfg->max_tokens < 32 ? cfg->max_tokens : 32, 1, NT, h->num_sms);
+  const size_t counters = h->counters = tile_counters(cfg->max_tokens, cfg->max_tokens < 32 ? cfg->max_tokens : 32, 1, NT, h->num_sms);
   bool wide = false;
   for (int m = 1; m <= cfg->max_tokens && !wide; ++m) wide = linear_granule(*cfg, m, h->num_sms) == 128;
   if (e == cudaSuccess) e = dalloc(&h->parts, part_floats(wide, false, h->num_sms));
@@ -370,7 +375,7 @@ pop_status pop_qlinear_set_wait_limit(pop_qlinear_t h, uint64_t ns) {
 
 pop_status pop_qlinear_check(pop_qlinear_t h) {
   if (!h) return q_fail(POP_ERR_INVALID_ARG, "pop_qlinear_check", "NULL handle");
-  return check_word(h->err, "pop_qlinear_check");
+  return check_word(h->err, h->done, h->counters, "pop_qlinear_check");
 }
 
 // -------------------------------------------------------------------------------- experts
@@ -422,7 +427,7 @@ pop_status pop_qmoe_create(const pop_qmoe_config* cfg, const void* const* Wg, co
   if (e == cudaSuccess) e = dalloc(&m->h_s, rows * NT);
   if (e == cudaSuccess) e = dalloc(&m->o, static_cast<size_t>(rows) * cfg->D);
   const long long few = static_cast<long long>(cfg->max_tokens < 32 ? cfg->max_tokens : 32) * cfg->top_k;
-  const size_t counters = tile_counters(pairs, few, E, NT > DT ? NT : DT, m->num_sms);
+  const size_t counters = m->counters = tile_counters(pairs, few, E, NT > DT ? NT : DT, m->num_sms);
   if (e == cudaSuccess) e = dalloc(&m->parts, part_floats(wide, true, m->num_sms));
   if (e == cudaSuccess) e = dalloc(&m->done, counters);
   if (e == cudaSuccess) e = dalloc(&m->err, 1);
@@ -547,7 +552,7 @@ pop_status pop_qmoe_set_wait_limit(pop_qmoe_t m, uint64_t ns) {
 
 pop_status pop_qmoe_check(pop_qmoe_t m) {
   if (!m) return q_fail(POP_ERR_INVALID_ARG, "pop_qmoe_check", "NULL handle");
-  return check_word(m->err, "pop_qmoe_check");
+  return check_word(m->err, m->done, m->counters, "pop_qmoe_check");
 }
 
 }  // extern "C"
