@@ -433,18 +433,22 @@ pop_status pop_route(const pop_route_config* cfg, const void* logits, int logits
     return bad("pop_route: renorm must be 0 or 1, scale finite");
   if (logits_bf16 != 0 && logits_bf16 != 1) return bad("pop_route: logits_bf16 must be 0 or 1");
   if (T < 0 || T > (1 << 27)) return bad("pop_route: T outside [0, 2^27]");
-  if (T == 0) return POP_OK;
-  if (!logits || !experts || !weights) return bad("pop_route: NULL logits, experts or weights");
-  if (ld_logits < c.n_experts) return bad("pop_route: ld_logits < n_experts");
   const auto off = [](const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; };
-  if (off(logits, logits_bf16 ? 2 : 4) || off(bias, 4) || off(experts, 4) || off(weights, 4) || off(counts, 4))
-    return bad("pop_route: a pointer is not aligned to its element");
+  if (T == 0 && !counts) return POP_OK;
+  if (T > 0) {
+    if (!logits || !experts || !weights) return bad("pop_route: NULL logits, experts or weights");
+    if (ld_logits < c.n_experts) return bad("pop_route: ld_logits < n_experts");
+    if (off(logits, logits_bf16 ? 2 : 4) || off(bias, 4) || off(experts, 4) || off(weights, 4))
+      return bad("pop_route: a pointer is not aligned to its element");
+  }
+  if (off(counts, 4)) return bad("pop_route: counts is not aligned to its element");
   const pop_status dev = device_supported();
   if (dev != POP_OK) return route_fail(dev, "pop_route: needs an sm_103 device");
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   if (counts) e = cudaMemsetAsync(counts, 0, sizeof(int) * c.n_experts, st);
   if (e != cudaSuccess) return route_fail(POP_ERR_CUDA, cudaGetErrorString(e));
+  if (T == 0) return POP_OK;  // no slots: the counts are 0
   RouteArgs a{logits,       ld_logits,   bias,     T,       c.n_experts, c.top_k, c.score == POP_ROUTE_SIGMOID,
               c.n_groups,   c.top_groups, c.group_sum, c.renorm, c.scale,     experts, weights,
               counts};
