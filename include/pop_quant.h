@@ -20,6 +20,8 @@
  *
  * Conventions are those of pop_ffn.h (device pointers 16-byte aligned unless stated; stream-ordered
  * calls; status returns; device failures from the _check calls; a handle's calls must not overlap).
+ * Everything a call is given lies on the current device. A handle belongs to the device that was current when
+ * it was made, and its calls are refused (INVALID_ARG) while another one is.
  * Rows of x and y may lie farther apart than their length (ldx, ldy, in elements); the rows' starts
  * must be 16-byte aligned (8-byte for e4m3 rows), so the strides are multiples of 8 (bf16, e4m3) or 4
  * (float32) elements. Zero rows are allowed and do nothing.

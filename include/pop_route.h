@@ -44,7 +44,7 @@ typedef struct {
   float scale;     /* finite */
 } pop_route_config;
 
-/* Routes T tokens (T >= 0; with 0 only counts is written).
+/* Routes T tokens (T >= 0; with 0 only counts is written), on the current device, where all that is given lies.
  *   logits: device [T, E], float32 (logits_bf16 = 0) or bf16 (1), rows ld_logits >= E elements apart,
  *           aligned to its element.
  *   bias:   device float32 [E], or NULL.

@@ -532,16 +532,38 @@ def _whole_arg(t, name, dtype, shape):
              f"{tuple(t.shape)} on {t.device}")
 
 
-def _on(stream, t, *others):
-    """The stream of a call on t's device: (raw handle, what new outputs are to be made under, or None for the
-    current stream). New outputs belong to the call's stream, and inputs that another stream allocated are
-    not given to others before it is done with them."""
+_gpus = None  # that this process sees, once it has been asked
+
+
+def _one_device(t, *others):
+    """Checks that all of a call's tensors are on the current device: the library launches there."""
+    global _gpus
     import torch
-    raw = torch._C._cuda_getCurrentRawStream(t.get_device())
+    if _gpus is None:
+        _gpus = torch.cuda.device_count()
+    dev = t.get_device()
+    for x in others:
+        if x is not None and x.get_device() != dev:
+            _bad(f"tensors of one call on {t.device} and {x.device}")
+    if dev != torch._C._cuda_getDevice():
+        _bad(f"tensors on {t.device}, which is not the current device")
+
+
+def _on(stream, t, *others):
+    """The stream of a call, whose tensors are all on the current device: (raw handle, what new outputs are to be
+    made under, or None for the current stream). New outputs belong to the call's stream, and inputs that another
+    stream allocated are not given to others before it is done with them."""
+    import torch
+    dev = t.get_device()
+    if _gpus != 1:  # (with one there is no other, and the check takes a fraction of a microsecond)
+        _one_device(t, *others)
+    raw = torch._C._cuda_getCurrentRawStream(dev)
     if stream is None:
         return raw, None
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
+    if stream.device_index != dev:
+        _bad(f"a stream of cuda:{stream.device_index} for tensors on cuda:{dev}")
     if stream.cuda_stream == raw:
         return raw, None
     for x in (t, *others):
@@ -681,6 +703,7 @@ class PopQLinear(_QHandle):
 
     def __init__(self, W, S=None, max_tokens: int = 2048, out_f32: bool = False, stream=None):
         _matrix_arg(W, S, "W")
+        _one_device(W, S)
         self.N, self.K = W.shape
         self.cfg = pop_qlinear_config(N=self.N, K=self.K, max_tokens=max_tokens, out_f32=1 if out_f32 else 0)
         h = _vp()
@@ -739,6 +762,7 @@ class PopQMoE(_QHandle):
                 _matrix_arg(m, s, name)
                 if tuple(m.shape) != shape:
                     _bad(f"{name}: expected matrices of shape {shape}, got {tuple(m.shape)}")
+        _one_device(*(t for ts in mats + scales for t in ts))
         self.cfg = pop_qmoe_config(n_experts=self.E, top_k=top_k, D=self.D, D_FF=self.N, max_tokens=max_tokens,
                                    out_f32=1 if out_f32 else 0)
         arrays = [(_vp * self.E)(*[_ptr(m) for m in ms]) for ms in mats]

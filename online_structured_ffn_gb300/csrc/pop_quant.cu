@@ -41,6 +41,29 @@ int sm_count() {
   return n > 0 ? n : 1;
 }
 
+int current_device() {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess ? dev : -1;
+}
+
+// A handle's calls launch on the current device, with its pointers.
+pop_status same_device(int device, const char* call) {
+  if (current_device() == device) return POP_OK;
+  return q_fail(POP_ERR_INVALID_ARG, call, "the handle was made on another device than the current one");
+}
+
+// Makes a device the current one for as long as it lives.
+struct OnDevice {
+  int was;
+  explicit OnDevice(int device) : was(current_device()) {
+    if (was != device) cudaSetDevice(device);
+    else was = -1;
+  }
+  ~OnDevice() {
+    if (was >= 0) cudaSetDevice(was);
+  }
+};
+
 constexpr long long MAX_ROWS = 1ll << 27;
 
 // The device error word's first failure. After a wait that ran out the tiles' counters hold what the CTAs that gave up
@@ -84,7 +107,7 @@ pop_status device_supported() {
 
 using namespace pop;
 
-struct pop_qlinear {
+struct pop_qlinear {  // (the pointers are of `device`)
   pop_qlinear_config cfg;
   uint8_t* w = nullptr;    // matrix image
   float* ws = nullptr;
@@ -95,6 +118,7 @@ struct pop_qlinear {
   size_t counters = 0;     // of done
   unsigned* err = nullptr;
   QWait wait;
+  int device = 0;
   int num_sms = 1;
 };
 
@@ -111,6 +135,7 @@ struct pop_qmoe {
   size_t counters = 0;     // of done
   unsigned* err = nullptr;
   QWait wait;
+  int device = 0;
   int num_sms = 1;
 };
 
@@ -296,6 +321,7 @@ pop_status pop_qlinear_create(const pop_qlinear_config* cfg, const void* W, cons
   pop_qlinear* h = new (std::nothrow) pop_qlinear();
   if (!h) return q_fail(POP_ERR_OOM, call, "out of host memory");
   h->cfg = *cfg;
+  h->device = current_device();
   h->num_sms = sm_count();
   const size_t rows = static_cast<size_t>(qceil(cfg->max_tokens, 128)) * 128;
   const size_t NT = qceil(cfg->N, QB), KB = qceil(cfg->K, QB);
@@ -326,6 +352,7 @@ pop_status pop_qlinear_create(const pop_qlinear_config* cfg, const void* W, cons
 
 void pop_qlinear_destroy(pop_qlinear_t h) {
   if (!h) return;
+  const OnDevice on(h->device);
   cudaDeviceSynchronize();
   free_linear(h);
   delete h;
@@ -338,7 +365,7 @@ static pop_status linear_check_y(const pop_qlinear* h, int M, const void* x, con
   if (!x || !y) return q_fail(POP_ERR_INVALID_ARG, call, "NULL x or y");
   if (ldy < h->cfg.N) return q_fail(POP_ERR_INVALID_ARG, call, "ldy < N");
   if (off(y, h->cfg.out_f32 ? 4 : 2)) return q_fail(POP_ERR_INVALID_ARG, call, "y is not aligned to its element");
-  return POP_OK;
+  return same_device(h->device, call);
 }
 
 pop_status pop_qlinear_forward(pop_qlinear_t h, const void* x, long long ldx, int M, void* y, long long ldy,
@@ -375,6 +402,7 @@ pop_status pop_qlinear_set_wait_limit(pop_qlinear_t h, uint64_t ns) {
 
 pop_status pop_qlinear_check(pop_qlinear_t h) {
   if (!h) return q_fail(POP_ERR_INVALID_ARG, "pop_qlinear_check", "NULL handle");
+  if (const pop_status s = same_device(h->device, "pop_qlinear_check"); s != POP_OK) return s;
   return check_word(h->err, h->done, h->counters, "pop_qlinear_check");
 }
 
@@ -406,6 +434,7 @@ pop_status pop_qmoe_create(const pop_qmoe_config* cfg, const void* const* Wg, co
   pop_qmoe* m = new (std::nothrow) pop_qmoe();
   if (!m) return q_fail(POP_ERR_OOM, call, "out of host memory");
   m->cfg = *cfg;
+  m->device = current_device();
   m->num_sms = sm_count();
   const long long pairs = static_cast<long long>(cfg->max_tokens) * cfg->top_k;
   const long long used = pairs < E ? pairs : E;  // experts that can have rows
@@ -456,6 +485,7 @@ pop_status pop_qmoe_create(const pop_qmoe_config* cfg, const void* const* Wg, co
 
 void pop_qmoe_destroy(pop_qmoe_t m) {
   if (!m) return;
+  const OnDevice on(m->device);
   cudaDeviceSynchronize();
   free_qmoe(m);
   delete m;
@@ -473,6 +503,7 @@ pop_status pop_qmoe_forward(pop_qmoe_t m, const void* x, long long ldx, const in
   if (off(x, 16) || ldx < c.D || ldx % 8) return bad("x must be 16-byte aligned, ldx >= D a multiple of 8");
   if (off(y, 16) || ldy < c.D || ldy % (c.out_f32 ? 4 : 8)) return bad("y's rows must be 16-byte aligned, ldy >= D");
   if (off(experts, 4) || off(weights, 4)) return bad("experts or weights is not aligned to its element");
+  if (const pop_status s = same_device(m->device, call); s != POP_OK) return s;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const size_t NT = qceil(c.D_FF, QB), DT = qceil(c.D, QB);
   for (int t0 = 0; t0 < T; t0 += c.max_tokens) {
@@ -552,6 +583,7 @@ pop_status pop_qmoe_set_wait_limit(pop_qmoe_t m, uint64_t ns) {
 
 pop_status pop_qmoe_check(pop_qmoe_t m) {
   if (!m) return q_fail(POP_ERR_INVALID_ARG, "pop_qmoe_check", "NULL handle");
+  if (const pop_status s = same_device(m->device, "pop_qmoe_check"); s != POP_OK) return s;
   return check_word(m->err, m->done, m->counters, "pop_qmoe_check");
 }
 
