@@ -18,6 +18,16 @@
 
 namespace pop {
 
+// Launches a kernel. The status is this launch's own; cudaGetLastError would also give what an earlier call has left.
+template <class K, class... Args>
+cudaError_t launch_plain(K kernel, dim3 grid, int block, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.stream = st;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // POP_OK if the current device is a GB300 (sm_103). Looked up once per device.
 pop_status device_supported();
 

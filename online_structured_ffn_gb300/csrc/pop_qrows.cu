@@ -386,8 +386,7 @@ cudaError_t launch_quantize_rows(const QRowsArgs& in, const QRowsOut& out, cudaS
 
 cudaError_t launch_pack_matrix(const void* W, const float* Ws, int N, int K, uint8_t* img, float* s, int step,
                                int part, cudaStream_t st) {
-  k_pack_matrix<<<dim3(qceil(K, QB), qceil(N, QB)), 256, 0, st>>>(W, Ws, N, K, img, s, step, part);
-  return cudaGetLastError();
+  return launch_plain(k_pack_matrix, dim3(qceil(K, QB), qceil(N, QB)), 256, st, W, Ws, N, K, img, s, step, part);
 }
 
 cudaError_t launch_plan(const int* experts, int pairs, int E, int G, int* counts, int* row_of, unsigned* err,

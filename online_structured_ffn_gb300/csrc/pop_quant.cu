@@ -24,6 +24,7 @@ pop_status q_fail(pop_status s, const char* call, const char* why) noexcept {
 
 pop_status q_cuda(cudaError_t e, const char* call) noexcept {
   if (e == cudaSuccess) return POP_OK;
+  cudaGetLastError();  // it is reported here: a later call that asks the runtime for the last error is not to find it
   return q_fail(e == cudaErrorMemoryAllocation ? POP_ERR_OOM : POP_ERR_CUDA, call, cudaGetErrorString(e));
 }
 

@@ -380,11 +380,7 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t st) {
   // four values a load where rows and runs of four start on such a boundary and end with the experts
   const bool vec = a.E % 4 == 0 && a.ld % 4 == 0 && reinterpret_cast<uintptr_t>(a.logits) % (BF16 ? 8 : 16) == 0 &&
                    reinterpret_cast<uintptr_t>(a.bias) % 16 == 0;
-  if (vec)
-    k_route<BF16, UNIQUE, L, V, true><<<grid, 32 * RT_WARPS, 0, st>>>(a);
-  else
-    k_route<BF16, UNIQUE, L, V, false><<<grid, 32 * RT_WARPS, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_plain(vec ? k_route<BF16, UNIQUE, L, V, true> : k_route<BF16, UNIQUE, L, V, false>, dim3(grid), 32 * RT_WARPS, st, a);
 }
 
 template <bool BF16, bool UNIQUE>
@@ -400,6 +396,7 @@ cudaError_t launch_route(const RouteArgs& a, cudaStream_t st) {
 thread_local std::string g_route_msg;
 
 pop_status route_fail(pop_status s, const char* msg) {
+  if (s == POP_ERR_CUDA) cudaGetLastError();  // it is reported here: a later call is not to find it
   try {
     g_route_msg = msg;
   } catch (...) {
