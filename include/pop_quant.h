@@ -44,7 +44,8 @@ extern "C" {
 const char* pop_quant_last_error(void);
 
 /* Quantises M rows of K values. x: device bf16 (x_f32 = 0) or float32 (1), rows ldx elements apart;
- * q: device e4m3, rows ldq bytes apart; s: device float32 [M, ceil(K/128)]. K: a multiple of 8, >= 8. */
+ * q: device e4m3, rows ldq bytes apart; s: device float32 [M, ceil(K/128)]. K: a multiple of 8, 8 to
+ * 2^28 - 4096. */
 pop_status pop_quantize_rows(const void* x, int x_f32, long long ldx, int M, int K, void* q, long long ldq,
                              float* s, void* stream);
 

@@ -66,6 +66,7 @@ struct OnDevice {
 };
 
 constexpr long long MAX_ROWS = 1ll << 27;
+constexpr int MAX_ROW = 65535 * 32 * pop::QB;  // values that a grid's second dimension holds, of 32 blocks each
 
 // The device error word's first failure. After a wait that ran out the tiles' counters hold what the CTAs that gave up
 // left unfinished: they are cleared with it, or later calls would sum parts that are not there yet.
@@ -286,7 +287,7 @@ pop_status pop_quantize_rows(const void* x, int x_f32, long long ldx, int M, int
   const auto bad = [&](const char* why) { return q_fail(POP_ERR_INVALID_ARG, call, why); };
   if (x_f32 != 0 && x_f32 != 1) return bad("x_f32 must be 0 or 1");
   if (M < 0 || M > MAX_ROWS) return bad("M outside [0, 2^27]");
-  if (K < 8 || K % 8) return bad("K must be a positive multiple of 8");
+  if (K < 8 || K % 8 || K > MAX_ROW) return bad("K must be a multiple of 8 in [8, 2^28 - 4096]");
   if (M == 0) return POP_OK;
   if (!x || !q || !s) return bad("NULL x, q or s");
   if (off(x, 16) || off(q, 8) || off(s, 4)) return bad("x must be 16-byte aligned, q 8-byte, s 4-byte");

@@ -106,3 +106,10 @@ def test_tensors_of_another_device_are_refused(pop, monkeypatch):
 
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0, raising=False)
     refused(lambda: r.route(here, stream=Stream()))
+
+
+@pytest.mark.parametrize("K", [(1 << 28) - 4088, 1 << 28, (1 << 31) - 8])
+def test_rows_longer_than_a_grid_are_refused(pop, K):
+    lib = pop.load_library()
+    assert lib.pop_quantize_rows(4096, 0, K, 1, K, 4096, K, 4096, None) == pop.POP_ERR_INVALID_ARG
+    assert b"2^28" in lib.pop_quant_last_error()
