@@ -3,10 +3,10 @@
     python examples/moe_fp8.py                          # 8 experts of 4096 x 14336, top-2
     python examples/moe_fp8.py --experts 64 --dim 2048 --ff 1000 --top-k 6 --score sigmoid --groups 8
 
-The router's logits are a bf16 product of the tokens with a matrix of their own (``PopQLinear`` with as many outputs as
-there are experts); ``PopRouter`` chooses experts and weights, with a bias that evens out their load (moved after every
-batch against the counts, as a trainer would); ``PopQMoE`` runs the chosen experts. A prompt is followed by decode
-steps of a few tokens, the last of them replayed as a CUDA graph.
+The tokens come out of a projection in e4m3 (``PopQLinear``). The router's logits are a plain float32 product, as the choice
+of experts hangs on their order, which 8-bit operands would change; ``PopRouter`` chooses experts and weights, with
+a bias that evens out their load (moved after every batch against the counts, as a trainer would); ``PopQMoE`` runs the
+chosen experts. A prompt is followed by decode steps of a few tokens, the last of them replayed as a CUDA graph.
 """
 from __future__ import annotations
 
@@ -19,8 +19,24 @@ if ROOT not in sys.path:
     sys.path.insert(0, ROOT)
 
 
+def weights(g, n, k):
+    """A random bf16 matrix of N(0, 0.02^2)."""
+    import torch
+    return (torch.randn((n, k), generator=g, device="cuda") * 0.02).to(torch.bfloat16)
+
+
+class Gate:
+    """A token's logit for each expert, in float32."""
+
+    def __init__(self, w):
+        self.w = w.float().t().contiguous()
+
+    def forward(self, x):
+        return x.float() @ self.w
+
+
 class Block:
-    """Router and experts with random weights of N(0, 0.02^2)."""
+    """Router and experts with random weights."""
 
     def __init__(self, experts, dim, ff, top_k, score="softmax", groups=1, max_tokens=4096, seed=0):
         import torch
@@ -29,16 +45,15 @@ class Block:
         g = torch.Generator(device="cuda")
         g.manual_seed(seed)
 
-        def weights(n, k):
-            return (torch.randn((n, k), generator=g, device="cuda") * 0.02).to(torch.bfloat16)
+        def some(n, k):
+            return [weights(g, n, k) for _ in range(experts)]
 
-        self.gate = pop.PopQLinear(weights(experts, dim), max_tokens=max_tokens, out_f32=True)
+        self.gate = Gate(weights(g, experts, dim))
         self.router = pop.PopRouter(experts, top_k, score=score, n_groups=groups, top_groups=max(1, groups // 2),
                                     group_sum=2 if score == "sigmoid" and groups > 1 else 1)
         self.bias = torch.zeros((experts,), device="cuda") if score == "sigmoid" else None
         self.counts = torch.zeros((experts,), dtype=torch.int32, device="cuda")
-        self.ffn = pop.PopQMoE([weights(ff, dim) for _ in range(experts)], [weights(ff, dim) for _ in range(experts)],
-                               [weights(dim, ff) for _ in range(experts)], top_k=top_k, max_tokens=max_tokens)
+        self.ffn = pop.PopQMoE(some(ff, dim), some(ff, dim), some(dim, ff), top_k=top_k, max_tokens=max_tokens)
 
     def forward(self, x, balance=0.0):
         """x: bf16 [T, dim]. Returns (y bf16 [T, dim], experts, weights)."""
@@ -48,12 +63,13 @@ class Block:
         return self.ffn.forward(x, experts, weights), experts, weights
 
     def check(self):
-        self.gate.check()
         self.ffn.check()
 
 
 def main(argv=None):
     import torch
+
+    import online_structured_ffn_gb300 as pop
     p = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     p.add_argument("--experts", type=int, default=8)
     p.add_argument("--dim", type=int, default=4096)
@@ -68,6 +84,10 @@ def main(argv=None):
     block = Block(a.experts, a.dim, a.ff, a.top_k, a.score, a.groups, max_tokens=max(a.prompt, a.batch))
     g = torch.Generator(device="cuda")
     g.manual_seed(1)
+    before = pop.PopQLinear(weights(g, a.dim, a.dim), max_tokens=max(a.prompt, a.batch))
+
+    def step(x, balance=0.0):
+        return block.forward(before.forward(x), balance)
 
     def tokens(n):
         return torch.randn((n, a.dim), generator=g, device="cuda").to(torch.bfloat16)
@@ -83,16 +103,17 @@ def main(argv=None):
         print(f"{name}: {n} tokens in {start.elapsed_time(end) / a.steps * 1e3:.1f} us")
 
     x = tokens(a.prompt)
-    timed("prompt", a.prompt, lambda: block.forward(x, balance=0.001))
+    timed("prompt", a.prompt, lambda: step(x, balance=0.001))
     load = block.counts.float()
     print(f"experts' load: mean {load.mean():.0f}, most {load.max():.0f}, least {load.min():.0f}")
     x1 = tokens(a.batch)
-    timed("decode step", a.batch, lambda: block.forward(x1))
+    timed("decode step", a.batch, lambda: step(x1))
     graph = torch.cuda.CUDAGraph()
     torch.cuda.synchronize()
     with torch.cuda.graph(graph):
-        y, _, _ = block.forward(x1)
+        y, _, _ = step(x1)
     timed("decode step as a graph", a.batch, graph.replay)
+    before.check()
     block.check()
     return y
 
