@@ -562,7 +562,7 @@ def _on(stream, t, *others):
         return raw, None
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream) if stream else torch.cuda.default_stream()
-    if stream.device_index != dev:
+    if getattr(stream, "device_index", dev) != dev:
         _bad(f"a stream of cuda:{stream.device_index} for tensors on cuda:{dev}")
     if stream.cuda_stream == raw:
         return raw, None

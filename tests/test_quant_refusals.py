@@ -113,3 +113,15 @@ def test_rows_longer_than_a_grid_are_refused(pop, K):
     lib = pop.load_library()
     assert lib.pop_quantize_rows(4096, 0, K, 1, K, 4096, K, 4096, None) == pop.POP_ERR_INVALID_ARG
     assert b"2^28" in lib.pop_quant_last_error()
+
+
+def test_a_stream_that_names_no_device_is_taken_as_it_is(pop, monkeypatch):
+    """Any object with a raw handle will do for the current stream."""
+    import torch
+    monkeypatch.setattr(pop, "_gpus", 1)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 77, raising=False)
+
+    class Stream:
+        cuda_stream = 77
+
+    assert pop._on(Stream(), Stand((4, 8), torch.float32, 0)) == (77, None)
