@@ -79,9 +79,10 @@ pop_status pop_qlinear_forward(pop_qlinear_t h, const void* x, long long ldx, in
 pop_status pop_qlinear_forward_quantized(pop_qlinear_t h, const void* xq, long long ldq, const float* xs,
                                          long long lds, int M, void* y, long long ldy, void* stream);
 
-/* Limit, in nanoseconds, for every device-side wait of this handle's products (default 2 s). A wait that runs
- * out is recorded (POP_ERR_TIMEOUT from the check below) and the kernel returns. The outputs of that call
- * and of the calls after it are not valid until the check has reported it; then the handle is as new. ns >= 1. */
+/* Limit, in nanoseconds (>= 1), for every device-side wait of this handle's products from the next call on
+ * (default 2 s; a captured graph keeps its own). A wait that runs out is recorded (POP_ERR_TIMEOUT from the
+ * check below) and the kernel returns. The outputs of that call and of the calls after it are not valid until
+ * the check has reported it; then the handle is as new. */
 pop_status pop_qlinear_set_wait_limit(pop_qlinear_t h, uint64_t ns);
 
 /* Synchronizes the device and returns the first recorded device-side failure, or POP_OK; clears it, with

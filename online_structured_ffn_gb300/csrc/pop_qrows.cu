@@ -74,7 +74,8 @@ struct Places {
 // `per` whole rows that they hold. Bound by memory and nearly so by its instructions, of which every one counts:
 // 16 values take two each for the quotient (packed; four, and 9.8 us, without), half a rounding, one for bf16's
 // unpacking. 4096 x 4096 of bf16: 8.9 us (5.7 TB/s read and written), 16,384 x 4096 33.8 (6.0); 1001 x 11008 of float32
-// 8.5 (6.6; 9.4 with loads of 16 bytes).
+// 8.5 (6.6; 9.4 with loads of 16 bytes). Where the blocks do not fill a CTA's 32 groups the others idle: 16,384 x 4096 values in
+// rows of 4096 6.0 TB/s, of 7168 (28 of 32) 5.8, 6144 5.4, 2880 5.2, 5120 (20 of 32) 4.8, 4608 4.4, 4224 (33 of 64) 4.0.
 template <int KIND>
 __global__ void __launch_bounds__(256) k_quantize_rows(const __grid_constant__ QRowsArgs in, const __grid_constant__ QRowsOut out, int per) {
   // Behind the kernel that places the rows (row_of) x is complete, as that one has waited for it: only the places, and

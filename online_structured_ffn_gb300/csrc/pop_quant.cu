@@ -165,7 +165,10 @@ double thin_time(const Shape& s, int sms) {
   return static_cast<double>(s.groups * ((s.rows + 63) / 64) * s.NT) * s.KB * (s.gated ? 20 : 10) / sms;
 }
 
-constexpr long long THIN_MOST = 1024;  // rows of a group
+// Rows of a group above which no call is thin, so that the tiles' counters have a bound. The times above would choose thin
+// beyond it only by few outputs, where it hardly matters (thin/wide in us: 1025 rows by 8 x 4096 15.9/17.6, 4096 by 8 x 4096
+// 23.7/23.9, 4096 by 128 x 2048 17.1/16.0).
+constexpr long long THIN_MOST = 1024;
 
 // Rows of a run, which says which kernel a call takes: 128 (wide), else thin with tiles of as many rows as a group can
 // have if a token is in it once, up to 64.
