@@ -23,6 +23,7 @@ POP_OK, POP_ERR_INVALID_ARG, POP_ERR_STATE, POP_ERR_CUDA, POP_ERR_OOM, POP_ERR_T
 POP_MAX_D, POP_MAX_D_FF, POP_MAX_BATCH, POP_STATIC_MAX_D_FF = 16384, 49152, 64, 49152
 POP_ROUTE_SOFTMAX, POP_ROUTE_SIGMOID = 0, 1
 POP_ROUTE_MAX_EXPERTS, POP_ROUTE_MAX_TOP_K = 256, 16
+POP_GATED_MAX_DIM, POP_GATED_MAX_TOKENS = 65536, 1 << 20
 POP_QUANT_BLOCK, POP_QUANT_MAX_DIM, POP_QMOE_MAX_EXPERTS, POP_QMOE_MAX_TOP_K = 128, 65536, 256, 16
 
 
@@ -53,6 +54,11 @@ class pop_qlinear_config(ctypes.Structure):
 class pop_qmoe_config(ctypes.Structure):
     _fields_ = [("n_experts", ctypes.c_int), ("top_k", ctypes.c_int), ("D", ctypes.c_int), ("D_FF", ctypes.c_int),
                 ("max_tokens", ctypes.c_int), ("out_f32", ctypes.c_int)]
+
+
+class pop_gated_config(ctypes.Structure):
+    _fields_ = [("D", ctypes.c_int), ("D_FF", ctypes.c_int), ("max_tokens", ctypes.c_int), ("out_f32", ctypes.c_int),
+                ("grad_f32", ctypes.c_int)]
 
 
 class PopError(RuntimeError):
@@ -116,6 +122,15 @@ SIGNATURES = {
     "pop_qmoe_set_wait_limit": (_i32, [_vp, _u64]),
     "pop_qmoe_check": (_i32, [_vp]),
     "pop_quant_last_error": (ctypes.c_char_p, []),
+    # the gated MLP on the caller's matrices (include/pop_gated.h)
+    "pop_gated_create": (_i32, [ctypes.POINTER(pop_gated_config), ctypes.POINTER(_vp)]),
+    "pop_gated_destroy": (None, [_vp]),
+    "pop_gated_saved_bytes": (ctypes.c_size_t, [_i32, _i32]),
+    "pop_gated_forward": (_i32, [_vp, _vp, _i64, _i32, _vp, _vp, _vp, _vp, _i64, _vp, _vp]),
+    "pop_gated_backward": (_i32, [_vp, _vp, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i32, _vp]),
+    "pop_gated_set_wait_limit": (_i32, [_vp, _u64]),
+    "pop_gated_check": (_i32, [_vp]),
+    "pop_gated_last_error": (ctypes.c_char_p, []),
 }
 
 _lib = None
@@ -646,8 +661,9 @@ def quantize_rows(x, stream=None):
 
 
 class _QHandle:
-    """Owns a handle of include/pop_quant.h."""
+    """Owns a handle of include/pop_quant.h, or of a header with the same conventions."""
     _destroy = _checker = _limiter = ""
+    _last_error = "pop_quant_last_error"
     handle = None
 
     def close(self):
@@ -667,11 +683,11 @@ class _QHandle:
 
     def set_wait_limit(self, ns: int):
         """Limit of every device-side wait of the handle's products, in nanoseconds (2 s unless set)."""
-        _check_quant(getattr(load_library(), self._limiter)(self.handle, ns))
+        _check_with(self._last_error, getattr(load_library(), self._limiter)(self.handle, ns))
 
     def check(self):
         """Syncs and raises the first device-side failure since the last check."""
-        _check_quant(getattr(load_library(), self._checker)(self.handle))
+        _check_with(self._last_error, getattr(load_library(), self._checker)(self.handle))
 
     def _output(self, y, rows, cols, device, under, align):
         """(y, its row stride): a new [rows, cols] tensor, or the caller's, checked."""
@@ -785,6 +801,86 @@ class PopQMoE(_QHandle):
         if st != POP_OK:
             _check_quant(st)
         return y
+
+
+# ------------------------------------------------------------------ the gated MLP on the caller's matrices
+
+class PopGatedFFN(_QHandle):
+    """y = W2 (SiLU(Wg x) (.) (W1 x)) on bf16 matrices that the caller holds and trains, and its gradients
+    (``pop_gated``). ``include/pop_gated.h`` has the formulas and what is rounded where.
+
+    The object holds workspace, no weights: one serves all layers of its sizes, one call at a time.
+    max_tokens: the most rows of a call. out_f32: y and dx are float32 instead of bf16; grad_f32: the
+    matrices' gradients are."""
+    _destroy, _checker, _limiter = "pop_gated_destroy", "pop_gated_check", "pop_gated_set_wait_limit"
+    _last_error = "pop_gated_last_error"
+
+    def __init__(self, D: int, D_FF: int, max_tokens: int = 2048, out_f32: bool = False, grad_f32: bool = False):
+        self.D, self.N = D, D_FF
+        self.cfg = pop_gated_config(D=D, D_FF=D_FF, max_tokens=max_tokens, out_f32=1 if out_f32 else 0,
+                                    grad_f32=1 if grad_f32 else 0)
+        h = _vp()
+        _check_with(self._last_error, load_library().pop_gated_create(ctypes.byref(self.cfg), ctypes.byref(h)))
+        self.handle = h.value
+
+    def grad_dtype(self):
+        import torch
+        return torch.float32 if self.cfg.grad_f32 else torch.bfloat16
+
+    def _matrices(self, Wg, W1, W2):
+        import torch
+        for name, w, shape in (("Wg", Wg, (self.N, self.D)), ("W1", W1, (self.N, self.D)), ("W2", W2, (self.D, self.N))):
+            _whole_arg(w, name, torch.bfloat16, shape)
+
+    def forward(self, x, Wg, W1, W2, y=None, save=False, stream=None):
+        """x: bf16 [M, D] (rows may be strided), Wg and W1 [D_FF, D], W2 [D, D_FF] bf16. Returns y [M, D] of
+        out_dtype(), or with save (y, saved): saved is what backward() takes."""
+        import torch
+        M, ld = _rows_arg(x, "x", (torch.bfloat16,), self.D, 16)
+        self._matrices(Wg, W1, W2)
+        raw, under = _on(stream, x, Wg, W1, W2, y)
+        y, ldy = self._output(y, M, self.D, x.device, under, 16)
+        saved = None
+        if save:
+            saved = _empty(under, (_lib.pop_gated_saved_bytes(self.N, M),), torch.uint8, x.device)
+        st = _lib.pop_gated_forward(self.handle, x.data_ptr(), ld, M, Wg.data_ptr(), W1.data_ptr(), W2.data_ptr(), y.data_ptr(),
+                                    ldy, _ptr(saved), raw)
+        if st != POP_OK:
+            _check_with(self._last_error, st)
+        return (y, saved) if save else y
+
+    def backward(self, dy, x, Wg, W1, W2, saved, need=(True, True, True, True), grads=None, accumulate=False, stream=None):
+        """The gradients (dx, dWg, dW1, dW2) for dy, bf16 [M, D], of the forward call that gave `saved`, from the
+        same x and matrices. need: which of the four are wanted; the others are None. grads: (dWg, dW1, dW2),
+        tensors of grad_dtype() to write to instead of new ones (None where none is needed); with
+        accumulate they are added to."""
+        import torch
+        M, ld = _rows_arg(x, "x", (torch.bfloat16,), self.D, 16)
+        rows, lddy = _rows_arg(dy, "dy", (torch.bfloat16,), self.D, 16)
+        if rows != M:
+            _bad(f"dy: expected {M} rows, got {tuple(dy.shape)}")
+        self._matrices(Wg, W1, W2)
+        _whole_arg(saved, "saved", torch.uint8, (_lib.pop_gated_saved_bytes(self.N, M),))
+        if len(need) != 4 or (grads is not None and len(grads) != 3):
+            _bad("need has one entry for each of dx, dWg, dW1 and dW2, grads one for each of dWg, dW1 and dW2")
+        if accumulate and (grads is None or any(n and g is None for n, g in zip(need[1:], grads))):
+            _bad("accumulate needs the gradients to add to")
+        raw, under = _on(stream, x, dy, Wg, W1, W2, saved, *(grads or ()))
+        dx = _empty(under, (M, self.D), self.out_dtype(), x.device) if need[0] else None
+        out = []
+        for i, shape in enumerate(((self.N, self.D), (self.N, self.D), (self.D, self.N))):
+            g = grads[i] if grads is not None and need[i + 1] else None
+            if g is not None:
+                _whole_arg(g, ("dWg", "dW1", "dW2")[i], self.grad_dtype(), shape)
+            elif need[i + 1]:
+                g = _empty(under, shape, self.grad_dtype(), x.device)
+            out.append(g)
+        st = _lib.pop_gated_backward(self.handle, x.data_ptr(), ld, M, Wg.data_ptr(), W1.data_ptr(), W2.data_ptr(),
+                                     saved.data_ptr(), dy.data_ptr(), lddy, _ptr(dx), self.D, *(_ptr(g) for g in out),
+                                     1 if accumulate else 0, raw)
+        if st != POP_OK:
+            _check_with(self._last_error, st)
+        return (dx, *out)
 
 
 load_library()

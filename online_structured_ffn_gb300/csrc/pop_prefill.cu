@@ -353,6 +353,11 @@ bool encode_weight_maps(PrefillMaps* m, const uint16_t* Wp, int D, int N) {
          encode_2d(&m->w2, Wp + 2 * static_cast<size_t>(D), D, N, rb, 64, BK);
 }
 
+bool encode_map16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes, uint32_t box_in,
+                  uint32_t box_out) {
+  return encode_2d(m, base, inner, outer, row_bytes, box_in, box_out);
+}
+
 bool encode_x_map(CUtensorMap* m, const uint16_t* X, int M, int D) {
   return encode_2d(m, X, D, M, static_cast<uint64_t>(D) * 2, BK, BM);
 }

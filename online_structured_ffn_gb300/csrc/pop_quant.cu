@@ -8,62 +8,28 @@
 #include <new>
 #include <string>
 
+#include "pop_host.h"
 #include "pop_qinternal.h"
 
 namespace {
 
 thread_local std::string g_quant_msg;
 
-pop_status q_fail(pop_status s, const char* call, const char* why) noexcept {
-  try {
-    g_quant_msg = std::string(call) + ": " + why;
-  } catch (...) {
-  }
-  return s;
-}
+pop_status q_fail(pop_status s, const char* call, const char* why) noexcept { return pop::report(g_quant_msg, s, call, why); }
 
-pop_status q_cuda(cudaError_t e, const char* call) noexcept {
-  if (e == cudaSuccess) return POP_OK;
-  cudaGetLastError();  // it is reported here: a later call that asks the runtime for the last error is not to find it
-  return q_fail(e == cudaErrorMemoryAllocation ? POP_ERR_OOM : POP_ERR_CUDA, call, cudaGetErrorString(e));
-}
+pop_status q_cuda(cudaError_t e, const char* call) noexcept { return pop::report_cuda(g_quant_msg, e, call); }
 
-bool off(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) != 0; }
-
-template <class T>
-cudaError_t dalloc(T** p, size_t n) {
-  return cudaMalloc(reinterpret_cast<void**>(p), (n ? n : 1) * sizeof(T));
-}
-
-int sm_count() {
-  int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 1;
-  return n > 0 ? n : 1;
-}
-
-int current_device() {
-  int dev = -1;
-  return cudaGetDevice(&dev) == cudaSuccess ? dev : -1;
-}
+using pop::current_device;
+using pop::dalloc;
+using pop::off;
+using pop::OnDevice;
+using pop::sm_count;
 
 // A handle's calls launch on the current device, with its pointers.
 pop_status same_device(int device, const char* call) {
   if (current_device() == device) return POP_OK;
   return q_fail(POP_ERR_INVALID_ARG, call, "the handle was made on another device than the current one");
 }
-
-// Makes a device the current one for as long as it lives.
-struct OnDevice {
-  int was;
-  explicit OnDevice(int device) : was(current_device()) {
-    if (was != device) cudaSetDevice(device);
-    else was = -1;
-  }
-  ~OnDevice() {
-    if (was >= 0) cudaSetDevice(was);
-  }
-};
 
 constexpr long long MAX_ROWS = 1ll << 27;
 constexpr int MAX_ROW = 65535 * 32 * pop::QB;  // values that a grid's second dimension holds, of 32 blocks each

@@ -1,0 +1,60 @@
+// Internal interface of the wide products of 16-bit operands (pop_wide16.cu): the gated MLP on matrices that the
+// caller holds, forward and backward (pop_gated.h), and the products of 8-bit integers, which are exact in fp16
+// (pop_int8.h).
+#pragma once
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "pop_qinternal.h"
+
+namespace pop {
+
+// What a product computes. "k-major": an operand's rows have k contiguous; "mn-major": its k-th row has the M or N
+// values contiguous, as a matrix that is multiplied by its other side has.
+enum WKind {
+  W_GATED,     // h = SiLU(A B0^T) (.) A B1^T; A, B0, B1 k-major
+  W_PLAIN,     // y = A B^T; k-major
+  W_DGATED,    // dh = A B (B mn-major), from it and the kept gate and up values their gradients
+  W_DX,        // y = A0 B0 + A1 B1; A k-major, B mn-major
+  W_DW,        // y = A^T B, up to three of them; mn-major
+  W_I8,        // y = scales (.) A B^T, fp16
+  W_I8_GATED,  // fp32 h from two such products, and the largest |h| of each row
+};
+
+struct WArgs {
+  CUtensorMap map[6];  // A and B of each product (W_GATED, W_I8_GATED: A, B0, B1)
+  int problems;
+  int m[3], n[3];      // rows and columns of the outputs (gated: n channels)
+  int kb;              // k-blocks of 64 (W_DX: of either product)
+  // outputs
+  void* y[3];
+  long long ldy[3];
+  int out_f32, accumulate;
+  uint16_t* h;         // W_GATED: [m][n] bf16; W_DGATED: the gate's gradient
+  uint16_t* h2;        // W_DGATED: the up values' gradient
+  uint32_t* saved;     // W_GATED: what is kept of gate and up, or NULL; W_DGATED: the same
+  const float *sx, *sw, *sw1;  // W_I8*: scales of the rows, and of the columns (gated: of gate and up)
+  float* hf;           // W_I8_GATED: [m][n]
+  unsigned* amax;      // W_I8_GATED: bits of the largest |h| of each row (atomicMax)
+  unsigned* err;
+  QWait wait;
+  int num_sms;
+};
+
+cudaError_t launch_wide16(WKind kind, const WArgs& a, cudaStream_t st);
+
+// Kept gate and up values: for 32 rows and two channels three words a row, [ceil(m/32)][n/2][3][32]: the upper halves of
+// both gates, of both ups, and the next eight bits of the four. 16 significant bits each: with 8 of them (bf16) the
+// gradients were 1.7 times as far off as their own rounding makes them, with 16 1.4 times, with all 24 no less.
+inline size_t saved_words(int m, int n) { return static_cast<size_t>(qceil(m, 32)) * (n / 2) * 96; }
+
+// Tensor map of 16-bit values: `inner` contiguous ones, `outer` rows `row_bytes` apart, 128-byte swizzle, zeros outside.
+bool encode_map16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes, uint32_t box_in,
+                  uint32_t box_out);
+
+enum : unsigned {
+  WERR_TIMEOUT = 1u << 1,  // as QERR_TIMEOUT
+};
+
+}  // namespace pop
