@@ -149,6 +149,7 @@ pop_status pop_gated_forward(pop_gated_t h, const void* x, long long ldx, int M,
   down.y[0] = y;
   down.ldy[0] = ldy;
   down.out_f32 = h->cfg.out_f32;
+  down.b_early = 1;
   if (!map_k(&up.map[0], x, M, D, ldx) || !map_k(&up.map[1], Wg, N, D, D) || !map_k(&up.map[2], W1, N, D, D) ||
       !map_k(&down.map[0], hidden, M, N, N) || !map_k(&down.map[1], W2, D, N, N))
     return fail(POP_ERR_CUDA, call, "a tensor map could not be made");
@@ -198,6 +199,7 @@ pop_status pop_gated_backward(pop_gated_t h, const void* x, long long ldx, int M
     a.kb = qceil(M, 64);
     a.out_f32 = h->cfg.grad_f32;
     a.accumulate = accumulate;
+    a.b_early = dWg || dW1 ? 1 : 0;  // else nothing of this call has gone before
     const auto add = [&](void* out, const void* left, int rows, long long ldl, const void* right, int cols, long long ldr) {
       if (!out) return;
       const int p = a.problems++;
@@ -220,6 +222,7 @@ pop_status pop_gated_backward(pop_gated_t h, const void* x, long long ldx, int M
     a.y[0] = dx;
     a.ldy[0] = lddx;
     a.out_f32 = h->cfg.out_f32;
+    a.b_early = 1;
     maps = map_k(&a.map[0], h->a, M, N, N) && map_mn(&a.map[1], Wg, N, D, D) && map_k(&a.map[2], h->b, M, N, N) &&
            map_mn(&a.map[3], W1, N, D, D);
     if (maps) e = launch_wide16(W_DX, a, st);

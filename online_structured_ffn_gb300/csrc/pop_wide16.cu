@@ -7,10 +7,17 @@
 // no matrix is transposed in memory. Gate and up: the first CTA brings 128 rows of Wg, the second the same of W1,
 // so columns 0..127 of a tile are the gates and 128..255 the ups of 128 channels.
 //
+// Many tiles go round the pairs. Few tiles of long sums are each given to a cluster of S pairs, which take a run of the k-blocks
+// each; then every CTA sums 1 / S of the columns, the others' parts of them read from their shared memory, and has the
+// epilogue of those alone. (Tiles of a last round shared through global memory, summed by the pair that came last, cost 25 us
+// and more: 128 KB of each CTA's part written and read again, one CTA reading them all.)
+//
 // Persistent, one CTA per SM. Warp 0: copies. Warp 1: of the first CTA the products of both, of the second the news that
 // its operands have landed. Warps 4..11: epilogue, TMEM lane quarter warp % 4, half of the columns each. Every wait has a
 // limit; a CTA that gives up records WERR_TIMEOUT, lets its copies and products finish, frees TMEM and returns.
 #include "pop_wide16.h"
+
+#include <atomic>
 
 #include "pop_qdevice.cuh"
 
@@ -94,72 +101,89 @@ __device__ __forceinline__ Tile tile_at(const WArgs& a, int t) {
   r.m = group * GROUP + t - r.n * rows;
   return r;
 }
-template <WKind KIND>
-__device__ __forceinline__ int tile_count(const WArgs& a) {
-  int n = 0;
-  for (int p = 0; p < (KIND == W_DW ? a.problems : 1); ++p) n += qceil(a.m[p], 2 * BM) * qceil(a.n[p], Kind<KIND>::cols);
-  return n;
-}
 
 // sigma(g). __expf and __fdividef are off by a few units of 2^-23; what comes of them is rounded to bf16 or int8.
 __device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
 
+__device__ __forceinline__ uint32_t cluster_ctas() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
+  return r;
+}
+// The address of the same place in a CTA of the cluster; and 16 bytes from there.
+__device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t cta) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(cta));
+  return a;
+}
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+// Arrives on `bar` in the CTAs of `mask` once all products issued so far by this thread have completed.
+__device__ __forceinline__ void commit_pair(uint64_t* bar, uint32_t mask) {
+  asm volatile(
+      "{\n\t.reg .b16 m;\n\tcvt.u16.u32 m, %1;\n\t"
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n\t}" ::"r"(smem_u32(bar)),
+      "r"(mask)
+      : "memory");
+}
+
 using OutBuf = uint4 (*)[8];  // 32 rows of 128 bytes, a row's pieces of 16 in the order piece ^ (row % 8)
 
-// 32 rows of 128 bytes from the warp's lanes, a row each, out as whole lines. `limit`: bytes of a row that exist.
-__device__ __forceinline__ void put_rows(OutBuf buf, int lane, const uint4 (&w)[8], uint8_t* y, size_t row_bytes, int rows, int limit) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) buf[lane][i ^ (lane & 7)] = w[i];
+// A lane's 16 bytes of its row into the buffer, and 32 rows of up to 128 bytes out of it as whole lines. `limit`: bytes of a
+// row that exist.
+__device__ __forceinline__ void put(OutBuf buf, int lane, int piece, uint4 w) { buf[lane][piece ^ (lane & 7)] = w; }
+__device__ __forceinline__ void flush_rows(OutBuf buf, int lane, uint8_t* y, size_t row_bytes, int rows, int limit) {
   __syncwarp();
+  const int row = lane >> 3, piece = lane & 7;
+  y += row * row_bytes + 16 * piece;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int row = 4 * i + (lane >> 3), piece = lane & 7;
-    if (row < rows && 16 * piece < limit) *reinterpret_cast<uint4*>(y + row * row_bytes + 16 * piece) = buf[row][piece ^ (row & 7)];
-  }
+  for (int i = 0; i < 32; i += 4)
+    if (row + i < rows && 16 * piece < limit) *reinterpret_cast<uint4*>(y + i * row_bytes) = buf[row + i][piece ^ ((row + i) & 7)];
   __syncwarp();
 }
 
-// 32 fp32 columns of 32 rows, added to what y holds where asked, to y in its type: four columns a lane and row.
-__device__ __forceinline__ void put_f32(OutBuf buf, int lane, const float (&v)[32], void* y, size_t at, long long ldy, int rows, int cols,
-                                        bool f32, bool add, bool even) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    buf[lane][i ^ (lane & 7)] = make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]),
-                                           __float_as_uint(v[4 * i + 3]));
+// The same for 32 fp32 columns, added to what y holds where asked, to y in its type: four columns a lane and row.
+__device__ __forceinline__ void flush_f32(OutBuf buf, int lane, void* y, size_t at, long long ldy, int rows, int cols, bool f32, bool add,
+                                          bool even) {
   __syncwarp();
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int row = 4 * i + (lane >> 3), piece = lane & 7, n = min(4, cols - 4 * piece);
-    if (row >= rows || n <= 0) continue;
+  const int piece = lane & 7, n = min(4, cols - 4 * piece);
+#pragma unroll 1
+  for (int row = lane >> 3; row < rows && n > 0; row += 4) {
     const uint4 w = buf[row][piece ^ (row & 7)];
     float f[4] = {__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w)};
     const size_t o = at + static_cast<size_t>(row) * ldy + 4 * piece;
-    if (f32) {
-      float* p = static_cast<float*>(y) + o;
-      if (even && n == 4) {
-        float4 old = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (add) old = *reinterpret_cast<const float4*>(p);
-        *reinterpret_cast<float4*>(p) = make_float4(f[0] + old.x, f[1] + old.y, f[2] + old.z, f[3] + old.w);
-      } else {
-        for (int j = 0; j < n; ++j) p[j] = add ? p[j] + f[j] : f[j];
+    float* pf = static_cast<float*>(y) + o;
+    uint16_t* ph = static_cast<uint16_t*>(y) + o;
+    if (even && n == 4) {
+      if (add && f32) {
+        const float4 old = *reinterpret_cast<const float4*>(pf);
+        f[0] += old.x, f[1] += old.y, f[2] += old.z, f[3] += old.w;
+      } else if (add) {
+        const uint2 old = *reinterpret_cast<const uint2*>(ph);
+        f[0] += bf16lo(old.x), f[1] += bf16hi(old.x), f[2] += bf16lo(old.y), f[3] += bf16hi(old.y);
       }
+      if (f32)
+        *reinterpret_cast<float4*>(pf) = make_float4(f[0], f[1], f[2], f[3]);
+      else
+        *reinterpret_cast<uint2*>(ph) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
     } else {
-      uint16_t* p = static_cast<uint16_t*>(y) + o;
-      if (even && n == 4) {
-        if (add) {
-          const uint2 old = *reinterpret_cast<const uint2*>(p);
-          f[0] += bf16lo(old.x), f[1] += bf16hi(old.x), f[2] += bf16lo(old.y), f[3] += bf16hi(old.y);
-        }
-        *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
-      } else {
-        for (int j = 0; j < n; ++j) p[j] = static_cast<uint16_t>(pack_bf16x2(add ? f[j] + bf16lo(p[j]) : f[j], 0.f));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j >= n) continue;
+        if (f32)
+          pf[j] = add ? pf[j] + f[j] : f[j];
+        else
+          ph[j] = static_cast<uint16_t>(pack_bf16x2(add ? f[j] + bf16lo(ph[j]) : f[j], 0.f));
       }
     }
   }
   __syncwarp();
 }
 
-// Sixteen columns of tensor memory as floats.
+// Sixteen columns of tensor memory as floats, and back.
 __device__ __forceinline__ void columns16(uint32_t taddr, float* v) {
   uint32_t r[16];
   tmem_load(taddr, r);
@@ -167,19 +191,46 @@ __device__ __forceinline__ void columns16(uint32_t taddr, float* v) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
+__device__ __forceinline__ void columns32(uint32_t taddr, float* v) {
+  uint32_t r[2][16];
+  tmem_load(taddr, r[0]);
+  tmem_load(taddr + 16, r[1]);
+  tmem_wait(r[0]);
+  tmem_wait(r[1]);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i >> 4][i & 15]);
+}
+__device__ __forceinline__ void set_columns16(uint32_t taddr, const float* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]), "f"(v[10]),
+      "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+      : "memory");
+}
+
+// Kept gate and up values of sixteen channels, [channel pair][3 words].
+__device__ __forceinline__ void load_kept(const uint32_t* from, int c, int cols, uint32_t (&k)[24]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const bool is = c + 2 * j < cols;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) k[3 * j + i] = is ? __ldcs(from + (c / 2 + j) * 96 + 32 * i) : 0u;
+  }
+}
 
 template <WKind KIND>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wide16(const __grid_constant__ WArgs a) {
+__global__ void __launch_bounds__(THREADS, 1) k_wide16(const __grid_constant__ WArgs a) {
   using T = Kind<KIND>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Ctl ctl;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   volatile int* abort_flag = &ctl.abort_flag;
-  const int rank = static_cast<int>(cluster_rank());
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  const int tiles = tile_count<KIND>(a);
-  const int KB = a.kb * T::segments;
+  const int in_cluster = static_cast<int>(cluster_rank()), S = static_cast<int>(cluster_ctas()) >> 1;
+  const int rank = in_cluster & 1, part = in_cluster >> 1;  // within the pair; which run of the k-blocks
+  const uint32_t leader_cta = in_cluster & ~1;
+  const int tile0 = S == 1 ? blockIdx.x >> 1 : blockIdx.x / (2 * S), tile_step = S == 1 ? gridDim.x >> 1 : a.tiles;
+  const int KB = a.kb * T::segments, kb0 = KB * part / S, kb1 = KB * (part + 1) / S;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -212,39 +263,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wide16
       // ---------------------------------------------------------- copies (one thread)
       uint32_t issued = 0, s = 0, phase = 1;
       bool ok = true;
-      pdl_wait();
-      for (int t = pair; t < tiles && ok; t += pairs) {
+      // The first stages' B goes out before the kernel before this one has ended, where that does not write it.
+      int early = a.b_early ? min(STAGES, kb1 - kb0) : 0;
+      if (!early) pdl_wait();
+      for (int t = tile0; t < a.tiles && ok; t += tile_step) {
         const Tile tile = tile_at<KIND>(a, t);
         const int m0 = tile.m * 2 * BM + rank * BM;
+        // A CTA without rows multiplies what its stages hold, and nothing reads the products.
+        const bool any = m0 < a.m[tile.p];
         const int n0 = T::gated ? tile.n * 128 : tile.n * 256 + rank * BM;
         const CUtensorMap* ma = &a.map[KIND == W_DW ? 2 * tile.p : 0];
         const CUtensorMap* mb = T::gated ? &a.map[1 + rank] : ma + 1;
-        int kb = 0;
-        for (int i = 0; i < KB; ++i, ++kb) {
-          if (KIND == W_DX && i == a.kb) {
-            ma += 2;
-            mb += 2;
-            kb = 0;
+        const auto load = [&](int i, int stage, bool left, bool right) {
+          const bool second = KIND == W_DX && i >= a.kb;
+          const int x = (second ? i - a.kb : i) * BK;
+          const CUtensorMap *pa = ma + (second ? 2 : 0), *pb = mb + (second ? 2 : 0);
+          uint8_t* st = smem + stage * STAGE;
+          uint64_t* bar = &ctl.full[stage];
+          if (left && T::a_mn) {
+            tma_load_2d(st, pa, bar, m0, x);
+            tma_load_2d(st + BOX_MN, pa, bar, m0 + 64, x);
+          } else if (left) {
+            tma_load_2d(st, pa, bar, x, m0);
           }
+          if (right && T::b_mn) {
+            tma_load_2d(st + A_BYTES, pb, bar, n0, x);
+            tma_load_2d(st + A_BYTES + BOX_MN, pb, bar, n0 + 64, x);
+          } else if (right) {
+            tma_load_2d(st + A_BYTES, pb, bar, x, n0);
+          }
+        };
+        const uint32_t bytes = any ? STAGE : STAGE - A_BYTES;
+        if (early) {
+          for (int i = 0; i < early; ++i) {
+            mbar_arrive_expect_tx(&ctl.full[i], bytes);
+            load(kb0 + i, i, false, true);
+          }
+          pdl_wait();
+        }
+        for (int i = kb0; i < kb1; ++i) {
           if (!mbar_wait(&ctl.empty[s], phase, a.wait, abort_flag)) {
             fail();
             ok = false;
             break;
           }
-          uint8_t* st = smem + s * STAGE;
-          mbar_arrive_expect_tx(&ctl.full[s], STAGE);
-          if (T::a_mn) {
-            tma_load_2d(st, ma, &ctl.full[s], m0, kb * BK);
-            tma_load_2d(st + BOX_MN, ma, &ctl.full[s], m0 + 64, kb * BK);
-          } else {
-            tma_load_2d(st, ma, &ctl.full[s], kb * BK, m0);
-          }
-          if (T::b_mn) {
-            tma_load_2d(st + A_BYTES, mb, &ctl.full[s], n0, kb * BK);
-            tma_load_2d(st + A_BYTES + BOX_MN, mb, &ctl.full[s], n0 + 64, kb * BK);
-          } else {
-            tma_load_2d(st + A_BYTES, mb, &ctl.full[s], kb * BK, n0);
-          }
+          if (!early) mbar_arrive_expect_tx(&ctl.full[s], bytes);
+          load(i, s, any, !early);
+          if (early) --early;
           ++issued;
           if (++s == STAGES) s = 0, phase ^= 1;
         }
@@ -267,14 +332,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wide16
         // -------------------------------------------------------- products
         constexpr uint32_t IDESC = idesc_bf16_f32(2 * BM, 256, T::b_mn, T::a_mn) & ~(T::i8 ? (1u << 7) | (1u << 10) : 0u);
         const uint32_t a0 = operand_lo<T::a_mn>(smem_u32(smem)), b0 = operand_lo<T::b_mn>(smem_u32(smem) + A_BYTES);
+        const uint32_t mask = 3u << leader_cta;
         bool ok = true;
-        for (int t = pair; t < tiles && ok; t += pairs) {
+        for (int t = tile0; t < a.tiles && ok; t += tile_step) {
           if (!mbar_wait(&ctl.tempty[b], tphase, a.wait, abort_flag)) {
             if (leader) fail();
             break;
           }
           tc_fence_after();
-          for (int kb = 0; kb < KB; ++kb) {
+          for (int kb = kb0; kb < kb1; ++kb) {
             if (!mbar_wait(&ctl.full[s], phase, a.wait, abort_flag)) {
               if (leader) fail();
               ok = false;
@@ -282,9 +348,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wide16
             }
             tc_fence_after();
             if (leader) {
-              umma_pair16<T::a_mn, T::b_mn>(tmem_base + b * 256u, a0 + s * (STAGE >> 4), b0 + s * (STAGE >> 4), IDESC, kb == 0);
-              umma_commit_pair(&ctl.empty[s]);
-              if (kb == KB - 1) umma_commit_pair(&ctl.tfull[b]);
+              umma_pair16<T::a_mn, T::b_mn>(tmem_base + b * 256u, a0 + s * (STAGE >> 4), b0 + s * (STAGE >> 4), IDESC, kb == kb0);
+              commit_pair(&ctl.empty[s], mask);
+              if (kb == kb1 - 1) commit_pair(&ctl.tfull[b], mask);
             }
             __syncwarp();
             if (++s == STAGES) s = 0, phase ^= 1;
@@ -292,15 +358,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wide16
           b ^= 1u;
           tphase ^= b ^ 1u;
         }
-        if (leader) umma_commit_pair(&ctl.drain);
+        if (leader) commit_pair(&ctl.drain, mask);
         volatile int never = 0;
         if (!mbar_wait(&ctl.drain, 0, Q_DRAIN, &never) && leader) fail();
       } else {
         // -------------------------------------------------------- word of this CTA's operands
-        const uint32_t first0 = first_cta(&ctl.full[0]);
+        const uint32_t first0 = in_cta(&ctl.full[0], leader_cta);
         bool ok = true;
-        for (int t = pair; t < tiles && ok; t += pairs) {
-          for (int kb = 0; kb < KB; ++kb) {
+        for (int t = tile0; t < a.tiles && ok; t += tile_step) {
+          for (int kb = kb0; kb < kb1; ++kb) {
             if (!mbar_wait(&ctl.full[s], phase, a.wait, abort_flag)) {
               if (leader) fail();
               ok = false;
@@ -320,102 +386,139 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wide16
     pdl_trigger();
     const int q = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
-    const uint32_t tempty0 = first_cta(&ctl.tempty[0]), tempty1 = first_cta(&ctl.tempty[1]);
+    const uint32_t tempty0 = in_cta(&ctl.tempty[0], leader_cta), tempty1 = in_cta(&ctl.tempty[1], leader_cta);
     OutBuf buf = reinterpret_cast<OutBuf>(smem + STAGES * STAGE + (warp - 4) * (32 * 128));
     uint32_t b = 0, tphase = 0;
-    for (int t = pair; t < tiles; t += pairs) {
+    // Once a wait has run out the rest is gone through without waiting or storing, and nobody is told that a buffer has been
+    // read.
+    bool ok = true;
+    for (int t = tile0; t < a.tiles; t += tile_step) {
       const Tile tile = tile_at<KIND>(a, t);
       const int M = a.m[tile.p], N = a.n[tile.p];
       const int row0 = tile.m * 2 * BM + rank * BM + 32 * q;  // this warp's first row
       const int rows = min(32, M - row0);                     // may be none
-      if (!mbar_wait(&ctl.tfull[b], tphase, a.wait, abort_flag)) {
-        if (lane == 0) fail();
-        break;
+      const int own = T::cols / S;                            // outputs of this CTA
+      const int at0 = own * part + (own >> 1) * half;         // this warp's first one within the tile
+      const int col0 = tile.n * T::cols + at0;
+      const int cols = min(own >> 1, N - col0);               // may be none
+      const bool some = rows > 0 && cols > 0;
+      const uint32_t* from = KIND == W_DGATED ? a.saved + (static_cast<size_t>(row0 >> 5) * (N >> 1) + (col0 >> 1)) * 96 + lane : nullptr;
+      uint32_t k0[24], k1[24];
+      if (KIND == W_DGATED && some) {
+        load_kept(from, 0, cols, k0);
+        load_kept(from, 16, cols, k1);
       }
-      __syncwarp();
+      ok = ok && mbar_wait(&ctl.tfull[b], tphase, a.wait, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok && lane == 0) fail();
       tc_fence_after();
-      const uint32_t taddr = lane_base + b * 256u;
-      if (KIND == W_GATED || KIND == W_I8_GATED) {
-        const int ch0 = tile.n * 128 + 64 * half;
-        const int cols = min(64, N - ch0);
-        if (rows > 0 && cols > 0) {
-          if (KIND == W_GATED) {
-            uint32_t* keep = a.saved ? a.saved + (static_cast<size_t>(row0 >> 5) * (N >> 1) + (ch0 >> 1)) * 96 + lane : nullptr;
-            uint4 w[8];
+      const uint32_t taddr = lane_base + b * 256u + at0;  // gated: the ups are 128 further on
+      if (S > 1) {
+        // What the others are to sum goes to shared memory, where the products no longer read: [column / 4][row][4].
+        float4* mine = reinterpret_cast<float4*>(smem) + 32 * q + lane;
+        if (ok && rows > 0) {
+#pragma unroll 1
+          for (int c = 128 * half; c < 128 * half + 128; c += 32) {
+            if ((T::gated ? c & 127 : c) / own == part) continue;
+            float f[32];
+            columns32(lane_base + c, f);
 #pragma unroll
-            for (int c = 0; c < 64; c += 16) {
-              float g[16], u[16];
-              columns16(taddr + 64 * half + c, g);
-              columns16(taddr + 128 + 64 * half + c, u);
-              uint32_t p[8];
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const float h0 = silu_mul(g[2 * j], u[2 * j]), h1 = silu_mul(g[2 * j + 1], u[2 * j + 1]);
-                p[j] = pack_bf16x2(h0, h1);
-              }
-              w[c / 8] = make_uint4(p[0], p[1], p[2], p[3]);
-              w[c / 8 + 1] = make_uint4(p[4], p[5], p[6], p[7]);
-              if (keep && c < cols) {  // (cols is a multiple of 8)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  if (c + 2 * j >= cols) break;
-                  const uint32_t g0 = __float_as_uint(g[2 * j]), g1 = __float_as_uint(g[2 * j + 1]);
-                  const uint32_t u0 = __float_as_uint(u[2 * j]), u1 = __float_as_uint(u[2 * j + 1]);
-                  uint32_t* k = keep + (c / 2 + j) * 96;
-                  __stcs(k, __byte_perm(g0, g1, 0x7632));
-                  __stcs(k + 32, __byte_perm(u0, u1, 0x7632));
-                  __stcs(k + 64, __byte_perm(__byte_perm(g0, g1, 0x0051), __byte_perm(u0, u1, 0x0051), 0x5410));
-                }
-              }
-            }
-            put_rows(buf, lane, w, reinterpret_cast<uint8_t*>(a.h) + (static_cast<size_t>(row0) * N + ch0) * 2,
-                     static_cast<size_t>(N) * 2, rows, 2 * cols);
-          } else {
-            const float sx = lane < rows ? a.sx[row0 + lane] : 0.f;
-            float most = 0.f;
-#pragma unroll
-            for (int c = 0; c < 64; c += 32) {
-              if (c >= cols) break;
-              float v[32];
-#pragma unroll
-              for (int i = 0; i < 32; i += 16) {
-                float g[16], u[16];
-                columns16(taddr + 64 * half + c + i, g);
-                columns16(taddr + 128 + 64 * half + c + i, u);
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                  const int ch = min(ch0 + c + i + j, N - 1);
-                  v[i + j] = silu_mul(g[j] * (sx * __ldg(a.sw + ch)), u[j] * (sx * __ldg(a.sw1 + ch)));
-                  if (c + i + j < cols) most = max_abs(most, v[i + j], 0.f);
-                }
-              }
-              put_f32(buf, lane, v, a.hf, static_cast<size_t>(row0) * N + ch0 + c, N, rows, min(32, cols - c), true, false, true);
-            }
-            if (lane < rows) atomicMax(a.amax + row0 + lane, __float_as_uint(most));
+            for (int j = 0; j < 8; ++j) mine[(c / 4 + j) * BM] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
           }
         }
-      } else if (KIND == W_DGATED) {
-        const int ch0 = tile.n * 256 + 128 * half;
-        const int cols = min(128, N - ch0);
-        if (rows > 0 && cols > 0) {
-          const uint32_t* keep = a.saved + (static_cast<size_t>(row0 >> 5) * (N >> 1) + (ch0 >> 1)) * 96 + lane;
-          uint32_t k[2][24];
-          auto load = [&](int c, uint32_t (&r)[24]) {
+        cluster_sync();
+        // The parts in the order of k, this CTA's own from tensor memory, where the sums go.
+        if (ok && some) {
+#pragma unroll 1
+          for (int c = 0; c < (T::gated ? own : own >> 1); c += 16) {
+            // gated: (own / 2) gates, then as many ups
+            const int col = at0 + (T::gated && c >= (own >> 1) ? 128 - (own >> 1) : 0) + c;
+            float f[16], keep[16];
+            columns16(lane_base + col, keep);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const bool is = c + 2 * j < cols;
+            for (int j = 0; j < 16; ++j) f[j] = 0.f;
+#pragma unroll 1
+            for (int p = 0; p < S; ++p) {
+              if (p == part) {
 #pragma unroll
-              for (int i = 0; i < 3; ++i) r[3 * j + i] = is ? __ldcs(keep + (c / 2 + j) * 96 + 32 * i) : 0u;
+                for (int j = 0; j < 16; ++j) f[j] += keep[j];
+                continue;
+              }
+              const uint32_t from = in_cta(mine + col / 4 * BM, 2 * p + rank);
+              float4 x[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) x[j] = ld_cluster(from + j * BM * 16);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) f[4 * j] += x[j].x, f[4 * j + 1] += x[j].y, f[4 * j + 2] += x[j].z, f[4 * j + 3] += x[j].w;
             }
-          };
-          load(0, k[0]);
-          uint4 w[8];  // 32 channels: the gate's gradients, then the ups'
+            set_columns16(lane_base + col, f);
+          }
+          asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        }
+      }
+      // (Rolled loops: as straight-line code the largest of these epilogues was some 80 KB, and fetching it took longer
+      // than running it: a tile's 27 us.)
+      if (ok && some) {
+        if (KIND == W_GATED) {
+          uint32_t* keep = a.saved ? a.saved + (static_cast<size_t>(row0 >> 5) * (N >> 1) + (col0 >> 1)) * 96 + lane : nullptr;
+#pragma unroll 1
+          for (int c = 0; c < cols; c += 16) {
+            float g[16], u[16];
+            columns16(taddr + c, g);
+            columns16(taddr + 128 + c, u);
+            uint32_t p[8];
 #pragma unroll
-          for (int c = 0; c < 128; c += 16) {
-            uint32_t(&r)[24] = k[(c / 16) & 1];
-            if (c + 16 < 128) load(c + 16, k[(c / 16 + 1) & 1]);
+            for (int j = 0; j < 8; ++j) p[j] = pack_bf16x2(silu_mul(g[2 * j], u[2 * j]), silu_mul(g[2 * j + 1], u[2 * j + 1]));
+            put(buf, lane, c / 8, make_uint4(p[0], p[1], p[2], p[3]));
+            put(buf, lane, c / 8 + 1, make_uint4(p[4], p[5], p[6], p[7]));
+            if (keep) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                if (c + 2 * j >= cols) break;
+                const uint32_t g0 = __float_as_uint(g[2 * j]), g1 = __float_as_uint(g[2 * j + 1]);
+                const uint32_t u0 = __float_as_uint(u[2 * j]), u1 = __float_as_uint(u[2 * j + 1]);
+                uint32_t* k = keep + (c / 2 + j) * 96;
+                __stcs(k, __byte_perm(g0, g1, 0x7632));
+                __stcs(k + 32, __byte_perm(u0, u1, 0x7632));
+                __stcs(k + 64, __byte_perm(__byte_perm(g0, g1, 0x0051), __byte_perm(u0, u1, 0x0051), 0x5410));
+              }
+            }
+          }
+          flush_rows(buf, lane, reinterpret_cast<uint8_t*>(a.h) + (static_cast<size_t>(row0) * N + col0) * 2, static_cast<size_t>(N) * 2,
+                     rows, 2 * cols);
+        } else if (KIND == W_I8_GATED) {
+          const float sx = lane < rows ? a.sx[row0 + lane] : 0.f;
+          float most = 0.f;
+#pragma unroll 1
+          for (int c = 0; c < cols; c += 32) {
+#pragma unroll 1
+            for (int i = 0; i < 32; i += 16) {
+              float g[16], u[16];
+              columns16(taddr + c + i, g);
+              columns16(taddr + 128 + c + i, u);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const int ch = min(col0 + c + i + j, N - 1);
+                g[j] = silu_mul(g[j] * (sx * __ldg(a.sw + ch)), u[j] * (sx * __ldg(a.sw1 + ch)));
+                if (c + i + j < cols) most = max_abs(most, g[j], 0.f);
+              }
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                put(buf, lane, i / 4 + j, make_uint4(__float_as_uint(g[4 * j]), __float_as_uint(g[4 * j + 1]), __float_as_uint(g[4 * j + 2]),
+                                                     __float_as_uint(g[4 * j + 3])));
+            }
+            flush_f32(buf, lane, a.hf, static_cast<size_t>(row0) * N + col0 + c, N, rows, cols - c, true, false, true);
+          }
+          if (lane < rows) atomicMax(a.amax + row0 + lane, __float_as_uint(most));
+        } else if (KIND == W_DGATED) {
+#pragma unroll 1
+          for (int c = 0; c < cols; c += 16) {
+            uint32_t k[24];
+#pragma unroll
+            for (int j = 0; j < 24; ++j) k[j] = k0[j], k0[j] = k1[j];
+            load_kept(from, c + 32, cols, k1);  // two chunks ahead
             float dh[16];
-            columns16(taddr + 128 * half + c, dh);
+            columns16(taddr + c, dh);
             uint32_t dg[8], du[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
@@ -423,8 +526,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wide16
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 // (the lowest byte repeats the one above it: less than the bits that were not kept)
-                const float g = __uint_as_float(__byte_perm(r[3 * j], r[3 * j + 2], i ? 0x3255 : 0x1044));
-                const float u = __uint_as_float(__byte_perm(r[3 * j + 1], r[3 * j + 2], i ? 0x3277 : 0x1066));
+                const float g = __uint_as_float(__byte_perm(k[3 * j], k[3 * j + 2], i ? 0x3255 : 0x1044));
+                const float u = __uint_as_float(__byte_perm(k[3 * j + 1], k[3 * j + 2], i ? 0x3277 : 0x1066));
                 const float p = sigmoid(g), d = dh[2 * j + i];
                 o[0][i] = d * u * (p * fmaf(g, 1.f - p, 1.f));
                 o[1][i] = d * (g * p);
@@ -432,93 +535,131 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1) k_wide16
               dg[j] = pack_bf16x2(o[0][0], o[0][1]);
               du[j] = pack_bf16x2(o[1][0], o[1][1]);
             }
+            // 32 channels at a time: the gate's gradients, then the ups'
             const int at = (c >> 3) & 2;
-            w[at] = make_uint4(dg[0], dg[1], dg[2], dg[3]);
-            w[at + 1] = make_uint4(dg[4], dg[5], dg[6], dg[7]);
-            w[at + 4] = make_uint4(du[0], du[1], du[2], du[3]);
-            w[at + 5] = make_uint4(du[4], du[5], du[6], du[7]);
-            if ((c & 16) && c - 16 < cols) {
-              const int c0 = c - 16, left = min(32, cols - c0);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) buf[lane][i ^ (lane & 7)] = w[i];
+            put(buf, lane, at, make_uint4(dg[0], dg[1], dg[2], dg[3]));
+            put(buf, lane, at + 1, make_uint4(dg[4], dg[5], dg[6], dg[7]));
+            put(buf, lane, at + 4, make_uint4(du[0], du[1], du[2], du[3]));
+            put(buf, lane, at + 5, make_uint4(du[4], du[5], du[6], du[7]));
+            if (at || c + 16 >= cols) {
+              const int ch = c & ~31, row = lane >> 3, piece = lane & 7;
               __syncwarp();
+              uint16_t* o = (piece < 4 ? a.h : a.h2) + static_cast<size_t>(row0 + row) * N + col0 + ch + 8 * (piece & 3);
+              const bool is = ch + 8 * (piece & 3) < cols;
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const int row = 4 * i + (lane >> 3), piece = lane & 7;
-                uint16_t* o = (piece < 4 ? a.h : a.h2) + static_cast<size_t>(row0 + row) * N + ch0 + c0 + 8 * (piece & 3);
-                if (row < rows && 8 * (piece & 3) < left) *reinterpret_cast<uint4*>(o) = buf[row][piece ^ (row & 7)];
-              }
+              for (int i = 0; i < 32; i += 4)
+                if (row + i < rows && is) *reinterpret_cast<uint4*>(o + static_cast<size_t>(i) * N) = buf[row + i][piece ^ ((row + i) & 7)];
               __syncwarp();
             }
           }
-        }
-      } else {
-        const int col0 = tile.n * 256 + 128 * half;
-        const int cols = min(128, N - col0);
-        const long long ldy = a.ldy[tile.p];
-        void* y = a.y[tile.p];
-        const int size = a.out_f32 ? 4 : 2;
-        const bool even = KIND != W_I8 || (ldy * size % 16 == 0 && reinterpret_cast<uintptr_t>(y) % 16 == 0);
-        if (rows > 0 && cols > 0) {
-          float sx = 0.f;
-          if (KIND == W_I8 && lane < rows) sx = a.sx[row0 + lane];
+        } else {
+          const long long ldy = a.ldy[tile.p];
+          void* y = a.y[tile.p];
+          const int size = a.out_f32 ? 4 : 2;
+          const bool even = KIND != W_I8 || (ldy * size % 16 == 0 && reinterpret_cast<uintptr_t>(y) % 16 == 0);
           const bool direct = !a.out_f32 && !a.accumulate && even && (KIND != W_I8 || N % 8 == 0);
+          const float sx = KIND == W_I8 && lane < rows ? a.sx[row0 + lane] : 0.f;
+#pragma unroll 1
+          for (int c = 0; c < cols; c += 16) {
+            float f[16];
+            columns16(taddr + c, f);
+            if (KIND == W_I8) {
 #pragma unroll
-          for (int c = 0; c < 128; c += 64) {
-            if (c >= cols) break;
-            uint4 w[8];
-#pragma unroll
-            for (int i = 0; i < 64; i += 32) {
-              float v[32];
-              columns16(taddr + 128 * half + c + i, v);
-              columns16(taddr + 128 * half + c + i + 16, v + 16);
-              if (KIND == W_I8) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] *= sx * __ldg(a.sw + min(col0 + c + i + j, N - 1));
-              }
-              if (direct) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  w[i / 8 + j] = make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                                            pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
-              } else if (c + i < cols) {
-                put_f32(buf, lane, v, y, static_cast<size_t>(row0) * ldy + col0 + c + i, ldy, rows, min(32, cols - c - i), a.out_f32,
-                        a.accumulate, even);
-              }
+              for (int j = 0; j < 16; ++j) f[j] *= sx * __ldg(a.sw + min(col0 + c + j, N - 1));
             }
-            if (direct)
-              put_rows(buf, lane, w, static_cast<uint8_t*>(y) + (static_cast<size_t>(row0) * ldy + col0 + c) * 2, ldy * 2, rows,
-                       2 * min(64, cols - c));
+            if (direct) {
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                put(buf, lane, ((c >> 3) & 7) + j, make_uint4(pack_bf16x2(f[8 * j], f[8 * j + 1]), pack_bf16x2(f[8 * j + 2], f[8 * j + 3]),
+                                                              pack_bf16x2(f[8 * j + 4], f[8 * j + 5]), pack_bf16x2(f[8 * j + 6], f[8 * j + 7])));
+              if ((c & 48) == 48 || c + 16 >= cols)
+                flush_rows(buf, lane, static_cast<uint8_t*>(y) + (static_cast<size_t>(row0) * ldy + col0 + (c & ~63)) * 2, ldy * 2, rows,
+                           2 * (cols - (c & ~63)));
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                put(buf, lane, ((c >> 2) & 7) + j, make_uint4(__float_as_uint(f[4 * j]), __float_as_uint(f[4 * j + 1]), __float_as_uint(f[4 * j + 2]),
+                                                              __float_as_uint(f[4 * j + 3])));
+              if ((c & 16) || c + 16 >= cols)
+                flush_f32(buf, lane, y, static_cast<size_t>(row0) * ldy + col0 + (c & ~31), ldy, rows, cols - (c & ~31), a.out_f32, a.accumulate,
+                          even);
+            }
           }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_first(b ? tempty1 : tempty0);
+      if (ok && lane == 0) mbar_arrive_first(b ? tempty1 : tempty0);
       b ^= 1u;
       tphase ^= b ^ 1u;
     }
   }
 
+  if (S > 1 && warp < 4) cluster_sync();  // the others' exchange
   tc_fence_before();
-  cluster_sync();  // nothing of either CTA is still used by the other
+  cluster_sync();  // nothing of any CTA is still used by another
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem_base, TMEM_COLS);
   }
 }
 
+// Clusters of 2 S CTAs that the device holds at a time; asked once per kernel and device.
 template <WKind KIND>
-cudaError_t launch(const WArgs& a, cudaStream_t st) {
+int clusters_at_a_time(int S, size_t smem, int num_sms) {
+  static std::atomic<int> known[64][2];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::atomic<int>& k = known[dev][S >> 2];
+  int n = k.load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {static_cast<unsigned>(2 * S), 1, 1};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(num_sms / (2 * S) * 2 * S);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, k_wide16<KIND>, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    n = n > 0 ? n : -1;
+    k.store(n, std::memory_order_relaxed);
+  }
+  return n > 0 ? n : 0;
+}
+
+template <WKind KIND>
+cudaError_t launch(WArgs a, cudaStream_t st) {
   const size_t smem = STAGES * STAGE + OUT_BYTES + 1024;
-  const cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(&k_wide16<KIND>), smem);
+  cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(&k_wide16<KIND>), smem);
   if (e != cudaSuccess) return e;
   long long tiles = 0;
   for (int p = 0; p < (KIND == W_DW ? a.problems : 1); ++p)
     tiles += static_cast<long long>(qceil(a.m[p], 2 * BM)) * qceil(a.n[p], Kind<KIND>::cols);
-  const int most = a.num_sms & ~1;
-  const int grid = 2 * tiles < most ? static_cast<int>(2 * tiles) : most;
-  return launch_q(k_wide16<KIND>, dim3(grid), THREADS, smem, st, a);
+  if (tiles > (1 << 28)) return cudaErrorInvalidValue;
+  a.tiles = static_cast<int>(tiles);
+  const int KB = a.kb * Kind<KIND>::segments, pairs = a.num_sms / 2;
+  // As many pairs to a tile as there are for all tiles at once, with two k-blocks each at least.
+  int S = 1;
+  for (int s = 4; s > 1 && S == 1; s >>= 1)
+    if (tiles * s <= pairs && KB >= 2 * s && tiles <= clusters_at_a_time<KIND>(s, smem, a.num_sms)) S = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {static_cast<unsigned>(2 * S), 1, 1};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * S * (a.tiles < pairs ? a.tiles : pairs));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k_wide16<KIND>, a);
 }
 
 }  // namespace

@@ -40,6 +40,8 @@ struct WArgs {
   unsigned* err;
   QWait wait;
   int num_sms;
+  int b_early;         // 1: what the kernel before this one writes is not among the B operands
+  int tiles;           // set by launch_wide16
 };
 
 cudaError_t launch_wide16(WKind kind, const WArgs& a, cudaStream_t st);

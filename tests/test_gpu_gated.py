@@ -305,3 +305,55 @@ def test_a_wait_that_runs_out_is_reported(env):
             assert torch.equal(a, b)
         f.check()
     f.close()
+
+
+@pytest.mark.parametrize("M,D,N", [(1, 4096, 5504), (9, 8200, 264), (200, 2048, 9736), (777, 2048, 5496), (2560, 128, 264), (20, 72, 19464)])
+def test_tiles_shared_by_several_ctas(env, M, D, N):
+    """Few tiles of long sums, and last rounds that are cut: every product of a step."""
+    pop, torch, dev = env
+    t = make(env, 11, M, D, N)
+    w = (t["Wg"], t["W1"], t["W2"])
+    f = pop.PopGatedFFN(D, N, max_tokens=M)
+    y, saved = f.forward(t["x"], *w, save=True)
+    assert torch.equal(f.forward(t["x"], *w), y)
+    grads = f.backward(t["dy"], t["x"], *w, saved)
+    f.check()
+    want = reference(t)
+    near(y, want["y"], "y")
+    for name, got in zip(("dx", "dWg", "dW1", "dW2"), grads):
+        near(got, want[name], name)
+    for _ in range(3):
+        for a, b in zip(grads, f.backward(t["dy"], t["x"], *w, saved)):
+            assert torch.equal(a, b)
+    f.close()
+
+
+@pytest.mark.parametrize("M,D,N", [(40, 2048, 2736), (600, 4096, 1000)])
+def test_calls_after_a_wait_that_ran_out(env, M, D, N):
+    """At limits at which all, some or none of a shared tile's CTAs give up, what they leave is cleared by the check."""
+    pop, torch, dev = env
+    ts = [make(env, 12 + i, M, D, N) for i in range(2)]
+    f = pop.PopGatedFFN(D, N, max_tokens=M)
+
+    def step(t):
+        w = (t["Wg"], t["W1"], t["W2"])
+        y, saved = f.forward(t["x"], *w, save=True)
+        return (y, *f.backward(t["dy"], t["x"], *w, saved))
+
+    want = [step(t) for t in ts]
+    ran_out = 0
+    for ns in (1, 600, 1000, 1500, 2000, 2500, 3500):
+        f.set_wait_limit(ns)
+        step(ts[1])
+        f.set_wait_limit(2_000_000_000)
+        try:
+            f.check()
+        except pop.PopError as e:
+            assert e.status == pop.POP_ERR_TIMEOUT
+            ran_out += 1
+        for i in (0, 1, 0):
+            for a, b in zip(step(ts[i]), want[i]):
+                assert torch.equal(a, b), f"after a limit of {ns} ns"
+        f.check()
+    assert ran_out > 0
+    f.close()
