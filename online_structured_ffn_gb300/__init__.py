@@ -23,7 +23,7 @@ POP_OK, POP_ERR_INVALID_ARG, POP_ERR_STATE, POP_ERR_CUDA, POP_ERR_OOM, POP_ERR_T
 POP_MAX_D, POP_MAX_D_FF, POP_MAX_BATCH, POP_STATIC_MAX_D_FF = 16384, 49152, 64, 49152
 POP_ROUTE_SOFTMAX, POP_ROUTE_SIGMOID = 0, 1
 POP_ROUTE_MAX_EXPERTS, POP_ROUTE_MAX_TOP_K = 256, 16
-POP_GATED_MAX_DIM, POP_GATED_MAX_TOKENS = 65536, 1 << 20
+POP_GATED_MAX_DIM, POP_GATED_MAX_TOKENS, POP_INT8_MAX_DIM = 65536, 1 << 20, 65536
 POP_QUANT_BLOCK, POP_QUANT_MAX_DIM, POP_QMOE_MAX_EXPERTS, POP_QMOE_MAX_TOP_K = 128, 65536, 256, 16
 
 
@@ -59,6 +59,14 @@ class pop_qmoe_config(ctypes.Structure):
 class pop_gated_config(ctypes.Structure):
     _fields_ = [("D", ctypes.c_int), ("D_FF", ctypes.c_int), ("max_tokens", ctypes.c_int), ("out_f32", ctypes.c_int),
                 ("grad_f32", ctypes.c_int)]
+
+
+class pop_ilinear_config(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int), ("K", ctypes.c_int), ("max_tokens", ctypes.c_int), ("out_f32", ctypes.c_int)]
+
+
+class pop_iffn_config(ctypes.Structure):
+    _fields_ = [("D", ctypes.c_int), ("D_FF", ctypes.c_int), ("max_tokens", ctypes.c_int), ("out_f32", ctypes.c_int)]
 
 
 class PopError(RuntimeError):
@@ -131,6 +139,20 @@ SIGNATURES = {
     "pop_gated_set_wait_limit": (_i32, [_vp, _u64]),
     "pop_gated_check": (_i32, [_vp]),
     "pop_gated_last_error": (ctypes.c_char_p, []),
+    # 8-bit integers (include/pop_int8.h)
+    "pop_quantize_rows_int": (_i32, [_vp, _i32, _i64, _i32, _i32, _vp, _i64, _vp, _vp]),
+    "pop_ilinear_create": (_i32, [ctypes.POINTER(pop_ilinear_config), _vp, _vp, _vp, ctypes.POINTER(_vp)]),
+    "pop_ilinear_destroy": (None, [_vp]),
+    "pop_ilinear_forward": (_i32, [_vp, _vp, _i64, _i32, _vp, _i64, _vp]),
+    "pop_ilinear_forward_quantized": (_i32, [_vp, _vp, _i64, _vp, _i32, _vp, _i64, _vp]),
+    "pop_ilinear_set_wait_limit": (_i32, [_vp, _u64]),
+    "pop_ilinear_check": (_i32, [_vp]),
+    "pop_iffn_create": (_i32, [ctypes.POINTER(pop_iffn_config)] + [_vp] * 7 + [ctypes.POINTER(_vp)]),
+    "pop_iffn_destroy": (None, [_vp]),
+    "pop_iffn_forward": (_i32, [_vp, _vp, _i64, _i32, _vp, _i64, _vp]),
+    "pop_iffn_set_wait_limit": (_i32, [_vp, _u64]),
+    "pop_iffn_check": (_i32, [_vp]),
+    "pop_int_last_error": (ctypes.c_char_p, []),
 }
 
 _lib = None
@@ -881,6 +903,118 @@ class PopGatedFFN(_QHandle):
         if st != POP_OK:
             _check_with(self._last_error, st)
         return (dx, *out)
+
+
+# ------------------------------------------------------------------ 8-bit integers
+
+def quantize_rows_i8(x, stream=None):
+    """x: [M, K] bf16 or float32, K a multiple of 8 (rows may be strided). Returns (q int8 [M, K], scales
+    float32 [M]): element (m, k) stands for scales[m] * q[m, k]. ``include/pop_int8.h`` has the formula."""
+    import torch
+    if x.dim() != 2:
+        _bad(f"x: expected two dimensions, got {tuple(x.shape)}")
+    K = x.shape[1]
+    M, ld = _rows_arg(x, "x", (torch.bfloat16, torch.float32), K, 16)
+    raw, under = _on(stream, x)
+    device = x.device
+    q = _empty(under, (M, K), torch.int8, device)
+    s = _empty(under, (M,), torch.float32, device)
+    st = _lib.pop_quantize_rows_int(x.data_ptr(), 1 if x.dtype == torch.float32 else 0, ld, M, K, q.data_ptr(), K,
+                                   s.data_ptr(), raw)
+    if st != POP_OK:
+        _check_with("pop_int_last_error", st)
+    return q, s
+
+
+def _i8_matrix(W, S, name, shape=None):
+    """Checks one matrix: bf16 [N, K] (S None), or int8 [N, K] with float32 scales S [N]."""
+    import torch
+    if W.dim() != 2:
+        _bad(f"{name}: expected a matrix, got {tuple(W.shape)}")
+    _whole_arg(W, name, torch.bfloat16 if S is None else torch.int8, W.shape if shape is None else shape)
+    if S is not None:
+        _whole_arg(S, name + " scales", torch.float32, (W.shape[0],))
+
+
+class PopI8Linear(_QHandle):
+    """y = x W^T in 8-bit integers with a scale per token and per output channel (``pop_ilinear``).
+
+    W: torch bf16 [N, K], quantised here, or int8 [N, K] with float32 scales S [N]. The handle keeps its
+    own copy. max_tokens: rows that the workspace is made for; longer calls run in chunks."""
+    _destroy, _checker, _limiter = "pop_ilinear_destroy", "pop_ilinear_check", "pop_ilinear_set_wait_limit"
+    _last_error = "pop_int_last_error"
+
+    def __init__(self, W, S=None, max_tokens: int = 2048, out_f32: bool = False, stream=None):
+        _i8_matrix(W, S, "W")
+        _one_device(W, S)
+        self.N, self.K = W.shape
+        self.cfg = pop_ilinear_config(N=self.N, K=self.K, max_tokens=max_tokens, out_f32=1 if out_f32 else 0)
+        h = _vp()
+        _check_with(self._last_error, load_library().pop_ilinear_create(ctypes.byref(self.cfg), _ptr(W), _ptr(S),
+                                                                         _stream(stream), ctypes.byref(h)))
+        self.handle = h.value
+
+    def forward(self, x, y=None, stream=None):
+        """x: bf16 [M, K], quantised on the way. Returns y [M, N] of out_dtype()."""
+        import torch
+        M, ld = _rows_arg(x, "x", (torch.bfloat16,), self.K, 16)
+        raw, under = _on(stream, x, y)
+        y, ldy = self._output(y, M, self.N, x.device, under, 1)
+        st = _lib.pop_ilinear_forward(self.handle, x.data_ptr(), ld, M, y.data_ptr(), ldy, raw)
+        if st != POP_OK:
+            _check_with(self._last_error, st)
+        return y
+
+    def forward_q(self, xq, xs, y=None, stream=None):
+        """The same for rows that quantize_rows_i8 gave: xq int8 [M, K], xs float32 [M]."""
+        import torch
+        M, ldq = _rows_arg(xq, "xq", (torch.int8,), self.K, 8)
+        _whole_arg(xs, "xs", torch.float32, (M,))
+        raw, under = _on(stream, xq, xs, y)
+        y, ldy = self._output(y, M, self.N, xq.device, under, 1)
+        st = _lib.pop_ilinear_forward_quantized(self.handle, xq.data_ptr(), ldq, xs.data_ptr(), M, y.data_ptr(), ldy, raw)
+        if st != POP_OK:
+            _check_with(self._last_error, st)
+        return y
+
+
+class PopI8FFN(_QHandle):
+    """y = W2 (SiLU(Wg x) (.) (W1 x)) in 8-bit integers (``pop_iffn``): x and the hidden rows with a scale per
+    token, the matrices with one per output channel.
+
+    Wg, W1: [D_FF, D], W2: [D, D_FF], each bf16, quantised here, or all pairs (int8 matrix, float32 scales of
+    its rows). The handle keeps its own copy."""
+    _destroy, _checker, _limiter = "pop_iffn_destroy", "pop_iffn_check", "pop_iffn_set_wait_limit"
+    _last_error = "pop_int_last_error"
+
+    def __init__(self, Wg, W1, W2, max_tokens: int = 2048, out_f32: bool = False, stream=None):
+        scaled = [isinstance(w, (tuple, list)) for w in (Wg, W1, W2)]
+        if any(scaled) and (not all(scaled) or any(len(w) != 2 for w in (Wg, W1, W2))):
+            _bad("Wg, W1 and W2 must all be bf16 or all be (int8, scales) pairs")
+        mats = [w[0] if all(scaled) else w for w in (Wg, W1, W2)]
+        scales = [w[1] if all(scaled) else None for w in (Wg, W1, W2)]
+        if mats[0].dim() != 2:
+            _bad(f"Wg: expected a matrix, got {tuple(mats[0].shape)}")
+        self.N, self.D = mats[0].shape
+        for name, m, s, shape in zip(("Wg", "W1", "W2"), mats, scales, ((self.N, self.D), (self.N, self.D), (self.D, self.N))):
+            _i8_matrix(m, s, name, shape)
+        _one_device(*mats, *scales)
+        self.cfg = pop_iffn_config(D=self.D, D_FF=self.N, max_tokens=max_tokens, out_f32=1 if out_f32 else 0)
+        h = _vp()
+        _check_with(self._last_error, load_library().pop_iffn_create(
+            ctypes.byref(self.cfg), *(_ptr(m) for m in mats), *(_ptr(s) for s in scales), _stream(stream), ctypes.byref(h)))
+        self.handle = h.value
+
+    def forward(self, x, y=None, stream=None):
+        """x: bf16 [M, D]. Returns y [M, D] of out_dtype()."""
+        import torch
+        M, ld = _rows_arg(x, "x", (torch.bfloat16,), self.D, 16)
+        raw, under = _on(stream, x, y)
+        y, ldy = self._output(y, M, self.D, x.device, under, 16)
+        st = _lib.pop_iffn_forward(self.handle, x.data_ptr(), ld, M, y.data_ptr(), ldy, raw)
+        if st != POP_OK:
+            _check_with(self._last_error, st)
+        return y
 
 
 load_library()

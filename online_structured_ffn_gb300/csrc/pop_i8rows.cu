@@ -1,0 +1,179 @@
+// Rows and matrices in 8-bit integers: quantising with a scale per row, the fp16 rows that the products take, the matrix
+// images (include/pop_int8.h, pop_i8.h).
+#include "pop_i8.h"
+#include "pop_qdevice.cuh"
+
+namespace pop {
+namespace {
+
+constexpr int HELD = 8;  // runs of eight values that a thread holds between the two passes over its row
+
+// The nearest integer to each of two quotients, as the low byte of a float's bits: 1.5 * 2^23 + q.
+__device__ __forceinline__ uint2 nearest(float2 v) {
+  return make_uint2(__float_as_uint(v.x + 0x1.8p23f), __float_as_uint(v.y + 0x1.8p23f));
+}
+
+struct Eight {
+  float v[8];
+};
+template <bool F32>
+__device__ __forceinline__ Eight unpack(const uint4 (&w)[F32 ? 2 : 1]) {
+  Eight r;
+  if (F32) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint4 x = w[F32 ? i : 0];
+      r.v[4 * i] = __uint_as_float(x.x), r.v[4 * i + 1] = __uint_as_float(x.y);
+      r.v[4 * i + 2] = __uint_as_float(x.z), r.v[4 * i + 3] = __uint_as_float(x.w);
+    }
+  } else {
+    r.v[0] = bf16lo(w[0].x), r.v[1] = bf16hi(w[0].x), r.v[2] = bf16lo(w[0].y), r.v[3] = bf16hi(w[0].y);
+    r.v[4] = bf16lo(w[0].z), r.v[5] = bf16hi(w[0].z), r.v[6] = bf16lo(w[0].w), r.v[7] = bf16hi(w[0].w);
+  }
+  return r;
+}
+template <bool F32>
+__device__ __forceinline__ void load(const void* row, int i, uint4 (&w)[F32 ? 2 : 1]) {
+#pragma unroll
+  for (int j = 0; j < (F32 ? 2 : 1); ++j) w[j] = ldg_stream(static_cast<const uint4*>(row) + (F32 ? 2 * i + j : i));
+}
+
+// T threads to a row, a CTA of 256 (or T, if that is more) threads. A row's values stay in registers, as they stand in memory,
+// between the pass for the largest and the one that rounds; of rows longer than 8 * HELD * T the rest is read again.
+template <int T, bool F32>
+__global__ void __launch_bounds__(T > 256 ? T : 256) k_i8_rows(const __grid_constant__ I8RowsArgs a) {
+  constexpr int ROWS = T > 256 ? 1 : 256 / T, WARPS = T / 32;
+  __shared__ float s_most[ROWS][WARPS];
+  const int t = threadIdx.x % T, in = threadIdx.x / T;
+  const long long row = static_cast<long long>(blockIdx.x) * ROWS + in;
+  pdl_wait();
+  pdl_trigger();
+  const bool on = row < a.M;
+  const int n = on ? a.K >> 3 : 0;
+  const void* x = static_cast<const uint8_t*>(a.x) + (on ? row : 0) * a.ldx * (F32 ? 4 : 2);
+  uint4 held[HELD][F32 ? 2 : 1];
+#pragma unroll
+  for (int h = 0; h < HELD; ++h)
+    if (t + h * T < n) load<F32>(x, t + h * T, held[h]);
+  float most = __uint_as_float(AMAX_MIN_BITS);
+  if (a.amax) {
+    if (on) most = max_abs(most, __uint_as_float(__ldcg(a.amax + row)), 0.f);
+  } else {
+#pragma unroll
+    for (int h = 0; h < HELD; ++h) {
+      if (t + h * T >= n) continue;
+      const Eight e = unpack<F32>(held[h]);
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) most = max_abs(most, e.v[j], e.v[j + 1]);
+    }
+    for (int i = t + HELD * T; i < n; i += T) {
+      uint4 w[F32 ? 2 : 1];
+      load<F32>(x, i, w);
+      const Eight e = unpack<F32>(w);
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) most = max_abs(most, e.v[j], e.v[j + 1]);
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) most = max_abs(most, __shfl_xor_sync(0xffffffffu, most, o), 0.f);
+    if (WARPS > 1) {
+      if ((t & 31) == 0) s_most[in][t >> 5] = most;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) most = max_abs(most, s_most[in][w], 0.f);
+    }
+  }
+  if (!on) return;
+  const bool finite = most < INFINITY;
+  const BlockRatio ratio(finite ? most : 1.f, 127.f);
+  const auto put = [&](int i, const uint4 (&w)[F32 ? 2 : 1]) {
+    const Eight e = unpack<F32>(w);
+    uint2 r[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = finite ? nearest(ratio(e.v[2 * j], e.v[2 * j + 1])) : make_uint2(0x4b400000u, 0x4b400000u);
+    if (a.q) {
+      uint2 o;
+      o.x = __byte_perm(__byte_perm(r[0].x, r[0].y, 0x0040), __byte_perm(r[1].x, r[1].y, 0x0040), 0x5410);
+      o.y = __byte_perm(__byte_perm(r[2].x, r[2].y, 0x0040), __byte_perm(r[3].x, r[3].y, 0x0040), 0x5410);
+      *reinterpret_cast<uint2*>(a.q + row * a.ldq + 8 * i) = o;
+    } else {
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;"
+            : "=r"(o[j])
+            : "f"(__uint_as_float(r[j].y) - 0x1.8p23f), "f"(__uint_as_float(r[j].x) - 0x1.8p23f));
+      *reinterpret_cast<uint4*>(a.half + row * a.K + 8 * i) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
+  };
+#pragma unroll
+  for (int h = 0; h < HELD; ++h)
+    if (t + h * T < n) put(t + h * T, held[h]);
+  for (int i = t + HELD * T; i < n; i += T) {
+    uint4 w[F32 ? 2 : 1];
+    load<F32>(x, i, w);
+    put(i, w);
+  }
+  if (t == 0) {
+    a.s[row] = finite ? __fdiv_rn(most, 127.f) : __uint_as_float(0x7fffffffu);
+    if (a.clear) a.clear[row] = 0u;
+  }
+}
+
+__global__ void __launch_bounds__(256) k_i8_half(const int8_t* __restrict__ q, long long ldq, const float* __restrict__ s, long long lds,
+                                                 int K, uint16_t* __restrict__ half, float* __restrict__ sx) {
+  pdl_wait();
+  pdl_trigger();
+  const size_t row = blockIdx.x;
+  for (int i = blockIdx.y * 256 + threadIdx.x; i < K >> 3; i += 256 * gridDim.y) {
+    const uint2 w = *reinterpret_cast<const uint2*>(q + row * ldq + 8 * i);
+    *reinterpret_cast<uint4*>(half + row * K + 8 * i) = half8(w.x, w.y);
+  }
+  if (blockIdx.y == 0 && threadIdx.x == 0) sx[row] = s[row * lds];
+}
+
+// A CTA per block: two pieces of 16 bytes a thread.
+__global__ void __launch_bounds__(256) k_i8_pack(const int8_t* __restrict__ W, int N, int K, uint8_t* __restrict__ image) {
+  const size_t block = static_cast<size_t>(blockIdx.y) * gridDim.x + blockIdx.x;
+  const int r = threadIdx.x & 127, row = blockIdx.y * 128 + r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int j = (threadIdx.x >> 7) + 2 * i, k = blockIdx.x * 64 + 16 * j;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    const int8_t* p = W + static_cast<size_t>(row) * K + k;
+    if (row < N && k < K) {
+      const uint2 lo = *reinterpret_cast<const uint2*>(p);
+      v.x = lo.x, v.y = lo.y;
+    }
+    if (row < N && k + 8 < K) {
+      const uint2 hi = *reinterpret_cast<const uint2*>(p + 8);
+      v.z = hi.x, v.w = hi.y;
+    }
+    reinterpret_cast<uint4*>(image + block * W8_BLOCK)[j * 128 + r] = v;
+  }
+}
+
+template <int T>
+cudaError_t rows(const I8RowsArgs& a, cudaStream_t st) {
+  constexpr int ROWS = T > 256 ? 1 : 256 / T, BLOCK = T > 256 ? T : 256;
+  const dim3 grid(static_cast<unsigned>(qceil(a.M, ROWS)));
+  return a.f32 ? launch_q(k_i8_rows<T, true>, grid, BLOCK, 0, st, a) : launch_q(k_i8_rows<T, false>, grid, BLOCK, 0, st, a);
+}
+
+}  // namespace
+
+cudaError_t launch_i8_rows(const I8RowsArgs& a, cudaStream_t st) {
+  // four runs of eight values a thread, or fewer
+  if (a.K <= 1024) return rows<32>(a, st);
+  return a.K <= 8192 ? rows<128>(a, st) : rows<512>(a, st);
+}
+
+cudaError_t launch_i8_half(const int8_t* q, long long ldq, const float* s, long long lds, int M, int K, uint16_t* half, float* sx,
+                           cudaStream_t st) {
+  return launch_q(k_i8_half, dim3(M, qceil(K, 4096)), 256, 0, st, q, ldq, s, lds, K, half, sx);
+}
+
+cudaError_t launch_i8_pack(const int8_t* W, int N, int K, uint8_t* image, cudaStream_t st) {
+  return launch_plain(k_i8_pack, dim3(qceil(K, 64), qceil(N, 128)), 256, st, W, N, K, image);
+}
+
+}  // namespace pop

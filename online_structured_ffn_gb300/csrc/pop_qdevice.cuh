@@ -16,9 +16,9 @@ namespace pop {
 // values is, comes out exactly.
 struct BlockRatio {
   float k, a, y;
-  __device__ __forceinline__ explicit BlockRatio(float amax) {
+  __device__ __forceinline__ explicit BlockRatio(float amax, float top = 448.f) {
     const bool big = amax > 0x1p100f;
-    k = big ? 448.f * 0x1p-64f : 448.f;
+    k = big ? top * 0x1p-64f : top;
     a = big ? amax * 0x1p-64f : amax;
     y = __frcp_rn(a);
   }
@@ -67,6 +67,19 @@ __device__ __forceinline__ float block_scale(float a) {
 // SiLU(g) u. __expf and __fdividef are off by a few units of 2^-23, far less than the e4m3 rounding of
 // the result; the full-precision forms take about three times the instructions.
 __device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
+
+// ------------------------------------------------------------------ 8-bit integers
+// Eight 8-bit integers as fp16, exactly: 1024 + (128 + q) has 128 + q in its low bits.
+__device__ __forceinline__ uint4 half8(uint32_t lo, uint32_t hi) {
+  const auto two = [](uint32_t w, uint32_t sel) {
+    uint32_t h = __byte_perm(w, 0x64646464u, sel);
+    asm("sub.f16x2 %0, %0, %1;" : "+r"(h) : "r"(0x64806480u));  // 1152
+    return h;
+  };
+  lo ^= 0x80808080u;
+  hi ^= 0x80808080u;
+  return make_uint4(two(lo, 0x4140), two(lo, 0x4342), two(hi, 0x4140), two(hi, 0x4342));
+}
 
 // ------------------------------------------------------------------ launches
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }

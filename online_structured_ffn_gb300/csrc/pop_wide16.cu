@@ -12,6 +12,9 @@
 // epilogue of those alone. (Tiles of a last round shared through global memory, summed by the pair that came last, cost 25 us
 // and more: 128 KB of each CTA's part written and read again, one CTA reading them all.)
 //
+// 8-bit integers (there is no tensor-core product of them on sm_103a): exact in fp16, the rows are kept so; the matrix comes as
+// 8-bit blocks, which four more warps turn into fp16 operands in shared memory on the way.
+//
 // Persistent, one CTA per SM. Warp 0: copies. Warp 1: of the first CTA the products of both, of the second the news that
 // its operands have landed. Warps 4..11: epilogue, TMEM lane quarter warp % 4, half of the columns each. Every wait has a
 // limit; a CTA that gives up records WERR_TIMEOUT, lets its copies and products finish, frees TMEM and returns.
@@ -27,17 +30,19 @@ cudaError_t ensure_dyn_smem(const void* kernel, size_t bytes);
 
 namespace {
 
-constexpr int THREADS = 384;
 constexpr int BM = 128, BK = 64;
-constexpr int STAGES = 6;
+constexpr int MAX_STAGES = 6;
 constexpr uint32_t A_BYTES = BM * BK * 2, STAGE = 2 * A_BYTES;
 constexpr uint32_t BOX_MN = 64 * 64 * 2;  // one of an mn-major operand's two boxes
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t OUT_BYTES = 8 * 32 * 128;  // 128 bytes of 32 rows on their way out, of each epilogue warp
+constexpr int RING8 = 4;                      // blocks of 128 rows by 64 k of 8-bit integers on their way
+constexpr uint32_t BLOCK8 = W8_BLOCK;
 constexpr int GROUP = 8;                      // row tiles that share the columns' passes
 
 struct Ctl {
-  uint64_t full[STAGES], empty[STAGES];
+  uint64_t full[MAX_STAGES], empty[MAX_STAGES];
+  uint64_t full8[RING8], empty8[RING8];
   uint64_t tfull[2], tempty[2];
   uint64_t drain;
   uint32_t tmem_base;
@@ -52,6 +57,9 @@ struct Kind {
   static constexpr bool b_mn = KIND == W_DGATED || KIND == W_DX || KIND == W_DW;
   static constexpr int cols = gated ? 128 : 256;  // outputs (channels) of a tile
   static constexpr int segments = KIND == W_DX ? 2 : 1;
+  static constexpr int threads = i8 ? 512 : 384;
+  static constexpr int stages = i8 ? 5 : 6;
+  static constexpr uint32_t ring = stages * STAGE + (i8 ? RING8 * BLOCK8 : 0);
 };
 
 // kind::f16 on both CTAs' tensor cores, a k-block (four products of 16). a_lo, b_lo: the descriptors' low words; a k-major
@@ -219,8 +227,9 @@ __device__ __forceinline__ void load_kept(const uint32_t* from, int c, int cols,
 }
 
 template <WKind KIND>
-__global__ void __launch_bounds__(THREADS, 1) k_wide16(const __grid_constant__ WArgs a) {
+__global__ void __launch_bounds__(Kind<KIND>::threads, 1) k_wide16(const __grid_constant__ WArgs a) {
   using T = Kind<KIND>;
+  constexpr int STAGES = T::stages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Ctl ctl;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -234,12 +243,17 @@ __global__ void __launch_bounds__(THREADS, 1) k_wide16(const __grid_constant__ W
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&ctl.full[s], rank == 0 ? 2 : 1);  // the first CTA's: its own operands, and word of the second's
+      // its own operands (8-bit: and word of the four warps that convert B); the first CTA's: and word of the second's
+      mbar_init(&ctl.full[s], (rank == 0 ? 2 : 1) + (T::i8 ? 4 : 0));
       mbar_init(&ctl.empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&ctl.tfull[b], 1);
       mbar_init(&ctl.tempty[b], 16);  // the first CTA's: the epilogue warps of both
+    }
+    for (int s = 0; s < RING8 && T::i8; ++s) {
+      mbar_init(&ctl.full8[s], 1);
+      mbar_init(&ctl.empty8[s], 4);
     }
     mbar_init(&ctl.drain, 1);
     ctl.abort_flag = 0;
@@ -264,13 +278,14 @@ __global__ void __launch_bounds__(THREADS, 1) k_wide16(const __grid_constant__ W
       uint32_t issued = 0, s = 0, phase = 1;
       bool ok = true;
       // The first stages' B goes out before the kernel before this one has ended, where that does not write it.
-      int early = a.b_early ? min(STAGES, kb1 - kb0) : 0;
+      int early = a.b_early && !T::i8 ? min(STAGES, kb1 - kb0) : 0;
       if (!early) pdl_wait();
       for (int t = tile0; t < a.tiles && ok; t += tile_step) {
         const Tile tile = tile_at<KIND>(a, t);
         const int m0 = tile.m * 2 * BM + rank * BM;
         // A CTA without rows multiplies what its stages hold, and nothing reads the products.
         const bool any = m0 < a.m[tile.p];
+        constexpr uint32_t B_BYTES = T::i8 ? 0 : A_BYTES;
         const int n0 = T::gated ? tile.n * 128 : tile.n * 256 + rank * BM;
         const CUtensorMap* ma = &a.map[KIND == W_DW ? 2 * tile.p : 0];
         const CUtensorMap* mb = T::gated ? &a.map[1 + rank] : ma + 1;
@@ -289,11 +304,11 @@ __global__ void __launch_bounds__(THREADS, 1) k_wide16(const __grid_constant__ W
           if (right && T::b_mn) {
             tma_load_2d(st + A_BYTES, pb, bar, n0, x);
             tma_load_2d(st + A_BYTES + BOX_MN, pb, bar, n0 + 64, x);
-          } else if (right) {
+          } else if (right && !T::i8) {
             tma_load_2d(st + A_BYTES, pb, bar, x, n0);
           }
         };
-        const uint32_t bytes = any ? STAGE : STAGE - A_BYTES;
+        const uint32_t bytes = (any ? A_BYTES : 0) + B_BYTES;
         if (early) {
           for (int i = 0; i < early; ++i) {
             mbar_arrive_expect_tx(&ctl.full[i], bytes);
@@ -320,6 +335,36 @@ __global__ void __launch_bounds__(THREADS, 1) k_wide16(const __grid_constant__ W
       for (uint32_t i = lo; i < issued; ++i) {
         volatile int never = 0;
         if (!mbar_wait(&ctl.full[i % STAGES], (i / STAGES) & 1u, Q_DRAIN, &never)) {
+          fail();
+          break;
+        }
+      }
+    }
+    if (T::i8 && warp == 2 && lane == 0) {
+      // ---------------------------------------------------------- 8-bit blocks of the matrix (one thread)
+      uint32_t issued = 0, s = 0, phase = 1;
+      bool ok = true;
+      for (int t = tile0; t < a.tiles && ok; t += tile_step) {
+        const Tile tile = tile_at<KIND>(a, t);
+        const int last = qceil(a.n[0], 128) - 1;  // (a tile past it is not looked at)
+        const uint8_t* w = a.w8[T::gated ? rank : 0] +
+                           (static_cast<size_t>(T::gated ? tile.n : min(2 * tile.n + rank, last)) * KB + kb0) * BLOCK8;
+        for (int i = kb0; i < kb1; ++i, w += BLOCK8) {
+          if (!mbar_wait(&ctl.empty8[s], phase, a.wait, abort_flag)) {
+            fail();
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&ctl.full8[s], BLOCK8);
+          bulk_load(smem + STAGES * STAGE + s * BLOCK8, w, BLOCK8, &ctl.full8[s]);
+          ++issued;
+          if (++s == RING8) s = 0, phase ^= 1;
+        }
+      }
+      const uint32_t lo = issued > RING8 ? issued - RING8 : 0;
+      for (uint32_t i = lo; i < issued; ++i) {
+        volatile int never = 0;
+        if (!mbar_wait(&ctl.full8[i % RING8], (i / RING8) & 1u, Q_DRAIN, &never)) {
           fail();
           break;
         }
@@ -380,6 +425,40 @@ __global__ void __launch_bounds__(THREADS, 1) k_wide16(const __grid_constant__ W
       }
     }
     __syncwarp();
+  } else if (T::i8 && warp >= 12) {
+    // ------------------------------------------------------------ 8-bit integers to fp16 (warps 12..15, a row each thread)
+    const int r = threadIdx.x - 384;
+    uint32_t s = 0, phase = 1, s8 = 0, phase8 = 0;
+    bool ok = true;
+    for (int t = tile0; t < a.tiles && ok; t += tile_step) {
+      for (int kb = kb0; kb < kb1; ++kb) {
+        ok = mbar_wait(&ctl.full8[s8], phase8, a.wait, abort_flag) && mbar_wait(&ctl.empty[s], phase, a.wait, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {
+          if (lane == 0) fail();
+          break;
+        }
+        const uint4* from = reinterpret_cast<const uint4*>(smem + STAGES * STAGE + s8 * BLOCK8) + r;
+        uint8_t* to = smem + s * STAGE + A_BYTES + r * 128;
+        uint4 v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = from[128 * j];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          *reinterpret_cast<uint4*>(to + (((2 * j) ^ (r & 7)) << 4)) = half8(v[j].x, v[j].y);
+          *reinterpret_cast<uint4*>(to + (((2 * j + 1) ^ (r & 7)) << 4)) = half8(v[j].z, v[j].w);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&ctl.full[s]);
+          mbar_arrive(&ctl.empty8[s8]);
+        }
+        if (++s == STAGES) s = 0, phase ^= 1;
+        if (++s8 == RING8) s8 = 0, phase8 ^= 1;
+      }
+    }
+    __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue (warps 4..11)
     pdl_wait();  // what this kernel writes may still be read by the one before
@@ -387,7 +466,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_wide16(const __grid_constant__ W
     const int q = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(32 * q) << 16);
     const uint32_t tempty0 = in_cta(&ctl.tempty[0], leader_cta), tempty1 = in_cta(&ctl.tempty[1], leader_cta);
-    OutBuf buf = reinterpret_cast<OutBuf>(smem + STAGES * STAGE + (warp - 4) * (32 * 128));
+    OutBuf buf = reinterpret_cast<OutBuf>(smem + T::ring + (warp - 4) * (32 * 128));
     uint32_t b = 0, tphase = 0;
     // Once a wait has run out the rest is gone through without waiting or storing, and nobody is told that a buffer has been
     // read.
@@ -595,7 +674,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_wide16(const __grid_constant__ W
     }
   }
 
-  if (S > 1 && warp < 4) cluster_sync();  // the others' exchange
+  if (S > 1 && (warp < 4 || warp >= 12)) cluster_sync();  // the others' exchange
   tc_fence_before();
   cluster_sync();  // nothing of any CTA is still used by another
   if (warp == 1) {
@@ -618,7 +697,7 @@ int clusters_at_a_time(int S, size_t smem, int num_sms) {
     attr[0].val.clusterDim = {static_cast<unsigned>(2 * S), 1, 1};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(num_sms / (2 * S) * 2 * S);
-    cfg.blockDim = dim3(THREADS);
+    cfg.blockDim = dim3(Kind<KIND>::threads);
     cfg.dynamicSmemBytes = smem;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -634,7 +713,7 @@ int clusters_at_a_time(int S, size_t smem, int num_sms) {
 
 template <WKind KIND>
 cudaError_t launch(WArgs a, cudaStream_t st) {
-  const size_t smem = STAGES * STAGE + OUT_BYTES + 1024;
+  const size_t smem = Kind<KIND>::ring + OUT_BYTES + 1024;
   cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(&k_wide16<KIND>), smem);
   if (e != cudaSuccess) return e;
   long long tiles = 0;
@@ -654,7 +733,7 @@ cudaError_t launch(WArgs a, cudaStream_t st) {
   attr[1].val.clusterDim = {static_cast<unsigned>(2 * S), 1, 1};
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * S * (a.tiles < pairs ? a.tiles : pairs));
-  cfg.blockDim = dim3(THREADS);
+  cfg.blockDim = dim3(Kind<KIND>::threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;

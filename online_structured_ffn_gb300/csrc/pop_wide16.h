@@ -23,7 +23,7 @@ enum WKind {
 };
 
 struct WArgs {
-  CUtensorMap map[6];  // A and B of each product (W_GATED, W_I8_GATED: A, B0, B1)
+  CUtensorMap map[6];  // A and B of each product (W_GATED: A, B0, B1; W_I8*: A)
   int problems;
   int m[3], n[3];      // rows and columns of the outputs (gated: n channels)
   int kb;              // k-blocks of 64 (W_DX: of either product)
@@ -34,6 +34,7 @@ struct WArgs {
   uint16_t* h;         // W_GATED: [m][n] bf16; W_DGATED: the gate's gradient
   uint16_t* h2;        // W_DGATED: the up values' gradient
   uint32_t* saved;     // W_GATED: what is kept of gate and up, or NULL; W_DGATED: the same
+  const uint8_t* w8[2];        // W_I8*: images of the matrix (gated: of gate and up), instead of B's maps
   const float *sx, *sw, *sw1;  // W_I8*: scales of the rows, and of the columns (gated: of gate and up)
   float* hf;           // W_I8_GATED: [m][n]
   unsigned* amax;      // W_I8_GATED: bits of the largest |h| of each row (atomicMax)
@@ -45,6 +46,10 @@ struct WArgs {
 };
 
 cudaError_t launch_wide16(WKind kind, const WArgs& a, cudaStream_t st);
+
+// The image of a matrix [n, k] of 8-bit integers: blocks of 128 rows by 64 k, [ceil(n/128)][ceil(k/64)][4][128][16], zeros outside.
+constexpr int W8_BLOCK = 128 * 64;
+inline size_t image8_bytes(int n, int k) { return static_cast<size_t>(qceil(n, 128)) * qceil(k, 64) * W8_BLOCK; }
 
 // Kept gate and up values: for 32 rows and two channels three words a row, [ceil(m/32)][n/2][3][32]: the upper halves of
 // both gates, of both ups, and the next eight bits of the four. 16 significant bits each: with 8 of them (bf16) the
