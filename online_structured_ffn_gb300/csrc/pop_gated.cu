@@ -142,6 +142,9 @@ pop_status pop_gated_forward(pop_gated_t h, const void* x, long long ldx, int M,
   up.kb = qceil(D, 64);
   up.h = hidden;
   up.saved = static_cast<uint32_t*>(saved);
+  up.rows = x;
+  up.ld_rows = ldx;
+  up.k = D;
   WArgs down = base(h);
   down.m[0] = M;
   down.n[0] = D;
@@ -150,11 +153,14 @@ pop_status pop_gated_forward(pop_gated_t h, const void* x, long long ldx, int M,
   down.ldy[0] = ldy;
   down.out_f32 = h->cfg.out_f32;
   down.b_early = 1;
+  down.rows = hidden;
+  down.ld_rows = N;
+  down.k = N;
   if (!map_k(&up.map[0], x, M, D, ldx) || !map_k(&up.map[1], Wg, N, D, D) || !map_k(&up.map[2], W1, N, D, D) ||
       !map_k(&down.map[0], hidden, M, N, N) || !map_k(&down.map[1], W2, D, N, N))
     return fail(POP_ERR_CUDA, call, "a tensor map could not be made");
-  cudaError_t e = launch_wide16(W_GATED, up, st);
-  if (e == cudaSuccess) e = launch_wide16(W_PLAIN, down, st);
+  cudaError_t e = launch_rows16(W_GATED, up, st);
+  if (e == cudaSuccess) e = launch_rows16(W_PLAIN, down, st);
   return cuda(e, call);
 }
 

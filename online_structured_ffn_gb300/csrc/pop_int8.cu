@@ -97,7 +97,7 @@ struct Common {  // (the pointers are of `device`)
     a.y[0] = y;
     a.ldy[0] = ldy;
     a.out_f32 = out_f32;
-    return map_ ? launch_wide16(W_I8, a, st) : cudaErrorInvalidValue;
+    return map_ ? launch_rows16(W_I8, a, st) : cudaErrorInvalidValue;
   }
   WArgs args(const Matrix& w, const uint16_t* from, int n) const {
     WArgs a{};
@@ -111,6 +111,9 @@ struct Common {  // (the pointers are of `device`)
     a.err = err;
     a.wait = wait;
     a.num_sms = num_sms;
+    a.rows = from;
+    a.ld_rows = w.K;
+    a.k = w.K;
     map_ = encode_map16(&a.map[0], from, w.K, n, static_cast<uint64_t>(w.K) * 2, 64, 128);
     return a;
   }
@@ -362,7 +365,7 @@ pop_status pop_iffn_forward(pop_iffn_t h, const void* x, long long ldx, int M, v
     up.sw1 = h->w1.s;
     up.hf = h->h;
     up.amax = h->amax;
-    e = launch_wide16(W_I8_GATED, up, st);
+    e = launch_rows16(W_I8_GATED, up, st);
     if (e != cudaSuccess) return cuda(e, call);
     I8RowsArgs hidden{};
     hidden.x = h->h;

@@ -68,6 +68,9 @@ __device__ __forceinline__ float block_scale(float a) {
 // the result; the full-precision forms take about three times the instructions.
 __device__ __forceinline__ float silu_mul(float g, float u) { return __fdividef(g, 1.f + __expf(-g)) * u; }
 
+// sigma(g). __expf and __fdividef are off by a few units of 2^-23; what comes of them is rounded to bf16 or int8.
+__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
+
 // ------------------------------------------------------------------ 8-bit integers
 // Eight 8-bit integers as fp16, exactly: 1024 + (128 + q) has 128 + q in its low bits.
 __device__ __forceinline__ uint4 half8(uint32_t lo, uint32_t hi) {
@@ -181,6 +184,27 @@ __device__ __forceinline__ uint32_t first_cta(uint64_t* bar) {
 // release at cluster scope would also wait for every load still on its way.
 __device__ __forceinline__ void mbar_arrive_first(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ uint32_t cluster_ctas() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
+  return r;
+}
+// The address of the same place in a CTA of the cluster; and 16 bytes from there.
+__device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t cta) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(cta));
+  return a;
+}
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float ld_cluster1(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
 }
 __device__ __forceinline__ void tmem_alloc_pair(uint32_t* smem_result, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(smem_result)), "r"(ncols)

@@ -1,0 +1,386 @@
+// Products of few rows (tokens) and a matrix of bf16 or of 8-bit integers (pop_wide16.h): the matrix streams once.
+//
+// The matrix is the M operand, 128 of its rows a tile (gated: of gate and of up), the tokens the N operand, NT = 16, 32, 64
+// or 128 of them. A tile is given to a cluster of S CTAs, which take a run of the k-blocks each, as many as let all SMs
+// stream at once; then each has 1 / S of the tokens: it reads the others' parts of them from their shared memory, adds
+// them in the order of k and has their epilogue.
+//
+// 8-bit integers: a block of 128 rows by 64 k comes as it is; 128 threads read a row each, turn it into fp16 and put it into
+// tensor memory, from where the product takes it. (In shared memory the fp16 block would be written and read once more.)
+//
+// Warp 0: copies; the matrix's first stages go out before the kernel before this one has ended, where that does not write them.
+// Warp 1: products. Warps 4..11: conversion, then the epilogue. Every wait has a limit; a CTA that gives up records
+// WERR_TIMEOUT, lets its copies and products finish, frees TMEM and returns.
+#include "pop_qdevice.cuh"
+#include "pop_wide16.h"
+
+namespace pop {
+
+cudaError_t ensure_dyn_smem(const void* kernel, size_t bytes);
+
+namespace {
+
+constexpr int THREADS = 384;
+constexpr int BM = 128, BK = 64;
+constexpr int MAX_STAGES = 8;
+constexpr int NA = 4;  // blocks in tensor memory, of 32 columns
+
+template <bool I8_, bool GATED_, int NT_>
+struct Thin {
+  static constexpr bool I8 = I8_, GATED = GATED_;
+  static constexpr int NT = NT_, P = GATED ? 2 : 1;
+  static constexpr int PER_SM = NT <= 64 ? 2 : 1;
+  static constexpr uint32_t W_BYTES = I8 ? W8_BLOCK : BM * BK * 2, X_BYTES = NT * BK * 2;
+  static constexpr uint32_t X_OFF = P * W_BYTES, STAGE = X_OFF + X_BYTES;
+  static constexpr uint32_t BUDGET = (PER_SM == 2 ? 108 : 216) * 1024;
+  static constexpr int FIT = BUDGET / STAGE;
+  static constexpr int STAGES = FIT < MAX_STAGES ? FIT : MAX_STAGES;
+  static constexpr int COLS = P * NT + (I8 ? NA * 32 : 0);
+  static constexpr uint32_t TMEM_COLS = COLS <= 32 ? 32 : COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
+  static_assert(TMEM_COLS * PER_SM <= 512, "tensor memory of an SM");
+  static_assert(STAGE % 1024 == 0 && STAGES * STAGE >= P * NT * BM * 4, "a part fits into the ring");
+  static constexpr uint32_t SMEM = STAGES * STAGE + 1024;
+};
+
+struct Ctl {
+  uint64_t full[MAX_STAGES], empty[MAX_STAGES];
+  uint64_t afull[NA], aempty[NA];
+  uint64_t tfull;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+// kind::f16, A in tensor memory: a lane is a row, a column two values of k. A k-block is four products of 16.
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, bool first) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 b, {%2, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem + 8 * k), "r"(b_lo + 2 * k), "r"(idesc), "r"(DESC_HI), "r"(k > 0 || !first ? 1u : 0u)
+        : "memory");
+}
+// ... and both in shared memory.
+__device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool first) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo + 2 * k), "r"(b_lo + 2 * k), "r"(idesc), "r"(DESC_HI), "r"(k > 0 || !first ? 1u : 0u)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint4 (&v)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,"
+      "%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n\t"
+      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
+      "r"(v[0].x), "r"(v[0].y), "r"(v[0].z), "r"(v[0].w), "r"(v[1].x), "r"(v[1].y), "r"(v[1].z), "r"(v[1].w), "r"(v[2].x), "r"(v[2].y),
+      "r"(v[2].z), "r"(v[2].w), "r"(v[3].x), "r"(v[3].y), "r"(v[3].z), "r"(v[3].w), "r"(v[4].x), "r"(v[4].y), "r"(v[4].z), "r"(v[4].w),
+      "r"(v[5].x), "r"(v[5].y), "r"(v[5].z), "r"(v[5].w), "r"(v[6].x), "r"(v[6].y), "r"(v[6].z), "r"(v[6].w), "r"(v[7].x), "r"(v[7].y),
+      "r"(v[7].z), "r"(v[7].w)
+      : "memory");
+}
+
+template <class T>
+__global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_constant__ WArgs a) {
+  constexpr int STAGES = T::STAGES, NT = T::NT, P = T::P;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Ctl ctl;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  volatile int* abort_flag = &ctl.abort_flag;
+  const int rank = static_cast<int>(cluster_rank()), S = static_cast<int>(cluster_ctas());
+  const int tile = blockIdx.x / S;
+  const int kb0 = a.kb * rank / S, n = a.kb * (rank + 1) / S - kb0;  // this CTA's k-blocks
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&ctl.full[s], 1);
+      mbar_init(&ctl.empty[s], 1 + (T::I8 ? 4 * P : 0));
+    }
+    for (int i = 0; i < NA; ++i) {
+      mbar_init(&ctl.afull[i], 4);
+      mbar_init(&ctl.aempty[i], 1);
+    }
+    mbar_init(&ctl.tfull, 1);
+    ctl.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&ctl.tmem_base, T::TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = ctl.tmem_base, a_base = tmem_base + P * NT;
+
+  auto fail = [&]() {
+    if (!*abort_flag) {
+      *abort_flag = 1;
+      atomicOr(a.err, WERR_TIMEOUT);
+    }
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------------------------------------------------- copies (one thread)
+      const auto matrix = [&](int i, int s) {
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          uint8_t* to = smem + s * T::STAGE + p * T::W_BYTES;
+          if (T::I8)
+            bulk_load(to, a.w8[p] + (static_cast<size_t>(tile) * a.kb + kb0 + i) * W8_BLOCK, W8_BLOCK, &ctl.full[s]);
+          else
+            tma_load_2d(to, &a.map[1 + p], &ctl.full[s], (kb0 + i) * BK, tile * BM);
+        }
+      };
+      int early = T::I8 || a.b_early ? min(STAGES, n) : 0;
+      for (int i = 0; i < early; ++i) {
+        mbar_arrive_expect_tx(&ctl.full[i], T::STAGE);
+        matrix(i, i);
+      }
+      pdl_wait();
+      uint32_t s = 0, phase = 1;
+      int issued = 0;
+      for (; issued < n; ++issued) {
+        if (!mbar_wait(&ctl.empty[s], phase, a.wait, abort_flag)) {
+          fail();
+          break;
+        }
+        if (issued >= early) {
+          mbar_arrive_expect_tx(&ctl.full[s], T::STAGE);
+          matrix(issued, s);
+        }
+        tma_load_2d(smem + s * T::STAGE + T::X_OFF, &a.map[0], &ctl.full[s], (kb0 + issued) * BK, 0);
+        if (++s == STAGES) s = 0, phase ^= 1;
+      }
+      // no copy of this CTA may be in flight when it exits
+      for (int i = issued > STAGES ? issued - STAGES : 0; i < issued; ++i) {
+        volatile int never = 0;
+        if (!mbar_wait(&ctl.full[i % STAGES], (i / STAGES) & 1, Q_DRAIN, &never)) fail();
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ products
+    const bool leader = elect_one();
+    constexpr uint32_t IDESC = idesc_bf16_f32(BM, NT, false) & ~(T::I8 ? (1u << 7) | (1u << 10) : 0u);
+    const uint32_t w0 = desc_lo(smem_u32(smem)), x0 = desc_lo(smem_u32(smem) + T::X_OFF);
+    uint32_t s = 0, phase = 0, b = 0, bphase = 0;
+    bool ok = true;
+    for (int i = 0; i < n && ok; ++i) {
+      ok = mbar_wait(&ctl.full[s], phase, a.wait, abort_flag);
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        if (T::I8) ok = ok && mbar_wait(&ctl.afull[b], bphase, a.wait, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        if (leader) {
+          if (T::I8) {
+            umma_ts(tmem_base + p * NT, a_base + b * 32, x0 + s * (T::STAGE >> 4), IDESC, i == 0);
+            umma_commit(&ctl.aempty[b]);
+          } else {
+            umma_ss(tmem_base + p * NT, w0 + (s * T::STAGE + p * T::W_BYTES >> 4), x0 + s * (T::STAGE >> 4), IDESC, i == 0);
+          }
+          if (p == P - 1) umma_commit(&ctl.empty[s]);
+        }
+        __syncwarp();
+        if (T::I8 && ++b == NA) b = 0, bphase ^= 1;
+      }
+      if (++s == STAGES) s = 0, phase ^= 1;
+    }
+    if (!ok && leader) fail();
+    // (also what the end of the products is waited for with, whatever has become of them)
+    if (leader) umma_commit(&ctl.tfull);
+    volatile int never = 0;
+    if (!mbar_wait(&ctl.tfull, 0, Q_DRAIN, &never) && leader) fail();
+    __syncwarp();
+  } else if (warp >= 4) {
+    const int q = warp & 3, half = (warp - 4) >> 2, r = 32 * q + lane;
+    bool ok = true;
+    if (T::I8) {
+      // ---------------------------------------------------------- conversion: every other block, a row each thread
+      uint32_t b = half, bphase = 1;
+      for (int i = half; i < n * P && ok; i += 2) {
+        const int stage = i / P, s = stage % STAGES;
+        ok = mbar_wait(&ctl.full[s], (stage / STAGES) & 1, a.wait, abort_flag);
+        const uint4* from = reinterpret_cast<const uint4*>(smem + s * T::STAGE + (i % P) * W8_BLOCK) + r;
+        uint4 v[4], w[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = from[j * BM];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          w[2 * j] = half8(v[j].x, v[j].y);
+          w[2 * j + 1] = half8(v[j].z, v[j].w);
+        }
+        ok = ok && mbar_wait(&ctl.aempty[b], bphase, a.wait, abort_flag);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {
+          if (lane == 0) fail();
+          break;
+        }
+        if (lane == 0) mbar_arrive(&ctl.empty[s]);
+        tc_fence_after();
+        tmem_st32(a_base + b * 32 + (static_cast<uint32_t>(32 * q) << 16), w);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.afull[b]);
+        b ^= 2u;
+        if (b < 2) bphase ^= 1;
+      }
+    }
+    // ------------------------------------------------------------ this CTA's part: [column][row]
+    ok = ok && mbar_wait(&ctl.tfull, 0, a.wait, abort_flag);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok && lane == 0) fail();
+    tc_fence_after();
+    float* part = reinterpret_cast<float*>(smem) + r;
+    if (ok) {
+#pragma unroll 1
+      for (int c = 16 * half; c < P * NT; c += 32) {
+        if ((c & (NT - 1)) >= a.m[0]) continue;
+        uint32_t v[16];
+        tmem_load(tmem_base + (static_cast<uint32_t>(32 * q) << 16) + c, v);
+        tmem_wait(v);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) part[(c + j) * BM] = __uint_as_float(v[j]);
+      }
+    }
+  }
+  __syncwarp();
+  cluster_sync();
+  if (warp >= 4) {
+    // ------------------------------------------------------------ epilogue: tokens rank, rank + S, ...
+    pdl_wait();  // what this kernel writes may still be read by the one before
+    pdl_trigger();
+    const int q = warp & 3, half = (warp - 4) >> 2, r = 32 * q + lane;
+    const int M = a.m[0], N = a.n[0], ch = tile * BM + r;
+    const bool is = ch < N;
+    float sw = 1.f, sw1 = 1.f;
+    if (T::I8 && is) {
+      sw = __ldg(a.sw + ch);
+      if (T::GATED) sw1 = __ldg(a.sw1 + ch);
+    }
+    const uint32_t part = smem_u32(smem) + 4 * r;
+    constexpr int AT_ONCE = 4;
+#pragma unroll 1
+    for (int t0 = rank + S * half; t0 < M; t0 += 2 * S * AT_ONCE) {
+      float v[AT_ONCE][P];
+#pragma unroll
+      for (int j = 0; j < AT_ONCE; ++j)
+#pragma unroll
+        for (int p = 0; p < P; ++p) v[j][p] = 0.f;
+#pragma unroll 1
+      for (int c = 0; c < S; ++c) {
+        uint32_t from;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(part), "r"(c));
+#pragma unroll
+        for (int j = 0; j < AT_ONCE; ++j) {
+          const int t = min(t0 + 2 * S * j, M - 1);
+#pragma unroll
+          for (int p = 0; p < P; ++p) v[j][p] += ld_cluster1(from + (p * NT + t) * (BM * 4));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < AT_ONCE; ++j) {
+        const int t = t0 + 2 * S * j;
+        if (t >= M) break;
+        if (T::I8) {
+          const float sx = __ldcg(a.sx + t);
+          v[j][0] *= sx * sw;
+          if (T::GATED) v[j][P - 1] *= sx * sw1;
+        }
+        if (T::GATED) {
+          const float g = v[j][0], u = v[j][P - 1], h = silu_mul(g, u);
+          if (T::I8) {
+            if (is) a.hf[static_cast<size_t>(t) * N + ch] = h;
+            float most = is ? max_abs(0.f, h, 0.f) : 0.f;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) most = max_abs(most, __shfl_xor_sync(0xffffffffu, most, o), 0.f);
+            if (lane == 0) atomicMax(a.amax + t, __float_as_uint(most));
+          } else {
+            if (is) a.h[static_cast<size_t>(t) * N + ch] = static_cast<uint16_t>(pack_bf16x2(h, 0.f));
+            if (a.saved) {
+              // the words of two channels (pop_wide16.h): the even one's lane has the first and the last, the odd one's
+              // the second
+              const uint32_t gb = __float_as_uint(g), ub = __float_as_uint(u);
+              const uint32_t gn = __shfl_xor_sync(0xffffffffu, gb, 1), un = __shfl_xor_sync(0xffffffffu, ub, 1);
+              uint32_t* k = a.saved + (static_cast<size_t>(t >> 5) * (N >> 1) + (ch >> 1)) * 96 + (t & 31);
+              if (is && (lane & 1)) {
+                k[32] = __byte_perm(un, ub, 0x7632);
+              } else if (is) {
+                k[0] = __byte_perm(gb, gn, 0x7632);
+                k[64] = __byte_perm(__byte_perm(gb, gn, 0x0051), __byte_perm(ub, un, 0x0051), 0x5410);
+              }
+            }
+          }
+        } else if (is) {
+          const size_t o = static_cast<size_t>(t) * a.ldy[0] + ch;
+          if (a.out_f32)
+            static_cast<float*>(a.y[0])[o] = v[j][0];
+          else
+            static_cast<uint16_t*>(a.y[0])[o] = static_cast<uint16_t>(pack_bf16x2(v[j][0], 0.f));
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncwarp();
+  cluster_sync();  // nothing of this CTA is still used by another
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, T::TMEM_COLS);
+  }
+}
+
+template <class T>
+cudaError_t launch(WArgs a, cudaStream_t st) {
+  const cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(&k_thin16<T>), T::SMEM);
+  if (e != cudaSuccess) return e;
+  if (!encode_map16(&a.map[0], a.rows, a.k, a.m[0], static_cast<uint64_t>(a.ld_rows) * 2, BK, T::NT)) return cudaErrorInvalidValue;
+  const int tiles = qceil(a.n[0], BM), slots = T::PER_SM * a.num_sms;
+  // as many CTAs to a tile as the device holds for all tiles at once, with four k-blocks each at least
+  int S = slots / tiles < 8 ? slots / tiles : 8;
+  if (S > a.kb / 4) S = a.kb / 4;
+  if (S < 1) S = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {static_cast<unsigned>(S), 1, 1};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles) * S);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = T::SMEM;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k_thin16<T>, a);
+}
+
+template <bool I8, bool GATED>
+cudaError_t by_rows(const WArgs& a, cudaStream_t st) {
+  if (a.m[0] <= 16) return launch<Thin<I8, GATED, 16>>(a, st);
+  if (a.m[0] <= 32) return launch<Thin<I8, GATED, 32>>(a, st);
+  return a.m[0] <= 64 ? launch<Thin<I8, GATED, 64>>(a, st) : launch<Thin<I8, GATED, 128>>(a, st);
+}
+
+}  // namespace
+
+cudaError_t launch_thin16(WKind kind, const WArgs& a, cudaStream_t st) {
+  switch (kind) {
+    case W_GATED: return by_rows<false, true>(a, st);
+    case W_PLAIN: return by_rows<false, false>(a, st);
+    case W_I8: return by_rows<true, false>(a, st);
+    case W_I8_GATED: return by_rows<true, true>(a, st);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace pop

@@ -110,25 +110,6 @@ __device__ __forceinline__ Tile tile_at(const WArgs& a, int t) {
   return r;
 }
 
-// sigma(g). __expf and __fdividef are off by a few units of 2^-23; what comes of them is rounded to bf16 or int8.
-__device__ __forceinline__ float sigmoid(float g) { return __fdividef(1.f, 1.f + __expf(-g)); }
-
-__device__ __forceinline__ uint32_t cluster_ctas() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
-  return r;
-}
-// The address of the same place in a CTA of the cluster; and 16 bytes from there.
-__device__ __forceinline__ uint32_t in_cta(const void* p, uint32_t cta) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(cta));
-  return a;
-}
-__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
-  return v;
-}
 // Arrives on `bar` in the CTAs of `mask` once all products issued so far by this thread have completed.
 __device__ __forceinline__ void commit_pair(uint64_t* bar, uint32_t mask) {
   asm volatile(

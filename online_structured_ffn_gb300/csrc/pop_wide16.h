@@ -41,11 +41,22 @@ struct WArgs {
   unsigned* err;
   QWait wait;
   int num_sms;
+  // few rows (launch_rows16): A's rows, as its map was made of them
+  const void* rows;
+  long long ld_rows;
+  int k;
   int b_early;         // 1: what the kernel before this one writes is not among the B operands
   int tiles;           // set by launch_wide16
 };
 
 cudaError_t launch_wide16(WKind kind, const WArgs& a, cudaStream_t st);
+
+// W_GATED, W_PLAIN, W_I8 or W_I8_GATED: few rows by pop_thin16.cu, more by the wide products.
+constexpr int THIN16_MOST = 128;
+cudaError_t launch_thin16(WKind kind, const WArgs& a, cudaStream_t st);
+inline cudaError_t launch_rows16(WKind kind, const WArgs& a, cudaStream_t st) {
+  return a.m[0] <= THIN16_MOST ? launch_thin16(kind, a, st) : launch_wide16(kind, a, st);
+}
 
 // The image of a matrix [n, k] of 8-bit integers: blocks of 128 rows by 64 k, [ceil(n/128)][ceil(k/64)][4][128][16], zeros outside.
 constexpr int W8_BLOCK = 128 * 64;

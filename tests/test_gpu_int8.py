@@ -284,7 +284,7 @@ def test_replayed_graphs_and_another_stream(env, M):
     h.close()
 
 
-@pytest.mark.parametrize("M,D,N", [(1, 4096, 4096), (64, 4096, 2048), (400, 4096, 2048)])
+@pytest.mark.parametrize("M,D,N", [(1, 8192, 16384), (64, 8192, 8192), (400, 4096, 2048)])
 def test_calls_after_a_wait_that_ran_out(env, M, D, N):
     pop, torch, dev = env
     ms = [normal(env, i, *shape, scale=0.02) for i, shape in enumerate(((N, D), (N, D), (D, N)))]
@@ -294,7 +294,7 @@ def test_calls_after_a_wait_that_ran_out(env, M, D, N):
     for o in (f, h):
         want = [o.forward(x) for x in xs]
         ran_out = 0
-        for ns in (1, 1, 1, 600, 1000, 1500, 2000, 2500, 3500):
+        for ns in 10 * (1,) + (600, 1000, 1500, 2000, 2500, 3500):
             flush.zero_()
             torch.cuda.synchronize()
             o.set_wait_limit(ns)
