@@ -156,8 +156,7 @@ pop_status pop_gated_forward(pop_gated_t h, const void* x, long long ldx, int M,
   down.rows = hidden;
   down.ld_rows = N;
   down.k = N;
-  if (!map_k(&up.map[0], x, M, D, ldx) || !map_k(&up.map[1], Wg, N, D, D) || !map_k(&up.map[2], W1, N, D, D) ||
-      !map_k(&down.map[0], hidden, M, N, N) || !map_k(&down.map[1], W2, D, N, N))
+  if (!map_k(&up.map[1], Wg, N, D, D) || !map_k(&up.map[2], W1, N, D, D) || !map_k(&down.map[1], W2, D, N, N))
     return fail(POP_ERR_CUDA, call, "a tensor map could not be made");
   cudaError_t e = launch_rows16(W_GATED, up, st);
   if (e == cudaSuccess) e = launch_rows16(W_PLAIN, down, st);

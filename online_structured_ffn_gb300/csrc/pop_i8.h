@@ -10,7 +10,8 @@ struct I8RowsArgs {
   long long ldx;
   int f32;               // 1: float32, 0: bf16
   int M, K;
-  const unsigned* amax;  // bits of the rows' largest |x|, where they are known, or NULL
+  const unsigned* amax;  // bits of the rows' largest |x|, where they are known, or NULL: of `parts` parts of a row each,
+  int parts;             // [parts][THIN16_MOST], or of whole rows (1)
   // outputs
   int8_t* q;             // [M][ldq], or
   uint16_t* half;        // [M][K] the same integers in fp16

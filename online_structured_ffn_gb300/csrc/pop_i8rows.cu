@@ -6,73 +6,53 @@
 namespace pop {
 namespace {
 
-constexpr int HELD = 8;  // runs of eight values that a thread holds between the two passes over its row
+constexpr int HELD = 8;  // pieces of 16 bytes that a thread holds between the two passes over its row
 
-// The nearest integer to each of two quotients, as the low byte of a float's bits: 1.5 * 2^23 + q.
-__device__ __forceinline__ uint2 nearest(float2 v) {
-  return make_uint2(__float_as_uint(v.x + 0x1.8p23f), __float_as_uint(v.y + 0x1.8p23f));
-}
-
-struct Eight {
-  float v[8];
-};
 template <bool F32>
-__device__ __forceinline__ Eight unpack(const uint4 (&w)[F32 ? 2 : 1]) {
-  Eight r;
-  if (F32) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint4 x = w[F32 ? i : 0];
-      r.v[4 * i] = __uint_as_float(x.x), r.v[4 * i + 1] = __uint_as_float(x.y);
-      r.v[4 * i + 2] = __uint_as_float(x.z), r.v[4 * i + 3] = __uint_as_float(x.w);
+struct Piece {
+  static constexpr int V = F32 ? 4 : 8;  // values
+  float v[V];
+  __device__ __forceinline__ explicit Piece(const uint4& w) {
+    if constexpr (F32) {
+      v[0] = __uint_as_float(w.x), v[1] = __uint_as_float(w.y), v[2] = __uint_as_float(w.z), v[3] = __uint_as_float(w.w);
+    } else {
+      v[0] = bf16lo(w.x), v[1] = bf16hi(w.x), v[2] = bf16lo(w.y), v[3] = bf16hi(w.y);
+      v[4] = bf16lo(w.z), v[5] = bf16hi(w.z), v[6] = bf16lo(w.w), v[7] = bf16hi(w.w);
     }
-  } else {
-    r.v[0] = bf16lo(w[0].x), r.v[1] = bf16hi(w[0].x), r.v[2] = bf16lo(w[0].y), r.v[3] = bf16hi(w[0].y);
-    r.v[4] = bf16lo(w[0].z), r.v[5] = bf16hi(w[0].z), r.v[6] = bf16lo(w[0].w), r.v[7] = bf16hi(w[0].w);
   }
-  return r;
-}
-template <bool F32>
-__device__ __forceinline__ void load(const void* row, int i, uint4 (&w)[F32 ? 2 : 1]) {
+  __device__ __forceinline__ float most(float m) const {
 #pragma unroll
-  for (int j = 0; j < (F32 ? 2 : 1); ++j) w[j] = ldg_stream(static_cast<const uint4*>(row) + (F32 ? 2 * i + j : i));
-}
+    for (int j = 0; j < V; j += 2) m = max_abs(m, v[j], v[j + 1]);
+    return m;
+  }
+};
 
 // T threads to a row, a CTA of 256 (or T, if that is more) threads. A row's values stay in registers, as they stand in memory,
-// between the pass for the largest and the one that rounds; of rows longer than 8 * HELD * T the rest is read again.
+// between the pass for the largest and the one that rounds; of rows longer than HELD pieces a thread the rest is read again.
 template <int T, bool F32>
-__global__ void __launch_bounds__(T > 256 ? T : 256) k_i8_rows(const __grid_constant__ I8RowsArgs a) {
-  constexpr int ROWS = T > 256 ? 1 : 256 / T, WARPS = T / 32;
+__global__ void __launch_bounds__(T > 256 ? T : 256, T > 256 ? 2 : 4) k_i8_rows(const __grid_constant__ I8RowsArgs a) {
+  constexpr int ROWS = T > 256 ? 1 : 256 / T, WARPS = T / 32, V = Piece<F32>::V;
   __shared__ float s_most[ROWS][WARPS];
   const int t = threadIdx.x % T, in = threadIdx.x / T;
   const long long row = static_cast<long long>(blockIdx.x) * ROWS + in;
   pdl_wait();
   pdl_trigger();
   const bool on = row < a.M;
-  const int n = on ? a.K >> 3 : 0;
-  const void* x = static_cast<const uint8_t*>(a.x) + (on ? row : 0) * a.ldx * (F32 ? 4 : 2);
-  uint4 held[HELD][F32 ? 2 : 1];
+  const int n = on ? a.K / V : 0;
+  const uint4* x = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.x) + (on ? row : 0) * a.ldx * (F32 ? 4 : 2));
+  uint4 held[HELD];
 #pragma unroll
-  for (int h = 0; h < HELD; ++h)
-    if (t + h * T < n) load<F32>(x, t + h * T, held[h]);
+  for (int h = 0; h < HELD; ++h) held[h] = t + h * T < n ? ldg_stream(x + t + h * T) : make_uint4(0u, 0u, 0u, 0u);
   float most = __uint_as_float(AMAX_MIN_BITS);
   if (a.amax) {
-    if (on) most = max_abs(most, __uint_as_float(__ldcg(a.amax + row)), 0.f);
+    for (int i = a.parts > 1 ? t : 0; on && i < a.parts; i += a.parts > 1 ? T : 1)
+      most = max_abs(most, __uint_as_float(__ldcg(a.amax + static_cast<size_t>(i) * THIN16_MOST + row)), 0.f);
   } else {
 #pragma unroll
-    for (int h = 0; h < HELD; ++h) {
-      if (t + h * T >= n) continue;
-      const Eight e = unpack<F32>(held[h]);
-#pragma unroll
-      for (int j = 0; j < 8; j += 2) most = max_abs(most, e.v[j], e.v[j + 1]);
-    }
-    for (int i = t + HELD * T; i < n; i += T) {
-      uint4 w[F32 ? 2 : 1];
-      load<F32>(x, i, w);
-      const Eight e = unpack<F32>(w);
-#pragma unroll
-      for (int j = 0; j < 8; j += 2) most = max_abs(most, e.v[j], e.v[j + 1]);
-    }
+    for (int h = 0; h < HELD; ++h) most = Piece<F32>(held[h]).most(most);
+    for (int i = t + HELD * T; i < n; i += T) most = Piece<F32>(ldg_stream(x + i)).most(most);
+  }
+  if (!a.amax || a.parts > 1) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) most = max_abs(most, __shfl_xor_sync(0xffffffffu, most, o), 0.f);
     if (WARPS > 1) {
@@ -85,34 +65,35 @@ __global__ void __launch_bounds__(T > 256 ? T : 256) k_i8_rows(const __grid_cons
   if (!on) return;
   const bool finite = most < INFINITY;
   const BlockRatio ratio(finite ? most : 1.f, 127.f);
-  const auto put = [&](int i, const uint4 (&w)[F32 ? 2 : 1]) {
-    const Eight e = unpack<F32>(w);
-    uint2 r[4];
+  const auto put = [&](int i, const uint4& w) {
+    const Piece<F32> e(w);
+    uint2 r[V / 2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) r[j] = finite ? nearest(ratio(e.v[2 * j], e.v[2 * j + 1])) : make_uint2(0x4b400000u, 0x4b400000u);
+    for (int j = 0; j < V / 2; ++j) r[j] = finite ? nearest(ratio(e.v[2 * j], e.v[2 * j + 1])) : make_uint2(0x4b400000u, 0x4b400000u);
+    uint32_t o[V / 2];
     if (a.q) {
-      uint2 o;
-      o.x = __byte_perm(__byte_perm(r[0].x, r[0].y, 0x0040), __byte_perm(r[1].x, r[1].y, 0x0040), 0x5410);
-      o.y = __byte_perm(__byte_perm(r[2].x, r[2].y, 0x0040), __byte_perm(r[3].x, r[3].y, 0x0040), 0x5410);
-      *reinterpret_cast<uint2*>(a.q + row * a.ldq + 8 * i) = o;
-    } else {
-      uint32_t o[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        asm("cvt.rn.f16x2.f32 %0, %1, %2;"
-            : "=r"(o[j])
-            : "f"(__uint_as_float(r[j].y) - 0x1.8p23f), "f"(__uint_as_float(r[j].x) - 0x1.8p23f));
-      *reinterpret_cast<uint4*>(a.half + row * a.K + 8 * i) = make_uint4(o[0], o[1], o[2], o[3]);
+      for (int j = 0; j < V / 4; ++j)
+        o[j] = __byte_perm(__byte_perm(r[2 * j].x, r[2 * j].y, 0x0040), __byte_perm(r[2 * j + 1].x, r[2 * j + 1].y, 0x0040), 0x5410);
+      uint32_t* q = reinterpret_cast<uint32_t*>(a.q + row * a.ldq + V * i);
+      if constexpr (F32)
+        *q = o[0];
+      else
+        *reinterpret_cast<uint2*>(q) = make_uint2(o[0], o[1]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < V / 2; ++j) o[j] = half2_of(r[j]);
+      uint32_t* q = reinterpret_cast<uint32_t*>(a.half + row * a.K + V * i);
+      if constexpr (F32)
+        *reinterpret_cast<uint2*>(q) = make_uint2(o[0], o[1]);
+      else
+        *reinterpret_cast<uint4*>(q) = make_uint4(o[0], o[1], o[2], o[3]);
     }
   };
 #pragma unroll
   for (int h = 0; h < HELD; ++h)
     if (t + h * T < n) put(t + h * T, held[h]);
-  for (int i = t + HELD * T; i < n; i += T) {
-    uint4 w[F32 ? 2 : 1];
-    load<F32>(x, i, w);
-    put(i, w);
-  }
+  for (int i = t + HELD * T; i < n; i += T) put(i, ldg_stream(x + i));
   if (t == 0) {
     a.s[row] = finite ? __fdiv_rn(most, 127.f) : __uint_as_float(0x7fffffffu);
     if (a.clear) a.clear[row] = 0u;
@@ -162,9 +143,10 @@ cudaError_t rows(const I8RowsArgs& a, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_i8_rows(const I8RowsArgs& a, cudaStream_t st) {
-  // four runs of eight values a thread, or fewer
-  if (a.K <= 1024) return rows<32>(a, st);
-  return a.K <= 8192 ? rows<128>(a, st) : rows<512>(a, st);
+  // four pieces a thread, or fewer, where that many threads hold them
+  const int pieces = a.K / (a.f32 ? 4 : 8);
+  if (pieces <= 128) return rows<32>(a, st);
+  return pieces <= 1024 ? rows<128>(a, st) : rows<512>(a, st);
 }
 
 cudaError_t launch_i8_half(const int8_t* q, long long ldq, const float* s, long long lds, int M, int K, uint16_t* half, float* sx,

@@ -91,14 +91,7 @@ struct Common {  // (the pointers are of `device`)
     if (e != cudaSuccess) return cuda(e, call);
     return w ? fail(POP_ERR_TIMEOUT, call, "a wait of a product ran out") : POP_OK;
   }
-  // One product of the n rows in `from` (fp16 [n][w.K]).
-  cudaError_t product(const Matrix& w, const uint16_t* from, int n, void* y, long long ldy, int out_f32, cudaStream_t st) const {
-    WArgs a = args(w, from, n);
-    a.y[0] = y;
-    a.ldy[0] = ldy;
-    a.out_f32 = out_f32;
-    return map_ ? launch_rows16(W_I8, a, st) : cudaErrorInvalidValue;
-  }
+  // A product with n rows of fp16 integers, [n][w.K], and their scales in sx.
   WArgs args(const Matrix& w, const uint16_t* from, int n) const {
     WArgs a{};
     a.problems = 1;
@@ -114,10 +107,27 @@ struct Common {  // (the pointers are of `device`)
     a.rows = from;
     a.ld_rows = w.K;
     a.k = w.K;
-    map_ = encode_map16(&a.map[0], from, w.K, n, static_cast<uint64_t>(w.K) * 2, 64, 128);
     return a;
   }
-  mutable bool map_ = true;  // the last one's map could be made
+  // The same with rows x of bf16, quantised on the way into the product or before it. clear: [n] set to 0 by what comes before.
+  cudaError_t args_of(WArgs* a, const Matrix& w, const void* x, long long ldx, int n, unsigned* clear, cudaStream_t st) const {
+    *a = args(w, rows, n);
+    if (thin16_converts(1, n, w.N, w.K, num_sms)) {
+      a->rows = x;
+      a->ld_rows = ldx;
+      a->convert = 1;
+      return cudaSuccess;
+    }
+    I8RowsArgs r{};
+    r.x = x;
+    r.ldx = ldx;
+    r.M = n;
+    r.K = w.K;
+    r.half = rows;
+    r.s = sx;
+    r.clear = clear;
+    return launch_i8_rows(r, st);
+  }
 };
 
 }  // namespace
@@ -134,7 +144,7 @@ struct pop_iffn {
   Matrix wg, w1, w2;
   float* h = nullptr;         // [max_tokens][D_FF]
   uint16_t* hq = nullptr;     // the same, quantised, in fp16
-  unsigned* amax = nullptr;   // bits of the largest |h| of each row
+  unsigned* amax = nullptr;   // bits of the largest |h| of each row; few rows: of each tile's channels, [tile][THIN16_MOST]
 };
 
 namespace {
@@ -240,6 +250,13 @@ static uint8_t* rows_of(void* y, long long ldy, int m0, int out_f32) {
   return static_cast<uint8_t*>(y) + static_cast<size_t>(m0) * ldy * (out_f32 ? 4 : 2);
 }
 
+static cudaError_t product(pop_ilinear_t h, WArgs& a, void* y, long long ldy, int m0, cudaStream_t st) {
+  a.y[0] = rows_of(y, ldy, m0, h->cfg.out_f32);
+  a.ldy[0] = ldy;
+  a.out_f32 = h->cfg.out_f32;
+  return launch_rows16(W_I8, a, st);
+}
+
 pop_status pop_ilinear_forward(pop_ilinear_t h, const void* x, long long ldx, int M, void* y, long long ldy, void* stream) {
   const char* call = "pop_ilinear_forward";
   const pop_status s = linear_checked(h, x, M, y, ldy, call);
@@ -248,15 +265,9 @@ pop_status pop_ilinear_forward(pop_ilinear_t h, const void* x, long long ldx, in
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   for (int m0 = 0; m0 < M; m0 += h->cfg.max_tokens) {
     const int n = M - m0 < h->cfg.max_tokens ? M - m0 : h->cfg.max_tokens;
-    I8RowsArgs a{};
-    a.x = static_cast<const uint16_t*>(x) + static_cast<size_t>(m0) * ldx;
-    a.ldx = ldx;
-    a.M = n;
-    a.K = h->cfg.K;
-    a.half = h->c.rows;
-    a.s = h->c.sx;
-    cudaError_t e = launch_i8_rows(a, st);
-    if (e == cudaSuccess) e = h->c.product(h->w, h->c.rows, n, rows_of(y, ldy, m0, h->cfg.out_f32), ldy, h->cfg.out_f32, st);
+    WArgs a;
+    cudaError_t e = h->c.args_of(&a, h->w, static_cast<const uint16_t*>(x) + static_cast<size_t>(m0) * ldx, ldx, n, nullptr, st);
+    if (e == cudaSuccess) e = product(h, a, y, ldy, m0, st);
     if (e != cudaSuccess) return cuda(e, call);
   }
   return POP_OK;
@@ -272,9 +283,18 @@ pop_status pop_ilinear_forward_quantized(pop_ilinear_t h, const void* xq, long l
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   for (int m0 = 0; m0 < M; m0 += h->cfg.max_tokens) {
     const int n = M - m0 < h->cfg.max_tokens ? M - m0 : h->cfg.max_tokens;
-    cudaError_t e = launch_i8_half(static_cast<const int8_t*>(xq) + static_cast<size_t>(m0) * ldq, ldq, xs + m0, 1, n, h->cfg.K,
-                                   h->c.rows, h->c.sx, st);
-    if (e == cudaSuccess) e = h->c.product(h->w, h->c.rows, n, rows_of(y, ldy, m0, h->cfg.out_f32), ldy, h->cfg.out_f32, st);
+    const int8_t* q = static_cast<const int8_t*>(xq) + static_cast<size_t>(m0) * ldq;
+    WArgs a = h->c.args(h->w, h->c.rows, n);
+    cudaError_t e = cudaSuccess;
+    if (thin16_converts(3, n, h->cfg.N, h->cfg.K, h->c.num_sms)) {
+      a.rows = q;
+      a.ld_rows = ldq;
+      a.sx = xs + m0;
+      a.convert = 3;
+    } else {
+      e = launch_i8_half(q, ldq, xs + m0, 1, n, h->cfg.K, h->c.rows, h->c.sx, st);
+    }
+    if (e == cudaSuccess) e = product(h, a, y, ldy, m0, st);
     if (e != cudaSuccess) return cuda(e, call);
   }
   return POP_OK;
@@ -316,7 +336,8 @@ pop_status pop_iffn_create(const pop_iffn_config* cfg, const void* Wg, const voi
   cudaError_t e = h->c.make(cfg->max_tokens, cfg->D);
   if (e == cudaSuccess) e = dalloc(&h->h, hidden);
   if (e == cudaSuccess) e = dalloc(&h->hq, hidden);
-  if (e == cudaSuccess) e = dalloc(&h->amax, cfg->max_tokens);
+  const size_t most = static_cast<size_t>(qceil(cfg->D_FF, 128)) * THIN16_MOST;
+  if (e == cudaSuccess) e = dalloc(&h->amax, most > static_cast<size_t>(cfg->max_tokens) ? most : cfg->max_tokens);
   if (e == cudaSuccess) e = h->wg.make(Wg, Sg, cfg->D_FF, cfg->D, st);
   if (e == cudaSuccess) e = h->w1.make(W1, S1, cfg->D_FF, cfg->D, st);
   if (e == cudaSuccess) e = h->w2.make(W2, S2, cfg->D, cfg->D_FF, st);
@@ -349,35 +370,42 @@ pop_status pop_iffn_forward(pop_iffn_t h, const void* x, long long ldx, int M, v
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   for (int m0 = 0; m0 < M; m0 += c.max_tokens) {
     const int n = M - m0 < c.max_tokens ? M - m0 : c.max_tokens;
-    I8RowsArgs rows{};
-    rows.x = static_cast<const uint16_t*>(x) + static_cast<size_t>(m0) * ldx;
-    rows.ldx = ldx;
-    rows.M = n;
-    rows.K = c.D;
-    rows.half = h->c.rows;
-    rows.s = h->c.sx;
-    rows.clear = h->amax;
-    cudaError_t e = launch_i8_rows(rows, st);
+    const bool thin = n <= THIN16_MOST;
+    const int tiles = qceil(c.D_FF, 128);
+    WArgs up;
+    cudaError_t e = h->c.args_of(&up, h->wg, static_cast<const uint16_t*>(x) + static_cast<size_t>(m0) * ldx, ldx, n,
+                                 thin ? nullptr : h->amax, st);
     if (e != cudaSuccess) return cuda(e, call);
-    WArgs up = h->c.args(h->wg, h->c.rows, n);
-    if (!h->c.map_) return fail(POP_ERR_CUDA, call, "a tensor map could not be made");
     up.w8[1] = h->w1.image;
     up.sw1 = h->w1.s;
     up.hf = h->h;
     up.amax = h->amax;
     e = launch_rows16(W_I8_GATED, up, st);
     if (e != cudaSuccess) return cuda(e, call);
-    I8RowsArgs hidden{};
-    hidden.x = h->h;
-    hidden.ldx = c.D_FF;
-    hidden.f32 = 1;
-    hidden.M = n;
-    hidden.K = c.D_FF;
-    hidden.amax = h->amax;
-    hidden.half = h->hq;
-    hidden.s = h->c.sx;
-    e = launch_i8_rows(hidden, st);
-    if (e == cudaSuccess) e = h->c.product(h->w2, h->hq, n, rows_of(y, ldy, m0, c.out_f32), ldy, c.out_f32, st);
+    WArgs down = h->c.args(h->w2, h->hq, n);
+    if (thin16_converts(2, n, c.D, c.D_FF, h->c.num_sms)) {
+      down.rows = h->h;
+      down.convert = 2;
+      down.row_max = h->amax;
+      down.tiles_max = tiles;
+    } else {
+      I8RowsArgs hidden{};
+      hidden.x = h->h;
+      hidden.ldx = c.D_FF;
+      hidden.f32 = 1;
+      hidden.M = n;
+      hidden.K = c.D_FF;
+      hidden.amax = h->amax;
+      hidden.parts = thin ? tiles : 1;
+      hidden.half = h->hq;
+      hidden.s = h->c.sx;
+      e = launch_i8_rows(hidden, st);
+      if (e != cudaSuccess) return cuda(e, call);
+    }
+    down.y[0] = rows_of(y, ldy, m0, c.out_f32);
+    down.ldy[0] = ldy;
+    down.out_f32 = c.out_f32;
+    e = launch_rows16(W_I8, down, st);
     if (e != cudaSuccess) return cuda(e, call);
   }
   return POP_OK;

@@ -84,6 +84,19 @@ __device__ __forceinline__ uint4 half8(uint32_t lo, uint32_t hi) {
   return make_uint4(two(lo, 0x4140), two(lo, 0x4342), two(hi, 0x4140), two(hi, 0x4342));
 }
 
+// The nearest integer to each of two quotients, as the low byte of a float's bits: 1.5 * 2^23 + q.
+__device__ __forceinline__ uint2 nearest(float2 v) {
+  return make_uint2(__float_as_uint(v.x + 0x1.8p23f), __float_as_uint(v.y + 0x1.8p23f));
+}
+
+// ... as fp16.
+__device__ __forceinline__ uint32_t half2_of(uint2 bits) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(__uint_as_float(bits.y) - 0x1.8p23f), "f"(__uint_as_float(bits.x) - 0x1.8p23f));
+  return h;
+}
+__device__ __forceinline__ uint32_t half2_nearest(float2 v) { return half2_of(nearest(v)); }
+
 // ------------------------------------------------------------------ launches
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

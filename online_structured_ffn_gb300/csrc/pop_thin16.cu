@@ -8,6 +8,12 @@
 // 8-bit integers: a block of 128 rows by 64 k comes as it is; 128 threads read a row each, turn it into fp16 and put it into
 // tensor memory, from where the product takes it. (In shared memory the fp16 block would be written and read once more.)
 //
+// Up to 16 rows, where a CTA's k-blocks of them fit beside the ring, need no kernel before this one that quantises (or widens)
+// them: every CTA brings its own from bf16, float32 or integers into their fp16 operands while the matrix's first blocks are on
+// their way. The rows' largest magnitudes, which bf16 rows need first, it finds for itself; a gated MLP's hidden rows come
+// with those of each tile of channels. (Two warps that converted each stage's rows as they came took 0.4 us a k-block,
+// longer than its matrix takes.)
+//
 // Warp 0: copies; the matrix's first stages go out before the kernel before this one has ended, where that does not write them.
 // Warp 1: products. Warps 4..11: conversion, then the epilogue. Every wait has a limit; a CTA that gives up records
 // WERR_TIMEOUT, lets its copies and products finish, frees TMEM and returns.
@@ -25,29 +31,35 @@ constexpr int BM = 128, BK = 64;
 constexpr int MAX_STAGES = 8;
 constexpr int NA = 4;  // blocks in tensor memory, of 32 columns
 
-template <bool I8_, bool GATED_, int NT_>
+template <bool I8_, bool GATED_, int NT_, bool CONV_ = false>
 struct Thin {
   static constexpr bool I8 = I8_, GATED = GATED_;
+  static constexpr bool CONV = CONV_;  // the rows are converted on the way
   static constexpr int NT = NT_, P = GATED ? 2 : 1;
   static constexpr int PER_SM = NT <= 64 ? 2 : 1;
   static constexpr uint32_t W_BYTES = I8 ? W8_BLOCK : BM * BK * 2, X_BYTES = NT * BK * 2;
-  static constexpr uint32_t X_OFF = P * W_BYTES, STAGE = X_OFF + X_BYTES;
-  static constexpr uint32_t BUDGET = (PER_SM == 2 ? 108 : 216) * 1024;
+  // converted rows lie behind the ring, all k-blocks of this CTA
+  static constexpr uint32_t X_OFF = P * W_BYTES, STAGE = X_OFF + (CONV ? 0 : X_BYTES);
+  static constexpr uint32_t KEPT = CONV ? THIN16_KEPT * X_BYTES : 0;
+  static constexpr uint32_t BUDGET = (PER_SM == 2 ? 108 : 216) * 1024 - KEPT;
   static constexpr int FIT = BUDGET / STAGE;
   static constexpr int STAGES = FIT < MAX_STAGES ? FIT : MAX_STAGES;
   static constexpr int COLS = P * NT + (I8 ? NA * 32 : 0);
   static constexpr uint32_t TMEM_COLS = COLS <= 32 ? 32 : COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
   static_assert(TMEM_COLS * PER_SM <= 512, "tensor memory of an SM");
   static_assert(STAGE % 1024 == 0 && STAGES * STAGE >= P * NT * BM * 4, "a part fits into the ring");
-  static constexpr uint32_t SMEM = STAGES * STAGE + 1024;
+  static constexpr uint32_t SMEM = STAGES * STAGE + KEPT + 1024;
 };
 
 struct Ctl {
   uint64_t full[MAX_STAGES], empty[MAX_STAGES];
+  uint64_t xfull;
   uint64_t afull[NA], aempty[NA];
   uint64_t tfull;
   uint32_t tmem_base;
   int abort_flag;
+  unsigned most[THIN16_MOST];   // converted rows: bits of their largest magnitude
+  unsigned hmost[THIN16_MOST];  // gated: of this CTA's tokens' outputs
 };
 
 // kind::f16, A in tensor memory: a lane is a row, a column two values of k. A k-block is four products of 16.
@@ -86,6 +98,28 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint4 (&v)[8]) {
       : "memory");
 }
 
+// Eight values of a row as they stand in memory (bf16: lo alone), and quantised, as fp16.
+struct Raw {
+  uint4 lo, hi;
+};
+__device__ __forceinline__ uint4 half_of(const Raw& w, int size, bool finite, const BlockRatio& ratio) {
+  float v[8];
+  if (size == 2) {
+    v[0] = bf16lo(w.lo.x), v[1] = bf16hi(w.lo.x), v[2] = bf16lo(w.lo.y), v[3] = bf16hi(w.lo.y);
+    v[4] = bf16lo(w.lo.z), v[5] = bf16hi(w.lo.z), v[6] = bf16lo(w.lo.w), v[7] = bf16hi(w.lo.w);
+  } else {
+    v[0] = __uint_as_float(w.lo.x), v[1] = __uint_as_float(w.lo.y), v[2] = __uint_as_float(w.lo.z), v[3] = __uint_as_float(w.lo.w);
+    v[4] = __uint_as_float(w.hi.x), v[5] = __uint_as_float(w.hi.y), v[6] = __uint_as_float(w.hi.z), v[7] = __uint_as_float(w.hi.w);
+  }
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) o[j] = finite ? half2_nearest(ratio(v[2 * j], v[2 * j + 1])) : 0u;
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Barrier 2 of the eight warps.
+__device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 2, 256;" ::: "memory"); }
+
 template <class T>
 __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_constant__ WArgs a) {
   constexpr int STAGES = T::STAGES, NT = T::NT, P = T::P;
@@ -108,8 +142,13 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
       mbar_init(&ctl.aempty[i], 1);
     }
     mbar_init(&ctl.tfull, 1);
+    mbar_init(&ctl.xfull, 8);
     ctl.abort_flag = 0;
     fence_mbar_init();
+  }
+  for (int i = threadIdx.x; i < NT && T::I8; i += THREADS) {
+    ctl.most[i] = AMAX_MIN_BITS;
+    ctl.hmost[i] = 0u;
   }
   if (warp == 1) {
     tmem_alloc(&ctl.tmem_base, T::TMEM_COLS);
@@ -145,7 +184,7 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
         mbar_arrive_expect_tx(&ctl.full[i], T::STAGE);
         matrix(i, i);
       }
-      pdl_wait();
+      if (!T::CONV) pdl_wait();
       uint32_t s = 0, phase = 1;
       int issued = 0;
       for (; issued < n; ++issued) {
@@ -157,7 +196,7 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
           mbar_arrive_expect_tx(&ctl.full[s], T::STAGE);
           matrix(issued, s);
         }
-        tma_load_2d(smem + s * T::STAGE + T::X_OFF, &a.map[0], &ctl.full[s], (kb0 + issued) * BK, 0);
+        if (!T::CONV) tma_load_2d(smem + s * T::STAGE + T::X_OFF, &a.map[0], &ctl.full[s], (kb0 + issued) * BK, 0);
         if (++s == STAGES) s = 0, phase ^= 1;
       }
       // no copy of this CTA may be in flight when it exits
@@ -171,10 +210,11 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
     // ------------------------------------------------------------ products
     const bool leader = elect_one();
     constexpr uint32_t IDESC = idesc_bf16_f32(BM, NT, false) & ~(T::I8 ? (1u << 7) | (1u << 10) : 0u);
-    const uint32_t w0 = desc_lo(smem_u32(smem)), x0 = desc_lo(smem_u32(smem) + T::X_OFF);
+    const uint32_t w0 = desc_lo(smem_u32(smem)), x0 = desc_lo(smem_u32(smem) + (T::CONV ? STAGES * T::STAGE : T::X_OFF));
     uint32_t s = 0, phase = 0, b = 0, bphase = 0;
-    bool ok = true;
+    bool ok = !T::CONV || mbar_wait(&ctl.xfull, 0, a.wait, abort_flag);
     for (int i = 0; i < n && ok; ++i) {
+      const uint32_t x = x0 + (T::CONV ? i * T::X_BYTES : s * T::STAGE) / 16;
       ok = mbar_wait(&ctl.full[s], phase, a.wait, abort_flag);
 #pragma unroll
       for (int p = 0; p < P; ++p) {
@@ -183,10 +223,10 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
         tc_fence_after();
         if (leader) {
           if (T::I8) {
-            umma_ts(tmem_base + p * NT, a_base + b * 32, x0 + s * (T::STAGE >> 4), IDESC, i == 0);
+            umma_ts(tmem_base + p * NT, a_base + b * 32, x, IDESC, i == 0);
             umma_commit(&ctl.aempty[b]);
           } else {
-            umma_ss(tmem_base + p * NT, w0 + (s * T::STAGE + p * T::W_BYTES >> 4), x0 + s * (T::STAGE >> 4), IDESC, i == 0);
+            umma_ss(tmem_base + p * NT, w0 + (s * T::STAGE + p * T::W_BYTES >> 4), x, IDESC, i == 0);
           }
           if (p == P - 1) umma_commit(&ctl.empty[s]);
         }
@@ -204,6 +244,77 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
   } else if (warp >= 4) {
     const int q = warp & 3, half = (warp - 4) >> 2, r = 32 * q + lane;
     bool ok = true;
+    if constexpr (T::CONV) {
+      // ---------------------------------------------------------- rows: their largest magnitudes, then their values
+      pdl_wait();
+      const int M = a.m[0], t = threadIdx.x - 128;
+      if (a.convert == 1) {
+        const int w = warp - 4, share = M >= 8 ? 1 : M >= 4 ? 2 : M >= 2 ? 4 : 8;  // warps to a row
+        const int pieces = a.k >> 3, step = 32 * share;
+        for (int row = w / share; row < M; row += 8 / share) {
+          const uint4* x = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.rows) + static_cast<size_t>(row) * a.ld_rows);
+          float most = 0.f;
+          for (int i = (w % share) * 32 + lane; i < pieces; i += 8 * step) {
+            uint4 v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = i + j * step < pieces ? __ldcg(x + i + j * step) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              most = max_abs(most, bf16lo(v[j].x), bf16hi(v[j].x));
+              most = max_abs(most, bf16lo(v[j].y), bf16hi(v[j].y));
+              most = max_abs(most, bf16lo(v[j].z), bf16hi(v[j].z));
+              most = max_abs(most, bf16lo(v[j].w), bf16hi(v[j].w));
+            }
+          }
+          const unsigned bits = __reduce_max_sync(0xffffffffu, __float_as_uint(most));  // (NaN is above all)
+          if (lane == 0) atomicMax(&ctl.most[row], bits);
+        }
+        rows_sync();
+      } else if (a.convert == 2) {
+        const int row = t & 15;
+        unsigned most = 0u;
+        if (row < M)
+          for (int i = t >> 4; i < a.tiles_max; i += 8 * 16) {
+            unsigned v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              v[j] = i + 16 * j < a.tiles_max ? __ldcg(a.row_max + static_cast<size_t>(i + 16 * j) * THIN16_MOST + row) : 0u;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) most = max(most, v[j]);
+          }
+        if (row < M) atomicMax(&ctl.most[row], most);
+        rows_sync();
+      }
+      const int size = a.convert == 1 ? 2 : a.convert == 2 ? 4 : 1;
+      const int row_pieces = 8 * n;  // of eight values
+      uint8_t* kept = smem + STAGES * T::STAGE;
+      // (what the rows past the last hold goes into their own sums alone)
+      for (int row = 0; row < M; ++row) {
+        const float most = a.convert == 3 ? 1.f : __uint_as_float(ctl.most[row]);
+        const bool finite = most < INFINITY;
+        const BlockRatio ratio(finite ? most : 1.f, 127.f);
+        const uint8_t* x = static_cast<const uint8_t*>(a.rows) + (static_cast<size_t>(row) * a.ld_rows + kb0 * BK) * size;
+        for (int i = t; i < row_pieces; i += 256) {
+          uint4 w = make_uint4(0u, 0u, 0u, 0u);
+          if (kb0 * BK + 8 * i < a.k) {
+            const uint8_t* p = x + 8 * i * size;
+            if (size == 1) {
+              const uint2 v = __ldcg(reinterpret_cast<const uint2*>(p));
+              w = half8(v.x, v.y);
+            } else {
+              Raw v;
+              v.lo = __ldcg(reinterpret_cast<const uint4*>(p));
+              v.hi = size == 4 ? __ldcg(reinterpret_cast<const uint4*>(p) + 1) : make_uint4(0u, 0u, 0u, 0u);
+              w = half_of(v, size, finite, ratio);
+            }
+          }
+          *reinterpret_cast<uint4*>(kept + (i >> 3) * T::X_BYTES + row * 128 + (((i & 7) ^ (row & 7)) << 4)) = w;
+        }
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.xfull);
+    }
     if (T::I8) {
       // ---------------------------------------------------------- conversion: every other block, a row each thread
       uint32_t b = half, bphase = 1;
@@ -236,6 +347,8 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
       }
     }
     // ------------------------------------------------------------ this CTA's part: [column][row]
+    pdl_wait();  // what this kernel writes may still be read by the one before
+    pdl_trigger();
     ok = ok && mbar_wait(&ctl.tfull, 0, a.wait, abort_flag);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok && lane == 0) fail();
@@ -253,30 +366,39 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
       }
     }
   }
-  __syncwarp();
-  cluster_sync();
-  if (warp >= 4) {
-    // ------------------------------------------------------------ epilogue: tokens rank, rank + S, ...
-    pdl_wait();  // what this kernel writes may still be read by the one before
-    pdl_trigger();
-    const int q = warp & 3, half = (warp - 4) >> 2, r = 32 * q + lane;
-    const int M = a.m[0], N = a.n[0], ch = tile * BM + r;
-    const bool is = ch < N;
-    float sw = 1.f, sw1 = 1.f;
-    if (T::I8 && is) {
+  // ------------------------------------------------------------ epilogue: tokens rank, rank + S, ... of either half in turn
+  const int M = a.m[0], N = a.n[0], q = warp & 3, half = (warp - 4) >> 2, r = 32 * q + lane, ch = tile * BM + r;
+  const bool is = ch < N;
+  float sw = 1.f, sw1 = 1.f, sx_own = 0.f;  // sx_own: of the lane-th of this warp's tokens
+  if (T::I8 && warp >= 4) {
+    if (is) {
       sw = __ldg(a.sw + ch);
       if (T::GATED) sw1 = __ldg(a.sw1 + ch);
     }
+    const int t = rank + S * half + 2 * S * lane;
+    if (t < M) {
+      if (T::CONV && a.convert != 3) {
+        const float most = __uint_as_float(ctl.most[t]);
+        sx_own = most < INFINITY ? __fdiv_rn(most, 127.f) : __uint_as_float(0x7fffffffu);
+      } else {
+        sx_own = __ldcg(a.sx + t);
+      }
+    }
+  }
+  __syncwarp();
+  cluster_sync();
+  if (warp >= 4) {
     const uint32_t part = smem_u32(smem) + 4 * r;
     constexpr int AT_ONCE = 4;
+    int at = 0;  // which of this warp's tokens
 #pragma unroll 1
-    for (int t0 = rank + S * half; t0 < M; t0 += 2 * S * AT_ONCE) {
+    for (int t0 = rank + S * half; t0 < M; t0 += 2 * S * AT_ONCE, at += AT_ONCE) {
       float v[AT_ONCE][P];
 #pragma unroll
       for (int j = 0; j < AT_ONCE; ++j)
 #pragma unroll
         for (int p = 0; p < P; ++p) v[j][p] = 0.f;
-#pragma unroll 1
+#pragma unroll 2
       for (int c = 0; c < S; ++c) {
         uint32_t from;
         asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(part), "r"(c));
@@ -292,7 +414,8 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
         const int t = t0 + 2 * S * j;
         if (t >= M) break;
         if (T::I8) {
-          const float sx = __ldcg(a.sx + t);
+          // (at most 64 tokens a warp, of which the second 32 come with one CTA to 128 tokens alone)
+          const float sx = at + j < 32 ? __shfl_sync(0xffffffffu, sx_own, (at + j) & 31) : __ldcg(a.sx + t);
           v[j][0] *= sx * sw;
           if (T::GATED) v[j][P - 1] *= sx * sw1;
         }
@@ -300,10 +423,8 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
           const float g = v[j][0], u = v[j][P - 1], h = silu_mul(g, u);
           if (T::I8) {
             if (is) a.hf[static_cast<size_t>(t) * N + ch] = h;
-            float most = is ? max_abs(0.f, h, 0.f) : 0.f;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) most = max_abs(most, __shfl_xor_sync(0xffffffffu, most, o), 0.f);
-            if (lane == 0) atomicMax(a.amax + t, __float_as_uint(most));
+            const unsigned most = __reduce_max_sync(0xffffffffu, is ? __float_as_uint(max_abs(0.f, h, 0.f)) : 0u);
+            if (lane == 0) atomicMax(&ctl.hmost[t], most);
           } else {
             if (is) a.h[static_cast<size_t>(t) * N + ch] = static_cast<uint16_t>(pack_bf16x2(h, 0.f));
             if (a.saved) {
@@ -329,6 +450,16 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
         }
       }
     }
+    if (T::I8 && T::GATED) {
+      if (half)  // the half's four warps
+        asm volatile("bar.sync 4, 128;" ::: "memory");
+      else
+        asm volatile("bar.sync 3, 128;" ::: "memory");
+      for (int i = 32 * q + lane; rank + S * (half + 2 * i) < M; i += 128) {
+        const int t = rank + S * (half + 2 * i);
+        a.amax[static_cast<size_t>(tile) * THIN16_MOST + t] = ctl.hmost[t];
+      }
+    }
   }
   tc_fence_before();
   __syncwarp();
@@ -343,12 +474,8 @@ template <class T>
 cudaError_t launch(WArgs a, cudaStream_t st) {
   const cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(&k_thin16<T>), T::SMEM);
   if (e != cudaSuccess) return e;
-  if (!encode_map16(&a.map[0], a.rows, a.k, a.m[0], static_cast<uint64_t>(a.ld_rows) * 2, BK, T::NT)) return cudaErrorInvalidValue;
-  const int tiles = qceil(a.n[0], BM), slots = T::PER_SM * a.num_sms;
-  // as many CTAs to a tile as the device holds for all tiles at once, with four k-blocks each at least
-  int S = slots / tiles < 8 ? slots / tiles : 8;
-  if (S > a.kb / 4) S = a.kb / 4;
-  if (S < 1) S = 1;
+  if (!T::CONV && !encode_map16(&a.map[0], a.rows, a.k, a.m[0], static_cast<uint64_t>(a.ld_rows) * 2, BK, T::NT)) return cudaErrorInvalidValue;
+  const int tiles = qceil(a.n[0], BM), S = thin16_split(a.n[0], a.kb, T::PER_SM * a.num_sms);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -366,6 +493,7 @@ cudaError_t launch(WArgs a, cudaStream_t st) {
 
 template <bool I8, bool GATED>
 cudaError_t by_rows(const WArgs& a, cudaStream_t st) {
+  if (I8 && a.convert) return launch<Thin<I8, GATED, 16, I8>>(a, st);
   if (a.m[0] <= 16) return launch<Thin<I8, GATED, 16>>(a, st);
   if (a.m[0] <= 32) return launch<Thin<I8, GATED, 32>>(a, st);
   return a.m[0] <= 64 ? launch<Thin<I8, GATED, 64>>(a, st) : launch<Thin<I8, GATED, 128>>(a, st);

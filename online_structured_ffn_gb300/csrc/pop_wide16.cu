@@ -737,4 +737,10 @@ cudaError_t launch_wide16(WKind kind, const WArgs& a, cudaStream_t st) {
   return cudaErrorInvalidValue;
 }
 
+cudaError_t launch_rows16(WKind kind, WArgs a, cudaStream_t st) {
+  if (a.m[0] <= THIN16_MOST) return launch_thin16(kind, a, st);
+  if (!encode_map16(&a.map[0], a.rows, a.k, a.m[0], static_cast<uint64_t>(a.ld_rows) * 2, BK, BM)) return cudaErrorInvalidValue;
+  return launch_wide16(kind, a, st);
+}
+
 }  // namespace pop

@@ -23,7 +23,7 @@ enum WKind {
 };
 
 struct WArgs {
-  CUtensorMap map[6];  // A and B of each product (W_GATED: A, B0, B1; W_I8*: A)
+  CUtensorMap map[6];  // A and B of each product (W_GATED: A, B0, B1; W_I8*: A), but for the A of launch_rows16
   int problems;
   int m[3], n[3];      // rows and columns of the outputs (gated: n channels)
   int kb;              // k-blocks of 64 (W_DX: of either product)
@@ -37,14 +37,18 @@ struct WArgs {
   const uint8_t* w8[2];        // W_I8*: images of the matrix (gated: of gate and up), instead of B's maps
   const float *sx, *sw, *sw1;  // W_I8*: scales of the rows, and of the columns (gated: of gate and up)
   float* hf;           // W_I8_GATED: [m][n]
-  unsigned* amax;      // W_I8_GATED: bits of the largest |h| of each row (atomicMax)
+  unsigned* amax;      // W_I8_GATED: bits of the largest |h| of each row (atomicMax; thin: of each tile's channels, [tile][THIN16_MOST])
   unsigned* err;
   QWait wait;
   int num_sms;
-  // few rows (launch_rows16): A's rows, as its map was made of them
+  // launch_rows16: A's rows, of k values; of few rows also, W_I8*, rows that are quantised or widened on the way:
+  // `convert` 1: bf16, 2: float32 with `tiles_max` largest values of each row's parts in row_max, 3: integers with scales sx
   const void* rows;
   long long ld_rows;
   int k;
+  int convert;
+  const unsigned* row_max;  // [tiles_max][THIN16_MOST]
+  int tiles_max;
   int b_early;         // 1: what the kernel before this one writes is not among the B operands
   int tiles;           // set by launch_wide16
 };
@@ -53,10 +57,20 @@ cudaError_t launch_wide16(WKind kind, const WArgs& a, cudaStream_t st);
 
 // W_GATED, W_PLAIN, W_I8 or W_I8_GATED: few rows by pop_thin16.cu, more by the wide products.
 constexpr int THIN16_MOST = 128;
-cudaError_t launch_thin16(WKind kind, const WArgs& a, cudaStream_t st);
-inline cudaError_t launch_rows16(WKind kind, const WArgs& a, cudaStream_t st) {
-  return a.m[0] <= THIN16_MOST ? launch_thin16(kind, a, st) : launch_wide16(kind, a, st);
+// CTAs to a tile of 128 outputs: as many as the device holds (`slots`) for all tiles at once.
+constexpr int thin16_split(int n, int kb, int slots) {
+  const int fit = slots / ((n + 127) / 128), most = fit < 8 ? fit : 8;
+  return most > kb ? kb : most < 1 ? 1 : most;
 }
+// Whether a product can take its rows by `convert`: the k-blocks of a CTA have to fit beside its ring, and every CTA goes
+// through all values of bf16 rows first.
+constexpr int THIN16_KEPT = 24;
+constexpr bool thin16_converts(int convert, int m, int n, int k, int num_sms) {
+  const int kb = (k + 63) / 64, split = thin16_split(n, kb, 2 * num_sms);
+  return m <= 16 && (kb + split - 1) / split <= THIN16_KEPT && (convert != 1 || static_cast<long long>(m) * k <= 32768);
+}
+cudaError_t launch_thin16(WKind kind, const WArgs& a, cudaStream_t st);
+cudaError_t launch_rows16(WKind kind, WArgs a, cudaStream_t st);
 
 // The image of a matrix [n, k] of 8-bit integers: blocks of 128 rows by 64 k, [ceil(n/128)][ceil(k/64)][4][128][16], zeros outside.
 constexpr int W8_BLOCK = 128 * 64;
