@@ -839,6 +839,7 @@ class PopGatedFFN(_QHandle):
 
     def __init__(self, D: int, D_FF: int, max_tokens: int = 2048, out_f32: bool = False, grad_f32: bool = False):
         self.D, self.N = D, D_FF
+        self._shapes, self._kept_bytes = ((D_FF, D), (D, D_FF)), {}
         self.cfg = pop_gated_config(D=D, D_FF=D_FF, max_tokens=max_tokens, out_f32=1 if out_f32 else 0,
                                     grad_f32=1 if grad_f32 else 0)
         h = _vp()
@@ -849,24 +850,40 @@ class PopGatedFFN(_QHandle):
         import torch
         return torch.float32 if self.cfg.grad_f32 else torch.bfloat16
 
-    def _matrices(self, Wg, W1, W2):
+    def _matrices(self, Wg, W1, W2, dtype):
+        up, down = self._shapes
+        if not (Wg.shape == up and W1.shape == up and W2.shape == down and Wg.dtype == W1.dtype == W2.dtype == dtype and Wg.is_cuda
+                and W1.is_cuda and W2.is_cuda and Wg.is_contiguous() and W1.is_contiguous() and W2.is_contiguous()):
+            for name, w, shape in (("Wg", Wg, up), ("W1", W1, up), ("W2", W2, down)):
+                _whole_arg(w, name, dtype, shape)
+
+    def _kept(self, M):
+        if M not in self._kept_bytes:
+            self._kept_bytes[M] = _lib.pop_gated_saved_bytes(self.N, M)
+        return self._kept_bytes[M]
+
+    def _like(self, x, under, f32):
+        """A new contiguous tensor of x's shape, bf16 as x is, or float32."""
         import torch
-        for name, w, shape in (("Wg", Wg, (self.N, self.D)), ("W1", W1, (self.N, self.D)), ("W2", W2, (self.D, self.N))):
-            _whole_arg(w, name, torch.bfloat16, shape)
+        if under is None and not f32 and x.is_contiguous():
+            return torch.empty_like(x)  # (the shortest way there)
+        return _empty(under, x.shape, torch.float32 if f32 else torch.bfloat16, x.device)
 
     def forward(self, x, Wg, W1, W2, y=None, save=False, stream=None):
         """x: bf16 [M, D] (rows may be strided), Wg and W1 [D_FF, D], W2 [D, D_FF] bf16. Returns y [M, D] of
         out_dtype(), or with save (y, saved): saved is what backward() takes."""
         import torch
-        M, ld = _rows_arg(x, "x", (torch.bfloat16,), self.D, 16)
-        self._matrices(Wg, W1, W2)
+        bf16 = torch.bfloat16
+        M, ld = _rows_arg(x, "x", (bf16,), self.D, 16)
+        self._matrices(Wg, W1, W2, bf16)
         raw, under = _on(stream, x, Wg, W1, W2, y)
-        y, ldy = self._output(y, M, self.D, x.device, under, 16)
-        saved = None
-        if save:
-            saved = _empty(under, (_lib.pop_gated_saved_bytes(self.N, M),), torch.uint8, x.device)
+        if y is None:
+            y, ldy = self._like(x, under, self.cfg.out_f32), self.D
+        else:
+            y, ldy = self._output(y, M, self.D, x.device, under, 16)
+        saved = _empty(under, (self._kept(M),), torch.uint8, x.device) if save else None
         st = _lib.pop_gated_forward(self.handle, x.data_ptr(), ld, M, Wg.data_ptr(), W1.data_ptr(), W2.data_ptr(), y.data_ptr(),
-                                    ldy, _ptr(saved), raw)
+                                    ldy, saved.data_ptr() if save else None, raw)
         if st != POP_OK:
             _check_with(self._last_error, st)
         return (y, saved) if save else y
@@ -877,32 +894,33 @@ class PopGatedFFN(_QHandle):
         tensors of grad_dtype() to write to instead of new ones (None where none is needed); with
         accumulate they are added to."""
         import torch
-        M, ld = _rows_arg(x, "x", (torch.bfloat16,), self.D, 16)
-        rows, lddy = _rows_arg(dy, "dy", (torch.bfloat16,), self.D, 16)
+        bf16 = torch.bfloat16
+        M, ld = _rows_arg(x, "x", (bf16,), self.D, 16)
+        rows, lddy = _rows_arg(dy, "dy", (bf16,), self.D, 16)
         if rows != M:
             _bad(f"dy: expected {M} rows, got {tuple(dy.shape)}")
-        self._matrices(Wg, W1, W2)
-        _whole_arg(saved, "saved", torch.uint8, (_lib.pop_gated_saved_bytes(self.N, M),))
+        self._matrices(Wg, W1, W2, bf16)
+        _whole_arg(saved, "saved", torch.uint8, (self._kept(M),))
         if len(need) != 4 or (grads is not None and len(grads) != 3):
             _bad("need has one entry for each of dx, dWg, dW1 and dW2, grads one for each of dWg, dW1 and dW2")
         if accumulate and (grads is None or any(n and g is None for n, g in zip(need[1:], grads))):
             _bad("accumulate needs the gradients to add to")
         raw, under = _on(stream, x, dy, Wg, W1, W2, saved, *(grads or ()))
-        dx = _empty(under, (M, self.D), self.out_dtype(), x.device) if need[0] else None
-        out = []
-        for i, shape in enumerate(((self.N, self.D), (self.N, self.D), (self.D, self.N))):
+        f32 = self.cfg.grad_f32
+        out = [self._like(x, under, self.cfg.out_f32) if need[0] else None]
+        for i, w in enumerate((Wg, W1, W2)):
             g = grads[i] if grads is not None and need[i + 1] else None
             if g is not None:
-                _whole_arg(g, ("dWg", "dW1", "dW2")[i], self.grad_dtype(), shape)
+                _whole_arg(g, ("dWg", "dW1", "dW2")[i], self.grad_dtype(), w.shape)
             elif need[i + 1]:
-                g = _empty(under, shape, self.grad_dtype(), x.device)
+                g = self._like(w, under, f32)
             out.append(g)
         st = _lib.pop_gated_backward(self.handle, x.data_ptr(), ld, M, Wg.data_ptr(), W1.data_ptr(), W2.data_ptr(),
-                                     saved.data_ptr(), dy.data_ptr(), lddy, _ptr(dx), self.D, *(_ptr(g) for g in out),
-                                     1 if accumulate else 0, raw)
+                                     saved.data_ptr(), dy.data_ptr(), lddy, _ptr(out[0]), self.D, _ptr(out[1]), _ptr(out[2]),
+                                     _ptr(out[3]), 1 if accumulate else 0, raw)
         if st != POP_OK:
             _check_with(self._last_error, st)
-        return (dx, *out)
+        return tuple(out)
 
 
 # ------------------------------------------------------------------ 8-bit integers

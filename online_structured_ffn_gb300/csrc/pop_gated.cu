@@ -37,10 +37,10 @@ void free_gated(pop_gated* h) {
 
 bool in_range(int dim) { return dim >= 8 && dim % 8 == 0 && dim <= POP_GATED_MAX_DIM; }
 
-// The k-th box of a map of a row-major matrix [outer][inner] as an operand with the inner side contiguous: 64 of it by 128
-// rows where k is inner, by 64 where k is outer.
-bool map_k(CUtensorMap* m, const void* p, int outer, int inner, long long ld) {
-  return encode_map16(m, p, inner, outer, static_cast<uint64_t>(ld) * 2, 64, 128);
+// Maps of a row-major matrix [outer][inner] as an operand: boxes of 64 k by `rows` where k is inner, of 64 values by 64 k where it
+// is outer.
+bool map_k(CUtensorMap* m, const void* p, int outer, int inner, long long ld, int rows = 128) {
+  return encode_map16(m, p, inner, outer, static_cast<uint64_t>(ld) * 2, 64, rows);
 }
 bool map_mn(CUtensorMap* m, const void* p, int outer, int inner, long long ld) {
   return encode_map16(m, p, inner, outer, static_cast<uint64_t>(ld) * 2, 64, 64);
@@ -156,7 +156,12 @@ pop_status pop_gated_forward(pop_gated_t h, const void* x, long long ldx, int M,
   down.rows = hidden;
   down.ld_rows = N;
   down.k = N;
-  if (!map_k(&up.map[1], Wg, N, D, D) || !map_k(&up.map[2], W1, N, D, D) || !map_k(&down.map[1], W2, D, N, N))
+  if (M > THIN16_MOST) {
+    up.width = wide16_width(W_GATED, M, N, h->num_sms);
+    down.width = wide16_width(W_PLAIN, M, D, h->num_sms);
+  }
+  const int up_rows = up.width ? up.width / 2 : 128, down_rows = down.width ? down.width / 2 : 128;
+  if (!map_k(&up.map[1], Wg, N, D, D, up_rows) || !map_k(&up.map[2], W1, N, D, D, up_rows) || !map_k(&down.map[1], W2, D, N, N, down_rows))
     return fail(POP_ERR_CUDA, call, "a tensor map could not be made");
   cudaError_t e = launch_rows16(W_GATED, up, st);
   if (e == cudaSuccess) e = launch_rows16(W_PLAIN, down, st);
@@ -195,6 +200,7 @@ pop_status pop_gated_backward(pop_gated_t h, const void* x, long long ldx, int M
     a.h = h->a;
     a.h2 = h->b;
     a.saved = static_cast<uint32_t*>(const_cast<void*>(saved));
+    a.width = wide16_width(W_DGATED, M, N, h->num_sms);
     maps = map_k(&a.map[0], dy, M, D, lddy) && map_mn(&a.map[1], W2, D, N, N);
     if (maps) e = launch_wide16(W_DGATED, a, st);
   }
@@ -204,6 +210,7 @@ pop_status pop_gated_backward(pop_gated_t h, const void* x, long long ldx, int M
     a.kb = qceil(M, 64);
     a.out_f32 = h->cfg.grad_f32;
     a.accumulate = accumulate;
+    a.width = wide16_width(W_DW, N, D, h->num_sms);
     a.b_early = dWg || dW1 ? 1 : 0;  // else nothing of this call has gone before
     const auto add = [&](void* out, const void* left, int rows, long long ldl, const void* right, int cols, long long ldr) {
       if (!out) return;
@@ -228,6 +235,7 @@ pop_status pop_gated_backward(pop_gated_t h, const void* x, long long ldx, int M
     a.ldy[0] = lddx;
     a.out_f32 = h->cfg.out_f32;
     a.b_early = 1;
+    a.width = wide16_width(W_DX, M, D, h->num_sms);
     maps = map_k(&a.map[0], h->a, M, N, N) && map_mn(&a.map[1], Wg, N, D, D) && map_k(&a.map[2], h->b, M, N, N) &&
            map_mn(&a.map[3], W1, N, D, D);
     if (maps) e = launch_wide16(W_DX, a, st);

@@ -5,7 +5,8 @@
 // that the epilogue of one tile runs under the products of the next. An operand with k contiguous is one box of
 // 64 x 128; one with the other side contiguous two boxes of 64 values by 64 k, and the tensor cores read it mn-major, so
 // no matrix is transposed in memory. Gate and up: the first CTA brings 128 rows of Wg, the second the same of W1,
-// so columns 0..127 of a tile are the gates and 128..255 the ups of 128 channels.
+// so columns 0..127 of a tile are the gates and 128..255 the ups of 128 channels. Tiles may be narrower (wide16_width), so
+// that the last round of them is full.
 //
 // Many tiles go round the pairs. Few tiles of long sums are each given to a cluster of S pairs, which take a run of the k-blocks
 // each; then every CTA sums 1 / S of the columns, the others' parts of them read from their shared memory, and has the
@@ -38,6 +39,7 @@ constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t OUT_BYTES = 8 * 32 * 128;  // 128 bytes of 32 rows on their way out, of each epilogue warp
 constexpr int RING8 = 4;                      // blocks of 128 rows by 64 k of 8-bit integers on their way
 constexpr uint32_t BLOCK8 = W8_BLOCK;
+constexpr int WIDEST = 256;                    // columns of a tile
 constexpr int GROUP = 8;                      // row tiles that share the columns' passes
 
 struct Ctl {
@@ -55,7 +57,6 @@ struct Kind {
   static constexpr bool i8 = KIND == W_I8 || KIND == W_I8_GATED;
   static constexpr bool a_mn = KIND == W_DW;
   static constexpr bool b_mn = KIND == W_DGATED || KIND == W_DX || KIND == W_DW;
-  static constexpr int cols = gated ? 128 : 256;  // outputs (channels) of a tile
   static constexpr int segments = KIND == W_DX ? 2 : 1;
   static constexpr int threads = i8 ? 512 : 384;
   static constexpr int stages = i8 ? 5 : 6;
@@ -90,8 +91,9 @@ struct Tile {
 // their rows' and their columns' operands in L2.
 template <WKind KIND>
 __device__ __forceinline__ Tile tile_at(const WArgs& a, int t) {
+  const int cols = Kind<KIND>::gated ? a.width >> 1 : a.width;
   Tile r{0, 0, 0};
-  int mt = qceil(a.m[0], 2 * BM), nt = qceil(a.n[0], Kind<KIND>::cols);
+  int mt = qceil(a.m[0], 2 * BM), nt = qceil(a.n[0], cols);
   if (KIND == W_DW) {
 #pragma unroll
     for (int p = 1; p < 3; ++p) {
@@ -99,7 +101,7 @@ __device__ __forceinline__ Tile tile_at(const WArgs& a, int t) {
       t -= mt * nt;
       r.p = p;
       mt = qceil(a.m[p], 2 * BM);
-      nt = qceil(a.n[p], Kind<KIND>::cols);
+      nt = qceil(a.n[p], cols);
     }
   }
   const int group = t / (GROUP * nt);
@@ -203,7 +205,7 @@ __device__ __forceinline__ void load_kept(const uint32_t* from, int c, int cols,
   for (int j = 0; j < 8; ++j) {
     const bool is = c + 2 * j < cols;
 #pragma unroll
-    for (int i = 0; i < 3; ++i) k[3 * j + i] = is ? __ldcs(from + (c / 2 + j) * 96 + 32 * i) : 0u;
+    for (int i = 0; i < 3; ++i) k[3 * j + i] = is ? __ldcg(from + (c / 2 + j) * 96 + 32 * i) : 0u;
   }
 }
 
@@ -220,6 +222,7 @@ __global__ void __launch_bounds__(Kind<KIND>::threads, 1) k_wide16(const __grid_
   const int rank = in_cluster & 1, part = in_cluster >> 1;  // within the pair; which run of the k-blocks
   const uint32_t leader_cta = in_cluster & ~1;
   const int tile0 = S == 1 ? blockIdx.x >> 1 : blockIdx.x / (2 * S), tile_step = S == 1 ? gridDim.x >> 1 : a.tiles;
+  const int W2 = a.width >> 1, out_cols = T::gated ? W2 : a.width;  // columns of either CTA's B; outputs (channels) of a tile
   const int KB = a.kb * T::segments, kb0 = KB * part / S, kb1 = KB * (part + 1) / S;
 
   if (threadIdx.x == 0) {
@@ -266,8 +269,8 @@ __global__ void __launch_bounds__(Kind<KIND>::threads, 1) k_wide16(const __grid_
         const int m0 = tile.m * 2 * BM + rank * BM;
         // A CTA without rows multiplies what its stages hold, and nothing reads the products.
         const bool any = m0 < a.m[tile.p];
-        constexpr uint32_t B_BYTES = T::i8 ? 0 : A_BYTES;
-        const int n0 = T::gated ? tile.n * 128 : tile.n * 256 + rank * BM;
+        const uint32_t b_bytes = T::i8 ? 0 : T::b_mn ? (W2 > 64 ? 2 : 1) * BOX_MN : W2 * BK * 2;
+        const int n0 = T::gated ? tile.n * W2 : tile.n * a.width + rank * W2;
         const CUtensorMap* ma = &a.map[KIND == W_DW ? 2 * tile.p : 0];
         const CUtensorMap* mb = T::gated ? &a.map[1 + rank] : ma + 1;
         const auto load = [&](int i, int stage, bool left, bool right) {
@@ -284,12 +287,12 @@ __global__ void __launch_bounds__(Kind<KIND>::threads, 1) k_wide16(const __grid_
           }
           if (right && T::b_mn) {
             tma_load_2d(st + A_BYTES, pb, bar, n0, x);
-            tma_load_2d(st + A_BYTES + BOX_MN, pb, bar, n0 + 64, x);
+            if (W2 > 64) tma_load_2d(st + A_BYTES + BOX_MN, pb, bar, n0 + 64, x);
           } else if (right && !T::i8) {
             tma_load_2d(st + A_BYTES, pb, bar, x, n0);
           }
         };
-        const uint32_t bytes = (any ? A_BYTES : 0) + B_BYTES;
+        const uint32_t bytes = (any ? A_BYTES : 0) + b_bytes;
         if (early) {
           for (int i = 0; i < early; ++i) {
             mbar_arrive_expect_tx(&ctl.full[i], bytes);
@@ -356,7 +359,7 @@ __global__ void __launch_bounds__(Kind<KIND>::threads, 1) k_wide16(const __grid_
       uint32_t s = 0, phase = 0, b = 0, tphase = 1;
       if (rank == 0) {
         // -------------------------------------------------------- products
-        constexpr uint32_t IDESC = idesc_bf16_f32(2 * BM, 256, T::b_mn, T::a_mn) & ~(T::i8 ? (1u << 7) | (1u << 10) : 0u);
+        const uint32_t idesc = idesc_bf16_f32(2 * BM, a.width, T::b_mn, T::a_mn) & ~(T::i8 ? (1u << 7) | (1u << 10) : 0u);
         const uint32_t a0 = operand_lo<T::a_mn>(smem_u32(smem)), b0 = operand_lo<T::b_mn>(smem_u32(smem) + A_BYTES);
         const uint32_t mask = 3u << leader_cta;
         bool ok = true;
@@ -374,7 +377,7 @@ __global__ void __launch_bounds__(Kind<KIND>::threads, 1) k_wide16(const __grid_
             }
             tc_fence_after();
             if (leader) {
-              umma_pair16<T::a_mn, T::b_mn>(tmem_base + b * 256u, a0 + s * (STAGE >> 4), b0 + s * (STAGE >> 4), IDESC, kb == kb0);
+              umma_pair16<T::a_mn, T::b_mn>(tmem_base + b * 256u, a0 + s * (STAGE >> 4), b0 + s * (STAGE >> 4), idesc, kb == kb0);
               commit_pair(&ctl.empty[s], mask);
               if (kb == kb1 - 1) commit_pair(&ctl.tfull[b], mask);
             }
@@ -457,10 +460,10 @@ __global__ void __launch_bounds__(Kind<KIND>::threads, 1) k_wide16(const __grid_
       const int M = a.m[tile.p], N = a.n[tile.p];
       const int row0 = tile.m * 2 * BM + rank * BM + 32 * q;  // this warp's first row
       const int rows = min(32, M - row0);                     // may be none
-      const int own = T::cols / S;                            // outputs of this CTA
-      const int at0 = own * part + (own >> 1) * half;         // this warp's first one within the tile
-      const int col0 = tile.n * T::cols + at0;
-      const int cols = min(own >> 1, N - col0);               // may be none
+      const int own = out_cols / S, lower = (own / 2 + 15) & ~15;  // outputs of this CTA, and of its warps of the lower half
+      const int at0 = own * part + (half ? lower : 0);        // this warp's first one within the tile
+      const int col0 = tile.n * out_cols + at0;
+      const int cols = min(half ? own - lower : lower, N - col0);  // may be none
       const bool some = rows > 0 && cols > 0;
       const uint32_t* from = KIND == W_DGATED ? a.saved + (static_cast<size_t>(row0 >> 5) * (N >> 1) + (col0 >> 1)) * 96 + lane : nullptr;
       uint32_t k0[24], k1[24];
@@ -472,7 +475,7 @@ __global__ void __launch_bounds__(Kind<KIND>::threads, 1) k_wide16(const __grid_
       ok = __all_sync(0xffffffffu, ok);
       if (!ok && lane == 0) fail();
       tc_fence_after();
-      const uint32_t taddr = lane_base + b * 256u + at0;  // gated: the ups are 128 further on
+      const uint32_t taddr = lane_base + b * 256u + at0;  // gated: the ups are W2 further on
       if (S > 1) {
         // What the others are to sum goes to shared memory, where the products no longer read: [column / 4][row][4].
         float4* mine = reinterpret_cast<float4*>(smem) + 32 * q + lane;
@@ -525,7 +528,7 @@ __global__ void __launch_bounds__(Kind<KIND>::threads, 1) k_wide16(const __grid_
           for (int c = 0; c < cols; c += 16) {
             float g[16], u[16];
             columns16(taddr + c, g);
-            columns16(taddr + 128 + c, u);
+            columns16(taddr + W2 + c, u);
             uint32_t p[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) p[j] = pack_bf16x2(silu_mul(g[2 * j], u[2 * j]), silu_mul(g[2 * j + 1], u[2 * j + 1]));
@@ -538,9 +541,9 @@ __global__ void __launch_bounds__(Kind<KIND>::threads, 1) k_wide16(const __grid_
                 const uint32_t g0 = __float_as_uint(g[2 * j]), g1 = __float_as_uint(g[2 * j + 1]);
                 const uint32_t u0 = __float_as_uint(u[2 * j]), u1 = __float_as_uint(u[2 * j + 1]);
                 uint32_t* k = keep + (c / 2 + j) * 96;
-                __stcs(k, __byte_perm(g0, g1, 0x7632));
-                __stcs(k + 32, __byte_perm(u0, u1, 0x7632));
-                __stcs(k + 64, __byte_perm(__byte_perm(g0, g1, 0x0051), __byte_perm(u0, u1, 0x0051), 0x5410));
+                __stcg(k, __byte_perm(g0, g1, 0x7632));
+                __stcg(k + 32, __byte_perm(u0, u1, 0x7632));
+                __stcg(k + 64, __byte_perm(__byte_perm(g0, g1, 0x0051), __byte_perm(u0, u1, 0x0051), 0x5410));
               }
             }
           }
@@ -555,7 +558,7 @@ __global__ void __launch_bounds__(Kind<KIND>::threads, 1) k_wide16(const __grid_
             for (int i = 0; i < 32; i += 16) {
               float g[16], u[16];
               columns16(taddr + c + i, g);
-              columns16(taddr + 128 + c + i, u);
+              columns16(taddr + W2 + c + i, u);
 #pragma unroll
               for (int j = 0; j < 16; ++j) {
                 const int ch = min(col0 + c + i + j, N - 1);
@@ -699,14 +702,14 @@ cudaError_t launch(WArgs a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   long long tiles = 0;
   for (int p = 0; p < (KIND == W_DW ? a.problems : 1); ++p)
-    tiles += static_cast<long long>(qceil(a.m[p], 2 * BM)) * qceil(a.n[p], Kind<KIND>::cols);
+    tiles += static_cast<long long>(qceil(a.m[p], 2 * BM)) * qceil(a.n[p], Kind<KIND>::gated ? a.width / 2 : a.width);
   if (tiles > (1 << 28)) return cudaErrorInvalidValue;
   a.tiles = static_cast<int>(tiles);
   const int KB = a.kb * Kind<KIND>::segments, pairs = a.num_sms / 2;
   // As many pairs to a tile as there are for all tiles at once, with two k-blocks each at least.
   int S = 1;
   for (int s = 4; s > 1 && S == 1; s >>= 1)
-    if (tiles * s <= pairs && KB >= 2 * s && tiles <= clusters_at_a_time<KIND>(s, smem, a.num_sms)) S = s;
+    if (a.width == WIDEST && tiles * s <= pairs && KB >= 2 * s && tiles <= clusters_at_a_time<KIND>(s, smem, a.num_sms)) S = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -724,6 +727,26 @@ cudaError_t launch(WArgs a, cudaStream_t st) {
 
 }  // namespace
 
+// The width for which the rounds of tiles over the pairs take least. Where the widest tiles leave half the pairs idle those are
+// shared instead. A round takes its columns' time, and that of some 24 more. An mn-major B's boxes do not get narrower
+// with the tile, so there it takes that of 350 more, and widths between whole pieces of 32 columns are slower still. 8-bit
+// matrices come in blocks of 128 rows. (Forward of 4096 x 4096 x 11008 in us, at 256 columns 646, 240 617, 224 567, 208 595, 192
+// 615, 160 656; of 1000 rows 156, 153, 157, 187, 191, 195. Gradients of x and the hidden values, 4096 rows 645, 765, 628, 812,
+// 728, 800; 777 x 2048 x 5496 65, 112, 89, 110, 88, 87, and 62 with 160 columns for the hidden ones alone.)
+int wide16_width(WKind kind, int m, int n, int num_sms) {
+  const int pairs = num_sms / 2;
+  const bool gated = kind == W_GATED, mn = kind == W_DGATED || kind == W_DX;
+  const long long mt = qceil(m, 2 * BM);
+  if (kind == W_I8 || kind == W_I8_GATED || kind == W_DW || mt * qceil(n, gated ? WIDEST / 2 : WIDEST) * 2 <= pairs) return WIDEST;
+  int best = WIDEST;
+  long long least = -1;
+  for (int w = WIDEST; w >= 128; w -= mn ? 32 : 16) {
+    const long long rounds = (mt * qceil(n, gated ? w / 2 : w) + pairs - 1) / pairs, cost = rounds * (w + (mn ? 350 : 24));
+    if (least < 0 || cost < least) least = cost, best = w;
+  }
+  return best;
+}
+
 cudaError_t launch_wide16(WKind kind, const WArgs& a, cudaStream_t st) {
   switch (kind) {
     case W_GATED: return launch<W_GATED>(a, st);
@@ -739,6 +762,7 @@ cudaError_t launch_wide16(WKind kind, const WArgs& a, cudaStream_t st) {
 
 cudaError_t launch_rows16(WKind kind, WArgs a, cudaStream_t st) {
   if (a.m[0] <= THIN16_MOST) return launch_thin16(kind, a, st);
+  if (!a.width) a.width = wide16_width(kind, a.m[0], a.n[0], a.num_sms);
   if (!encode_map16(&a.map[0], a.rows, a.k, a.m[0], static_cast<uint64_t>(a.ld_rows) * 2, BK, BM)) return cudaErrorInvalidValue;
   return launch_wide16(kind, a, st);
 }

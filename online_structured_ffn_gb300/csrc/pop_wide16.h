@@ -49,11 +49,15 @@ struct WArgs {
   int convert;
   const unsigned* row_max;  // [tiles_max][THIN16_MOST]
   int tiles_max;
+  int width;           // columns of a tile, as wide16_width gives them (gated: gate and up values, of half as many channels)
   int b_early;         // 1: what the kernel before this one writes is not among the B operands
   int tiles;           // set by launch_wide16
 };
 
 cudaError_t launch_wide16(WKind kind, const WArgs& a, cudaStream_t st);
+
+// Columns of a tile. A k-major B's box has half as many rows. m, n: rows and columns of the outputs (gated: channels).
+int wide16_width(WKind kind, int m, int n, int num_sms);
 
 // W_GATED, W_PLAIN, W_I8 or W_I8_GATED: few rows by pop_thin16.cu, more by the wide products.
 constexpr int THIN16_MOST = 128;

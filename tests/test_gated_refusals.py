@@ -39,7 +39,7 @@ def test_bytes_that_are_kept(pop):
 
 def gone(pop):
     f = pop.PopGatedFFN.__new__(pop.PopGatedFFN)  # one whose handle is never reached
-    f.__dict__.update(D=16, N=8, cfg=pop.pop_gated_config(D=16, D_FF=8, max_tokens=4, out_f32=0, grad_f32=0))
+    f.__dict__.update(D=16, N=8, _shapes=((8, 16), (16, 8)), _kept_bytes={}, cfg=pop.pop_gated_config(D=16, D_FF=8, max_tokens=4, out_f32=0, grad_f32=0))
     return f
 
 

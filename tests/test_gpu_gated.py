@@ -357,3 +357,23 @@ def test_calls_after_a_wait_that_ran_out(env, M, D, N):
         f.check()
     assert ran_out > 0
     f.close()
+
+
+@pytest.mark.parametrize("M,D,N", [(300, 136, 2736), (300, 136, 5496), (520, 136, 2000), (520, 136, 2736), (520, 4096, 264), (777, 4096, 264),
+                                   (1030, 136, 2736), (1030, 2048, 264), (1290, 136, 1032), (1290, 136, 2000), (1540, 136, 1032),
+                                   (2048, 136, 1032), (2048, 2048, 264), (3100, 136, 264), (3100, 520, 264), (3100, 1000, 264),
+                                   (3100, 136, 520), (3100, 2048, 264)])
+def test_tiles_of_every_width(env, M, D, N):
+    """On 152 SMs these take tiles of each width from 128 to 256 columns, in each product that has a choice."""
+    pop, torch, dev = env
+    t = make(env, 13, M, D, N)
+    w = (t["Wg"], t["W1"], t["W2"])
+    f = pop.PopGatedFFN(D, N, max_tokens=M, out_f32=M % 2 == 1)
+    y, saved = f.forward(t["x"], *w, save=True)
+    grads = f.backward(t["dy"], t["x"], *w, saved)
+    f.check()
+    want = reference(t)
+    near(y, want["y"], "y")
+    for name, got in zip(("dx", "dWg", "dW1", "dW2"), grads):
+        near(got, want[name], name)
+    f.close()
