@@ -6,8 +6,6 @@
 namespace pop {
 namespace {
 
-constexpr int HELD = 8;  // pieces of 16 bytes that a thread holds between the two passes over its row
-
 template <bool F32>
 struct Piece {
   static constexpr int V = F32 ? 4 : 8;  // values
@@ -27,10 +25,12 @@ struct Piece {
   }
 };
 
-// T threads to a row, a CTA of 256 (or T, if that is more) threads. A row's values stay in registers, as they stand in memory,
+// T threads to a row, which hold HELD pieces of 16 bytes each between the two passes over it, a CTA of 256 (or T, if that is more) threads. A row's values stay in registers, as they stand in memory,
 // between the pass for the largest and the one that rounds; of rows longer than HELD pieces a thread the rest is read again.
-template <int T, bool F32>
-__global__ void __launch_bounds__(T > 256 ? T : 256, T > 256 ? 2 : 4) k_i8_rows(const __grid_constant__ I8RowsArgs a) {
+// Bound by memory, with the row's largest in the way: 4096 x 4096 of bf16 9.8 us (5.1 TB/s read and written), 1001 x 11008 of
+// float32 11.3 (4.9), 16,384 x 1024 of bf16 9.3 (5.4).
+template <int T, int HELD, bool F32>
+__global__ void __launch_bounds__(T > 256 ? T : 256, (HELD > 4 ? 1024 : 1536) / (T > 256 ? T : 256)) k_i8_rows(const __grid_constant__ I8RowsArgs a) {
   constexpr int ROWS = T > 256 ? 1 : 256 / T, WARPS = T / 32, V = Piece<F32>::V;
   __shared__ float s_most[ROWS][WARPS];
   const int t = threadIdx.x % T, in = threadIdx.x / T;
@@ -133,20 +133,25 @@ __global__ void __launch_bounds__(256) k_i8_pack(const int8_t* __restrict__ W, i
   }
 }
 
-template <int T>
+template <int T, int HELD>
 cudaError_t rows(const I8RowsArgs& a, cudaStream_t st) {
   constexpr int ROWS = T > 256 ? 1 : 256 / T, BLOCK = T > 256 ? T : 256;
   const dim3 grid(static_cast<unsigned>(qceil(a.M, ROWS)));
-  return a.f32 ? launch_q(k_i8_rows<T, true>, grid, BLOCK, 0, st, a) : launch_q(k_i8_rows<T, false>, grid, BLOCK, 0, st, a);
+  return a.f32 ? launch_q(k_i8_rows<T, HELD, true>, grid, BLOCK, 0, st, a) : launch_q(k_i8_rows<T, HELD, false>, grid, BLOCK, 0, st, a);
 }
 
 }  // namespace
 
 cudaError_t launch_i8_rows(const I8RowsArgs& a, cudaStream_t st) {
-  // four pieces a thread, or fewer, where that many threads hold them
   const int pieces = a.K / (a.f32 ? 4 : 8);
-  if (pieces <= 128) return rows<32>(a, st);
-  return pieces <= 1024 ? rows<128>(a, st) : rows<512>(a, st);
+  // As few threads as hold the row in eight pieces each: the sum over a CTA's warps costs more than the longer threads. (us with 64
+  // threads and eight, 128 and four, 128 and eight: 4096 rows of 512 pieces 9.8, 10.0, 11.6; 1000 of them 3.9, 4.7, 3.8; 2048 of
+  // 2048, with 256 and eight, 512 and four, 512 and eight: 12.4, 14.2, 17.4.)
+  if (pieces <= 32 * 4) return rows<32, 4>(a, st);
+  if (pieces <= 32 * 8) return rows<32, 8>(a, st);
+  if (pieces <= 64 * 8) return rows<64, 8>(a, st);
+  if (pieces <= 128 * 8) return rows<128, 8>(a, st);
+  return pieces <= 256 * 8 ? rows<256, 8>(a, st) : rows<512, 8>(a, st);
 }
 
 cudaError_t launch_i8_half(const int8_t* q, long long ldq, const float* s, long long lds, int M, int K, uint16_t* half, float* sx,

@@ -86,7 +86,12 @@ __device__ __forceinline__ uint4 half8(uint32_t lo, uint32_t hi) {
 
 // The nearest integer to each of two quotients, as the low byte of a float's bits: 1.5 * 2^23 + q.
 __device__ __forceinline__ uint2 nearest(float2 v) {
-  return make_uint2(__float_as_uint(v.x + 0x1.8p23f), __float_as_uint(v.y + 0x1.8p23f));
+  uint64_t b;
+  uint2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(v.x), "f"(v.y));
+  asm("add.rn.f32x2 %0, %0, %1;" : "+l"(b) : "l"(0x4b4000004b400000ull));
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(r.x), "=r"(r.y) : "l"(b));
+  return r;
 }
 
 // ... as fp16.

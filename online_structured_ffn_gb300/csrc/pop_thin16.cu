@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
       for (int j = 0; j < AT_ONCE; ++j)
 #pragma unroll
         for (int p = 0; p < P; ++p) v[j][p] = 0.f;
-#pragma unroll 2
+#pragma unroll 4
       for (int c = 0; c < S; ++c) {
         uint32_t from;
         asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(part), "r"(c));
@@ -475,7 +475,7 @@ cudaError_t launch(WArgs a, cudaStream_t st) {
   const cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(&k_thin16<T>), T::SMEM);
   if (e != cudaSuccess) return e;
   if (!T::CONV && !encode_map16(&a.map[0], a.rows, a.k, a.m[0], static_cast<uint64_t>(a.ld_rows) * 2, BK, T::NT)) return cudaErrorInvalidValue;
-  const int tiles = qceil(a.n[0], BM), S = thin16_split(a.n[0], a.kb, T::PER_SM * a.num_sms);
+  const int tiles = qceil(a.n[0], BM), S = thin16_split(a.m[0], a.n[0], a.kb, T::PER_SM * a.num_sms);
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -61,16 +61,19 @@ int wide16_width(WKind kind, int m, int n, int num_sms);
 
 // W_GATED, W_PLAIN, W_I8 or W_I8_GATED: few rows by pop_thin16.cu, more by the wide products.
 constexpr int THIN16_MOST = 128;
-// CTAs to a tile of 128 outputs: as many as the device holds (`slots`) for all tiles at once.
-constexpr int thin16_split(int n, int kb, int slots) {
+// CTAs to a tile of 128 outputs: as many as the device holds (`slots`) for all tiles at once, if each has four k-blocks or if
+// there are 16 tokens for each: a cluster of more takes longer to meet than it saves (16 rows by 2 x 2736 x 1000, back and
+// forth: 45 us with 8, 40 with 4; 64 rows by 2 x 1024 x 256, a block each: 33 with 4, 41 with 1).
+constexpr int thin16_split(int m, int n, int kb, int slots) {
   const int fit = slots / ((n + 127) / 128), most = fit < 8 ? fit : 8;
-  return most > kb ? kb : most < 1 ? 1 : most;
+  const int use = kb / 4 > (m + 15) / 16 ? kb / 4 : (m + 15) / 16, S = most < use ? most : use;
+  return S > kb ? kb : S < 1 ? 1 : S;
 }
 // Whether a product can take its rows by `convert`: the k-blocks of a CTA have to fit beside its ring, and every CTA goes
 // through all values of bf16 rows first.
 constexpr int THIN16_KEPT = 24;
 constexpr bool thin16_converts(int convert, int m, int n, int k, int num_sms) {
-  const int kb = (k + 63) / 64, split = thin16_split(n, kb, 2 * num_sms);
+  const int kb = (k + 63) / 64, split = thin16_split(m, n, kb, 2 * num_sms);
   return m <= 16 && (kb + split - 1) / split <= THIN16_KEPT && (convert != 1 || static_cast<long long>(m) * k <= 32768);
 }
 cudaError_t launch_thin16(WKind kind, const WArgs& a, cudaStream_t st);
