@@ -14,7 +14,7 @@
 // and more: 128 KB of each CTA's part written and read again, one CTA reading them all.)
 //
 // 8-bit integers (there is no tensor-core product of them on sm_103a): exact in fp16, the rows are kept so; the matrix comes as
-// 8-bit blocks, which four more warps turn into fp16 operands in shared memory on the way.
+// 8-bit blocks, which eight more warps turn into fp16 operands in shared memory on the way.
 //
 // Persistent, one CTA per SM. Warp 0: copies. Warp 1: of the first CTA the products of both, of the second the news that
 // its operands have landed. Warps 4..11: epilogue, TMEM lane quarter warp % 4, half of the columns each. Every wait has a
@@ -58,7 +58,7 @@ struct Kind {
   static constexpr bool a_mn = KIND == W_DW;
   static constexpr bool b_mn = KIND == W_DGATED || KIND == W_DX || KIND == W_DW;
   static constexpr int segments = KIND == W_DX ? 2 : 1;
-  static constexpr int threads = i8 ? 512 : 384;
+  static constexpr int threads = i8 ? 640 : 384;
   static constexpr int stages = i8 ? 5 : 6;
   static constexpr uint32_t ring = stages * STAGE + (i8 ? RING8 * BLOCK8 : 0);
 };
@@ -410,37 +410,38 @@ __global__ void __launch_bounds__(Kind<KIND>::threads, 1) k_wide16(const __grid_
     }
     __syncwarp();
   } else if (T::i8 && warp >= 12) {
-    // ------------------------------------------------------------ 8-bit integers to fp16 (warps 12..15, a row each thread)
-    const int r = threadIdx.x - 384;
-    uint32_t s = 0, phase = 1, s8 = 0, phase8 = 0;
-    bool ok = true;
-    for (int t = tile0; t < a.tiles && ok; t += tile_step) {
-      for (int kb = kb0; kb < kb1; ++kb) {
-        ok = mbar_wait(&ctl.full8[s8], phase8, a.wait, abort_flag) && mbar_wait(&ctl.empty[s], phase, a.wait, abort_flag);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) {
-          if (lane == 0) fail();
-          break;
-        }
-        const uint4* from = reinterpret_cast<const uint4*>(smem + STAGES * STAGE + s8 * BLOCK8) + r;
-        uint8_t* to = smem + s * STAGE + A_BYTES + r * 128;
-        uint4 v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = from[128 * j];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          *reinterpret_cast<uint4*>(to + (((2 * j) ^ (r & 7)) << 4)) = half8(v[j].x, v[j].y);
-          *reinterpret_cast<uint4*>(to + (((2 * j + 1) ^ (r & 7)) << 4)) = half8(v[j].z, v[j].w);
-        }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&ctl.full[s]);
-          mbar_arrive(&ctl.empty8[s8]);
-        }
-        if (++s == STAGES) s = 0, phase ^= 1;
-        if (++s8 == RING8) s8 = 0, phase8 ^= 1;
+    // ------------------------------------------------------------ 8-bit integers to fp16 (warps 12..19)
+    // A row each thread, every other k-block either four warps: a block takes a warp longer than its products take.
+    const int r = threadIdx.x & 127;
+    int left = -((warp - 12) >> 2);  // blocks of this CTA
+    for (int t = tile0; t < a.tiles; t += tile_step) left += kb1 - kb0;
+    uint32_t s = (warp - 12) >> 2, phase = 1, s8 = s, phase8 = 0;
+    for (; left > 0; left -= 2) {
+      const bool ok = mbar_wait(&ctl.full8[s8], phase8, a.wait, abort_flag) && mbar_wait(&ctl.empty[s], phase, a.wait, abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) {
+        if (lane == 0) fail();
+        break;
       }
+      const uint4* from = reinterpret_cast<const uint4*>(smem + STAGES * STAGE + s8 * BLOCK8) + r;
+      uint8_t* to = smem + s * STAGE + A_BYTES + r * 128;
+      uint4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = from[128 * j];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        *reinterpret_cast<uint4*>(to + (((2 * j) ^ (r & 7)) << 4)) = half8(v[j].x, v[j].y);
+        *reinterpret_cast<uint4*>(to + (((2 * j + 1) ^ (r & 7)) << 4)) = half8(v[j].z, v[j].w);
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&ctl.full[s]);
+        mbar_arrive(&ctl.empty8[s8]);
+      }
+      s += 2;
+      if (s >= STAGES) s -= STAGES, phase ^= 1;
+      s8 += 2;
+      if (s8 >= RING8) s8 -= RING8, phase8 ^= 1;
     }
     __syncwarp();
   } else {
