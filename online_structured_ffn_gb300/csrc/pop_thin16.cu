@@ -43,7 +43,10 @@ struct Thin {
   static constexpr uint32_t KEPT = CONV ? THIN16_KEPT * X_BYTES : 0;
   static constexpr uint32_t BUDGET = (PER_SM == 2 ? 108 : 216) * 1024 - KEPT;
   static constexpr int FIT = BUDGET / STAGE;
-  static constexpr int STAGES = FIT < MAX_STAGES ? FIT : MAX_STAGES;
+  // A stage's block is converted by the same four warps every time (two sets of them take turns, plain: block by block), as one
+  // that looks at a stage for the first time cannot tell a block that has not landed from the one before it; copies may land
+  // out of order.
+  static constexpr int STAGES = (FIT < MAX_STAGES ? FIT : MAX_STAGES) & (I8 && !GATED ? ~1 : ~0);
   static constexpr int COLS = P * NT + (I8 ? NA * 32 : 0);
   static constexpr uint32_t TMEM_COLS = COLS <= 32 ? 32 : COLS <= 64 ? 64 : COLS <= 128 ? 128 : COLS <= 256 ? 256 : 512;
   static_assert(TMEM_COLS * PER_SM <= 512, "tensor memory of an SM");

@@ -411,7 +411,10 @@ __global__ void __launch_bounds__(Kind<KIND>::threads, 1) k_wide16(const __grid_
     __syncwarp();
   } else if (T::i8 && warp >= 12) {
     // ------------------------------------------------------------ 8-bit integers to fp16 (warps 12..19)
-    // A row each thread, every other k-block either four warps: a block takes a warp longer than its products take.
+    // A row each thread, every other k-block either four warps: a block takes a warp longer than its products take. A slot of the
+    // ring has the same four every time: others, who have not looked at it before, could not tell a block that has not landed
+    // from the one before it, and copies may land out of order.
+    static_assert(RING8 % 2 == 0, "a slot's warps");
     const int r = threadIdx.x & 127;
     int left = -((warp - 12) >> 2);  // blocks of this CTA
     for (int t = tile0; t < a.tiles; t += tile_step) left += kb1 - kb0;
