@@ -291,27 +291,39 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
       const int size = a.convert == 1 ? 2 : a.convert == 2 ? 4 : 1;
       const int row_pieces = 8 * n;  // of eight values
       uint8_t* kept = smem + STAGES * T::STAGE;
-      // (what the rows past the last hold goes into their own sums alone)
-      for (int row = 0; row < M; ++row) {
-        const float most = a.convert == 3 ? 1.f : __uint_as_float(ctl.most[row]);
-        const bool finite = most < INFINITY;
-        const BlockRatio ratio(finite ? most : 1.f, 127.f);
-        const uint8_t* x = static_cast<const uint8_t*>(a.rows) + (static_cast<size_t>(row) * a.ld_rows + kb0 * BK) * size;
-        for (int i = t; i < row_pieces; i += 256) {
-          uint4 w = make_uint4(0u, 0u, 0u, 0u);
-          if (kb0 * BK + 8 * i < a.k) {
-            const uint8_t* p = x + 8 * i * size;
-            if (size == 1) {
-              const uint2 v = __ldcg(reinterpret_cast<const uint2*>(p));
-              w = half8(v.x, v.y);
-            } else {
-              Raw v;
-              v.lo = __ldcg(reinterpret_cast<const uint4*>(p));
-              v.hi = size == 4 ? __ldcg(reinterpret_cast<const uint4*>(p) + 1) : make_uint4(0u, 0u, 0u, 0u);
-              w = half_of(v, size, finite, ratio);
-            }
+      // Four pieces a thread on their way, of whatever rows. (What the rows past the last hold goes into their own sums alone.)
+      constexpr int AT_A_TIME = 4;
+      for (int i0 = t; i0 < M * row_pieces; i0 += 256 * AT_A_TIME) {
+        Raw v[AT_A_TIME];
+        int row[AT_A_TIME], piece[AT_A_TIME];
+#pragma unroll
+        for (int j = 0; j < AT_A_TIME; ++j) {
+          const int i = i0 + 256 * j;
+          row[j] = i / row_pieces;
+          piece[j] = i - row[j] * row_pieces;
+          v[j].lo = v[j].hi = make_uint4(0u, 0u, 0u, 0u);
+          if (row[j] >= M || kb0 * BK + 8 * piece[j] >= a.k) continue;
+          const uint8_t* p = static_cast<const uint8_t*>(a.rows) + (static_cast<size_t>(row[j]) * a.ld_rows + kb0 * BK + 8 * piece[j]) * size;
+          if (size == 1) {
+            const uint2 w = __ldcg(reinterpret_cast<const uint2*>(p));
+            v[j].lo.x = w.x, v[j].lo.y = w.y;
+          } else {
+            v[j].lo = __ldcg(reinterpret_cast<const uint4*>(p));
+            if (size == 4) v[j].hi = __ldcg(reinterpret_cast<const uint4*>(p) + 1);
           }
-          *reinterpret_cast<uint4*>(kept + (i >> 3) * T::X_BYTES + row * 128 + (((i & 7) ^ (row & 7)) << 4)) = w;
+        }
+#pragma unroll
+        for (int j = 0; j < AT_A_TIME; ++j) {
+          if (row[j] >= M) break;
+          uint4 w;
+          if (size == 1) {
+            w = half8(v[j].lo.x, v[j].lo.y);
+          } else {
+            const float most = __uint_as_float(ctl.most[row[j]]);
+            const bool finite = most < INFINITY;
+            w = half_of(v[j], size, finite, BlockRatio(finite ? most : 1.f, 127.f));
+          }
+          *reinterpret_cast<uint4*>(kept + (piece[j] >> 3) * T::X_BYTES + row[j] * 128 + (((piece[j] & 7) ^ (row[j] & 7)) << 4)) = w;
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");

@@ -69,12 +69,15 @@ constexpr int thin16_split(int m, int n, int kb, int slots) {
   const int use = kb / 4 > (m + 15) / 16 ? kb / 4 : (m + 15) / 16, S = most < use ? most : use;
   return S > kb ? kb : S < 1 ? 1 : S;
 }
-// Whether a product can take its rows by `convert`: the k-blocks of a CTA have to fit beside its ring, and every CTA goes
-// through all values of bf16 rows first.
+// Whether a product takes its rows by `convert`: the k-blocks of a CTA have to fit beside its ring; and every CTA goes through all
+// values of bf16 rows first, and there are as many CTAs as keep the device busy, so with many values a kernel of its own is
+// faster (us with one and without: gate and up of 4 rows by 2 x 11008 x 4096, 16 K values, 0.5 more, of 2 rows 0.2 less; down
+// projections of hidden rows, 44 K values 0.3 less, 88 K 1.0 more; 16 rows of integers by 4096 x 4096 1.0 less).
 constexpr int THIN16_KEPT = 24;
 constexpr bool thin16_converts(int convert, int m, int n, int k, int num_sms) {
   const int kb = (k + 63) / 64, split = thin16_split(m, n, kb, 2 * num_sms);
-  return m <= 16 && (kb + split - 1) / split <= THIN16_KEPT && (convert != 1 || static_cast<long long>(m) * k <= 32768);
+  const long long values = static_cast<long long>(m) * k;
+  return m <= 16 && (kb + split - 1) / split <= THIN16_KEPT && (convert == 3 || values <= (convert == 1 ? 12288 : 45056));
 }
 cudaError_t launch_thin16(WKind kind, const WArgs& a, cudaStream_t st);
 cudaError_t launch_rows16(WKind kind, WArgs a, cudaStream_t st);
