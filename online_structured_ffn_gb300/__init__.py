@@ -8,7 +8,9 @@ There is no CPU fallback: importing fails loudly when the library is missing.
 The names mirror the C ABI in ``include/pop_ffn.h`` (``pop_ffn_create``,
 ``pop_prefill_partition``, ``pop_decode_step``, ``pop_ffn_dense_ref``, ...);
 ``PopFFN`` wraps a handle for convenience. Routing (``PopRouter``, ``include/pop_route.h``) and the
-8-bit operators (``quantize_rows``, ``PopQLinear``, ``PopQMoE``, ``include/pop_quant.h``) follow below.
+8-bit operators (``quantize_rows``, ``PopQLinear``, ``PopQMoE``, ``include/pop_quant.h``) follow below, then the gated
+MLP on matrices that the caller trains (``PopGatedFFN``, ``include/pop_gated.h``) and 8-bit integers
+(``quantize_rows_i8``, ``PopI8Linear``, ``PopI8FFN``, ``include/pop_int8.h``).
 """
 from __future__ import annotations
 

@@ -14,6 +14,10 @@
 // with those of each tile of channels. (Two warps that converted each stage's rows as they came took 0.4 us a k-block,
 // longer than its matrix takes.)
 //
+// Bound by the matrix's bytes, and with short ones by what comes before and after them (some 5 us: first bytes 1.2, the
+// cluster's meeting 1.2, the others' parts 0.7, its end 1). Back to back: gate and up and down of one token, bf16 46.5 us for 270
+// MB (5.8 TB/s); 8-bit: 16 rows by 8192 x 28672 with their quantising 44 us (5.4), one row by 11008 x 4096 11.4 (4.0).
+//
 // Warp 0: copies; the matrix's first stages go out before the kernel before this one has ended, where that does not write them.
 // Warp 1: products. Warps 4..11: conversion, then the epilogue. Every wait has a limit; a CTA that gives up records
 // WERR_TIMEOUT, lets its copies and products finish, frees TMEM and returns.

@@ -1,7 +1,7 @@
 // Products of 16-bit operands on 256 x 256 tiles with fused epilogues (pop_wide16.h).
 //
 // Two CTAs of a cluster work as a pair on 256 rows by 256 columns (cta_group::2): each brings its own 128 rows and 128
-// columns of a k-block of 64, 32 KB by TMA into a ring of six, and has its rows' 256 fp32 sums in tensor memory, twice, so
+// columns of a k-block of 64, 32 KB by TMA into a ring of six (8-bit: of four), and has its rows' 256 fp32 sums in tensor memory, twice, so
 // that the epilogue of one tile runs under the products of the next. An operand with k contiguous is one box of
 // 64 x 128; one with the other side contiguous two boxes of 64 values by 64 k, and the tensor cores read it mn-major, so
 // no matrix is transposed in memory. Gate and up: the first CTA brings 128 rows of Wg, the second the same of W1,
@@ -14,7 +14,12 @@
 // and more: 128 KB of each CTA's part written and read again, one CTA reading them all.)
 //
 // 8-bit integers (there is no tensor-core product of them on sm_103a): exact in fp16, the rows are kept so; the matrix comes as
-// 8-bit blocks, which eight more warps turn into fp16 operands in shared memory on the way.
+// 8-bit blocks, which twelve more warps turn into fp16 operands in shared memory on the way.
+//
+// Bound by the tensor cores, of many rows by the power limit: gate and up of 2048 tokens by 2 x 11008 x 4096 188 us (1.96 PFLOP/s,
+// tensor cores busy 95 %), down 98 (1.88; 92 %); gradients of the matrices of 1024 tokens 162 (1.71; 81 %, as their tiles have
+// 16 k-blocks), of the hidden values 71, whose epilogue reads 6 bytes a value and writes 4 (69 %). A k-block of a pair takes
+// 0.27 us; of 8-bit integers 0.30.
 //
 // Persistent, one CTA per SM. Warp 0: copies. Warp 1: of the first CTA the products of both, of the second the news that
 // its operands have landed. Warps 4..11: epilogue, TMEM lane quarter warp % 4, half of the columns each. Every wait has a
@@ -37,7 +42,7 @@ constexpr uint32_t A_BYTES = BM * BK * 2, STAGE = 2 * A_BYTES;
 constexpr uint32_t BOX_MN = 64 * 64 * 2;  // one of an mn-major operand's two boxes
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t OUT_BYTES = 8 * 32 * 128;  // 128 bytes of 32 rows on their way out, of each epilogue warp
-constexpr int RING8 = 4;                      // blocks of 128 rows by 64 k of 8-bit integers on their way
+constexpr int RING8 = 6;                      // blocks of 128 rows by 64 k of 8-bit integers on their way
 constexpr uint32_t BLOCK8 = W8_BLOCK;
 constexpr int WIDEST = 256;                    // columns of a tile
 constexpr int GROUP = 8;                      // row tiles that share the columns' passes
@@ -58,8 +63,8 @@ struct Kind {
   static constexpr bool a_mn = KIND == W_DW;
   static constexpr bool b_mn = KIND == W_DGATED || KIND == W_DX || KIND == W_DW;
   static constexpr int segments = KIND == W_DX ? 2 : 1;
-  static constexpr int threads = i8 ? 640 : 384;
-  static constexpr int stages = i8 ? 5 : 6;
+  static constexpr int threads = i8 ? 768 : 384;
+  static constexpr int stages = i8 ? 4 : 6;
   static constexpr uint32_t ring = stages * STAGE + (i8 ? RING8 * BLOCK8 : 0);
 };
 
@@ -410,16 +415,18 @@ __global__ void __launch_bounds__(Kind<KIND>::threads, 1) k_wide16(const __grid_
     }
     __syncwarp();
   } else if (T::i8 && warp >= 12) {
-    // ------------------------------------------------------------ 8-bit integers to fp16 (warps 12..19)
-    // A row each thread, every other k-block either four warps: a block takes a warp longer than its products take. A slot of the
-    // ring has the same four every time: others, who have not looked at it before, could not tell a block that has not landed
-    // from the one before it, and copies may land out of order.
-    static_assert(RING8 % 2 == 0, "a slot's warps");
+    // ------------------------------------------------------------ 8-bit integers to fp16 (warps 12..23)
+    // A row each thread, every third k-block the same four warps: a block takes a warp longer than its products take (with one set
+    // of warps 0.36 us and more a k-block, two 0.32, three 0.30). A slot of the ring has the same four every time: others, who
+    // have not looked at it before, could not tell a block that has not landed from the one before it, and copies may land out of
+    // order. (Stages are freed in order.)
+    constexpr int SETS = 3;
+    static_assert(RING8 % SETS == 0 && (!T::i8 || T::threads == 384 + 128 * SETS), "a slot's warps");
     const int r = threadIdx.x & 127;
     int left = -((warp - 12) >> 2);  // blocks of this CTA
     for (int t = tile0; t < a.tiles; t += tile_step) left += kb1 - kb0;
     uint32_t s = (warp - 12) >> 2, phase = 1, s8 = s, phase8 = 0;
-    for (; left > 0; left -= 2) {
+    for (; left > 0; left -= SETS) {
       const bool ok = mbar_wait(&ctl.full8[s8], phase8, a.wait, abort_flag) && mbar_wait(&ctl.empty[s], phase, a.wait, abort_flag);
       if (!__all_sync(0xffffffffu, ok)) {
         if (lane == 0) fail();
@@ -441,9 +448,9 @@ __global__ void __launch_bounds__(Kind<KIND>::threads, 1) k_wide16(const __grid_
         mbar_arrive(&ctl.full[s]);
         mbar_arrive(&ctl.empty8[s8]);
       }
-      s += 2;
+      s += SETS;
       if (s >= STAGES) s -= STAGES, phase ^= 1;
-      s8 += 2;
+      s8 += SETS;
       if (s8 >= RING8) s8 -= RING8, phase8 ^= 1;
     }
     __syncwarp();

@@ -59,7 +59,9 @@ cudaError_t launch_wide16(WKind kind, const WArgs& a, cudaStream_t st);
 // Columns of a tile. A k-major B's box has half as many rows. m, n: rows and columns of the outputs (gated: channels).
 int wide16_width(WKind kind, int m, int n, int num_sms);
 
-// W_GATED, W_PLAIN, W_I8 or W_I8_GATED: few rows by pop_thin16.cu, more by the wide products.
+// W_GATED, W_PLAIN, W_I8 or W_I8_GATED: few rows by pop_thin16.cu, more by the wide products. (us of a whole MLP thin against wide,
+// 4096 x 11008: bf16 65 rows 56/66, 128 61/67; 8-bit 57/86, 70/88; 1000 x 2736 bf16 16/19, 19/20; 8192 x 28672 bf16 231/227,
+// 244/230, 8-bit 185/219, 212/225.)
 constexpr int THIN16_MOST = 128;
 // CTAs to a tile of 128 outputs: as many as the device holds (`slots`) for all tiles at once, if each has four k-blocks or if
 // there are 16 tokens for each: a cluster of more takes longer to meet than it saves (16 rows by 2 x 2736 x 1000, back and
