@@ -310,3 +310,33 @@ def test_calls_after_a_wait_that_ran_out(env, M, D, N):
             o.check()
         assert ran_out > 0
         o.close()
+
+
+@pytest.mark.parametrize("M,D,N", [(1, 1000, 2736), (8, 1024, 2048), (3, 4096, 11008)])
+def test_rows_quantised_on_the_way_after_short_limits(env, M, D, N):
+    """The same where the rows are converted inside the products and the hidden rows' largest values come from the tiles. (Waits
+    this short mostly end within their first tries: none need run out.)"""
+    pop, torch, dev = env
+    ms = [normal(env, i, *shape, scale=0.02) for i, shape in enumerate(((N, D), (N, D), (D, N)))]
+    f, h = pop.PopI8FFN(*ms, max_tokens=M), pop.PopI8Linear(ms[0], max_tokens=M)
+    xs = [normal(env, 5 + i, M, D) for i in range(2)]
+    q, s = pop.quantize_rows_i8(xs[0])
+    flush = torch.empty((64 << 20,), device=dev)
+    for o, calls in ((f, (f.forward,)), (h, (h.forward, lambda x: h.forward_q(*pop.quantize_rows_i8(x))))):
+        for call in calls:
+            want = [call(x) for x in xs]
+            for ns in (1, 1, 500, 1000, 2000):
+                flush.zero_()
+                torch.cuda.synchronize()
+                o.set_wait_limit(ns)
+                call(xs[1])
+                o.set_wait_limit(2_000_000_000)
+                try:
+                    o.check()
+                except pop.PopError as e:
+                    assert e.status == pop.POP_ERR_TIMEOUT
+                for i in (0, 1, 0):
+                    assert torch.equal(call(xs[i]), want[i]), f"after a limit of {ns} ns"
+                o.check()
+        o.close()
+    assert torch.equal(q, steps(xs[0])[0])
