@@ -21,6 +21,9 @@
 // Warp 0: copies; the matrix's first stages go out before the kernel before this one has ended, where that does not write them.
 // Warp 1: products. Warps 4..11: conversion, then the epilogue. Every wait has a limit; a CTA that gives up records
 // WERR_TIMEOUT, lets its copies and products finish, frees TMEM and returns.
+#include <algorithm>
+#include <atomic>
+
 #include "pop_qdevice.cuh"
 #include "pop_wide16.h"
 
@@ -494,7 +497,8 @@ cudaError_t launch(WArgs a, cudaStream_t st) {
   const cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(&k_thin16<T>), T::SMEM);
   if (e != cudaSuccess) return e;
   if (!T::CONV && !encode_map16(&a.map[0], a.rows, a.k, a.m[0], static_cast<uint64_t>(a.ld_rows) * 2, BK, T::NT)) return cudaErrorInvalidValue;
-  const int tiles = qceil(a.n[0], BM), S = thin16_split(a.m[0], a.n[0], a.kb, T::PER_SM * a.num_sms);
+  const int tiles = qceil(a.n[0], BM), S = thin16_split(T::I8, a.m[0], a.n[0], a.kb, a.num_sms);
+  if (T::CONV && qceil(a.kb, S) > THIN16_KEPT) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -518,7 +522,64 @@ cudaError_t by_rows(const WArgs& a, cudaStream_t st) {
   return a.m[0] <= 64 ? launch<Thin<I8, GATED, 64>>(a, st) : launch<Thin<I8, GATED, 128>>(a, st);
 }
 
+// Clusters of S CTAs that the device holds at a time with a CTA on each SM; asked once per device. (Of 152 SMs 36 of 4, 23
+// of 6, 15 of 7 or 8.)
+int clusters_at_a_time(int S, int num_sms) {
+  using T = Thin<false, false, 128>;
+  static std::atomic<int> known[64][9];
+  int dev = 0;
+  if (S == 1) return num_sms;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = known[dev][S].load(std::memory_order_relaxed);
+  if (n == 0) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {static_cast<unsigned>(S), 1, 1};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(num_sms / S * S);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = T::SMEM;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (ensure_dyn_smem(reinterpret_cast<const void*>(&k_thin16<T>), T::SMEM) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, k_thin16<T>, &cfg) != cudaSuccess) {
+      cudaGetLastError();
+      n = 0;
+    }
+    n = n > 0 ? n : -1;
+    known[dev][S].store(n, std::memory_order_relaxed);
+  }
+  return n > 0 ? n : 0;
+}
+
 }  // namespace
+
+// As many CTAs to a tile as have an SM each, in clusters of their number; a few clusters that have to wait for the others
+// cost as much again (64 rows by 2 x 5496 x 2048 and back: 33 us in clusters of 7, 22 in clusters of 3). Two on an SM where each
+// still has 16 k-blocks (one row by 2 x 11008 x 4096 and back: clusters of 3 47.9 us, of 1 53.8), or 6, where else only one
+// would be at a tile and SMs idle (32 rows of 8 bits by 11008 x 2048: 11.1 with 3, 14.1 with 1; 128 rows by 11008 x 8192, one
+// after the other: 39.5 and 48.7). No more than have four k-blocks or 16 tokens each: a larger cluster takes longer to
+// meet than it saves (16 rows by 2 x 2736 x 1000, back and forth: 45 us with 8, 40 with 4; 64 rows by 2 x 1024 x 256, a block
+// each: 33 with 4, 41 with 1).
+int thin16_split(bool i8, int m, int n, int kb, int num_sms) {
+  const int tiles = qceil(n, BM);
+  int one = 1, two = 1;
+  for (int S = 2; S <= 8; ++S) {
+    const int held = clusters_at_a_time(S, num_sms);
+    if (held >= tiles) one = S;
+    if (tiles * S <= 2 * num_sms && 2 * held * 11 >= tiles * 10) two = S;  // (a tenth too many does no harm)
+  }
+  const bool pays = one == 1 ? kb / two >= 6 && (i8 || m <= 64) : kb / two >= 16 && m <= 64;  // (of more rows one fits on an SM)
+  const int use = std::max(kb / 4, qceil(m, 16));
+  return std::max(1, std::min({pays ? std::max(one, two) : one, use, kb}));
+}
+
+bool thin16_converts(int convert, int m, int n, int k, int num_sms) {
+  if (m > 16) return false;
+  const int kb = qceil(k, BK);
+  const long long values = static_cast<long long>(m) * k;
+  return qceil(kb, thin16_split(true, m, n, kb, num_sms)) <= THIN16_KEPT && (convert == 3 || values <= (convert == 1 ? 12288 : 45056));
+}
 
 cudaError_t launch_thin16(WKind kind, const WArgs& a, cudaStream_t st) {
   switch (kind) {

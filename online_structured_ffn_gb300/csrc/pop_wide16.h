@@ -63,24 +63,14 @@ int wide16_width(WKind kind, int m, int n, int num_sms);
 // 4096 x 11008: bf16 65 rows 56/66, 128 61/67; 8-bit 57/86, 70/88; 1000 x 2736 bf16 16/19, 19/20; 8192 x 28672 bf16 231/227,
 // 244/230, 8-bit 185/219, 212/225.)
 constexpr int THIN16_MOST = 128;
-// CTAs to a tile of 128 outputs: as many as the device holds (`slots`) for all tiles at once, if each has four k-blocks or if
-// there are 16 tokens for each: a cluster of more takes longer to meet than it saves (16 rows by 2 x 2736 x 1000, back and
-// forth: 45 us with 8, 40 with 4; 64 rows by 2 x 1024 x 256, a block each: 33 with 4, 41 with 1).
-constexpr int thin16_split(int m, int n, int kb, int slots) {
-  const int fit = slots / ((n + 127) / 128), most = fit < 8 ? fit : 8;
-  const int use = kb / 4 > (m + 15) / 16 ? kb / 4 : (m + 15) / 16, S = most < use ? most : use;
-  return S > kb ? kb : S < 1 ? 1 : S;
-}
+// CTAs to a tile of 128 outputs (pop_thin16.cu).
+int thin16_split(bool i8, int m, int n, int kb, int num_sms);
 // Whether a product takes its rows by `convert`: the k-blocks of a CTA have to fit beside its ring; and every CTA goes through all
 // values of bf16 rows first, and there are as many CTAs as keep the device busy, so with many values a kernel of its own is
 // faster (us with one and without: gate and up of 4 rows by 2 x 11008 x 4096, 16 K values, 0.5 more, of 2 rows 0.2 less; down
 // projections of hidden rows, 44 K values 0.3 less, 88 K 1.0 more; 16 rows of integers by 4096 x 4096 1.0 less).
 constexpr int THIN16_KEPT = 24;
-constexpr bool thin16_converts(int convert, int m, int n, int k, int num_sms) {
-  const int kb = (k + 63) / 64, split = thin16_split(m, n, kb, 2 * num_sms);
-  const long long values = static_cast<long long>(m) * k;
-  return m <= 16 && (kb + split - 1) / split <= THIN16_KEPT && (convert == 3 || values <= (convert == 1 ? 12288 : 45056));
-}
+bool thin16_converts(int convert, int m, int n, int k, int num_sms);
 cudaError_t launch_thin16(WKind kind, const WArgs& a, cudaStream_t st);
 cudaError_t launch_rows16(WKind kind, WArgs a, cudaStream_t st);
 

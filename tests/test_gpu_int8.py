@@ -340,3 +340,20 @@ def test_rows_quantised_on_the_way_after_short_limits(env, M, D, N):
                 o.check()
         o.close()
     assert torch.equal(q, steps(xs[0])[0])
+
+
+@pytest.mark.parametrize("M", [1, 20, 64, 100])
+@pytest.mark.parametrize("N", [264, 2000, 2400, 3080, 4200, 4800, 9600, 9800, 20000])
+def test_tiles_shared_by_one_to_eight(env, M, N):
+    """Short sums and longer ones: on 152 SMs clusters of every number of CTAs, one and two on an SM."""
+    pop, torch, dev = env
+    for K in (200, 2056):
+        W, x = integers(env, N, N, K, -9, 9), integers(env, N + 1, M, K, -9, 9)
+        sx, sw = torch.rand((M,), device=dev) + 0.5, torch.rand((N,), device=dev) + 0.5
+        h = pop.PopI8Linear(W, sw, max_tokens=M, out_f32=True)
+        y = h.forward_q(x, sx)
+        h.check()
+        # the sums are whole numbers below 2^24, and exact: what is left is two products' roundings
+        value = (x.double() @ W.double().t()) * sx.double()[:, None] * sw.double()
+        assert bool(((y.double() - value).abs() <= value.abs() * (2 * 2.0 ** -24) * (1 + 2.0 ** -20)).all())
+        h.close()
