@@ -51,9 +51,12 @@ struct WArgs {
   int tiles_max;
   int width;           // columns of a tile, as wide16_width gives them (gated: gate and up values, of half as many channels)
   int b_early;         // 1: what the kernel before this one writes is not among the B operands
-  int tiles;           // set by launch_wide16
+  int tiles, a_rows, stages;  // set by launch_wide16
 };
 
+// Rows of a k-major A's box (16-bit operands): few rows leave room for more stages. (Forward and backward of 8 rows by
+// 2 x 11008 x 4096 171 us with nine stages, 187 with six.)
+constexpr int wide16_a_rows(int m) { return m <= 32 ? 32 : m <= 64 ? 64 : 128; }
 cudaError_t launch_wide16(WKind kind, const WArgs& a, cudaStream_t st);
 
 // Columns of a tile. A k-major B's box has half as many rows. m, n: rows and columns of the outputs (gated: channels).

@@ -377,3 +377,20 @@ def test_tiles_of_every_width(env, M, D, N):
     for name, got in zip(("dx", "dWg", "dW1", "dW2"), grads):
         near(got, want[name], name)
     f.close()
+
+
+@pytest.mark.parametrize("M", [31, 32, 33, 63, 64, 65])
+def test_few_rows_of_long_sums(env, M):
+    """Boxes of each height, and rings of each length, gone round several times."""
+    pop, torch, dev = env
+    t = make(env, 14, M, 1288, 1544)
+    w = (t["Wg"], t["W1"], t["W2"])
+    f = pop.PopGatedFFN(1288, 1544, max_tokens=M)
+    y, saved = f.forward(t["x"], *w, save=True)
+    grads = f.backward(t["dy"], t["x"], *w, saved)
+    f.check()
+    want = reference(t)
+    near(y, want["y"], "y")
+    for name, got in zip(("dx", "dWg", "dW1", "dW2"), grads):
+        near(got, want[name], name)
+    f.close()
