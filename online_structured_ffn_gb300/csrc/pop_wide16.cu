@@ -474,10 +474,12 @@ __global__ void __launch_bounds__(Kind<KIND>::threads, 1) k_wide16(const __grid_
       const int M = a.m[tile.p], N = a.n[tile.p];
       const int row0 = tile.m * 2 * BM + rank * BM + 32 * q;  // this warp's first row
       const int rows = min(32, M - row0);                     // may be none
-      const int own = out_cols / S, lower = (own / 2 + 15) & ~15;  // outputs of this CTA, and of its warps of the lower half
-      const int at0 = own * part + (half ? lower : 0);        // this warp's first one within the tile
+      // outputs of this CTA (of three, whole pieces of 32), and of its warps of the lower half
+      const int first = S == 1 ? 0 : (out_cols * part / S) & ~31, end = S == 1 ? out_cols : (out_cols * (part + 1) / S) & ~31;
+      const int lower = ((end - first) / 2 + 15) & ~15, wide = half ? end - first - lower : lower;
+      const int at0 = first + (half ? lower : 0);             // this warp's first one within the tile
       const int col0 = tile.n * out_cols + at0;
-      const int cols = min(half ? own - lower : lower, N - col0);  // may be none
+      const int cols = min(wide, N - col0);                   // may be none
       const bool some = rows > 0 && cols > 0;
       const uint32_t* from = KIND == W_DGATED ? a.saved + (static_cast<size_t>(row0 >> 5) * (N >> 1) + (col0 >> 1)) * 96 + lane : nullptr;
       uint32_t k0[24], k1[24];
@@ -496,7 +498,8 @@ __global__ void __launch_bounds__(Kind<KIND>::threads, 1) k_wide16(const __grid_
         if (ok && rows > 0) {
 #pragma unroll 1
           for (int c = 128 * half; c < 128 * half + 128; c += 32) {
-            if ((T::gated ? c & 127 : c) / own == part) continue;
+            const int o = T::gated ? c & 127 : c;
+            if (o >= first && o < end) continue;
             float f[32];
             columns32(lane_base + c, f);
 #pragma unroll
@@ -507,9 +510,9 @@ __global__ void __launch_bounds__(Kind<KIND>::threads, 1) k_wide16(const __grid_
         // The parts in the order of k, this CTA's own from tensor memory, where the sums go.
         if (ok && some) {
 #pragma unroll 1
-          for (int c = 0; c < (T::gated ? own : own >> 1); c += 16) {
-            // gated: (own / 2) gates, then as many ups
-            const int col = at0 + (T::gated && c >= (own >> 1) ? 128 - (own >> 1) : 0) + c;
+          for (int c = 0; c < (T::gated ? 2 * wide : wide); c += 16) {
+            // gated: the gates, then as many ups
+            const int col = at0 + (T::gated && c >= wide ? 128 - wide : 0) + c;
             float f[16], keep[16];
             columns16(lane_base + col, keep);
 #pragma unroll
@@ -684,10 +687,10 @@ __global__ void __launch_bounds__(Kind<KIND>::threads, 1) k_wide16(const __grid_
 // Clusters of 2 S CTAs that the device holds at a time; asked once per kernel and device.
 template <WKind KIND>
 int clusters_at_a_time(int S, size_t smem, int num_sms) {
-  static std::atomic<int> known[64][2];
+  static std::atomic<int> known[64][3];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-  std::atomic<int>& k = known[dev][S >> 2];
+  std::atomic<int>& k = known[dev][S - 2];
   int n = k.load(std::memory_order_relaxed);
   if (n == 0) {
     cudaLaunchAttribute attr[1];
@@ -722,10 +725,12 @@ cudaError_t launch(WArgs a, cudaStream_t st) {
   a.a_rows = wide16_a_rows(a.m[0]);
   a.stages = Kind<KIND>::any_stages ? Kind<KIND>::ring / (a.a_rows * BK * 2 + A_BYTES) : 0;
   const int KB = a.kb * Kind<KIND>::segments, pairs = a.num_sms / 2;
-  // As many pairs to a tile as there are for all tiles at once, with two k-blocks each at least.
+  // As many pairs to a tile as there are for all tiles at once, with two k-blocks each at least, of three with sixteen. (200 rows
+  // by 2 x 11008 x 4096 and back, whose second product has 16 tiles of 172: 64 us with 3, 69 with 2; gate and up by 2 x 2736 x 1000, 22
+  // tiles of 16: 2.3 us more.)
   int S = 1;
-  for (int s = 4; s > 1 && S == 1; s >>= 1)
-    if (a.width == WIDEST && tiles * s <= pairs && KB >= 2 * s && tiles <= clusters_at_a_time<KIND>(s, smem, a.num_sms)) S = s;
+  for (int s = 4; s > 1 && S == 1; --s)
+    if (a.width == WIDEST && tiles * s <= pairs && KB >= (s == 3 ? 48 : 2 * s) && tiles <= clusters_at_a_time<KIND>(s, smem, a.num_sms)) S = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

@@ -394,3 +394,20 @@ def test_few_rows_of_long_sums(env, M):
     for name, got in zip(("dx", "dWg", "dW1", "dW2"), grads):
         near(got, want[name], name)
     f.close()
+
+
+@pytest.mark.parametrize("M,D,N", [(150, 4040, 4200), (200, 5000, 2056), (300, 2056, 3208)])
+def test_tiles_shared_by_three_pairs(env, M, D, N):
+    """On 152 SMs these are, in the products forward and of x and the hidden values backward."""
+    pop, torch, dev = env
+    t = make(env, 15, M, D, N)
+    w = (t["Wg"], t["W1"], t["W2"])
+    f = pop.PopGatedFFN(D, N, max_tokens=M, out_f32=True)
+    y, saved = f.forward(t["x"], *w, save=True)
+    grads = f.backward(t["dy"], t["x"], *w, saved)
+    f.check()
+    want = reference(t)
+    near(y, want["y"], "y")
+    for name, got in zip(("dx", "dWg", "dW1", "dW2"), grads):
+        near(got, want[name], name)
+    f.close()
