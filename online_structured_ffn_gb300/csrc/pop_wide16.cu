@@ -782,9 +782,10 @@ cudaError_t launch_wide16(WKind kind, const WArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_rows16(WKind kind, WArgs a, cudaStream_t st) {
+  static_assert(wide16_a_rows(THIN16_MOST + 1) == BM, "the map below");
   if (a.m[0] <= THIN16_MOST) return launch_thin16(kind, a, st);
   if (!a.width) a.width = wide16_width(kind, a.m[0], a.n[0], a.num_sms);
-  if (!encode_map16(&a.map[0], a.rows, a.k, a.m[0], static_cast<uint64_t>(a.ld_rows) * 2, BK, Kind<W_GATED>::any_stages && kind < W_I8 ? wide16_a_rows(a.m[0]) : BM)) return cudaErrorInvalidValue;
+  if (!encode_map16(&a.map[0], a.rows, a.k, a.m[0], static_cast<uint64_t>(a.ld_rows) * 2, BK, BM)) return cudaErrorInvalidValue;
   return launch_wide16(kind, a, st);
 }
 
