@@ -200,9 +200,11 @@ pop_status pop_gated_backward(pop_gated_t h, const void* x, long long ldx, int M
     a.h = h->a;
     a.h2 = h->b;
     a.saved = static_cast<uint32_t*>(const_cast<void*>(saved));
-    a.width = wide16_width(W_DGATED, M, N, h->num_sms);
-    maps = map_k(&a.map[0], dy, M, D, lddy, wide16_a_rows(M)) && map_mn(&a.map[1], W2, D, N, N);
-    if (maps) e = launch_wide16(W_DGATED, a, st);
+    a.rows = dy;
+    a.ld_rows = lddy;
+    a.k = D;
+    maps = map_mn(&a.map[1], W2, D, N, N);
+    if (maps) e = launch_rows16(W_DGATED, a, st);
   }
   if (maps && e == cudaSuccess && (dWg || dW1 || dW2)) {
     WArgs a = base(h);
@@ -235,10 +237,12 @@ pop_status pop_gated_backward(pop_gated_t h, const void* x, long long ldx, int M
     a.ldy[0] = lddx;
     a.out_f32 = h->cfg.out_f32;
     a.b_early = 1;
-    a.width = wide16_width(W_DX, M, D, h->num_sms);
-    maps = map_k(&a.map[0], h->a, M, N, N, wide16_a_rows(M)) && map_mn(&a.map[1], Wg, N, D, D) && map_k(&a.map[2], h->b, M, N, N, wide16_a_rows(M)) &&
-           map_mn(&a.map[3], W1, N, D, D);
-    if (maps) e = launch_wide16(W_DX, a, st);
+    a.rows = h->a;
+    a.rows2 = h->b;
+    a.ld_rows = N;
+    a.k = N;
+    maps = map_mn(&a.map[1], Wg, N, D, D) && map_mn(&a.map[3], W1, N, D, D);
+    if (maps) e = launch_rows16(W_DX, a, st);
   }
   if (!maps) return fail(POP_ERR_CUDA, call, "a tensor map could not be made");
   return cuda(e, call);

@@ -5,6 +5,10 @@
 // stream at once; then each has 1 / S of the tokens: it reads the others' parts of them from their shared memory, adds
 // them in the order of k and has their epilogue.
 //
+// Backward the matrix is multiplied by its other side: its blocks come as two boxes of 64 values by 64 k and the tensor cores
+// read them mn-major. The gradient of the rows is the sum of two such products, one after the other in k; that of the hidden
+// values goes on to the gate's and the up's in the epilogue.
+//
 // 8-bit integers: a block of 128 rows by 64 k comes as it is; 128 threads read a row each, turn it into fp16 and put it into
 // tensor memory, from where the product takes it. (In shared memory the fp16 block would be written and read once more.)
 //
@@ -36,11 +40,17 @@ namespace {
 constexpr int THREADS = 384;
 constexpr int BM = 128, BK = 64;
 constexpr int MAX_STAGES = 8;
+constexpr uint32_t BOX_MN = 64 * 64 * 2;  // one of the two boxes of a matrix that has its outputs' side contiguous
 constexpr int NA = 4;  // blocks in tensor memory, of 32 columns
 
-template <bool I8_, bool GATED_, int NT_, bool CONV_ = false>
+enum Back { FORWARD, DHIDDEN, DROWS };  // not a gradient; of the hidden values (W_DGATED), of the rows (W_DX)
+
+template <bool I8_, bool GATED_, int NT_, bool CONV_ = false, Back BACK_ = FORWARD>
 struct Thin {
   static constexpr bool I8 = I8_, GATED = GATED_;
+  static constexpr Back BACK = BACK_;
+  static constexpr bool MN = BACK != FORWARD;               // the matrix has its outputs' side contiguous
+  static constexpr int SEGMENTS = BACK == DROWS ? 2 : 1;  // products that are added
   static constexpr bool CONV = CONV_;  // the rows are converted on the way
   static constexpr int NT = NT_, P = GATED ? 2 : 1;
   static constexpr int PER_SM = NT <= 64 ? 2 : 1;
@@ -84,7 +94,8 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32
         "r"(a_tmem + 8 * k), "r"(b_lo + 2 * k), "r"(idesc), "r"(DESC_HI), "r"(k > 0 || !first ? 1u : 0u)
         : "memory");
 }
-// ... and both in shared memory.
+// ... and both in shared memory; a matrix with its outputs' side contiguous: two boxes of 64 by 64 k, 16 rows on.
+template <bool A_MN>
 __device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool first) {
 #pragma unroll
   for (int k = 0; k < 4; ++k)
@@ -93,7 +104,7 @@ __device__ __forceinline__ void umma_ss(uint32_t d_tmem, uint32_t a_lo, uint32_t
         "setp.ne.b32 p, %5, 0;\n\t"
         "mov.b64 a, {%1, %4};\n\tmov.b64 b, {%2, %4};\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_lo + 2 * k), "r"(b_lo + 2 * k), "r"(idesc), "r"(DESC_HI), "r"(k > 0 || !first ? 1u : 0u)
+        "r"(a_lo + (A_MN ? 128 : 2) * k), "r"(b_lo + 2 * k), "r"(idesc), "r"(DESC_HI), "r"(k > 0 || !first ? 1u : 0u)
         : "memory");
 }
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint4 (&v)[8]) {
@@ -140,7 +151,7 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
   volatile int* abort_flag = &ctl.abort_flag;
   const int rank = static_cast<int>(cluster_rank()), S = static_cast<int>(cluster_ctas());
   const int tile = blockIdx.x / S;
-  const int kb0 = a.kb * rank / S, n = a.kb * (rank + 1) / S - kb0;  // this CTA's k-blocks
+  const int KB = a.kb * T::SEGMENTS, kb0 = KB * rank / S, n = KB * (rank + 1) / S - kb0;  // this CTA's k-blocks
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -180,14 +191,22 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
     if (lane == 0) {
       // ---------------------------------------------------------- copies (one thread)
       const auto matrix = [&](int i, int s) {
+        const int second = T::SEGMENTS == 2 && kb0 + i >= a.kb, k = (kb0 + i - (second ? a.kb : 0)) * BK;
 #pragma unroll
         for (int p = 0; p < P; ++p) {
           uint8_t* to = smem + s * T::STAGE + p * T::W_BYTES;
           if (T::I8)
             bulk_load(to, a.w8[p] + (static_cast<size_t>(tile) * a.kb + kb0 + i) * W8_BLOCK, W8_BLOCK, &ctl.full[s]);
-          else
-            tma_load_2d(to, &a.map[1 + p], &ctl.full[s], (kb0 + i) * BK, tile * BM);
+          else if (T::MN) {
+            tma_load_2d(to, &a.map[second ? 3 : 1], &ctl.full[s], tile * BM, k);
+            tma_load_2d(to + BOX_MN, &a.map[second ? 3 : 1], &ctl.full[s], tile * BM + 64, k);
+          } else
+            tma_load_2d(to, &a.map[1 + p], &ctl.full[s], k, tile * BM);
         }
+      };
+      const auto rows = [&](int i, int s) {
+        const int second = T::SEGMENTS == 2 && kb0 + i >= a.kb, k = (kb0 + i - (second ? a.kb : 0)) * BK;
+        tma_load_2d(smem + s * T::STAGE + T::X_OFF, &a.map[second ? 2 : 0], &ctl.full[s], k, 0);
       };
       int early = T::I8 || a.b_early ? min(STAGES, n) : 0;
       for (int i = 0; i < early; ++i) {
@@ -206,7 +225,7 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
           mbar_arrive_expect_tx(&ctl.full[s], T::STAGE);
           matrix(issued, s);
         }
-        if (!T::CONV) tma_load_2d(smem + s * T::STAGE + T::X_OFF, &a.map[0], &ctl.full[s], (kb0 + issued) * BK, 0);
+        if (!T::CONV) rows(issued, s);
         if (++s == STAGES) s = 0, phase ^= 1;
       }
       // no copy of this CTA may be in flight when it exits
@@ -219,8 +238,9 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
   } else if (warp == 1) {
     // ------------------------------------------------------------ products
     const bool leader = elect_one();
-    constexpr uint32_t IDESC = idesc_bf16_f32(BM, NT, false) & ~(T::I8 ? (1u << 7) | (1u << 10) : 0u);
-    const uint32_t w0 = desc_lo(smem_u32(smem)), x0 = desc_lo(smem_u32(smem) + (T::CONV ? STAGES * T::STAGE : T::X_OFF));
+    constexpr uint32_t IDESC = idesc_bf16_f32(BM, NT, false, T::MN) & ~(T::I8 ? (1u << 7) | (1u << 10) : 0u);
+    const uint32_t w0 = T::MN ? desc_lo(smem_u32(smem)) & 0x3fffu | (BOX_MN >> 4) << 16 : desc_lo(smem_u32(smem));
+    const uint32_t x0 = desc_lo(smem_u32(smem) + (T::CONV ? STAGES * T::STAGE : T::X_OFF));
     uint32_t s = 0, phase = 0, b = 0, bphase = 0;
     bool ok = !T::CONV || mbar_wait(&ctl.xfull, 0, a.wait, abort_flag);
     for (int i = 0; i < n && ok; ++i) {
@@ -236,7 +256,7 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
             umma_ts(tmem_base + p * NT, a_base + b * 32, x, IDESC, i == 0);
             umma_commit(&ctl.aempty[b]);
           } else {
-            umma_ss(tmem_base + p * NT, w0 + (s * T::STAGE + p * T::W_BYTES >> 4), x, IDESC, i == 0);
+            umma_ss<T::MN>(tmem_base + p * NT, w0 + (s * T::STAGE + p * T::W_BYTES >> 4), x, IDESC, i == 0);
           }
           if (p == P - 1) umma_commit(&ctl.empty[s]);
         }
@@ -420,6 +440,14 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
       for (int j = 0; j < AT_ONCE; ++j)
 #pragma unroll
         for (int p = 0; p < P; ++p) v[j][p] = 0.f;
+      uint32_t kept[AT_ONCE][3];  // gate and up values of two channels, of which this lane's is one
+#pragma unroll
+      for (int j = 0; j < AT_ONCE && T::BACK == DHIDDEN; ++j) {
+        const int t = min(t0 + 2 * S * j, M - 1);
+        const uint32_t* k = a.saved + (static_cast<size_t>(t >> 5) * (N >> 1) + (min(ch, N - 1) >> 1)) * 96 + (t & 31);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) kept[j][i] = __ldcg(k + 32 * i);
+      }
 #pragma unroll 4
       for (int c = 0; c < S; ++c) {
         uint32_t from;
@@ -463,6 +491,15 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
               }
             }
           }
+        } else if (T::BACK == DHIDDEN) {
+          const float g = __uint_as_float(__byte_perm(kept[j][0], kept[j][2], lane & 1 ? 0x3255 : 0x1044));
+          const float u = __uint_as_float(__byte_perm(kept[j][1], kept[j][2], lane & 1 ? 0x3277 : 0x1066));
+          const float p = sigmoid(g), d = v[j][0];
+          const size_t o = static_cast<size_t>(t) * N + ch;
+          if (is) {
+            a.h[o] = static_cast<uint16_t>(pack_bf16x2(d * u * (p * fmaf(g, 1.f - p, 1.f)), 0.f));
+            a.h2[o] = static_cast<uint16_t>(pack_bf16x2(d * (g * p), 0.f));
+          }
         } else if (is) {
           const size_t o = static_cast<size_t>(t) * a.ldy[0] + ch;
           if (a.out_f32)
@@ -496,8 +533,9 @@ template <class T>
 cudaError_t launch(WArgs a, cudaStream_t st) {
   const cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(&k_thin16<T>), T::SMEM);
   if (e != cudaSuccess) return e;
-  if (!T::CONV && !encode_map16(&a.map[0], a.rows, a.k, a.m[0], static_cast<uint64_t>(a.ld_rows) * 2, BK, T::NT)) return cudaErrorInvalidValue;
-  const int tiles = qceil(a.n[0], BM), S = thin16_split(T::I8, a.m[0], a.n[0], a.kb, a.num_sms);
+  for (int i = 0; i < T::SEGMENTS && !T::CONV; ++i)
+    if (!encode_map16(&a.map[2 * i], i ? a.rows2 : a.rows, a.k, a.m[0], static_cast<uint64_t>(a.ld_rows) * 2, BK, T::NT)) return cudaErrorInvalidValue;
+  const int tiles = qceil(a.n[0], BM), S = thin16_split(T::I8, a.m[0], a.n[0], a.kb * T::SEGMENTS, a.num_sms);
   if (T::CONV && qceil(a.kb, S) > THIN16_KEPT) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -514,12 +552,12 @@ cudaError_t launch(WArgs a, cudaStream_t st) {
   return cudaLaunchKernelEx(&cfg, k_thin16<T>, a);
 }
 
-template <bool I8, bool GATED>
+template <bool I8, bool GATED, Back BACK = FORWARD>
 cudaError_t by_rows(const WArgs& a, cudaStream_t st) {
   if (I8 && a.convert) return launch<Thin<I8, GATED, 16, I8>>(a, st);
-  if (a.m[0] <= 16) return launch<Thin<I8, GATED, 16>>(a, st);
-  if (a.m[0] <= 32) return launch<Thin<I8, GATED, 32>>(a, st);
-  return a.m[0] <= 64 ? launch<Thin<I8, GATED, 64>>(a, st) : launch<Thin<I8, GATED, 128>>(a, st);
+  if (a.m[0] <= 16) return launch<Thin<I8, GATED, 16, false, BACK>>(a, st);
+  if (a.m[0] <= 32) return launch<Thin<I8, GATED, 32, false, BACK>>(a, st);
+  return a.m[0] <= 64 ? launch<Thin<I8, GATED, 64, false, BACK>>(a, st) : launch<Thin<I8, GATED, 128, false, BACK>>(a, st);
 }
 
 // Clusters of S CTAs that the device holds at a time with a CTA on each SM; asked once per device. (Of 152 SMs 36 of 4, 23
@@ -585,6 +623,8 @@ cudaError_t launch_thin16(WKind kind, const WArgs& a, cudaStream_t st) {
   switch (kind) {
     case W_GATED: return by_rows<false, true>(a, st);
     case W_PLAIN: return by_rows<false, false>(a, st);
+    case W_DGATED: return by_rows<false, false, DHIDDEN>(a, st);
+    case W_DX: return by_rows<false, false, DROWS>(a, st);
     case W_I8: return by_rows<true, false>(a, st);
     case W_I8_GATED: return by_rows<true, true>(a, st);
     default: return cudaErrorInvalidValue;

@@ -1,12 +1,12 @@
 // Products of 16-bit operands on 256 x 256 tiles with fused epilogues (pop_wide16.h).
 //
 // Two CTAs of a cluster work as a pair on 256 rows by 256 columns (cta_group::2): each brings its own 128 rows and 128
-// columns of a k-block of 64, 32 KB by TMA into a ring of six (8-bit: of four; up to 64 rows come in lower boxes, and the
-// ring has eight or nine), and has its rows' 256 fp32 sums in tensor memory, twice, so that the epilogue of one tile runs
-// under the products of the next. An operand with k contiguous is one box of 64 x 128; one with the other side contiguous
-// two boxes of 64 values by 64 k, and the tensor cores read it mn-major, so no matrix is transposed in memory. Gate and
-// up: the first CTA brings 128 rows of Wg, the second the same of W1, so columns 0..127 of a tile are the gates and
-// 128..255 the ups of 128 channels. Tiles may be narrower (wide16_width), so that the last round of them is full.
+// columns of a k-block of 64, 32 KB by TMA into a ring of six (8-bit: of four), and has its rows' 256 fp32 sums in tensor
+// memory, twice, so that the epilogue of one tile runs under the products of the next. An operand with k contiguous is one box
+// of 64 x 128; one with the other side contiguous two boxes of 64 values by 64 k, and the tensor cores read it mn-major,
+// so no matrix is transposed in memory. Gate and up: the first CTA brings 128 rows of Wg, the second the same of W1, so
+// columns 0..127 of a tile are the gates and 128..255 the ups of 128 channels. Tiles may be narrower (wide16_width), so
+// that the last round of them is full.
 //
 // Many tiles go round the pairs. Few tiles of long sums are each given to a cluster of S pairs, which take a run of the k-blocks
 // each; then every CTA sums 1 / S of the columns, the others' parts of them read from their shared memory, and has the
@@ -37,7 +37,7 @@ cudaError_t ensure_dyn_smem(const void* kernel, size_t bytes);
 namespace {
 
 constexpr int BM = 128, BK = 64;
-constexpr int MAX_STAGES = 9;
+constexpr int MAX_STAGES = 6;
 constexpr uint32_t A_BYTES = BM * BK * 2, STAGE = 2 * A_BYTES;
 constexpr uint32_t BOX_MN = 64 * 64 * 2;  // one of an mn-major operand's two boxes
 constexpr uint32_t TMEM_COLS = 512;
@@ -64,7 +64,6 @@ struct Kind {
   static constexpr bool b_mn = KIND == W_DGATED || KIND == W_DX || KIND == W_DW;
   static constexpr int segments = KIND == W_DX ? 2 : 1;
   static constexpr int threads = i8 ? 768 : 384;
-  static constexpr bool any_stages = !i8 && !a_mn;  // stages hold WArgs::a_rows rows of A
   static constexpr int stages = i8 ? 4 : 6;
   static constexpr uint32_t ring = stages * STAGE + (i8 ? RING8 * BLOCK8 : 0);
 };
@@ -218,9 +217,7 @@ __device__ __forceinline__ void load_kept(const uint32_t* from, int c, int cols,
 template <WKind KIND>
 __global__ void __launch_bounds__(Kind<KIND>::threads, 1) k_wide16(const __grid_constant__ WArgs a) {
   using T = Kind<KIND>;
-  // What the tensor cores read below a box of few rows is the stage's B: products that nothing reads.
-  const uint32_t a_bytes = T::any_stages ? a.a_rows * BK * 2 : A_BYTES, stage_bytes = a_bytes + A_BYTES;
-  const int STAGES = T::any_stages ? a.stages : T::stages;
+  constexpr int STAGES = T::stages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Ctl ctl;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -285,7 +282,7 @@ __global__ void __launch_bounds__(Kind<KIND>::threads, 1) k_wide16(const __grid_
           const bool second = KIND == W_DX && i >= a.kb;
           const int x = (second ? i - a.kb : i) * BK;
           const CUtensorMap *pa = ma + (second ? 2 : 0), *pb = mb + (second ? 2 : 0);
-          uint8_t* st = smem + stage * stage_bytes;
+          uint8_t* st = smem + stage * STAGE;
           uint64_t* bar = &ctl.full[stage];
           if (left && T::a_mn) {
             tma_load_2d(st, pa, bar, m0, x);
@@ -294,13 +291,13 @@ __global__ void __launch_bounds__(Kind<KIND>::threads, 1) k_wide16(const __grid_
             tma_load_2d(st, pa, bar, x, m0);
           }
           if (right && T::b_mn) {
-            tma_load_2d(st + a_bytes, pb, bar, n0, x);
-            if (W2 > 64) tma_load_2d(st + a_bytes + BOX_MN, pb, bar, n0 + 64, x);
+            tma_load_2d(st + A_BYTES, pb, bar, n0, x);
+            if (W2 > 64) tma_load_2d(st + A_BYTES + BOX_MN, pb, bar, n0 + 64, x);
           } else if (right && !T::i8) {
-            tma_load_2d(st + a_bytes, pb, bar, x, n0);
+            tma_load_2d(st + A_BYTES, pb, bar, x, n0);
           }
         };
-        const uint32_t bytes = (any ? a_bytes : 0) + b_bytes;
+        const uint32_t bytes = (any ? A_BYTES : 0) + b_bytes;
         if (early) {
           for (int i = 0; i < early; ++i) {
             mbar_arrive_expect_tx(&ctl.full[i], bytes);
@@ -348,7 +345,7 @@ __global__ void __launch_bounds__(Kind<KIND>::threads, 1) k_wide16(const __grid_
             break;
           }
           mbar_arrive_expect_tx(&ctl.full8[s], BLOCK8);
-          bulk_load(smem + T::stages * STAGE + s * BLOCK8, w, BLOCK8, &ctl.full8[s]);
+          bulk_load(smem + STAGES * STAGE + s * BLOCK8, w, BLOCK8, &ctl.full8[s]);
           ++issued;
           if (++s == RING8) s = 0, phase ^= 1;
         }
@@ -368,7 +365,7 @@ __global__ void __launch_bounds__(Kind<KIND>::threads, 1) k_wide16(const __grid_
       if (rank == 0) {
         // -------------------------------------------------------- products
         const uint32_t idesc = idesc_bf16_f32(2 * BM, a.width, T::b_mn, T::a_mn) & ~(T::i8 ? (1u << 7) | (1u << 10) : 0u);
-        const uint32_t a0 = operand_lo<T::a_mn>(smem_u32(smem)), b0 = operand_lo<T::b_mn>(smem_u32(smem) + a_bytes);
+        const uint32_t a0 = operand_lo<T::a_mn>(smem_u32(smem)), b0 = operand_lo<T::b_mn>(smem_u32(smem) + A_BYTES);
         const uint32_t mask = 3u << leader_cta;
         bool ok = true;
         for (int t = tile0; t < a.tiles && ok; t += tile_step) {
@@ -385,7 +382,7 @@ __global__ void __launch_bounds__(Kind<KIND>::threads, 1) k_wide16(const __grid_
             }
             tc_fence_after();
             if (leader) {
-              umma_pair16<T::a_mn, T::b_mn>(tmem_base + b * 256u, a0 + s * (stage_bytes >> 4), b0 + s * (stage_bytes >> 4), idesc, kb == kb0);
+              umma_pair16<T::a_mn, T::b_mn>(tmem_base + b * 256u, a0 + s * (STAGE >> 4), b0 + s * (STAGE >> 4), idesc, kb == kb0);
               commit_pair(&ctl.empty[s], mask);
               if (kb == kb1 - 1) commit_pair(&ctl.tfull[b], mask);
             }
@@ -435,7 +432,7 @@ __global__ void __launch_bounds__(Kind<KIND>::threads, 1) k_wide16(const __grid_
         if (lane == 0) fail();
         break;
       }
-      const uint4* from = reinterpret_cast<const uint4*>(smem + T::stages * STAGE + s8 * BLOCK8) + r;
+      const uint4* from = reinterpret_cast<const uint4*>(smem + STAGES * STAGE + s8 * BLOCK8) + r;
       uint8_t* to = smem + s * STAGE + A_BYTES + r * 128;
       uint4 v[4];
 #pragma unroll
@@ -722,8 +719,6 @@ cudaError_t launch(WArgs a, cudaStream_t st) {
     tiles += static_cast<long long>(qceil(a.m[p], 2 * BM)) * qceil(a.n[p], Kind<KIND>::gated ? a.width / 2 : a.width);
   if (tiles > (1 << 28)) return cudaErrorInvalidValue;
   a.tiles = static_cast<int>(tiles);
-  a.a_rows = wide16_a_rows(a.m[0]);
-  a.stages = Kind<KIND>::any_stages ? Kind<KIND>::ring / (a.a_rows * BK * 2 + A_BYTES) : 0;
   const int KB = a.kb * Kind<KIND>::segments, pairs = a.num_sms / 2;
   // As many pairs to a tile as there are for all tiles at once, with two k-blocks each at least, of three with sixteen. (200 rows
   // by 2 x 11008 x 4096 and back, whose second product has 16 tiles of 172: 64 us with 3, 69 with 2; gate and up by 2 x 2736 x 1000, 22
@@ -782,10 +777,11 @@ cudaError_t launch_wide16(WKind kind, const WArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_rows16(WKind kind, WArgs a, cudaStream_t st) {
-  static_assert(wide16_a_rows(THIN16_MOST + 1) == BM, "the map below");
   if (a.m[0] <= THIN16_MOST) return launch_thin16(kind, a, st);
   if (!a.width) a.width = wide16_width(kind, a.m[0], a.n[0], a.num_sms);
-  if (!encode_map16(&a.map[0], a.rows, a.k, a.m[0], static_cast<uint64_t>(a.ld_rows) * 2, BK, BM)) return cudaErrorInvalidValue;
+  for (int i = 0; i < (kind == W_DX ? 2 : 1); ++i)
+    if (!encode_map16(&a.map[2 * i], i ? a.rows2 : a.rows, a.k, a.m[0], static_cast<uint64_t>(a.ld_rows) * 2, BK, BM))
+      return cudaErrorInvalidValue;
   return launch_wide16(kind, a, st);
 }
 

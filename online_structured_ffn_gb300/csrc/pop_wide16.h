@@ -43,7 +43,7 @@ struct WArgs {
   int num_sms;
   // launch_rows16: A's rows, of k values; of few rows also, W_I8*, rows that are quantised or widened on the way:
   // `convert` 1: bf16, 2: float32 with `tiles_max` largest values of each row's parts in row_max, 3: integers with scales sx
-  const void* rows;
+  const void *rows, *rows2;  // (W_DX: of both products)
   long long ld_rows;
   int k;
   int convert;
@@ -51,20 +51,18 @@ struct WArgs {
   int tiles_max;
   int width;           // columns of a tile, as wide16_width gives them (gated: gate and up values, of half as many channels)
   int b_early;         // 1: what the kernel before this one writes is not among the B operands
-  int tiles, a_rows, stages;  // set by launch_wide16
+  int tiles;           // set by launch_wide16
 };
 
-// Rows of a k-major A's box (16-bit operands): few rows leave room for more stages. (Forward and backward of 8 rows by
-// 2 x 11008 x 4096 171 us with nine stages, 187 with six.)
-constexpr int wide16_a_rows(int m) { return m <= 32 ? 32 : m <= 64 ? 64 : 128; }
 cudaError_t launch_wide16(WKind kind, const WArgs& a, cudaStream_t st);
 
 // Columns of a tile. A k-major B's box has half as many rows. m, n: rows and columns of the outputs (gated: channels).
 int wide16_width(WKind kind, int m, int n, int num_sms);
 
-// W_GATED, W_PLAIN, W_I8 or W_I8_GATED: few rows by pop_thin16.cu, more by the wide products. (us of a whole MLP thin against wide,
-// 4096 x 11008: bf16 65 rows 56/66, 128 61/67; 8-bit 57/86, 70/88; 1000 x 2736 bf16 16/19, 19/20; 8192 x 28672 bf16 231/227,
-// 244/230, 8-bit 185/219, 212/225.)
+// All but W_DW: few rows by pop_thin16.cu, more by the wide products. (us of a whole MLP thin against wide, 4096 x 11008: bf16 65
+// rows 56/66, 128 61/67; 8-bit 57/86, 70/88; 1000 x 2736 bf16 16/19, 19/20; 8192 x 28672 bf16 231/227, 244/230, 8-bit 185/219,
+// 212/225. Forward and backward, the latter thin against wide: 4096 x 11008 8 rows 151/187, 100 202/203, 128 214/211; 2048 x 5496
+// 59/74, 79/83, 85/87; 1000 x 2736 32/40, 47/53, 50/55.)
 constexpr int THIN16_MOST = 128;
 // CTAs to a tile of 128 outputs (pop_thin16.cu).
 int thin16_split(bool i8, int m, int n, int kb, int num_sms);
