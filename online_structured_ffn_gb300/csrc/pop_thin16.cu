@@ -187,6 +187,19 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
     }
   };
 
+  // The epilogue's: a channel each lane; of the tokens, AT_ONCE at a time, either half of the warps in turn has every (2 S)-th, or
+  // AT_ONCE neighbours, whose kept words are one load.
+  constexpr int AT_ONCE = 4;
+  const int M = a.m[0], N = a.n[0], q = warp & 3, half = (warp - 4) >> 2, r = 32 * q + lane, ch = tile * BM + r;
+  const int first = (rank + S * half) * (T::BACK == DHIDDEN ? AT_ONCE : 1), apart = T::BACK == DHIDDEN ? 1 : 2 * S;
+  uint4 next[3];  // W_DGATED: kept gate and up values of two channels, of which this lane's is one
+  const auto load_kept = [&](int t0) {
+    if (T::BACK != DHIDDEN || t0 >= M || ch >= N) return;
+    const uint32_t* k = a.saved + (static_cast<size_t>(t0 >> 5) * (N >> 1) + (ch >> 1)) * 96 + (t0 & 31);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) next[i] = __ldcg(reinterpret_cast<const uint4*>(k) + 8 * i);
+  };
+
   if (warp == 0) {
     if (lane == 0) {
       // ---------------------------------------------------------- copies (one thread)
@@ -272,12 +285,11 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
     if (!mbar_wait(&ctl.tfull, 0, Q_DRAIN, &never) && leader) fail();
     __syncwarp();
   } else if (warp >= 4) {
-    const int q = warp & 3, half = (warp - 4) >> 2, r = 32 * q + lane;
     bool ok = true;
     if constexpr (T::CONV) {
       // ---------------------------------------------------------- rows: their largest magnitudes, then their values
       pdl_wait();
-      const int M = a.m[0], t = threadIdx.x - 128;
+      const int t = threadIdx.x - 128;
       if (a.convert == 1) {
         const int w = warp - 4, share = M >= 8 ? 1 : M >= 4 ? 2 : M >= 2 ? 4 : 8;  // warps to a row
         const int pieces = a.k >> 3, step = 32 * share;
@@ -391,6 +403,7 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
     // ------------------------------------------------------------ this CTA's part: [column][row]
     pdl_wait();  // what this kernel writes may still be read by the one before
     pdl_trigger();
+    load_kept(first);
     ok = ok && mbar_wait(&ctl.tfull, 0, a.wait, abort_flag);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok && lane == 0) fail();
@@ -408,8 +421,7 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
       }
     }
   }
-  // ------------------------------------------------------------ epilogue: tokens rank, rank + S, ... of either half in turn
-  const int M = a.m[0], N = a.n[0], q = warp & 3, half = (warp - 4) >> 2, r = 32 * q + lane, ch = tile * BM + r;
+  // ------------------------------------------------------------ epilogue
   const bool is = ch < N;
   float sw = 1.f, sw1 = 1.f, sx_own = 0.f;  // sx_own: of the lane-th of this warp's tokens
   if (T::I8 && warp >= 4) {
@@ -431,37 +443,32 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
   cluster_sync();
   if (warp >= 4) {
     const uint32_t part = smem_u32(smem) + 4 * r;
-    constexpr int AT_ONCE = 4;
     int at = 0;  // which of this warp's tokens
 #pragma unroll 1
-    for (int t0 = rank + S * half; t0 < M; t0 += 2 * S * AT_ONCE, at += AT_ONCE) {
+    for (int t0 = first; t0 < M; t0 += 2 * S * AT_ONCE, at += AT_ONCE) {
       float v[AT_ONCE][P];
 #pragma unroll
       for (int j = 0; j < AT_ONCE; ++j)
 #pragma unroll
         for (int p = 0; p < P; ++p) v[j][p] = 0.f;
-      uint32_t kept[AT_ONCE][3];  // gate and up values of two channels, of which this lane's is one
+      uint32_t kept[3][AT_ONCE];
 #pragma unroll
-      for (int j = 0; j < AT_ONCE && T::BACK == DHIDDEN; ++j) {
-        const int t = min(t0 + 2 * S * j, M - 1);
-        const uint32_t* k = a.saved + (static_cast<size_t>(t >> 5) * (N >> 1) + (min(ch, N - 1) >> 1)) * 96 + (t & 31);
-#pragma unroll
-        for (int i = 0; i < 3; ++i) kept[j][i] = __ldcg(k + 32 * i);
-      }
+      for (int i = 0; i < 3 && T::BACK == DHIDDEN; ++i) kept[i][0] = next[i].x, kept[i][1] = next[i].y, kept[i][2] = next[i].z, kept[i][3] = next[i].w;
+      load_kept(t0 + 2 * S * AT_ONCE);
 #pragma unroll 4
       for (int c = 0; c < S; ++c) {
         uint32_t from;
         asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(part), "r"(c));
 #pragma unroll
         for (int j = 0; j < AT_ONCE; ++j) {
-          const int t = min(t0 + 2 * S * j, M - 1);
+          const int t = min(t0 + apart * j, M - 1);
 #pragma unroll
           for (int p = 0; p < P; ++p) v[j][p] += ld_cluster1(from + (p * NT + t) * (BM * 4));
         }
       }
 #pragma unroll
       for (int j = 0; j < AT_ONCE; ++j) {
-        const int t = t0 + 2 * S * j;
+        const int t = t0 + apart * j;
         if (t >= M) break;
         if (T::I8) {
           // (at most 64 tokens a warp, of which the second 32 come with one CTA to 128 tokens alone)
@@ -492,8 +499,8 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
             }
           }
         } else if (T::BACK == DHIDDEN) {
-          const float g = __uint_as_float(__byte_perm(kept[j][0], kept[j][2], lane & 1 ? 0x3255 : 0x1044));
-          const float u = __uint_as_float(__byte_perm(kept[j][1], kept[j][2], lane & 1 ? 0x3277 : 0x1066));
+          const float g = __uint_as_float(__byte_perm(kept[0][j], kept[2][j], lane & 1 ? 0x3255 : 0x1044));
+          const float u = __uint_as_float(__byte_perm(kept[1][j], kept[2][j], lane & 1 ? 0x3277 : 0x1066));
           const float p = sigmoid(g), d = v[j][0];
           const size_t o = static_cast<size_t>(t) * N + ch;
           if (is) {
