@@ -188,10 +188,11 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
   };
 
   // The epilogue's: a channel each lane; of the tokens, AT_ONCE at a time, either half of the warps in turn has every (2 S)-th, or
-  // AT_ONCE neighbours, whose kept words are one load.
+  // AT_ONCE neighbours, whose kept words are 16 bytes.
   constexpr int AT_ONCE = 4;
   const int M = a.m[0], N = a.n[0], q = warp & 3, half = (warp - 4) >> 2, r = 32 * q + lane, ch = tile * BM + r;
-  const int first = (rank + S * half) * (T::BACK == DHIDDEN ? AT_ONCE : 1), apart = T::BACK == DHIDDEN ? 1 : 2 * S;
+  constexpr bool KEEPS = T::BACK == DHIDDEN || (T::GATED && !T::I8);
+  const int first = (rank + S * half) * (KEEPS ? AT_ONCE : 1), apart = KEEPS ? 1 : 2 * S;
   uint4 next[3];  // W_DGATED: kept gate and up values of two channels, of which this lane's is one
   const auto load_kept = [&](int t0) {
     if (T::BACK != DHIDDEN || t0 >= M || ch >= N) return;
@@ -451,7 +452,7 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
       for (int j = 0; j < AT_ONCE; ++j)
 #pragma unroll
         for (int p = 0; p < P; ++p) v[j][p] = 0.f;
-      uint32_t kept[3][AT_ONCE];
+      uint32_t kept[3][AT_ONCE] = {};
 #pragma unroll
       for (int i = 0; i < 3 && T::BACK == DHIDDEN; ++i) kept[i][0] = next[i].x, kept[i][1] = next[i].y, kept[i][2] = next[i].z, kept[i][3] = next[i].w;
       load_kept(t0 + 2 * S * AT_ONCE);
@@ -489,13 +490,9 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
               // the second
               const uint32_t gb = __float_as_uint(g), ub = __float_as_uint(u);
               const uint32_t gn = __shfl_xor_sync(0xffffffffu, gb, 1), un = __shfl_xor_sync(0xffffffffu, ub, 1);
-              uint32_t* k = a.saved + (static_cast<size_t>(t >> 5) * (N >> 1) + (ch >> 1)) * 96 + (t & 31);
-              if (is && (lane & 1)) {
-                k[32] = __byte_perm(un, ub, 0x7632);
-              } else if (is) {
-                k[0] = __byte_perm(gb, gn, 0x7632);
-                k[64] = __byte_perm(__byte_perm(gb, gn, 0x0051), __byte_perm(ub, un, 0x0051), 0x5410);
-              }
+              kept[0][j] = __byte_perm(gb, gn, 0x7632);
+              kept[1][j] = __byte_perm(un, ub, 0x7632);
+              kept[2][j] = __byte_perm(__byte_perm(gb, gn, 0x0051), __byte_perm(ub, un, 0x0051), 0x5410);
             }
           }
         } else if (T::BACK == DHIDDEN) {
@@ -514,6 +511,13 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
           else
             static_cast<uint16_t*>(a.y[0])[o] = static_cast<uint16_t>(pack_bf16x2(v[j][0], 0.f));
         }
+      }
+      if (T::GATED && !T::I8 && a.saved && is) {
+        // (of a last few tokens also the words behind them, which 32 rows together have room for)
+        uint4* k = reinterpret_cast<uint4*>(a.saved + (static_cast<size_t>(t0 >> 5) * (N >> 1) + (ch >> 1)) * 96 + (t0 & 31));
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+          if ((lane & 1) == (i & 1)) __stcg(k + 8 * i, make_uint4(kept[i][0], kept[i][1], kept[i][2], kept[i][3]));
       }
     }
     if (T::I8 && T::GATED) {
