@@ -19,8 +19,8 @@
 // longer than its matrix takes.)
 //
 // Bound by the matrix's bytes, and with short ones by what comes before and after them (some 5 us: first bytes 1.2, the
-// cluster's meeting 1.2, the others' parts 0.7, its end 1). Back to back: gate and up and down of one token, bf16 46.5 us for 270
-// MB (5.8 TB/s); 8-bit: 16 rows by 8192 x 28672 with their quantising 44 us (5.4), one row by 11008 x 4096 11.4 (4.0).
+// cluster's meeting 1.2, the others' parts 0.7, its end 1). Back to back: gate and up and down of one token, bf16 46 us for 270
+// MB (5.9 TB/s); 8-bit: 16 rows by 8192 x 28672 with their quantising 44 us (5.4), one row by 11008 x 4096 11.4 (4.0).
 //
 // Warp 0: copies; the matrix's first stages go out before the kernel before this one has ended, where that does not write them.
 // Warp 1: products. Warps 4..11: conversion, then the epilogue. Every wait has a limit; a CTA that gives up records
@@ -540,9 +540,26 @@ __global__ void __launch_bounds__(THREADS, T::PER_SM) k_thin16(const __grid_cons
   }
 }
 
+// The kernel's shared memory. Every one of them wants all of it for its SMs: otherwise they are set up for two CTAs of its own
+// size, and the next kernel's wait for those to leave (64 rows by 2 x 5496 x 2048 and back 25 -> 20 us, 40 by 2 x 2736 x 1000 14.4 ->
+// 13.3). The kernels that quantise rows do without: 24 rows of the latter in 8 bits, 16.1 us, took 0.6 more.
+template <class T>
+cudaError_t prepare() {
+  static std::atomic<bool> known[64];
+  const void* kernel = reinterpret_cast<const void*>(&k_thin16<T>);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && known[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+  e = ensure_dyn_smem(kernel, T::SMEM);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  if (e == cudaSuccess && dev < 64) known[dev].store(true, std::memory_order_relaxed);
+  return e;
+}
+
 template <class T>
 cudaError_t launch(WArgs a, cudaStream_t st) {
-  const cudaError_t e = ensure_dyn_smem(reinterpret_cast<const void*>(&k_thin16<T>), T::SMEM);
+  const cudaError_t e = prepare<T>();
   if (e != cudaSuccess) return e;
   for (int i = 0; i < T::SEGMENTS && !T::CONV; ++i)
     if (!encode_map16(&a.map[2 * i], i ? a.rows2 : a.rows, a.k, a.m[0], static_cast<uint64_t>(a.ld_rows) * 2, BK, T::NT)) return cudaErrorInvalidValue;
@@ -590,7 +607,7 @@ int clusters_at_a_time(int S, int num_sms) {
     cfg.dynamicSmemBytes = T::SMEM;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (ensure_dyn_smem(reinterpret_cast<const void*>(&k_thin16<T>), T::SMEM) != cudaSuccess ||
+    if (prepare<T>() != cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&n, k_thin16<T>, &cfg) != cudaSuccess) {
       cudaGetLastError();
       n = 0;
