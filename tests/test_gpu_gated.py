@@ -411,3 +411,42 @@ def test_tiles_shared_by_three_pairs(env, M, D, N):
     for name, got in zip(("dx", "dWg", "dW1", "dW2"), grads):
         near(got, want[name], name)
     f.close()
+
+
+@pytest.mark.parametrize("M", [100, 129, 300])
+def test_rows_apart_subsets_and_rows_that_are_not_finite_of_more_rows(env, M):
+    pop, torch, dev = env
+    D, N = 136, 392
+    t = make(env, 16, M, D, N, ldx=152)
+    w = (t["Wg"], t["W1"], t["W2"])
+    f = pop.PopGatedFFN(D, N, max_tokens=M)
+    wide = torch.full((M + 1, D + 16), 7.0, dtype=torch.bfloat16, device=dev)
+    apart = torch.zeros((M, D + 24), dtype=torch.bfloat16, device=dev)
+    apart[:, 8:8 + D] = t["dy"]
+    dy = apart[:, 8:8 + D]
+    y, saved = f.forward(t["x"], *w, y=wide[:M, 8:8 + D], save=True)
+    every = f.backward(dy, t["x"], *w, saved)
+    want = reference(t)
+    near(y, want["y"], "y")
+    for name, got in zip(("dx", "dWg", "dW1", "dW2"), every):
+        near(got, want[name], name)
+    assert (wide[M] == 7).all() and (wide[:, :8] == 7).all() and (wide[:, 8 + D:] == 7).all()
+    for mask in (1, 2, 4, 8, 9, 14):
+        need = [bool(mask >> i & 1) for i in range(4)]
+        for n, a, b in zip(need, f.backward(dy, t["x"], *w, saved, need=need), every):
+            assert torch.equal(a, b) if n else a is None
+    into = [torch.randn_like(m) for m in w]
+    old = [g.clone() for g in into]
+    f.backward(dy, t["x"], *w, saved, grads=into, accumulate=True)
+    for name, got, o in zip(("dWg", "dW1", "dW2"), into, old):
+        near(got, want[name], name, old=o)
+    x = t["x"].clone()
+    x[3, 5], x[M - 1, 0] = float("nan"), float("inf")
+    rest = [i for i in range(M) if i not in (3, M - 1)]
+    y2, s2 = f.forward(x, *w, save=True)
+    grads = f.backward(dy, x, *w, s2)
+    assert y2[3].isnan().all() and torch.equal(y2[rest], y[rest])
+    assert grads[0][3].isnan().all() and torch.equal(grads[0][rest], every[0][rest])
+    assert all(g.isnan().any() for g in grads[1:])
+    f.check()
+    f.close()
