@@ -723,9 +723,14 @@ cudaError_t launch(WArgs a, cudaStream_t st) {
   // As many pairs to a tile as there are for all tiles at once, with two k-blocks each at least, of three with sixteen. (200 rows
   // by 2 x 11008 x 4096 and back, whose second product has 16 tiles of 172: 64 us with 3, 69 with 2; gate and up by 2 x 2736 x 1000, 22
   // tiles of 16: 2.3 us more.)
+  // The gradients of the matrices go by the tiles of all three, whichever are asked for, as S is how a gradient's sum is split: what
+  // else is wanted is not to change its bits. (All three have as many tiles. That of W2 alone, with S by its own tiles and by all
+  // of them: 512 x 512 x 1024 9.1 and 7.4 us, 600 x 264 x 1032 9.3 and 8.1, 1000 x 264 x 2056 9.2 and 10.2, 2048 x 1024 x 1024 10.7 and
+  // 12.9.)
+  const long long sharing = KIND == W_DW ? 3ll * qceil(a.m[0], 2 * BM) * qceil(a.n[0], a.width) : tiles;
   int S = 1;
   for (int s = 4; s > 1 && S == 1; --s)
-    if (a.width == WIDEST && tiles * s <= pairs && KB >= (s == 3 ? 48 : 2 * s) && tiles <= clusters_at_a_time<KIND>(s, smem, a.num_sms)) S = s;
+    if (a.width == WIDEST && sharing * s <= pairs && KB >= (s == 3 ? 48 : 2 * s) && sharing <= clusters_at_a_time<KIND>(s, smem, a.num_sms)) S = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
