@@ -22,7 +22,8 @@ if ROOT not in sys.path:
 
 
 class Gated(torch.autograd.Function):
-    """``PopGatedFFN`` with gradients of x and the three matrices: Gated.apply(x, Wg, W1, W2, ffn)."""
+    """``PopGatedFFN`` with gradients of x and the three matrices: Gated.apply(x, Wg, W1, W2, ffn). The gradient that comes in is
+    rounded to bf16."""
 
     @staticmethod
     def forward(ctx, x, Wg, W1, W2, ffn):
@@ -34,7 +35,8 @@ class Gated(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy):
         x, Wg, W1, W2, saved = ctx.saved_tensors
-        return (*ctx.ffn.backward(dy.contiguous(), x, Wg, W1, W2, saved, need=ctx.needs_input_grad[:4]), None)
+        dy = dy.to(torch.bfloat16).contiguous()  # (of float32 outputs it is float32)
+        return (*ctx.ffn.backward(dy, x, Wg, W1, W2, saved, need=ctx.needs_input_grad[:4]), None)
 
 
 def kept_channels(Wg, W1, W2, prompt, rate):

@@ -891,8 +891,8 @@ class PopGatedFFN(_QHandle):
         return (y, saved) if save else y
 
     def backward(self, dy, x, Wg, W1, W2, saved, need=(True, True, True, True), grads=None, accumulate=False, stream=None):
-        """The gradients (dx, dWg, dW1, dW2) for dy, bf16 [M, D], of the forward call that gave `saved`, from the
-        same x and matrices. need: which of the four are wanted; the others are None. grads: (dWg, dW1, dW2),
+        """The gradients (dx, dWg, dW1, dW2) for dy, bf16 [M, D] (with out_f32 too), of the forward call that gave
+        `saved`, from the same x and matrices. need: which of the four are wanted; the others are None. grads: (dWg, dW1, dW2),
         tensors of grad_dtype() to write to instead of new ones (None where none is needed); with
         accumulate they are added to."""
         import torch

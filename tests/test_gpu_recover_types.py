@@ -1,0 +1,34 @@
+"""The example's function with gradients on handles whose outputs and gradients are float32: autograd hands it a float32 dy
+then, and takes gradients of a leaf in the leaf's own type."""
+import pytest
+
+from test_gpu_gated import env, make, near, reference  # noqa: F401
+from test_gpu_recover import example  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("grad_f32", [False, True])
+@pytest.mark.parametrize("M,D,N", [(5, 64, 136), (150, 264, 520)])
+def test_gradients_through_autograd_of_float32_outputs(env, example, M, D, N, grad_f32):  # noqa: F811
+    pop, torch, dev = env
+    t = make(env, 60, M, D, N)
+    f = pop.PopGatedFFN(D, N, max_tokens=M, out_f32=True, grad_f32=grad_f32)
+    leaves = [t[n].clone().requires_grad_() for n in ("x", "Wg", "W1", "W2")]
+    y = example.Gated.apply(*leaves, f)
+    assert y.dtype == torch.float32
+    y.backward(t["dy"].float())  # (exact in bf16: the reference has the same dy)
+    want = reference(t)
+    near(y.detach(), want["y"], "y")
+    for name, leaf in zip(("dx", "dWg", "dW1", "dW2"), leaves):
+        assert leaf.grad.dtype == torch.bfloat16
+        near(leaf.grad, want[name], name)
+    # one that is not is rounded to bf16 first
+    g = torch.Generator(device=dev)
+    g.manual_seed(61)
+    dy = torch.randn((M, D), generator=g, device=dev)
+    got = torch.autograd.grad(example.Gated.apply(*leaves, f), leaves, dy)
+    again = torch.autograd.grad(example.Gated.apply(*leaves, f), leaves, dy.to(torch.bfloat16).float())
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    f.check()
+    f.close()
