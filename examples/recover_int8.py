@@ -27,6 +27,8 @@ class Gated(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, Wg, W1, W2, ffn):
+        if not any(ctx.needs_input_grad):
+            return ffn.forward(x, Wg, W1, W2)
         y, saved = ffn.forward(x, Wg, W1, W2, save=True)
         ctx.save_for_backward(x, Wg, W1, W2, saved)
         ctx.ffn = ffn

@@ -1,5 +1,5 @@
 """The example's function with gradients on handles whose outputs and gradients are float32: autograd hands it a float32 dy
-then, and takes gradients of a leaf in the leaf's own type."""
+then, and takes gradients of a leaf in the leaf's own type. Where no gradient is wanted nothing is kept."""
 import pytest
 
 from test_gpu_gated import env, make, near, reference  # noqa: F401
@@ -31,4 +31,25 @@ def test_gradients_through_autograd_of_float32_outputs(env, example, M, D, N, gr
     again = torch.autograd.grad(example.Gated.apply(*leaves, f), leaves, dy.to(torch.bfloat16).float())
     assert all(torch.equal(a, b) for a, b in zip(got, again))
     f.check()
+    f.close()
+
+
+def test_nothing_is_kept_where_no_gradient_is_wanted(env, example, monkeypatch):  # noqa: F811
+    pop, torch, dev = env
+    M, D, N = 20, 64, 136
+    t = make(env, 62, M, D, N)
+    f = pop.PopGatedFFN(D, N, max_tokens=M)
+    asked = []
+    forward = f.forward
+
+    def watched(*args, **kw):
+        asked.append(bool(kw.get("save")))
+        return forward(*args, **kw)
+
+    monkeypatch.setattr(f, "forward", watched)
+    args = [t[n] for n in ("x", "Wg", "W1", "W2")]
+    y = example.Gated.apply(*args, f)
+    assert asked == [False] and not y.requires_grad and torch.equal(y, forward(*args))
+    z = example.Gated.apply(args[0], args[1].clone().requires_grad_(), *args[2:], f)
+    assert asked == [False, True] and z.requires_grad and torch.equal(y, z)
     f.close()
