@@ -213,7 +213,9 @@ pop_status pop_gated_backward(pop_gated_t h, const void* x, long long ldx, int M
     a.out_f32 = h->cfg.grad_f32;
     a.accumulate = accumulate;
     a.width = wide16_width(W_DW, N, D, h->num_sms);
-    a.b_early = dWg || dW1 ? 1 : 0;  // else nothing of this call has gone before
+    // The kernel in front is then the one above, which writes neither of the B operands, x and h, and lets this one start only after
+    // its own wait. With dW2 alone it is one of before this call, which may write them.
+    a.b_early = dx || dWg || dW1 ? 1 : 0;
     const auto add = [&](void* out, const void* left, int rows, long long ldl, const void* right, int cols, long long ldr) {
       if (!out) return;
       const int p = a.problems++;
