@@ -21,9 +21,8 @@ struct I8RowsArgs {
 };
 cudaError_t launch_i8_rows(const I8RowsArgs& a, cudaStream_t st);
 
-// Integers as fp16 rows, their scales side by side.
-cudaError_t launch_i8_half(const int8_t* q, long long ldq, const float* s, long long lds, int M, int K, uint16_t* half, float* sx,
-                           cudaStream_t st);
+// Integers as fp16 rows, and a copy of their scales.
+cudaError_t launch_i8_half(const int8_t* q, long long ldq, const float* s, int M, int K, uint16_t* half, float* sx, cudaStream_t st);
 
 // A matrix [N, K] of integers into its image (pop_wide16.h).
 cudaError_t launch_i8_pack(const int8_t* W, int N, int K, uint8_t* image, cudaStream_t st);

@@ -100,8 +100,8 @@ __global__ void __launch_bounds__(T > 256 ? T : 256, (HELD > 4 ? 1024 : 1536) / 
   }
 }
 
-__global__ void __launch_bounds__(256) k_i8_half(const int8_t* __restrict__ q, long long ldq, const float* __restrict__ s, long long lds,
-                                                 int K, uint16_t* __restrict__ half, float* __restrict__ sx) {
+__global__ void __launch_bounds__(256) k_i8_half(const int8_t* __restrict__ q, long long ldq, const float* __restrict__ s, int K,
+                                                 uint16_t* __restrict__ half, float* __restrict__ sx) {
   pdl_wait();
   pdl_trigger();
   const size_t row = blockIdx.x;
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(256) k_i8_half(const int8_t* __restrict__ q, l
     const uint2 w = *reinterpret_cast<const uint2*>(q + row * ldq + 8 * i);
     *reinterpret_cast<uint4*>(half + row * K + 8 * i) = half8(w.x, w.y);
   }
-  if (blockIdx.y == 0 && threadIdx.x == 0) sx[row] = s[row * lds];
+  if (blockIdx.y == 0 && threadIdx.x == 0) sx[row] = s[row];
 }
 
 // A CTA per block: two pieces of 16 bytes a thread.
@@ -154,9 +154,8 @@ cudaError_t launch_i8_rows(const I8RowsArgs& a, cudaStream_t st) {
   return pieces <= 256 * 8 ? rows<256, 8>(a, st) : rows<512, 8>(a, st);
 }
 
-cudaError_t launch_i8_half(const int8_t* q, long long ldq, const float* s, long long lds, int M, int K, uint16_t* half, float* sx,
-                           cudaStream_t st) {
-  return launch_q(k_i8_half, dim3(M, qceil(K, 4096)), 256, 0, st, q, ldq, s, lds, K, half, sx);
+cudaError_t launch_i8_half(const int8_t* q, long long ldq, const float* s, int M, int K, uint16_t* half, float* sx, cudaStream_t st) {
+  return launch_q(k_i8_half, dim3(M, qceil(K, 4096)), 256, 0, st, q, ldq, s, K, half, sx);
 }
 
 cudaError_t launch_i8_pack(const int8_t* W, int N, int K, uint8_t* image, cudaStream_t st) {

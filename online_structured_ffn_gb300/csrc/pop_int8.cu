@@ -292,7 +292,7 @@ pop_status pop_ilinear_forward_quantized(pop_ilinear_t h, const void* xq, long l
       a.sx = xs + m0;
       a.convert = 3;
     } else {
-      e = launch_i8_half(q, ldq, xs + m0, 1, n, h->cfg.K, h->c.rows, h->c.sx, st);
+      e = launch_i8_half(q, ldq, xs + m0, n, h->cfg.K, h->c.rows, h->c.sx, st);
     }
     if (e == cudaSuccess) e = product(h, a, y, ldy, m0, st);
     if (e != cudaSuccess) return cuda(e, call);
