@@ -6,6 +6,14 @@
 namespace pop {
 namespace {
 
+// 16 bytes that are read once. Not through the read-only path: this kernel starts before the one in front has ended, which may
+// be writing them.
+__device__ __forceinline__ uint4 ld_stream(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p) : "memory");
+  return r;
+}
+
 template <bool F32>
 struct Piece {
   static constexpr int V = F32 ? 4 : 8;  // values
@@ -42,7 +50,7 @@ __global__ void __launch_bounds__(T > 256 ? T : 256, (HELD > 4 ? 1024 : 1536) / 
   const uint4* x = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.x) + (on ? row : 0) * a.ldx * (F32 ? 4 : 2));
   uint4 held[HELD];
 #pragma unroll
-  for (int h = 0; h < HELD; ++h) held[h] = t + h * T < n ? ldg_stream(x + t + h * T) : make_uint4(0u, 0u, 0u, 0u);
+  for (int h = 0; h < HELD; ++h) held[h] = t + h * T < n ? ld_stream(x + t + h * T) : make_uint4(0u, 0u, 0u, 0u);
   float most = __uint_as_float(AMAX_MIN_BITS);
   if (a.amax) {
     for (int i = a.parts > 1 ? t : 0; on && i < a.parts; i += a.parts > 1 ? T : 1)
@@ -50,7 +58,7 @@ __global__ void __launch_bounds__(T > 256 ? T : 256, (HELD > 4 ? 1024 : 1536) / 
   } else {
 #pragma unroll
     for (int h = 0; h < HELD; ++h) most = Piece<F32>(held[h]).most(most);
-    for (int i = t + HELD * T; i < n; i += T) most = Piece<F32>(ldg_stream(x + i)).most(most);
+    for (int i = t + HELD * T; i < n; i += T) most = Piece<F32>(ld_stream(x + i)).most(most);
   }
   if (!a.amax || a.parts > 1) {
 #pragma unroll
@@ -93,23 +101,22 @@ __global__ void __launch_bounds__(T > 256 ? T : 256, (HELD > 4 ? 1024 : 1536) / 
 #pragma unroll
   for (int h = 0; h < HELD; ++h)
     if (t + h * T < n) put(t + h * T, held[h]);
-  for (int i = t + HELD * T; i < n; i += T) put(i, ldg_stream(x + i));
+  for (int i = t + HELD * T; i < n; i += T) put(i, ld_stream(x + i));
   if (t == 0) {
     a.s[row] = finite ? __fdiv_rn(most, 127.f) : __uint_as_float(0x7fffffffu);
     if (a.clear) a.clear[row] = 0u;
   }
 }
 
-__global__ void __launch_bounds__(256) k_i8_half(const int8_t* __restrict__ q, long long ldq, const float* __restrict__ s, int K,
-                                                 uint16_t* __restrict__ half, float* __restrict__ sx) {
+__global__ void __launch_bounds__(256) k_i8_half(const int8_t* q, long long ldq, const float* s, int K, uint16_t* half, float* sx) {
   pdl_wait();
   pdl_trigger();
   const size_t row = blockIdx.x;
   for (int i = blockIdx.y * 256 + threadIdx.x; i < K >> 3; i += 256 * gridDim.y) {
-    const uint2 w = *reinterpret_cast<const uint2*>(q + row * ldq + 8 * i);
+    const uint2 w = __ldcg(reinterpret_cast<const uint2*>(q + row * ldq + 8 * i));
     *reinterpret_cast<uint4*>(half + row * K + 8 * i) = half8(w.x, w.y);
   }
-  if (blockIdx.y == 0 && threadIdx.x == 0) sx[row] = s[row];
+  if (blockIdx.y == 0 && threadIdx.x == 0) sx[row] = __ldcg(s + row);
 }
 
 // A CTA per block: two pieces of 16 bytes a thread.
