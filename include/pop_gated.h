@@ -10,9 +10,11 @@
  *
  * x, dy and the matrices are bf16. The products run on the tensor cores and are summed in fp32; the activation
  * and its derivative are fp32. What one product hands to the next as an operand (h, dg, du) is rounded to bf16, once;
- * forward keeps g and u for backward with 16 significant bits (they are cut off there, an error of 2^-16) and h in
- * bf16. Outputs are rounded once to their type. The order of the additions depends on the sizes alone: the same call
- * gives the same bits. A row of x or dy that is not finite gives gradients of the matrices that are not; of y and
+ * forward keeps g and u for backward with 16 significant bits (they are cut off there, an error below 2^-15) and h in
+ * bf16. Outputs are rounded once to their type: out_f32 and grad_f32 spare that rounding, not those of h, dg and du (an
+ * output is 2.4e-3 of its norm from the definition in bf16, 1.7e-3 of it by its own rounding, 1.7e-3 in float32). The order of
+ * the additions depends on the sizes alone: the same call gives the same bits, and a gradient those that it has whichever
+ * others are asked for. A row of x or dy that is not finite gives gradients of the matrices that are not; of y and
  * dx it touches its own row alone.
  *
  * Conventions are those of pop_ffn.h (device pointers 16-byte aligned; stream-ordered calls; status returns; device
@@ -58,7 +60,7 @@ size_t pop_gated_saved_bytes(int D_FF, int M);
 pop_status pop_gated_forward(pop_gated_t h, const void* x, long long ldx, int M, const void* Wg, const void* W1,
                              const void* W2, void* y, long long ldy, void* saved, void* stream);
 
-/* The gradients of the call that filled `saved`, for the same x, M and matrices. dx, dWg, dW1, dW2: any of them may be
+/* The gradients of the call that filled `saved`, for the same x, M and matrices. dy is bf16 whatever y's type. dx, dWg, dW1, dW2: any of them may be
  * NULL and is then not computed. accumulate 1: the matrices' gradients are added to what dWg, dW1 and dW2 hold (in fp32,
  * before the rounding to their type); 0: they are overwritten, with M = 0 by zeros. `saved` is only read: a
  * second call gives the same. */

@@ -11,8 +11,10 @@
  * NaN; the other rows are not touched by it. q is never -128 then, but may be where it is given.
  *
  * Products: y[m, n] = s_x[m] * s_w[n] * (sum over k of q_x[m, k] * q_w[n, k]). The integers are exact in fp16 and so are
- * their products; they are summed in fp32 on the tensor cores, exactly as long as no partial sum passes 2^24, and
- * otherwise to the rounding of fp32. (sm_103a has no tensor-core product of 8-bit integers.) y is rounded once to its
+ * their products; they are summed in fp32 on the tensor cores, exactly as long as no partial sum passes 2^24. Beyond that an
+ * addition may be cut off at 2^-23 of the partial sum, so the error grows with K: at most K 2^-23 of the sum of the products'
+ * magnitudes. (sm_103a has no tensor-core product of 8-bit integers: the format saves memory, and time where the matrix's bytes
+ * are what a call takes; many rows take no less time than in bf16, and more than in e4m3, pop_quant.h.) y is rounded once to its
  * type. The order of the additions depends on the sizes alone: the same call gives the same bits.
  *
  * Conventions are those of pop_ffn.h (device pointers 16-byte aligned unless stated; stream-ordered calls; status returns;

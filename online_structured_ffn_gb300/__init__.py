@@ -833,7 +833,9 @@ class PopGatedFFN(_QHandle):
     """y = W2 (SiLU(Wg x) (.) (W1 x)) on bf16 matrices that the caller holds and trains, and its gradients
     (``pop_gated``). ``include/pop_gated.h`` has the formulas and what is rounded where.
 
-    The object holds workspace, no weights: one serves all layers of its sizes, one call at a time.
+    The object holds workspace, no weights: one serves all layers of its sizes, one call at a time. Its calls are
+    plain ones, of which autograd knows nothing: outputs have no gradients of their own, whatever inputs want some
+    (``examples/recover_int8.py`` makes a ``torch.autograd.Function`` of them).
     max_tokens: the most rows of a call. out_f32: y and dx are float32 instead of bf16; grad_f32: the
     matrices' gradients are."""
     _destroy, _checker, _limiter = "pop_gated_destroy", "pop_gated_check", "pop_gated_set_wait_limit"

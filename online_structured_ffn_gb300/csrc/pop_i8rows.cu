@@ -33,8 +33,9 @@ struct Piece {
   }
 };
 
-// T threads to a row, which hold HELD pieces of 16 bytes each between the two passes over it, a CTA of 256 (or T, if that is more) threads. A row's values stay in registers, as they stand in memory,
-// between the pass for the largest and the one that rounds; of rows longer than HELD pieces a thread the rest is read again.
+// T threads to a row, which hold HELD pieces of 16 bytes each between the two passes over it, a CTA of 256 (or T, if that is
+// more) threads. A row's values stay in registers, as they stand in memory, between the pass for the largest and the one that
+// rounds; of rows longer than HELD pieces a thread the rest is read again.
 // Bound by memory, with the row's largest in the way: 4096 x 4096 of bf16 9.8 us (5.1 TB/s read and written), 1001 x 11008 of
 // float32 11.3 (4.9), 16,384 x 1024 of bf16 9.3 (5.4).
 template <int T, int HELD, bool F32>

@@ -417,9 +417,9 @@ __global__ void __launch_bounds__(Kind<KIND>::threads, 1) k_wide16(const __grid_
   } else if (T::i8 && warp >= 12) {
     // ------------------------------------------------------------ 8-bit integers to fp16 (warps 12..23)
     // A row each thread, every third k-block the same four warps: a block takes a warp longer than its products take (with one set
-    // of warps 0.36 us and more a k-block, two 0.32, three 0.30). A slot of the ring has the same four every time: others, who
-    // have not looked at it before, could not tell a block that has not landed from the one before it, and copies may land out of
-    // order. (Stages are freed in order.)
+    // of warps 0.36 us and more a k-block, two 0.32, three 0.30; at the power limit, 4001 x 28672 x 8192, three are 2 % behind two).
+    // A slot of the ring has the same four every time: others, who have not looked at it before, could not tell a block that has
+    // not landed from the one before it, and copies may land out of order. (Stages are freed in order.)
     constexpr int SETS = 3;
     static_assert(RING8 % SETS == 0 && (!T::i8 || T::threads == 384 + 128 * SETS), "a slot's warps");
     const int r = threadIdx.x & 127;

@@ -62,7 +62,8 @@ int wide16_width(WKind kind, int m, int n, int num_sms);
 // All but W_DW: few rows by pop_thin16.cu, more by the wide products. (us of a whole MLP thin against wide, 4096 x 11008: bf16 65
 // rows 56/66, 128 61/67; 8-bit 57/86, 70/88; 1000 x 2736 bf16 16/19, 19/20; 8192 x 28672 bf16 231/227, 244/230, 8-bit 185/219,
 // 212/225. Forward and backward, the latter thin against wide: 4096 x 11008 8 rows 148/187, 100 181/203, 128 187/211; 2048 x 5496
-// 57/74, 72/83, 76/87; 1000 x 2736 30/40, 45/53, 46/55.)
+// 57/74, 72/83, 76/87; 1000 x 2736 30/40, 45/53, 46/55.) One border for all sizes: of bf16 matrices as large as 8192 x 28672 the thin
+// form of more than 64 rows is 2 to 6 % behind.
 constexpr int THIN16_MOST = 128;
 // CTAs to a tile of 128 outputs (pop_thin16.cu).
 int thin16_split(bool i8, int m, int n, int kb, int num_sms);
